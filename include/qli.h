@@ -333,6 +333,124 @@ qli_status qli_sparse_attention(const qli_attn_args *a, void *stream);
 /* sizeof(qli_attn_args) the library was built with. */
 int64_t qli_attn_args_size(void);
 
+/* ---- 8-bit KV rows ------------------------------------------------------------
+ * The KV rows of qli_sparse_attention at half the bytes: row r of a page holds
+ * D = 512 codes, one byte each, at kv_offset + r * 512 and one FP16 scale at
+ * kv_scale_offset + r * 2; the row's values are code * scale. Codes are INT8
+ * (quant_mode QLI_QUANT_INT8) or E4M3 (QLI_QUANT_FP8), the row quantisation is
+ * the index-K writer's (amax over the 512 values, Q = 127 or 448), and the
+ * index K and its scales may follow in the same page: the geometry is the
+ * caller's. One scale per row, because pages fill one position at a time: a
+ * scale over several rows would have to requantise the earlier ones. */
+
+/* Quantises n rows kv (row i: 512 BF16 values at kv + i * kv_stride; stride in
+ * elements, a multiple of 8, at least 512; 16-byte aligned) into the page slots
+ * slot_mapping[i] = page * rows_per_page + row. Negative slots, slots past the
+ * pool, distinctness, err_word and geometry checks as for qli_write_index_k.
+ * Inf and NaN inputs leave unspecified codes in their own row. One kernel on
+ * `stream`; asynchronous; n = 0 launches nothing. */
+qli_status qli_write_kv(const uint16_t *kv, int64_t kv_stride, int64_t n,
+                        const int64_t *slot_mapping, uint8_t *cache, int64_t num_pages,
+                        int64_t page_stride, int32_t rows_per_page, int64_t kv_offset,
+                        int64_t kv_scale_offset, int32_t quant_mode, uint32_t *err_word,
+                        void *stream);
+
+/* Reads back the rows named by slots[i]: out[i * out_stride + d] =
+ * BF16(code * scale) (stride in elements, a multiple of 8, at least 512; out
+ * 16-byte aligned). A negative slot gives a row of zeros, and so does one past
+ * the pool, which also sets QLI_DEVERR_PAGE. One kernel on `stream`. */
+qli_status qli_read_kv(const uint8_t *cache, int64_t num_pages, int64_t page_stride,
+                       int32_t rows_per_page, int64_t kv_offset, int64_t kv_scale_offset,
+                       int32_t quant_mode, const int64_t *slots, int64_t n, uint16_t *out,
+                       int64_t out_stride, uint32_t *err_word, void *stream);
+
+/* Softmax attention over 8-bit KV rows, one shared KV head, the row serving as
+ * key and value. For token t of request b and head h over the positions J(t):
+ *     kv_j = code_j * scale_j,   z_j = scale * sum_d q[t, h, d] * kv_j[d]
+ *     out[t, h, :] = BF16( sum_j exp(z_j - m) kv_j / sum_j exp(z_j - m) ),
+ *     lse[t, h] = m + ln(sum_j exp(z_j - m)),    m = max_j z_j;
+ * an empty J gives out = 0 and lse = -inf.
+ *  - With `indices`: J(t) = the entries >= 0 of indices[t, 0, :], as for
+ *    qli_sparse_attention (a position listed twice counts twice; a listed
+ *    position past the block table is skipped and flagged).
+ *  - Without: the positions the indexer's causal mask shows token t, V(t) of
+ *    them (k_lens, residual and ratio as in qli_args; a token no request covers
+ *    sees none), or the last `window` of them when window > 0.
+ * A block-table entry outside the pool skips its positions and is flagged.
+ * Rows no token attends to may hold anything. Scales must not be negative.
+ * The codes are multiplied as they are on the tensor cores (FP16, exact), q as
+ * FP16 times a power of two per head (exact unless a value is below 2^-24 of
+ * the head's largest), sums are FP32, and the weights times the row scales are
+ * rounded to FP16: out agrees with the definition to about 2^-11 of the largest
+ * value attended to, besides its own rounding. */
+typedef struct qli_kv_attn_args {
+    const uint16_t *q;           /* BF16 [T, H, 512]: (t, h, d) at q[t*q_stride_t + h*q_stride_h + d]
+                                    (strides in elements, multiples of 8, at least 512) */
+    int64_t q_stride_t, q_stride_h;
+    int32_t T, H, D;             /* tokens, heads (1..128), values per row (512) */
+    const int32_t *cu_seqlens_q; /* [B+1] raw query boundaries */
+    int32_t B;
+    const uint8_t *cache;        /* page pool; page p at cache + p * page_stride */
+    int64_t page_stride, num_pages;
+    int32_t rows_per_page;       /* 64 or 128 */
+    int32_t quant_mode;          /* QLI_QUANT_INT8 or QLI_QUANT_FP8 */
+    int64_t kv_offset;           /* bytes to row 0's codes (multiple of 16) */
+    int64_t kv_scale_offset;     /* bytes to row 0's scale (multiple of 2) */
+    const int32_t *block_table;  /* [B, bt_stride] page IDs */
+    int32_t bt_stride;
+    int32_t K;                   /* entries per token (>= 1) when indices is given */
+    const int32_t *indices;      /* [T, 1, K] positions, or NULL: every visible position */
+    const int32_t *k_lens;       /* [B], without indices */
+    const int32_t *residual;     /* [B] or NULL, without indices; NULL when ratio is 1 */
+    int32_t ratio;               /* 1 or 2, without indices */
+    int32_t window;              /* positions a token sees at most, 0: all (must be 0 with indices) */
+    float scale;                 /* softmax scale (finite) */
+    uint16_t *out;               /* BF16, strides in elements (multiples of 8, at least 512); 16-byte aligned */
+    int64_t out_stride_t, out_stride_h;
+    float *lse;                  /* [T, H] natural-log LSE, or NULL */
+    uint32_t *err_word;          /* device word or NULL: QLI_DEVERR_* bits are OR'ed in */
+} qli_kv_attn_args;
+
+/* Bytes of device workspace qli_kv_attention needs (from T, H and the device's
+ * SM count; no device memory is read). */
+qli_status qli_kv_attention_workspace_size(const qli_kv_attn_args *a, size_t *bytes);
+
+/* Queues the attention on `stream`. `workspace`: 256-byte aligned device memory
+ * of at least that size, contents irrelevant on entry, the caller's until the
+ * queued work is done; calls that share one run in order on one stream.
+ * Allocates nothing, never synchronises; nothing is launched on a non-OK
+ * status. The result does not depend on timing: the same call gives the same
+ * bits. */
+qli_status qli_kv_attention(const qli_kv_attn_args *a, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/* sizeof(qli_kv_attn_args) the library was built with. */
+int64_t qli_kv_attn_args_size(void);
+
+/* Joins attention results over disjoint sets of positions (for example a
+ * window's and the selected positions') by their log-sum-exps:
+ *     M = max_i lse_i,  w_i = exp(lse_i - M),
+ *     out = BF16( sum_i w_i out_i / sum_i w_i ),  lse = M + ln(sum_i w_i).
+ * A part whose lse is -inf drops out whatever its row holds; if all do, out = 0
+ * and lse = -inf. Sums are FP32. */
+#define QLI_MERGE_MAX 4
+typedef struct qli_merge_args {
+    const void *part_out[QLI_MERGE_MAX];     /* [T, H, 512] each, 16-byte aligned */
+    int64_t part_stride_t[QLI_MERGE_MAX];    /* elements, multiples of 16 bytes; 0 broadcasts */
+    int64_t part_stride_h[QLI_MERGE_MAX];
+    const float *part_lse[QLI_MERGE_MAX];    /* [T, H] each */
+    int32_t parts;                           /* 1..QLI_MERGE_MAX */
+    int32_t parts_f32;                       /* 0: BF16 parts, 1: FP32 parts */
+    int32_t T, H, D;                         /* D = 512 */
+    uint16_t *out;                           /* BF16, strides multiples of 8, at least 512 */
+    int64_t out_stride_t, out_stride_h;
+    float *lse;                              /* [T, H], or NULL */
+} qli_merge_args;
+qli_status qli_merge_attention(const qli_merge_args *a, void *stream);
+
+/* sizeof(qli_merge_args) the library was built with. */
+int64_t qli_merge_args_size(void);
+
 /* Human-readable name of a status. Never NULL. */
 const char *qli_status_string(qli_status s);
 

@@ -1,6 +1,7 @@
 // Device-side reading of the per-request metadata, shared by the planning
-// stage and the single-launch path for small batches, so that both clamp,
-// flag and assign tokens identically.
+// stage, the single-launch path for small batches and the attention over the
+// 8-bit KV rows, so that all clamp, flag and assign tokens identically (A is
+// any argument block with cu, k_lens, residual, T, B, ratio and cap).
 //
 // Guide "DeepSeek V4.1 QLI V2 与候选集成", section 数据流: raw query boundaries
 // (cu_seqlens_q), compressed K lengths and the raw length mod ratio (absent
@@ -27,8 +28,9 @@ __device__ __forceinline__ int32_t visible_count(int32_t lk, int32_t res, int32_
 // Request b on its own: the query range clamped into [0, T], the compressed
 // length into [0, cap] and the residual into [0, ratio); returns the error
 // bits of what was clamped.
-__device__ __forceinline__ uint32_t sanitize_request(const DevArgs& a, int b, int32_t& q0,
-                                                     int32_t& q1, int32_t& lk, int32_t& res) {
+template <class A>
+__device__ __forceinline__ uint32_t sanitize_request(const A& a, int b, int32_t& q0, int32_t& q1,
+                                                     int32_t& lk, int32_t& res) {
   uint32_t e = 0u;
   const int32_t c0 = a.cu[b], c1 = a.cu[b + 1];
   lk = a.k_lens[b];
@@ -51,7 +53,8 @@ __device__ __forceinline__ uint32_t sanitize_request(const DevArgs& a, int b, in
 // Token t's request is the last one starting at or before it (the sanitised
 // starts never decrease for valid metadata; a token no request covers has
 // V = 0 and owner -1). Returns V(t).
-__device__ __forceinline__ int32_t token_owner(const DevArgs& a, const int32_t* q0s,
+template <class A>
+__device__ __forceinline__ int32_t token_owner(const A& a, const int32_t* q0s,
                                                const int32_t* q1s, const int32_t* lks,
                                                const int32_t* ress, int t, int32_t& owner) {
   int32_t lo = 0, hi = a.B - 1;

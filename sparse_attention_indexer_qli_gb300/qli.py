@@ -69,12 +69,47 @@ class AttnArgs(ctypes.Structure):
     ]
 
 
+class KVAttnArgs(ctypes.Structure):
+    """Mirror of `qli_kv_attn_args` (field order and types as in include/qli.h)."""
+    _fields_ = [
+        ("q", c_void_p), ("q_stride_t", c_int64), ("q_stride_h", c_int64),
+        ("T", c_int32), ("H", c_int32), ("D", c_int32),
+        ("cu_seqlens_q", c_void_p), ("B", c_int32),
+        ("cache", c_void_p), ("page_stride", c_int64), ("num_pages", c_int64),
+        ("rows_per_page", c_int32), ("quant_mode", c_int32),
+        ("kv_offset", c_int64), ("kv_scale_offset", c_int64),
+        ("block_table", c_void_p), ("bt_stride", c_int32),
+        ("K", c_int32), ("indices", c_void_p), ("k_lens", c_void_p), ("residual", c_void_p),
+        ("ratio", c_int32), ("window", c_int32), ("scale", ctypes.c_float),
+        ("out", c_void_p), ("out_stride_t", c_int64), ("out_stride_h", c_int64),
+        ("lse", c_void_p), ("err_word", c_void_p),
+    ]
+
+
+MERGE_MAX = 4
+
+
+class MergeArgs(ctypes.Structure):
+    """Mirror of `qli_merge_args` (field order and types as in include/qli.h)."""
+    _fields_ = [
+        ("part_out", c_void_p * MERGE_MAX),
+        ("part_stride_t", c_int64 * MERGE_MAX), ("part_stride_h", c_int64 * MERGE_MAX),
+        ("part_lse", c_void_p * MERGE_MAX),
+        ("parts", c_int32), ("parts_f32", c_int32),
+        ("T", c_int32), ("H", c_int32), ("D", c_int32),
+        ("out", c_void_p), ("out_stride_t", c_int64), ("out_stride_h", c_int64),
+        ("lse", c_void_p),
+    ]
+
+
 EXPORTS = ["qli_validate", "qli_workspace_size", "qli_run", "qli_run_stage", "qli_launch_count",
            "qli_scores_layout", "qli_read_device_error", "qli_status_string", "qli_abi_version",
            "qli_args_size", "qli_run_static", "qli_read_static_device_error",
            "qli_quantize_q", "qli_write_index_k", "qli_quantize_q_fp8", "qli_write_index_k_fp8",
            "qli_check_quant_rounding",
-           "qli_sparse_attention", "qli_attn_args_size"]
+           "qli_sparse_attention", "qli_attn_args_size",
+           "qli_write_kv", "qli_read_kv", "qli_kv_attention", "qli_kv_attention_workspace_size",
+           "qli_kv_attn_args_size", "qli_merge_attention", "qli_merge_args_size"]
 
 _lib = None
 
@@ -120,6 +155,22 @@ def lib(path: Optional[str] = None) -> ctypes.CDLL:
     L.qli_attn_args_size.restype = c_int64
     if L.qli_attn_args_size() != ctypes.sizeof(AttnArgs):
         raise ImportError("qli_attn_args layout mismatch")
+    L.qli_write_kv.argtypes = [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_int64, c_int64,
+                               c_int32, c_int64, c_int64, c_int32, c_void_p, c_void_p]
+    L.qli_read_kv.argtypes = [c_void_p, c_int64, c_int64, c_int32, c_int64, c_int64, c_int32,
+                              c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p]
+    L.qli_kv_attention.argtypes = [ctypes.POINTER(KVAttnArgs), c_void_p, c_size_t, c_void_p]
+    L.qli_kv_attention_workspace_size.argtypes = [ctypes.POINTER(KVAttnArgs),
+                                                  ctypes.POINTER(c_size_t)]
+    L.qli_merge_attention.argtypes = [ctypes.POINTER(MergeArgs), c_void_p]
+    for name in ("qli_write_kv", "qli_read_kv", "qli_kv_attention",
+                 "qli_kv_attention_workspace_size", "qli_merge_attention"):
+        getattr(L, name).restype = c_int32
+    for name, mirror in (("qli_kv_attn_args", KVAttnArgs), ("qli_merge_args", MergeArgs)):
+        size = getattr(L, name + "_size")
+        size.restype = c_int64
+        if size() != ctypes.sizeof(mirror):
+            raise ImportError("%s layout mismatch" % name)
     for name in ["qli_validate", "qli_workspace_size", "qli_run", "qli_run_stage",
                  "qli_launch_count", "qli_scores_layout", "qli_read_device_error"]:
         getattr(L, name).restype = c_int32
@@ -374,3 +425,173 @@ def sparse_attention(q, cu_seqlens_q, cache, block_table, indices, *, rows_per_p
     _check(lib().qli_sparse_attention(ctypes.byref(a), _stream(stream)), "qli_sparse_attention")
     return out, lse
 
+
+
+def write_kv(kv, slot_mapping, cache, *, rows_per_page: int, page_stride: int, kv_offset: int,
+             kv_scale_offset: int, err_word=None, stream=None, quant_mode=QUANT_INT8):
+    """qli_write_kv: quantises the rows of kv [n, 512] (BF16, CUDA, unit stride
+    in the last dim) to INT8 or, with quant_mode=QUANT_FP8, E4M3 codes with an
+    FP16 scale per row, and writes them into the page pool `cache` (uint8,
+    CUDA) at slot_mapping [n] (int64: page * rows_per_page + row; negative =
+    skip)."""
+    import torch
+    _require_cuda("kv", kv, torch.bfloat16)
+    _require_cuda("slot_mapping", slot_mapping, torch.int64)
+    _require_cuda("cache", cache, torch.uint8)
+    _require_cuda("err_word", err_word, torch.int32)
+    if kv.dim() != 2 or kv.shape[1] != 512 or kv.stride(1) != 1:
+        raise ValueError("kv must be [n, 512] with unit stride in the last dim")
+    if not cache.is_contiguous() or not slot_mapping.is_contiguous():
+        raise ValueError("cache and slot_mapping must be contiguous")
+    n = kv.shape[0]
+    if slot_mapping.numel() != n:
+        raise ValueError("one slot per row")
+    _check(lib().qli_write_kv(kv.data_ptr(), kv.stride(0) if n > 1 else 512, n,
+                              slot_mapping.data_ptr(), cache.data_ptr(),
+                              cache.numel() // page_stride, page_stride, rows_per_page, kv_offset,
+                              kv_scale_offset, quant_mode, _ptr(err_word), _stream(stream)),
+           "qli_write_kv")
+
+
+def read_kv(cache, slots, *, rows_per_page: int, page_stride: int, kv_offset: int,
+            kv_scale_offset: int, out=None, err_word=None, stream=None, quant_mode=QUANT_INT8):
+    """qli_read_kv: the rows named by slots [n] (int64: page * rows_per_page +
+    row; negative = zeros) of the page pool `cache` as BF16 [n, 512]."""
+    import torch
+    _require_cuda("cache", cache, torch.uint8)
+    _require_cuda("slots", slots, torch.int64)
+    _require_cuda("err_word", err_word, torch.int32)
+    if not cache.is_contiguous() or not slots.is_contiguous():
+        raise ValueError("cache and slots must be contiguous")
+    n = slots.numel()
+    if out is None:
+        out = torch.empty((n, 512), dtype=torch.bfloat16, device=cache.device)
+    _require_cuda("out", out, torch.bfloat16)
+    if out.dim() != 2 or tuple(out.shape) != (n, 512) or out.stride(1) != 1:
+        raise ValueError("out must be [n, 512] with unit stride in the last dim")
+    _check(lib().qli_read_kv(cache.data_ptr(), cache.numel() // page_stride, page_stride,
+                             rows_per_page, kv_offset, kv_scale_offset, quant_mode,
+                             slots.data_ptr(), n, out.data_ptr(), out.stride(0) if n > 1 else 512,
+                             _ptr(err_word), _stream(stream)), "qli_read_kv")
+    return out
+
+
+def _attn_outputs(q_shape, device, out, lse):
+    """Output tensors of an attention over q [T, H, 512], made or checked."""
+    import torch
+    T, H, D = q_shape
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=device)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=device)
+    _require_cuda("out", out, torch.bfloat16)
+    _require_cuda("lse", lse, torch.float32)
+    if tuple(out.shape) != (T, H, D) or out.stride(2) != 1:
+        raise ValueError("out must be [T, H, 512] with unit stride in the last dim")
+    if tuple(lse.shape) != (T, H) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous [T, H] tensor")
+    return out, lse
+
+
+def kv_attention_workspace_bytes(T: int, H: int) -> int:
+    """Bytes of device workspace kv_attention needs for T tokens of H heads on
+    the current device."""
+    # the size comes from T and H alone; the other arguments are only checked
+    a = KVAttnArgs(256, H * 512, 512, T, H, 512, 256, 1, 256, 128 * 514, 1, 128, QUANT_INT8, 0,
+                   128 * 512, 256, 1, 1, 256, None, None, 1, 0, 1.0, 256, H * 512, 512, None, None)
+    n = c_size_t(0)
+    _check(lib().qli_kv_attention_workspace_size(ctypes.byref(a), ctypes.byref(n)),
+           "qli_kv_attention_workspace_size")
+    return int(n.value)
+
+
+def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, page_stride: int,
+                 kv_offset: int, kv_scale_offset: int, scale: float, indices=None, k_lens=None,
+                 residual=None, ratio: int = 1, window: int = 0, out=None, lse=None,
+                 workspace=None, err_word=None, stream=None, quant_mode=QUANT_INT8):
+    """qli_kv_attention: softmax attention of q [T, H, 512] (BF16, CUDA) over
+    8-bit KV rows read through block_table from the page pool `cache`: over the
+    positions of indices [T, 1, K] (int32, -1 skipped), or without indices over
+    the positions k_lens, residual and ratio make visible to each token (the
+    last `window` of them if window > 0). workspace: a 256-byte
+    aligned uint8 tensor of at least kv_attention_workspace_bytes(T, H) bytes,
+    allocated when not given. Returns
+    (out [T, H, 512] BF16, lse [T, H] float32)."""
+    import torch
+    _require_cuda("q", q, torch.bfloat16)
+    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("block_table", block_table),
+                    ("indices", indices), ("k_lens", k_lens), ("residual", residual),
+                    ("err_word", err_word)):
+        _require_cuda(name, t, torch.int32)
+    _require_cuda("cache", cache, torch.uint8)
+    if q.dim() != 3 or q.stride(2) != 1:
+        raise ValueError("q must be [T, H, 512] with unit stride in the last dim")
+    if not cache.is_contiguous() or not cu_seqlens_q.is_contiguous():
+        raise ValueError("cache and cu_seqlens_q must be contiguous")
+    if block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise ValueError("block_table must be [B, bt_stride] row-major")
+    T, H, D = q.shape
+    B = cu_seqlens_q.numel() - 1
+    if block_table.shape[0] < B:
+        raise ValueError("block_table needs a row per request")
+    K = 0
+    if indices is not None:
+        if indices.dim() != 3 or indices.shape[0] != T or indices.shape[1] != 1 \
+                or not indices.is_contiguous():
+            raise ValueError("indices must be a contiguous [T, 1, K] tensor")
+        K = indices.shape[2]
+    elif k_lens is None:
+        raise ValueError("either indices or k_lens must be given")
+    for name, t in (("k_lens", k_lens), ("residual", residual)):
+        if t is not None and (t.numel() != B or not t.is_contiguous()):
+            raise ValueError("%s must be a contiguous [B] tensor" % name)
+    out, lse = _attn_outputs(q.shape, q.device, out, lse)
+    a = KVAttnArgs(q.data_ptr(), q.stride(0), q.stride(1), T, H, D, cu_seqlens_q.data_ptr(), B,
+                   cache.data_ptr(), page_stride, cache.numel() // page_stride, rows_per_page,
+                   quant_mode, kv_offset, kv_scale_offset, block_table.data_ptr(),
+                   block_table.stride(0), K, _ptr(indices), _ptr(k_lens), _ptr(residual), ratio,
+                   window, scale, out.data_ptr(), out.stride(0), out.stride(1), lse.data_ptr(),
+                   _ptr(err_word))
+    if workspace is None:
+        workspace = torch.empty(max(256, kv_attention_workspace_bytes(T, H)), dtype=torch.uint8,
+                                device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    _require_cuda("workspace", workspace, torch.uint8)
+    _check(lib().qli_kv_attention(ctypes.byref(a), workspace.data_ptr(), workspace.numel(),
+                                  _stream(stream)), "qli_kv_attention")
+    return out, lse
+
+
+def merge_attention(outs, lses, *, out=None, lse=None, stream=None):
+    """qli_merge_attention: joins attention results over disjoint sets of
+    positions by their log-sum-exps. outs: one to four [T, H, 512] tensors (all
+    BF16 or all float32), lses: their contiguous [T, H] float32 log-sum-exps.
+    Returns (out [T, H, 512] BF16, lse [T, H] float32)."""
+    import torch
+    n = len(outs)
+    if n < 1 or n > MERGE_MAX or len(lses) != n:
+        raise ValueError("one to %d parts, each with its lse" % MERGE_MAX)
+    dtype, shape = outs[0].dtype, outs[0].shape
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("outs must be bfloat16 or float32")
+    if len(shape) != 3:
+        raise ValueError("outs must be [T, H, 512]")
+    a = MergeArgs()
+    for i, (o, l) in enumerate(zip(outs, lses)):
+        _require_cuda("outs[%d]" % i, o, dtype)
+        _require_cuda("lses[%d]" % i, l, torch.float32)
+        if o.shape != shape or o.stride(2) != 1:
+            raise ValueError("outs must share one [T, H, 512] shape with unit stride in the last dim")
+        if l.shape != shape[:2] or not l.is_contiguous():
+            raise ValueError("lses must be contiguous [T, H] tensors")
+        a.part_out[i] = o.data_ptr()
+        a.part_stride_t[i], a.part_stride_h[i] = o.stride(0), o.stride(1)
+        a.part_lse[i] = l.data_ptr()
+    out, lse = _attn_outputs(shape, outs[0].device, out, lse)
+    a.parts, a.parts_f32 = n, int(dtype == torch.float32)
+    a.T, a.H, a.D = shape
+    a.out, a.out_stride_t, a.out_stride_h = out.data_ptr(), out.stride(0), out.stride(1)
+    a.lse = lse.data_ptr()
+    _check(lib().qli_merge_attention(ctypes.byref(a), _stream(stream)), "qli_merge_attention")
+    return out, lse

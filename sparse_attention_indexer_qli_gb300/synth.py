@@ -42,6 +42,18 @@ def page_offsets(rows_per_page: int) -> tuple:
     return k_off, s_off
 
 
+def kv8_layout(rows_per_page: int) -> dict:
+    """A page of 8-bit KV rows, as byte offsets: the rows' codes (one byte per
+    value), their FP16 scales, the index-K rows and the FP16 index scales; the
+    stride is theirs together, 41216 for 64 rows and 82432 for 128."""
+    R = rows_per_page
+    s_kv = R * ATTN_D
+    k_off = s_kv + 2 * R
+    s_off = k_off + R * D
+    return {"kv_offset": 0, "kv_scale_offset": s_kv, "k_offset": k_off, "scale_offset": s_off,
+            "page_stride": s_off + 2 * R}
+
+
 def _fp16_bits(x: np.ndarray) -> np.ndarray:
     return np.ascontiguousarray(x.astype(np.float16).view(np.uint16))
 
