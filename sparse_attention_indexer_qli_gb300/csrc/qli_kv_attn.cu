@@ -3,9 +3,32 @@
 //   kv_j = c_j s_j,  z_j = scale q . kv_j,
 //   o = sum_j e^(z_j - m) kv_j / sum_j e^(z_j - m),  lse = m + ln sum.
 //
-// One CTA per (head, token): 32 positions at a time, a warp takes eight of
-// their dots (lanes split the 512 values), then every thread adds the 32
-// weighted rows to its four values of o.
+// With x_j = z_j log2 e, y_j = x_j + log2 s_j and a running reference M >=
+// max y_j - kSlack, the weight p_j = 2^(y_j - M + kShift) carries the row's
+// scale, so the value product runs on the codes themselves,
+//   o = sum p_j c_j / sum (p_j / s_j),
+// and p_j never leaves FP16 whatever the scales are: at most 2^(kSlack +
+// kShift) = 2^14, and what falls below 2^-25 is under 2^-31 of the largest.
+// Codes of both types are FP16 values; a BF16 query times a power of two per
+// head is one too (11 significand bits >= 8). So both contractions are
+// kind::f16 with exact products, and only p_j is rounded (2^-11).
+//
+// A unit of work is (token, 64 heads, 128 positions). The units of a launch
+// are split evenly and contiguously over one CTA per SM; a row tile (token,
+// 64 heads) that lies across CTAs leaves normalised FP32 pieces and their LSE
+// in the workspace, joined by merge_pieces_kernel. Thirteen warps:
+//   0-7   softmax: S (lane = position, column = head) from TMEM, weights to
+//         shared memory, at the end of a row tile the output from TMEM
+//   8-11  loaders: the row tile's queries; per unit the 128 rows' codes, two
+//         128-value quarters of the tile in flight in registers, widened to
+//         FP16 and stored in the 128-byte-swizzled tile
+//   12    MMA issuer: S[128 positions, 64 heads] = K Q^T quarter by quarter as
+//         the tile fills, then O^T[128 values, 64 heads] += V^T P^T for each
+//         quarter, from the same tile read MN-major; a pair of quarters is
+//         handed back as soon as its products are done
+// TMEM: two S accumulators (even and odd 16-value steps) of 64 columns, four
+// O^T quarters of 64. Shared memory: the FP16 tile (128 KB), the queries
+// (64 KB), the weights (16 KB).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -20,8 +43,38 @@ namespace kvattn {
 namespace {
 
 constexpr int kD = 512;
-constexpr int kThreads = 128;
-constexpr int kChunk = 32;
+constexpr int kHT = 64;                        // heads per row tile (MMA N)
+constexpr int kPos = 128;                      // positions per unit
+constexpr int kSoftWarps = 8, kLoadWarps = 4;
+constexpr int kLoadWarp0 = kSoftWarps, kMmaWarp = kSoftWarps + kLoadWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kRegion = kPos * 128;            // 64 values of every row of the tile
+constexpr int kQRegion = kHT * 128;            // 64 values of every query row
+constexpr int kChunkT = 2048;                  // tokens planned per launch
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSCol = 0, kOCol = 256;
+constexpr float kSlack = 8.0f, kShift = 6.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kPieceRow = kHT * kD;            // floats of a piece
+
+struct Smem {
+  uint8_t kv[8 * kRegion];                     // 1024-aligned
+  uint8_t q[8 * kQRegion];                     // 1024-aligned
+  uint8_t p[kPos * 128];                       // 1024-aligned
+  int32_t tokV[kChunkT];                       // visible positions of the launch's tokens
+  float rs[2][kPos];                           // row scales by unit parity; -inf: no position
+  float sl2[kHT];                              // softmax scale in log2, times the query's power of two
+  float m[kHT], alpha[kHT];
+  float part[2][4][32];                        // [head half][lane quarter][head]
+  int32_t flag[2][2][4];                       // [unit parity][head half][lane quarter]
+  int64_t warp_sum[kMmaWarp + 1];
+  int64_t start_u;                             // first unit of the CTA's first row tile's token
+  int32_t start_t;
+  uint64_t full[4], empty[2], sfull, pready, pvdone, done;
+  uint32_t tmem_base;
+};
+constexpr int kSmemBytes = static_cast<int>(sizeof(Smem)) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 struct Args {
   const uint16_t* q;
@@ -34,7 +87,7 @@ struct Args {
   int64_t cap;                 // bt_stride * R
   const uint8_t* cache;
   int64_t page_stride, num_pages, kv_off, sc_off;
-  int32_t R;
+  int32_t R, log2R;
   const int32_t* bt;
   int32_t bt_stride;
   const int32_t* idx;
@@ -44,138 +97,731 @@ struct Args {
   int64_t o_st, o_sh;
   float* lse;
   uint32_t* err;
+  int32_t t0, tc;              // tokens of this launch: t0 .. t0 + tc
+  int32_t hg;                  // row tiles per token
+  // workspace
+  int64_t* tok_start;          // [tc + 1] first unit of each token
+  float* piece;                // [2 * CTAs][64][512]
+  float* piece_lse;            // [2 * CTAs][64], log2
 };
 
-// Four codes to FP32 (lowest byte first).
+// Instruction descriptor, kind::f16 with FP16 A and B, FP32 D, M = 128, N = n;
+// a_mn / b_mn select MN-major operands.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t n, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) |
+         ((128u >> 4) << 24);
+}
+
+// Shared-memory descriptor, 128-byte swizzle. K-major: sbo = bytes between
+// 8-row groups (lbo unused). MN-major: lbo = bytes between 64-value atoms
+// along M or N, sbo = bytes between 8-row groups along K.
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+
+// Byte offset of 16-byte unit u of row r in a swizzled region of 128-byte rows.
+__device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t u) {
+  return r * 128u + ((u ^ (r & 7u)) << 4);
+}
+
+// 2^x by the SFU's approximation (a few ulp; 2^-inf = +0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void named_bar(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+// 16 codes to 16 FP16 values (exact), lowest byte first.
 template <bool kFp8>
-__device__ __forceinline__ void codes4(uint32_t w, float* f) {
+__device__ __forceinline__ void widen16(const uint4 v, uint32_t (&o)[8]) {
   if constexpr (kFp8) {
+    e4m3x16_to_f16x16(v, o);
+  } else {
+    // 0x64xx is the FP16 number 1024 + xx; the code plus 128 is xx
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const __half2 bias = __floats2half2_rn(-1152.0f, -1152.0f);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t h = e4m3x2_to_f16x2((w >> (16 * i)) & 0xffffu);
-      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      f[2 * i] = p.x;
-      f[2 * i + 1] = p.y;
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t u = w[k] ^ 0x80808080u;
+      const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+      const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&lo), bias);
+      const __half2 b = __hadd2(*reinterpret_cast<const __half2*>(&hi), bias);
+      o[2 * k] = *reinterpret_cast<const uint32_t*>(&a);
+      o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// The launch's units in order: token, row tile of the token, unit of 128
+// positions. A token has at least one unit, so that every output is written.
+__device__ __forceinline__ int32_t positions_of(const Args& a, int32_t V) {
+  return a.idx ? a.K : (a.window > 0 ? min(V, a.window) : V);
+}
+__device__ __forceinline__ int32_t units_of(const Args& a, int32_t V) {
+  const int32_t n = positions_of(a, V);
+  return n <= kPos ? 1 : (n - 1) / kPos + 1;
+}
+
+struct Walk {
+  int64_t u, u1;               // this unit, end of the CTA's share
+  int32_t t, g, i, n;          // token (within the launch), row tile, unit of it, its units
+  bool first;                  // first unit of the row tile in this CTA
+  __device__ __forceinline__ Walk(const Args& a, const Smem& S, int64_t u0, int64_t end)
+      : u(u0), u1(end), t(S.start_t), first(true) {
+    const int64_t off = u0 - S.start_u;
+    n = units_of(a, S.tokV[t]);
+    g = static_cast<int32_t>(off / n);
+    i = static_cast<int32_t>(off % n);
+  }
+  __device__ __forceinline__ bool valid() const { return u < u1; }
+  __device__ __forceinline__ bool last() const { return i == n - 1 || u + 1 == u1; }
+  __device__ __forceinline__ void next(const Args& a, const Smem& S) {
+    first = false;
+    ++u;
+    if (++i < n) return;
+    i = 0;
+    first = true;
+    if (++g < a.hg) return;
+    g = 0;
+    if (++t < a.tc) n = units_of(a, S.tokV[t]);
+  }
+};
+
+// Request of token t (absolute): the last one starting at or before it.
+// `cu` is the raw array or its copy in shared memory.
+__device__ __forceinline__ int32_t request_of(const int32_t* cu, int32_t B, int32_t T, int32_t t) {
+  int32_t lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) >> 1;
+    if (min(max(cu[mid], 0), T) <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Plans the launch: every token's visible positions and the CTA's first unit.
+// Returns all units of the launch. One pass over the tokens by the whole CTA.
+__device__ __forceinline__ int64_t plan(const Args& a, Smem& S, int64_t& u0, int64_t& u1) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the boundaries go through the (still unused) tile when they fit
+  int32_t* cu_s = reinterpret_cast<int32_t*>(S.kv);
+  const bool local = a.B <= static_cast<int32_t>(sizeof(S.kv) / 4);
+  if (!a.idx) {
+    if (local)
+      for (int b = tid; b < a.B; b += kThreads) cu_s[b] = __ldg(a.cu + b);
+    if (blockIdx.x == 0 && a.t0 == 0 && a.err) {
+      uint32_t e = 0u;
+      for (int b = tid; b < a.B; b += kThreads) {
+        int32_t q0, q1, lk, res;
+        e |= sanitize_request(a, b, q0, q1, lk, res);
+      }
+      if (e) atomicOr(a.err, e);
+    }
+    __syncthreads();
+    for (int i = tid; i < a.tc; i += kThreads) {
+      const int32_t t = a.t0 + i;
+      const int32_t b = request_of(local ? cu_s : a.cu, a.B, a.T, t);
+      int32_t q0, q1, lk, res;
+      sanitize_request(a, b, q0, q1, lk, res);
+      S.tokV[i] = q0 <= t && t < q1 ? visible_count(lk, res, a.ratio, q1 - q0, t - q0) : 0;
     }
   } else {
+    for (int i = tid; i < a.tc; i += kThreads) S.tokV[i] = 0;
+  }
+  __syncthreads();
+  const int per = (a.tc + kThreads - 1) / kThreads;
+  const int lo = min(a.tc, tid * per), hi = min(a.tc, lo + per);
+  int64_t mine = 0;
+  for (int i = lo; i < hi; ++i) mine += units_of(a, S.tokV[i]);
+  mine *= a.hg;
+  int64_t incl = mine;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      f[i] = static_cast<float>(static_cast<int8_t>((w >> (8 * i)) & 0xffu));
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) S.warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w <= kMmaWarp; ++w) {
+    const int64_t v = S.warp_sum[w];
+    if (w < warp) before += v;
+    total += v;
+  }
+  int64_t at = before + incl - mine;
+  u0 = total * blockIdx.x / gridDim.x;
+  u1 = total * (blockIdx.x + 1) / gridDim.x;
+  for (int i = lo; i < hi; ++i) {
+    const int64_t n = static_cast<int64_t>(units_of(a, S.tokV[i])) * a.hg;
+    if (blockIdx.x == 0) a.tok_start[i] = at;
+    if (at <= u0 && u0 < at + n) {
+      S.start_t = i;
+      S.start_u = at;
+    }
+    at += n;
+  }
+  if (blockIdx.x == 0 && tid == 0) a.tok_start[a.tc] = total;
+  __syncthreads();
+  return total;
+}
+
+// ---- loaders ----------------------------------------------------------------
+// One of the tile's rows: its codes, and its scale (-inf: no position there).
+struct Row {
+  const uint8_t* codes;
+  float s;
+};
+
+// Row r of unit (t, i). Positions past the table and pages outside the pool
+// are skipped and flagged.
+__device__ __forceinline__ Row find_row(const Args& a, const Smem& S, const Walk& w, int32_t b,
+                                        int r, bool& bad) {
+  Row x{nullptr, -INFINITY};
+  const int32_t V = S.tokV[w.t], n = positions_of(a, V), e = w.i * kPos + r;
+  if (e >= n) return x;
+  int64_t j = static_cast<int64_t>(V) - n + e;
+  if (a.idx) {
+    j = __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e);
+    if (j < 0) return x;
+    if (j >= a.cap) {
+      bad = true;
+      return x;
+    }
+  }
+  const int32_t page = __ldg(a.bt + static_cast<int64_t>(b) * a.bt_stride + (j >> a.log2R));
+  if (page < 0 || page >= a.num_pages) {
+    bad = true;
+    return x;
+  }
+  const uint8_t* base = a.cache + static_cast<int64_t>(page) * a.page_stride;
+  const int32_t row = static_cast<int32_t>(j) & (a.R - 1);
+  x.codes = base + a.kv_off + row * kD;
+  x.s = __half2float(__ushort_as_half(
+      __ldg(reinterpret_cast<const uint16_t*>(base + a.sc_off + row * 2))));
+  return x;
+}
+
+// The row tile's queries as FP16 times a power of two per head that brings the
+// head's largest magnitude to [2^13, 2^14); rows past H are zero.
+__device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, int32_t g, int lw) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kRows = kHT / kLoadWarps, kBatch = 4;
+#pragma unroll 1
+  for (int r0 = lw * kRows; r0 < (lw + 1) * kRows; r0 += kBatch) {
+    uint4 v[kBatch][2];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = g * kHT + r0 + k;
+      v[k][0] = v[k][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (h < a.H) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+                               a.q + static_cast<int64_t>(a.t0 + t) * a.q_st + h * a.q_sh) + lane;
+        v[k][0] = __ldg(src);
+        v[k][1] = __ldg(src + 32);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = r0 + k;
+      const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                             v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+      // magnitudes compare as integers (NaN above all)
+      uint32_t top = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        top = max(top, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = min(100, 13 - (static_cast<int>(top >> 23) - 127));
+      const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        o[i] = pack_half2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+      uint8_t* dst = S.q + (lane >> 3) * kQRegion + sw(r, lane & 7);
+      *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(dst + 4 * kQRegion) = make_uint4(o[4], o[5], o[6], o[7]);
+      if (lane == 0)
+        S.sl2[r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    }
   }
 }
 
-// Entry e of the token's positions as a row pointer; nullptr when skipped.
-__device__ __forceinline__ const uint8_t* row_of(const Args& a, int t, int b, int64_t j,
-                                                 int& row, bool& bad) {
-  (void)t;
-  if (j < 0) return nullptr;
-  if (j >= a.cap) {
-    bad = true;
-    return nullptr;
+// A warp's 32 rows of one quarter of the tile: eight loads a lane, each warp
+// instruction 128 bytes of four rows.
+struct Quarter {
+  uint4 v[8];
+};
+
+__device__ __forceinline__ void load_quarter(Quarter& b, const uint8_t* mine, int e, int lane) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint8_t* row = reinterpret_cast<const uint8_t*>(__shfl_sync(
+        0xffffffffu, reinterpret_cast<uintptr_t>(mine), 4 * k + (lane >> 3)));
+    b.v[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (row) b.v[k] = __ldg(reinterpret_cast<const uint4*>(row + e * 128) + (lane & 7));
   }
-  const int32_t page = __ldg(a.bt + static_cast<int64_t>(b) * a.bt_stride + j / a.R);
-  if (page < 0 || page >= a.num_pages) {
-    bad = true;
-    return nullptr;
+}
+
+// live: bit r set where row r's codes count (a row under a zero scale stands
+// for zeros whatever its codes are).
+template <bool kFp8>
+__device__ __forceinline__ void store_quarter(Smem& S, const Quarter& b, uint32_t live, int e, int lw,
+                                              int lane) {
+  const int j = lane & 7;
+  // lanes 4-7 of eight write their second unit first, so that eight lanes
+  // always cover all banks
+  const int swap = j >> 2;
+  uint8_t* region = S.kv + (2 * e + (j >> 2)) * kRegion;
+  const uint32_t u0 = ((2 * j) & 7) + swap, u1 = ((2 * j) & 7) + (swap ^ 1);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int rr = 4 * k + (lane >> 3);
+    const uint32_t r = 32 * lw + rr;
+    uint4 v = b.v[k];
+    if (!((live >> rr) & 1u)) v = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t o[8];
+    widen16<kFp8>(v, o);
+    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(region + sw(r, u0)) = swap ? hi : lo;
+    *reinterpret_cast<uint4*>(region + sw(r, u1)) = swap ? lo : hi;
   }
-  row = static_cast<int>(j % a.R);
-  return a.cache + page * a.page_stride;
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kThreads) kv_attn_kernel(Args a) {
-  __shared__ float qs[kD];
-  __shared__ float z[kChunk], rs[kChunk];
-  __shared__ const uint8_t* base[kChunk];
-  __shared__ int32_t tok[3];                   // request, first position, end
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x, t = blockIdx.y;
-  if (tid == 0) {
-    int32_t lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int32_t mid = (lo + hi + 1) >> 1;
-      if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    tok[0] = lo;
-    tok[1] = 0;
-    tok[2] = a.K;
-    if (a.idx == nullptr) {
-      int32_t q0, q1, lk, res;
-      const uint32_t e = sanitize_request(a, lo, q0, q1, lk, res);
-      if (e != 0u && a.err != nullptr) atomicOr(a.err, e);
-      const int32_t V = q0 <= t && t < q1 ? visible_count(lk, res, a.ratio, q1 - q0, t - q0) : 0;
-      tok[1] = a.window > 0 ? max(0, V - a.window) : 0;
-      tok[2] = V;
-    }
-  }
-  for (int d = tid; d < kD; d += kThreads)
-    qs[d] = __uint_as_float(static_cast<uint32_t>(a.q[t * a.q_st + h * a.q_sh + d]) << 16);
-  __syncthreads();
-  float qr[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) qr[i] = qs[16 * lane + i];
-  float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  bool bad = false;
-  for (int64_t p0 = tok[1]; p0 < tok[2]; p0 += kChunk) {
-    __syncthreads();
-    if (tid < kChunk) {
-      const int64_t e = p0 + tid;
-      int64_t j = -1;
-      if (e < tok[2]) j = a.idx ? __ldg(a.idx + static_cast<int64_t>(t) * a.K + e) : e;
-      int row = 0;
-      const uint8_t* page = row_of(a, t, tok[0], j, row, bad);
-      base[tid] = page ? page + a.kv_off + row * kD : nullptr;
-      rs[tid] = page ? __half2float(*reinterpret_cast<const __half*>(page + a.sc_off + row * 2)) : 0.0f;
-    }
-    __syncthreads();
-    for (int i = warp; i < kChunk; i += kThreads / 32) {
-      float s = 0.0f;
-      if (base[i]) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(base[i]) + lane);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float f[4];
-          codes4<kFp8>(w[k], f);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) s = fmaf(f[x], qr[4 * k + x], s);
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+__device__ __forceinline__ bool run_loaders(const Args& a, Smem& S, int64_t u0, int64_t u1) {
+  const int lane = threadIdx.x & 31, lw = (threadIdx.x >> 5) - kLoadWarp0, r = 32 * lw + lane;
+  bool bad = false, ok = true;
+  Walk w(a, S, u0, u1), ahead(a, S, u0, u1);
+  int32_t b = request_of(a.cu, a.B, a.T, a.t0 + w.t), bt = w.t;
+  Row cur = find_row(a, S, ahead, b, r, bad);
+  Quarter x, y;
+  load_quarter(x, cur.codes, 0, lane);
+  load_quarter(y, cur.codes, 1, lane);
+  for (uint32_t n = 0; w.valid(); ++n) {
+    // the next unit's rows, whose loads go out during this one
+    ahead.next(a, S);
+    Row nxt{nullptr, -INFINITY};
+    if (ahead.valid()) {
+      if (ahead.t != bt) {
+        bt = ahead.t;
+        b = request_of(a.cu, a.B, a.T, a.t0 + bt);
       }
-      if (lane == 0) z[i] = base[i] ? s * rs[i] * a.scale : -INFINITY;
+      nxt = find_row(a, S, ahead, b, r, bad);
     }
-    __syncthreads();
-    float top = m;
+    const uint32_t live = __ballot_sync(0xffffffffu, cur.codes != nullptr && cur.s != 0.0f);
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) top = fmaxf(top, z[i]);
-    if (top == -INFINITY) continue;
-    const float alpha = expf(m - top);
-    m = top;
-    l *= alpha;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) o[x] *= alpha;
-    for (int i = 0; i < kChunk; ++i) {
-      if (!base[i]) continue;
-      const float p = expf(z[i] - m);
-      l += p;
-      float f[4];
-      codes4<kFp8>(__ldg(reinterpret_cast<const uint32_t*>(base[i]) + tid), f);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[x] = fmaf(p * rs[i], f[x], o[x]);
+    for (int pair = 0; pair < 2; ++pair) {
+      if (ok && !mbar_wait_warp(&S.empty[pair], (n & 1) ^ 1)) ok = false;
+      if (!ok) break;
+      if (pair == 0) {
+        if (w.first) {
+          // the products with the previous queries are done: the tile's second
+          // pair was handed back after them
+          if (!mbar_wait_warp(&S.empty[1], (n & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          load_queries(a, S, w.t, w.g, lw);
+        }
+        S.rs[n & 1][r] = cur.s;
+      }
+      store_quarter<kFp8>(S, x, live, 2 * pair, lw, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.full[2 * pair]);
+      load_quarter(x, pair ? nxt.codes : cur.codes, pair ? 0 : 2, lane);
+      store_quarter<kFp8>(S, y, live, 2 * pair + 1, lw, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.full[2 * pair + 1]);
+      load_quarter(y, pair ? nxt.codes : cur.codes, pair ? 1 : 3, lane);
     }
+    if (!ok) break;
+    cur = nxt;
+    w.next(a, S);
   }
-  if (bad && a.err != nullptr) atomicOr(a.err, QLI_DEVERR_PAGE);
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  uint16_t* dst = a.out + t * a.o_st + h * a.o_sh + 4 * tid;
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    const __nv_bfloat16 y = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[x] * inv);
-    dst[x] = *reinterpret_cast<const uint16_t*>(&y);
-  }
-  if (tid == 0 && a.lse != nullptr)
-    a.lse[static_cast<int64_t>(t) * a.H + h] = l == 0.0f ? -INFINITY : m + logf(l);
+  if (bad && a.err) atomicOr(a.err, QLI_DEVERR_PAGE);
+  return ok;
 }
+
+// ---- MMA issuer (one thread) --------------------------------------------------
+__device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem, int64_t u0, int64_t u1) {
+  constexpr uint32_t id_qk = idesc_f16(kHT, false, false), id_pv = idesc_f16(kHT, true, true);
+  const uint32_t kvb = smem_u32(S.kv), qb = smem_u32(S.q), pb = smem_u32(S.p);
+  bool ok = true;
+  uint32_t n = 0;
+  for (Walk w(a, S, u0, u1); w.valid(); w.next(a, S), ++n) {
+#pragma unroll 1
+    for (uint32_t e = 0; e < 4 && ok; ++e) {
+      if (!mbar_wait_bounded(&S.full[e], n & 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) {
+        const uint32_t reg = 2 * e + (k >> 2), off = (k & 3) * 32;
+        mma_f16_ss(tmem + kSCol + (k & 1) * kHT, sdesc(kvb + reg * kRegion + off, 16, 1024),
+                   sdesc(qb + reg * kQRegion + off, 16, 1024), id_qk, (e | (k >> 1)) ? 1u : 0u);
+      }
+    }
+    if (!ok) break;
+    mma_commit(&S.sfull);
+    if (!mbar_wait_bounded(&S.pready, n & 1)) {
+      ok = false;
+      break;
+    }
+    tc_fence_after();
+#pragma unroll 1
+    for (uint32_t pair = 0; pair < 2; ++pair) {
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) {
+#pragma unroll
+        for (uint32_t f = 0; f < 2; ++f) {
+          const uint32_t e = 2 * pair + f;
+          mma_f16_ss(tmem + kOCol + e * kHT, sdesc(kvb + 2 * e * kRegion + k * 2048, kRegion, 1024),
+                     sdesc(pb + k * 2048, 1024, 1024), id_pv, (w.first && k == 0) ? 0u : 1u);
+        }
+      }
+      mma_commit(&S.empty[pair]);
+    }
+    mma_commit(&S.pvdone);
+  }
+  return ok;
+}
+
+// ---- softmax ------------------------------------------------------------------
+// Combines 32 values a lane across the warp's 32 lanes: lane l gets value l's
+// result.
+template <class F>
+__device__ __forceinline__ float across(float (&v)[32], int lane, F f) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+  return v[0];
+}
+
+__device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tmem, int64_t u0,
+                                            int64_t u1) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int qw = warp & 3, half = warp >> 2;          // TMEM lane quarter; heads 32 half ..
+  const uint32_t lanes = static_cast<uint32_t>(32 * qw) << 16;
+  const int pos = 32 * qw + lane, bar = 1 + half;
+  float* part = S.part[half][0];
+  const float4* sl4 = reinterpret_cast<const float4*>(S.sl2 + 32 * half);
+  const float4* m4 = reinterpret_cast<const float4*>(S.m + 32 * half);
+  const float4* al4 = reinterpret_cast<const float4*>(S.alpha + 32 * half);
+  bool ok = true, seen = false;
+  float l[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) l[i] = 0.0f;
+  uint32_t n = 0;
+  // A wait that gives up clears `ok`; the warps still run through the same
+  // named barriers, on whatever TMEM holds, and write no output.
+  for (Walk w(a, S, u0, u1); w.valid(); w.next(a, S), ++n) {
+    if (ok && !mbar_wait_warp(&S.full[0], n & 1)) ok = false;     // the row scales are there
+    if (ok && !mbar_wait_warp(&S.sfull, n & 1)) ok = false;
+    tc_fence_after();
+    if (w.first) {
+      seen = false;
+      if (qw == 0) S.m[32 * half + lane] = 0.0f;
+      named_bar(bar, 128);
+    }
+    float x[32];
+    {
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tmem + lanes + kSCol + 32 * half, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+      tmem_ld_32x32b_x32(tmem + lanes + kSCol + kHT + 32 * half, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(r[i]);
+    }
+    // no position here: y = -inf, p = 0. A row of zeros (scale 0) counts in the
+    // normaliser only; the smallest scale keeps it from setting the reference.
+    const float raw = S.rs[n & 1][pos];
+    const bool valid = raw != -INFINITY;
+    const float s = valid ? (raw == 0.0f ? 5.9604645e-8f : raw) : 0.0f;
+    const float ls = valid ? log2f(s) : -INFINITY, inv_s = valid ? 1.0f / s : 0.0f;
+    float over = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 c = sl4[i], m = m4[i];
+      const float cc[4] = {c.x, c.y, c.z, c.w}, mm[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[4 * i + k] = fmaf(x[4 * i + k] * cc[k], s, ls);
+        over = fmaxf(over, x[4 * i + k] - mm[k]);
+      }
+    }
+    const bool rises = __any_sync(0xffffffffu, over > kSlack);
+    const bool some = __any_sync(0xffffffffu, valid);
+    if (lane == 0) S.flag[n & 1][half][qw] = (rises ? 1 : 0) | (some ? 2 : 0);
+    named_bar(bar, 128);
+    const int32_t* fl = S.flag[n & 1][half];
+    const int32_t flags = fl[0] | fl[1] | fl[2] | fl[3];
+    if ((flags & 1) || ((flags & 2) && !seen)) {
+      // move the references to the maxima so far
+      float y[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) y[i] = x[i];
+      part[qw * 32 + lane] = across(y, lane, [](float p, float q) { return fmaxf(p, q); });
+      const float old = S.m[32 * half + lane];
+      named_bar(bar, 128);
+      float top = fmaxf(fmaxf(part[lane], part[32 + lane]), fmaxf(part[64 + lane], part[96 + lane]));
+      // each head decides for itself; a non-finite one keeps its reference
+      if ((seen && !(top > old + kSlack)) || !(fabsf(top) < INFINITY)) top = old;
+      if (qw == 0) {
+        S.m[32 * half + lane] = top;
+        S.alpha[32 * half + lane] = seen ? ex2(old - top) : 1.0f;
+      }
+      named_bar(bar, 128);
+      if (seen) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 al = al4[i];
+          l[4 * i] *= al.x;
+          l[4 * i + 1] *= al.y;
+          l[4 * i + 2] *= al.z;
+          l[4 * i + 3] *= al.w;
+        }
+      }
+      if (!w.first) {
+        // the products of the units before are done: this unit's tile was
+        // filled after them
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+          uint32_t o[32];
+          const uint32_t at = tmem + lanes + kOCol + e * kHT + 32 * half;
+          tmem_ld_32x32b_x32(at, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * S.alpha[32 * half + i]);
+          tmem_st_32x32b_x32(at, o);
+        }
+        tmem_st_wait();
+      }
+      seen = true;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 ma = m4[2 * i], mb = m4[2 * i + 1];
+      const float mm[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+      float p[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        p[k] = ex2(x[8 * i + k] - (mm[k] - kShift));
+        l[8 * i + k] = fmaf(p[k], inv_s, l[8 * i + k]);
+      }
+      *reinterpret_cast<uint4*>(&S.p[sw(pos, 4 * half + i)]) =
+          make_uint4(pack_half2(p[0], p[1]), pack_half2(p[2], p[3]), pack_half2(p[4], p[5]),
+                     pack_half2(p[6], p[7]));
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.pready);
+    if (!w.last()) continue;
+
+    // ---- the row tile's end in this CTA: totals, then the output
+    part[qw * 32 + lane] = across(l, lane, [](float p, float q) { return p + q; });
+#pragma unroll
+    for (int i = 0; i < 32; ++i) l[i] = 0.0f;
+    named_bar(bar, 128);
+    const float total = (part[lane] + part[32 + lane]) + (part[64 + lane] + part[96 + lane]);
+    const float lse2 = total == 0.0f ? -INFINITY : S.m[32 * half + lane] - kShift + log2f(total);
+    named_bar(bar, 128);
+    if (qw == 0) S.alpha[32 * half + lane] = total == 0.0f ? 0.0f : 1.0f / total;
+    named_bar(bar, 128);
+    if (ok && !mbar_wait_warp(&S.pvdone, n & 1)) ok = false;
+    tc_fence_after();
+    const int32_t h = w.g * kHT + 32 * half;          // first head of this half
+    const bool whole = w.i == w.n - 1 && w.u - u0 >= w.n - 1;
+    if (!ok) {
+      // nothing to write
+    } else if (whole) {
+      if (qw == 0 && h + lane < a.H && a.lse)
+        a.lse[static_cast<int64_t>(a.t0 + w.t) * a.H + h + lane] = lse2 * kLn2;
+      uint16_t* orow = a.out + static_cast<int64_t>(a.t0 + w.t) * a.o_st + h * a.o_sh;
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tmem + lanes + kOCol + e * kHT + 32 * half, o);
+        tmem_ld_wait();
+        const int v = e * 128 + pos;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float inv = S.alpha[32 * half + i];
+          const __nv_bfloat16 y = __float2bfloat16_rn(__uint_as_float(o[i]) * inv);
+          if (h + i < a.H) orow[i * a.o_sh + v] = *reinterpret_cast<const uint16_t*>(&y);
+        }
+      }
+    } else {
+      // a row tile that began in an earlier CTA goes to slot 0, one that goes
+      // on in the next to slot 1
+      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.u - u0 >= w.i ? 1 : 0);
+      if (qw == 0) a.piece_lse[slot * kHT + 32 * half + lane] = lse2;
+      float* dst = a.piece + slot * kPieceRow + (32 * half) * kD;
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tmem + lanes + kOCol + e * kHT + 32 * half, o);
+        tmem_ld_wait();
+        const int v = e * 128 + pos;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (h + i < a.H) dst[i * kD + v] = __uint_as_float(o[i]) * S.alpha[32 * half + i];
+      }
+    }
+    named_bar(bar, 128);                              // the factors are read
+  }
+  return ok;
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem& S = *reinterpret_cast<Smem*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  if (warp == kMmaWarp) tmem_alloc(&S.tmem_base, kTmemCols);
+  if (tid == 0) {
+    for (int e = 0; e < 4; ++e) mbar_init(&S.full[e], kLoadWarps);
+    for (int e = 0; e < 2; ++e) mbar_init(&S.empty[e], 1);
+    mbar_init(&S.sfull, 1);
+    mbar_init(&S.pready, kSoftWarps);
+    mbar_init(&S.pvdone, 1);
+    mbar_init(&S.done, 1);
+    fence_mbar_init();
+  }
+  int64_t u0, u1;
+  tc_fence_before();
+  plan(a, S, u0, u1);                                 // ends with a barrier of the CTA
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  if (u0 < u1) {
+    bool ok = true;
+    if (warp < kSoftWarps) {
+      ok = run_softmax(a, S, tmem, u0, u1);
+    } else if (warp < kMmaWarp) {
+      ok = run_loaders<kFp8>(a, S, u0, u1);
+    } else if (lane == 0) {
+      ok = run_mma(a, S, tmem, u0, u1);
+      mma_commit(&S.done);                            // every product of the CTA
+      (void)mbar_wait_drain(&S.done, 0);
+    }
+    if (!ok && lane == 0 && a.err) atomicOr(a.err, QLI_DEVERR_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---- joining the pieces ---------------------------------------------------------
+// Block (c, k): the row tile that boundary c (between CTA c - 1 and CTA c) is
+// the first to cut, rows 8k .. 8k+7 of it, a warp per row.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = kJoinThreads / 32;
+
+__global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a, int32_t ctas) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31, c = blockIdx.x + 1;
+  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const int64_t U = a.tok_start[a.tc];
+  const int64_t uc = U * c / ctas, ub = U * (c - 1) / ctas;
+  if (uc == ub || uc >= U) return;
+  int32_t lo = 0, hi = a.tc - 1;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) >> 1;
+    if (a.tok_start[mid] <= uc) lo = mid; else hi = mid - 1;
+  }
+  const int64_t base = a.tok_start[lo], n = (a.tok_start[lo + 1] - base) / a.hg;
+  const int32_t g = static_cast<int32_t>((uc - base) / n);
+  const int64_t start = base + g * n, end = start + n;
+  const int32_t h = g * kHT + row;
+  if (uc == start || ub > start || h >= a.H) return;   // not cut, or cut before
+  // pieces: CTA c - 1's slot 1, then slot 0 of CTA c, c + 1, ... up to the end
+  int32_t last = c;
+  while (last + 1 < ctas && U * (last + 1) / ctas < end) ++last;
+  const int32_t count = last - c + 2;
+  const auto slot = [&](int32_t k) -> int64_t {
+    return k == 0 ? 2 * static_cast<int64_t>(c - 1) + 1 : 2 * static_cast<int64_t>(c - 1 + k);
+  };
+  // a CTA without units left no piece
+  const auto lse_of = [&](int32_t k) -> float {
+    const int64_t cta = c - 1 + k;
+    if (U * cta / ctas == U * (cta + 1) / ctas) return -INFINITY;
+    return a.piece_lse[slot(k) * kHT + row];
+  };
+  float m = -INFINITY;
+  for (int32_t k = lane; k < count; k += 32) m = fmaxf(m, lse_of(k));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float acc[16], total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+  for (int32_t k0 = 0; k0 < count; k0 += 32) {
+    const float mine = k0 + lane < count ? lse_of(k0 + lane) : -INFINITY;
+    const float wk = mine == -INFINITY ? 0.0f : ex2(mine - m);
+    const int32_t some = min(32, count - k0);
+#pragma unroll 4
+    for (int32_t k = 0; k < some; ++k) {
+      const float w = __shfl_sync(0xffffffffu, wk, k);
+      if (w == 0.0f) continue;
+      total += w;
+      const float4* src = reinterpret_cast<const float4*>(
+          a.piece + slot(k0 + k) * kPieceRow + static_cast<int64_t>(row) * kD);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = src[(i >> 1) * 64 + 2 * lane + (i & 1)];
+        acc[4 * i] = fmaf(w, v.x, acc[4 * i]);
+        acc[4 * i + 1] = fmaf(w, v.y, acc[4 * i + 1]);
+        acc[4 * i + 2] = fmaf(w, v.z, acc[4 * i + 2]);
+        acc[4 * i + 3] = fmaf(w, v.w, acc[4 * i + 3]);
+      }
+    }
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const int64_t t = a.t0 + lo;
+  uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.o_st + h * a.o_sh) + lane;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 y = __floats2bfloat162_rn(acc[8 * i + 2 * k] * inv, acc[8 * i + 2 * k + 1] * inv);
+      w[k] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    dst[32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (lane == 0 && a.lse)
+    a.lse[t * a.H + h] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
+}
+
+std::atomic<uint64_t> g_smem_kv_attn[2];
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
@@ -235,6 +881,7 @@ Args make_args(const qli_kv_attn_args& a) {
   d.kv_off = a.kv_offset;
   d.sc_off = a.kv_scale_offset;
   d.R = a.rows_per_page;
+  d.log2R = a.rows_per_page == 64 ? 6 : 7;
   d.bt = a.block_table;
   d.bt_stride = a.bt_stride;
   d.idx = a.indices;
@@ -245,7 +892,48 @@ Args make_args(const qli_kv_attn_args& a) {
   d.o_sh = a.out_stride_h;
   d.lse = a.lse;
   d.err = a.err_word;
+  d.hg = (a.H + kHT - 1) / kHT;
   return d;
+}
+
+// CTAs of a launch over tc tokens: one per SM, and no more than there can be
+// units (known on the host for lists only).
+int32_t ctas_for(const Args& d, int32_t tc, int sms) {
+  if (d.idx == nullptr) return sms;
+  const int64_t units = static_cast<int64_t>(tc) * d.hg * ((static_cast<int64_t>(d.K) - 1) / kPos + 1);
+  return static_cast<int32_t>(units < sms ? units : sms);
+}
+
+// Workspace: the tokens' first units, then two pieces and their LSE per SM.
+struct Layout {
+  size_t piece, lse, total;
+};
+Layout layout_for(int sms) {
+  Layout L{};
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  L.piece = up(sizeof(int64_t) * (kChunkT + 1));
+  L.lse = L.piece + up(sizeof(float) * 2 * static_cast<size_t>(sms) * kPieceRow);
+  L.total = L.lse + up(sizeof(float) * 2 * static_cast<size_t>(sms) * kHT);
+  return L;
+}
+
+template <bool kFp8>
+cudaError_t launch(Args d, int sms, cudaStream_t s) {
+  const auto kernel = kv_attn_kernel<kFp8>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kSmemBytes,
+                                    g_smem_kv_attn[kFp8 ? 1 : 0]);
+  for (d.t0 = 0; e == cudaSuccess && d.t0 < d.T; d.t0 += kChunkT) {
+    d.tc = d.T - d.t0 < kChunkT ? d.T - d.t0 : kChunkT;
+    const int32_t ctas = ctas_for(d, d.tc, sms);
+    kernel<<<static_cast<unsigned>(ctas), kThreads, kSmemBytes, s>>>(d);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && ctas > 1)
+      e = launch_pdl(merge_pieces_kernel,
+                     dim3(static_cast<unsigned>(ctas - 1),
+                          static_cast<unsigned>(((d.H < kHT ? d.H : kHT) + kJoinRows - 1) / kJoinRows)),
+                     dim3(kJoinThreads), 0, s, d, ctas);
+  }
+  return e;
 }
 
 }  // namespace
@@ -254,32 +942,36 @@ Args make_args(const qli_kv_attn_args& a) {
 
 extern "C" qli_status qli_kv_attention_workspace_size(const qli_kv_attn_args* a, size_t* bytes) {
   if (bytes == nullptr) return QLI_ERR_INVALID_ARG;
-  const qli_status st = qli::kvattn::validate(a);
+  qli_status st = qli::kvattn::validate(a);
   if (st != QLI_OK) return st;
   *bytes = 0;
-  return QLI_OK;
+  if (a->T == 0) return QLI_OK;
+  int sms = 0;
+  st = qli::device_sms(&sms);
+  if (st == QLI_OK) *bytes = qli::kvattn::layout_for(sms).total;
+  return st;
 }
 
 extern "C" qli_status qli_kv_attention(const qli_kv_attn_args* a, void* workspace,
                                        size_t workspace_bytes, void* stream) {
   using namespace qli::kvattn;
-  (void)workspace;
-  (void)workspace_bytes;
   qli_status st = validate(a);
   if (st != QLI_OK) return st;
   if (a->T == 0) return QLI_OK;
-  if (a->T > 65535) return QLI_ERR_UNSUPPORTED;
   int sms = 0;
   st = qli::device_sms(&sms);
   if (st != QLI_OK) return st;
-  const Args d = make_args(*a);
-  const dim3 grid(static_cast<unsigned>(a->H), static_cast<unsigned>(a->T));
+  const Layout L = layout_for(sms);
+  if (workspace == nullptr || workspace_bytes < L.total) return QLI_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(workspace, 256)) return QLI_ERR_ALIGNMENT;
+  Args d = make_args(*a);
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  d.tok_start = reinterpret_cast<int64_t*>(w);
+  d.piece = reinterpret_cast<float*>(w + L.piece);
+  d.piece_lse = reinterpret_cast<float*>(w + L.lse);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a->quant_mode == QLI_QUANT_FP8)
-    kv_attn_kernel<true><<<grid, kThreads, 0, s>>>(d);
-  else
-    kv_attn_kernel<false><<<grid, kThreads, 0, s>>>(d);
-  return cudaGetLastError() == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
+  const cudaError_t e = a->quant_mode == QLI_QUANT_FP8 ? launch<true>(d, sms, s) : launch<false>(d, sms, s);
+  return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
 }
 
 extern "C" int64_t qli_kv_attn_args_size(void) {
