@@ -47,7 +47,9 @@ constexpr int kHT = 64;                        // heads per row tile (MMA N)
 constexpr int kPos = 128;                      // positions per unit
 constexpr int kSoftWarps = 8, kLoadWarps = 4;
 constexpr int kLoadWarp0 = kSoftWarps, kMmaWarp = kSoftWarps + kLoadWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kThreads = 512;                  // four warpgroups; warps 13-15 only plan
+constexpr int kSoftRegs = 152, kLoadRegs = 152, kMmaRegs = 56;   // sum over four groups: 4 * 128
+static_assert(2 * kSoftRegs + kLoadRegs + kMmaRegs <= 4 * 128, "registers of the CTA");
 constexpr int kRegion = kPos * 128;            // 64 values of every row of the tile
 constexpr int kQRegion = kHT * 128;            // 64 values of every query row
 constexpr int kChunkT = 2048;                  // tokens planned per launch
@@ -62,14 +64,14 @@ struct Smem {
   uint8_t q[8 * kQRegion];                     // 1024-aligned
   uint8_t p[kPos * 128];                       // 1024-aligned
   int32_t tokV[kChunkT];                       // visible positions of the launch's tokens
+  const uint8_t* row[2][kPos];                 // the rows' codes by unit parity
   float rs[2][kPos];                           // row scales by unit parity; -inf: no position
   float sl2[kHT];                              // softmax scale in log2, times the query's power of two
   float m[kHT], alpha[kHT];
   float part[2][4][32];                        // [head half][lane quarter][head]
   int32_t flag[2][2][4];                       // [unit parity][head half][lane quarter]
-  int64_t warp_sum[kMmaWarp + 1];
-  int64_t start_u;                             // first unit of the CTA's first row tile's token
-  int32_t start_t;
+  int64_t warp_sum[kThreads / 32];
+  int32_t count, start_t, start_g, start_i;    // the CTA's share: units, first token, row tile, unit
   uint64_t full[4], empty[2], sfull, pready, pvdone, done;
   uint32_t tmem_base;
 };
@@ -114,7 +116,8 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t n, bool a_mn, bool b_m
 
 // Shared-memory descriptor, 128-byte swizzle. K-major: sbo = bytes between
 // 8-row groups (lbo unused). MN-major: lbo = bytes between 64-value atoms
-// along M or N, sbo = bytes between 8-row groups along K.
+// along M or N, sbo = bytes between 8-row groups along K. `off` bytes further
+// on is desc + (off >> 4): shared addresses stay within the 14 address bits.
 __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
          (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
@@ -127,6 +130,12 @@ __device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t u) {
   return r * 128u + ((u ^ (r & 7u)) << 4);
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y, uint32_t z,
+                                             uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
 // 2^x by the SFU's approximation (a few ulp; 2^-inf = +0).
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -136,6 +145,16 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ void named_bar(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+// The warpgroup's registers per thread (out of those the CTA was launched with).
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // 16 codes to 16 FP16 values (exact), lowest byte first.
@@ -174,25 +193,24 @@ __device__ __forceinline__ int32_t units_of(const Args& a, int32_t V) {
   return n <= kPos ? 1 : (n - 1) / kPos + 1;
 }
 
+// A CTA's share, unit by unit (fewer than 2^31 of them).
 struct Walk {
-  int64_t u, u1;               // this unit, end of the CTA's share
+  int32_t k, count;            // units behind, units of the share
   int32_t t, g, i, n;          // token (within the launch), row tile, unit of it, its units
-  bool first;                  // first unit of the row tile in this CTA
-  __device__ __forceinline__ Walk(const Args& a, const Smem& S, int64_t u0, int64_t end)
-      : u(u0), u1(end), t(S.start_t), first(true) {
-    const int64_t off = u0 - S.start_u;
+  __device__ __forceinline__ Walk(const Args& a, const Smem& S)
+      : k(0), count(S.count), t(S.start_t), g(S.start_g), i(S.start_i) {
     n = units_of(a, S.tokV[t]);
-    g = static_cast<int32_t>(off / n);
-    i = static_cast<int32_t>(off % n);
   }
-  __device__ __forceinline__ bool valid() const { return u < u1; }
-  __device__ __forceinline__ bool last() const { return i == n - 1 || u + 1 == u1; }
+  __device__ __forceinline__ bool valid() const { return k < count; }
+  // first and last unit of the row tile in this CTA
+  __device__ __forceinline__ bool first() const { return k == 0 || i == 0; }
+  __device__ __forceinline__ bool last() const { return i == n - 1 || k + 1 == count; }
+  // at its last unit: whether the row tile began in this CTA
+  __device__ __forceinline__ bool began_here() const { return k >= i; }
   __device__ __forceinline__ void next(const Args& a, const Smem& S) {
-    first = false;
-    ++u;
+    ++k;
     if (++i < n) return;
     i = 0;
-    first = true;
     if (++g < a.hg) return;
     g = 0;
     if (++t < a.tc) n = units_of(a, S.tokV[t]);
@@ -211,8 +229,8 @@ __device__ __forceinline__ int32_t request_of(const int32_t* cu, int32_t B, int3
 }
 
 // Plans the launch: every token's visible positions and the CTA's first unit.
-// Returns all units of the launch. One pass over the tokens by the whole CTA.
-__device__ __forceinline__ int64_t plan(const Args& a, Smem& S, int64_t& u0, int64_t& u1) {
+// One pass over the tokens by the whole CTA.
+__device__ __forceinline__ void plan(const Args& a, Smem& S) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // the boundaries go through the (still unused) tile when they fit
   int32_t* cu_s = reinterpret_cast<int32_t*>(S.kv);
@@ -254,62 +272,67 @@ __device__ __forceinline__ int64_t plan(const Args& a, Smem& S, int64_t& u0, int
   if (lane == 31) S.warp_sum[warp] = incl;
   __syncthreads();
   int64_t before = 0, total = 0;
-  for (int w = 0; w <= kMmaWarp; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     const int64_t v = S.warp_sum[w];
     if (w < warp) before += v;
     total += v;
   }
   int64_t at = before + incl - mine;
-  u0 = total * blockIdx.x / gridDim.x;
-  u1 = total * (blockIdx.x + 1) / gridDim.x;
+  const int64_t u0 = total * blockIdx.x / gridDim.x;
+  const int64_t u1 = total * (blockIdx.x + 1) / gridDim.x;
+  if (tid == 0) S.count = static_cast<int32_t>(u1 - u0);
   for (int i = lo; i < hi; ++i) {
-    const int64_t n = static_cast<int64_t>(units_of(a, S.tokV[i])) * a.hg;
+    const int64_t n = units_of(a, S.tokV[i]);
     if (blockIdx.x == 0) a.tok_start[i] = at;
-    if (at <= u0 && u0 < at + n) {
+    if (at <= u0 && u0 < at + n * a.hg) {
       S.start_t = i;
-      S.start_u = at;
+      S.start_g = static_cast<int32_t>((u0 - at) / n);
+      S.start_i = static_cast<int32_t>((u0 - at) % n);
     }
-    at += n;
+    at += n * a.hg;
   }
   if (blockIdx.x == 0 && tid == 0) a.tok_start[a.tc] = total;
   __syncthreads();
-  return total;
 }
 
 // ---- loaders ----------------------------------------------------------------
-// One of the tile's rows: its codes, and its scale (-inf: no position there).
-struct Row {
-  const uint8_t* codes;
-  float s;
-};
+// The order of a quarter's 128 values in the tile: 16-byte unit j of region
+// 2e + b holds values 128e + 16j + 8b .. + 7, so that a lane's 16 loaded codes
+// fill unit j of two regions and eight lanes cover all banks. The queries are
+// stored alike, and row 64b + 8j + x of O^T's quarter e is that value + x.
+__device__ __forceinline__ int value_of(int e, int row) {
+  return 128 * e + 16 * ((row >> 3) & 7) + 8 * (row >> 6) + (row & 7);
+}
 
-// Row r of unit (t, i). Positions past the table and pages outside the pool
-// are skipped and flagged.
-__device__ __forceinline__ Row find_row(const Args& a, const Smem& S, const Walk& w, int32_t b,
-                                        int r, bool& bad) {
-  Row x{nullptr, -INFINITY};
+// What rows without a position, and rows of zeros, are filled from.
+__device__ __align__(16) const uint8_t kZeroRow[kD] = {};
+
+// Row r of the walk's unit: its codes into S.row, its scale (-inf: no position
+// there). Positions past the table and pages outside the pool are skipped and
+// flagged. A row under a zero scale stands for zeros whatever its codes are.
+__device__ __forceinline__ float find_row(const Args& a, Smem& S, const Walk& w, int32_t b, int r,
+                                          uint32_t parity, bool& bad) {
   const int32_t V = S.tokV[w.t], n = positions_of(a, V), e = w.i * kPos + r;
-  if (e >= n) return x;
-  int64_t j = static_cast<int64_t>(V) - n + e;
-  if (a.idx) {
-    j = __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e);
-    if (j < 0) return x;
-    if (j >= a.cap) {
+  const uint8_t* codes = kZeroRow;
+  float s = -INFINITY;
+  int64_t j = -1;
+  if (e < n) j = a.idx ? __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e) : V - n + e;
+  if (j >= a.cap) {
+    bad = true;
+  } else if (j >= 0) {
+    const int32_t page = __ldg(a.bt + static_cast<int64_t>(b) * a.bt_stride + (j >> a.log2R));
+    if (page < 0 || page >= a.num_pages) {
       bad = true;
-      return x;
+    } else {
+      const uint8_t* base = a.cache + static_cast<int64_t>(page) * a.page_stride;
+      const int32_t row = static_cast<int32_t>(j) & (a.R - 1);
+      s = __half2float(__ushort_as_half(
+          __ldg(reinterpret_cast<const uint16_t*>(base + a.sc_off + row * 2))));
+      if (s != 0.0f) codes = base + a.kv_off + row * kD;
     }
   }
-  const int32_t page = __ldg(a.bt + static_cast<int64_t>(b) * a.bt_stride + (j >> a.log2R));
-  if (page < 0 || page >= a.num_pages) {
-    bad = true;
-    return x;
-  }
-  const uint8_t* base = a.cache + static_cast<int64_t>(page) * a.page_stride;
-  const int32_t row = static_cast<int32_t>(j) & (a.R - 1);
-  x.codes = base + a.kv_off + row * kD;
-  x.s = __half2float(__ushort_as_half(
-      __ldg(reinterpret_cast<const uint16_t*>(base + a.sc_off + row * 2))));
-  return x;
+  S.row[parity][r] = codes;
+  return s;
 }
 
 // The row tile's queries as FP16 times a power of two per head that brings the
@@ -317,6 +340,8 @@ __device__ __forceinline__ Row find_row(const Args& a, const Smem& S, const Walk
 __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, int32_t g, int lw) {
   const int lane = threadIdx.x & 31;
   constexpr int kRows = kHT / kLoadWarps, kBatch = 4;
+  // lane l holds values 16l .. 16l + 15: unit l & 7 of regions 2 (l >> 3), + 1
+  uint8_t* dst = S.q + (lane >> 3) * 2 * kQRegion;
 #pragma unroll 1
   for (int r0 = lw * kRows; r0 < (lw + 1) * kRows; r0 += kBatch) {
     uint4 v[kBatch][2];
@@ -326,9 +351,9 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
       v[k][0] = v[k][1] = make_uint4(0u, 0u, 0u, 0u);
       if (h < a.H) {
         const uint4* src = reinterpret_cast<const uint4*>(
-                               a.q + static_cast<int64_t>(a.t0 + t) * a.q_st + h * a.q_sh) + lane;
+                               a.q + static_cast<int64_t>(a.t0 + t) * a.q_st + h * a.q_sh) + 2 * lane;
         v[k][0] = __ldg(src);
-        v[k][1] = __ldg(src + 32);
+        v[k][1] = __ldg(src + 1);
       }
     }
 #pragma unroll
@@ -341,17 +366,15 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         top = max(top, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      top = __reduce_max_sync(0xffffffffu, top);
       const int e = min(100, 13 - (static_cast<int>(top >> 23) - 127));
       const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
       uint32_t o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         o[i] = pack_half2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-      uint8_t* dst = S.q + (lane >> 3) * kQRegion + sw(r, lane & 7);
-      *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(dst + 4 * kQRegion) = make_uint4(o[4], o[5], o[6], o[7]);
+      *reinterpret_cast<uint4*>(dst + sw(r, lane & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(dst + kQRegion + sw(r, lane & 7)) = make_uint4(o[4], o[5], o[6], o[7]);
       if (lane == 0)
         S.sl2[r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
@@ -364,105 +387,104 @@ struct Quarter {
   uint4 v[8];
 };
 
-__device__ __forceinline__ void load_quarter(Quarter& b, const uint8_t* mine, int e, int lane) {
+// rows: the lane's first row pointer (rows 4k apart follow); off: byte of the row.
+__device__ __forceinline__ void load_quarter(Quarter& b, const uint8_t* const* rows, int off) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint8_t* row = reinterpret_cast<const uint8_t*>(__shfl_sync(
-        0xffffffffu, reinterpret_cast<uintptr_t>(mine), 4 * k + (lane >> 3)));
-    b.v[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (row) b.v[k] = __ldg(reinterpret_cast<const uint4*>(row + e * 128) + (lane & 7));
-  }
+  for (int k = 0; k < 8; ++k) b.v[k] = __ldg(reinterpret_cast<const uint4*>(rows[4 * k] + off));
 }
 
-// live: bit r set where row r's codes count (a row under a zero scale stands
-// for zeros whatever its codes are).
+// dst: the lane's unit of its first row in the quarter's first region. Rows
+// 4k apart are 512 bytes apart; the swizzle flips bit 2 of the unit between
+// even and odd k.
 template <bool kFp8>
-__device__ __forceinline__ void store_quarter(Smem& S, const Quarter& b, uint32_t live, int e, int lw,
-                                              int lane) {
-  const int j = lane & 7;
-  // lanes 4-7 of eight write their second unit first, so that eight lanes
-  // always cover all banks
-  const int swap = j >> 2;
-  uint8_t* region = S.kv + (2 * e + (j >> 2)) * kRegion;
-  const uint32_t u0 = ((2 * j) & 7) + swap, u1 = ((2 * j) & 7) + (swap ^ 1);
+__device__ __forceinline__ void store_quarter(uint32_t even, uint32_t odd, const Quarter& b) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const int rr = 4 * k + (lane >> 3);
-    const uint32_t r = 32 * lw + rr;
-    uint4 v = b.v[k];
-    if (!((live >> rr) & 1u)) v = make_uint4(0u, 0u, 0u, 0u);
     uint32_t o[8];
-    widen16<kFp8>(v, o);
-    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-    *reinterpret_cast<uint4*>(region + sw(r, u0)) = swap ? hi : lo;
-    *reinterpret_cast<uint4*>(region + sw(r, u1)) = swap ? lo : hi;
+    widen16<kFp8>(b.v[k], o);
+    const uint32_t at = ((k & 1) ? odd : even) + k * 512;
+    st_shared_v4(at, o[0], o[1], o[2], o[3]);
+    st_shared_v4(at + kRegion, o[4], o[5], o[6], o[7]);
   }
 }
 
 template <bool kFp8>
-__device__ __forceinline__ bool run_loaders(const Args& a, Smem& S, int64_t u0, int64_t u1) {
+__device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
   const int lane = threadIdx.x & 31, lw = (threadIdx.x >> 5) - kLoadWarp0, r = 32 * lw + lane;
+  const int r0 = 32 * lw + (lane >> 3), off = (lane & 7) * 16;
+  const uint32_t even = smem_u32(S.kv) + sw(r0, lane & 7), odd = even ^ 64u;
   bool bad = false, ok = true;
-  Walk w(a, S, u0, u1), ahead(a, S, u0, u1);
-  int32_t b = request_of(a.cu, a.B, a.T, a.t0 + w.t), bt = w.t;
-  Row cur = find_row(a, S, ahead, b, r, bad);
+  Walk w(a, S);                                       // one unit ahead of the tile being filled
+  int32_t bt = w.t, b = request_of(a.cu, a.B, a.T, a.t0 + bt);
+  float s = find_row(a, S, w, b, r, 0u, bad);
+  __syncwarp();
   Quarter x, y;
-  load_quarter(x, cur.codes, 0, lane);
-  load_quarter(y, cur.codes, 1, lane);
+  load_quarter(x, &S.row[0][r0], off);
+  load_quarter(y, &S.row[0][r0], off + 128);
   for (uint32_t n = 0; w.valid(); ++n) {
+    const int32_t t = w.t, g = w.g;
+    const bool first = w.first();
     // the next unit's rows, whose loads go out during this one
-    ahead.next(a, S);
-    Row nxt{nullptr, -INFINITY};
-    if (ahead.valid()) {
-      if (ahead.t != bt) {
-        bt = ahead.t;
+    w.next(a, S);
+    float s_next = -INFINITY;
+    if (w.valid()) {
+      if (w.t != bt) {
+        bt = w.t;
         b = request_of(a.cu, a.B, a.T, a.t0 + bt);
       }
-      nxt = find_row(a, S, ahead, b, r, bad);
+      s_next = find_row(a, S, w, b, r, (n + 1) & 1, bad);
+    } else {
+      S.row[(n + 1) & 1][r] = kZeroRow;
     }
-    const uint32_t live = __ballot_sync(0xffffffffu, cur.codes != nullptr && cur.s != 0.0f);
-#pragma unroll
-    for (int pair = 0; pair < 2; ++pair) {
-      if (ok && !mbar_wait_warp(&S.empty[pair], (n & 1) ^ 1)) ok = false;
-      if (!ok) break;
+    __syncwarp();
+#pragma unroll 1
+    for (uint32_t pair = 0; pair < 2; ++pair) {
+      if (!mbar_wait_warp(&S.empty[pair], (n & 1) ^ 1)) {
+        ok = false;
+        break;
+      }
       if (pair == 0) {
-        if (w.first) {
+        if (first) {
           // the products with the previous queries are done: the tile's second
           // pair was handed back after them
           if (!mbar_wait_warp(&S.empty[1], (n & 1) ^ 1)) {
             ok = false;
             break;
           }
-          load_queries(a, S, w.t, w.g, lw);
+          load_queries(a, S, t, g, lw);
         }
-        S.rs[n & 1][r] = cur.s;
+        S.rs[n & 1][r] = s;
       }
-      store_quarter<kFp8>(S, x, live, 2 * pair, lw, lane);
+      // this unit's second pair, or the next unit's first
+      const uint8_t* const* rows = &S.row[(n + pair) & 1][r0];
+      const int next = off + (pair ? 0 : 256);
+      const uint32_t base = pair * 4 * kRegion;
+      store_quarter<kFp8>(even + base, odd + base, x);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.full[2 * pair]);
-      load_quarter(x, pair ? nxt.codes : cur.codes, pair ? 0 : 2, lane);
-      store_quarter<kFp8>(S, y, live, 2 * pair + 1, lw, lane);
+      load_quarter(x, rows, next);
+      store_quarter<kFp8>(even + base + 2 * kRegion, odd + base + 2 * kRegion, y);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.full[2 * pair + 1]);
-      load_quarter(y, pair ? nxt.codes : cur.codes, pair ? 1 : 3, lane);
+      load_quarter(y, rows, next + 128);
     }
     if (!ok) break;
-    cur = nxt;
-    w.next(a, S);
+    s = s_next;
   }
   if (bad && a.err) atomicOr(a.err, QLI_DEVERR_PAGE);
   return ok;
 }
 
 // ---- MMA issuer (one thread) --------------------------------------------------
-__device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem, int64_t u0, int64_t u1) {
+__device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem) {
   constexpr uint32_t id_qk = idesc_f16(kHT, false, false), id_pv = idesc_f16(kHT, true, true);
-  const uint32_t kvb = smem_u32(S.kv), qb = smem_u32(S.q), pb = smem_u32(S.p);
+  const uint64_t k_desc = sdesc(smem_u32(S.kv), 16, 1024), q_desc = sdesc(smem_u32(S.q), 16, 1024);
+  const uint64_t v_desc = sdesc(smem_u32(S.kv), kRegion, 1024), p_desc = sdesc(smem_u32(S.p), 1024, 1024);
   bool ok = true;
   uint32_t n = 0;
-  for (Walk w(a, S, u0, u1); w.valid(); w.next(a, S), ++n) {
+  for (Walk w(a, S); w.valid(); w.next(a, S), ++n) {
 #pragma unroll 1
     for (uint32_t e = 0; e < 4 && ok; ++e) {
       if (!mbar_wait_bounded(&S.full[e], n & 1)) {
@@ -473,11 +495,12 @@ __device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem, i
 #pragma unroll
       for (uint32_t k = 0; k < 8; ++k) {
         const uint32_t reg = 2 * e + (k >> 2), off = (k & 3) * 32;
-        mma_f16_ss(tmem + kSCol + (k & 1) * kHT, sdesc(kvb + reg * kRegion + off, 16, 1024),
-                   sdesc(qb + reg * kQRegion + off, 16, 1024), id_qk, (e | (k >> 1)) ? 1u : 0u);
+        mma_f16_ss(tmem + kSCol + (k & 1) * kHT, k_desc + ((reg * kRegion + off) >> 4),
+                   q_desc + ((reg * kQRegion + off) >> 4), id_qk, (e | (k >> 1)) ? 1u : 0u);
       }
     }
     if (!ok) break;
+    const bool fresh = w.first();
     mma_commit(&S.sfull);
     if (!mbar_wait_bounded(&S.pready, n & 1)) {
       ok = false;
@@ -491,8 +514,8 @@ __device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem, i
 #pragma unroll
         for (uint32_t f = 0; f < 2; ++f) {
           const uint32_t e = 2 * pair + f;
-          mma_f16_ss(tmem + kOCol + e * kHT, sdesc(kvb + 2 * e * kRegion + k * 2048, kRegion, 1024),
-                     sdesc(pb + k * 2048, 1024, 1024), id_pv, (w.first && k == 0) ? 0u : 1u);
+          mma_f16_ss(tmem + kOCol + e * kHT, v_desc + ((2 * e * kRegion + k * 2048) >> 4),
+                     p_desc + (k * 2048 >> 4), id_pv, (fresh && k == 0) ? 0u : 1u);
         }
       }
       mma_commit(&S.empty[pair]);
@@ -519,8 +542,7 @@ __device__ __forceinline__ float across(float (&v)[32], int lane, F f) {
   return v[0];
 }
 
-__device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tmem, int64_t u0,
-                                            int64_t u1) {
+__device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tmem) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int qw = warp & 3, half = warp >> 2;          // TMEM lane quarter; heads 32 half ..
   const uint32_t lanes = static_cast<uint32_t>(32 * qw) << 16;
@@ -536,11 +558,11 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
   uint32_t n = 0;
   // A wait that gives up clears `ok`; the warps still run through the same
   // named barriers, on whatever TMEM holds, and write no output.
-  for (Walk w(a, S, u0, u1); w.valid(); w.next(a, S), ++n) {
+  for (Walk w(a, S); w.valid(); w.next(a, S), ++n) {
     if (ok && !mbar_wait_warp(&S.full[0], n & 1)) ok = false;     // the row scales are there
     if (ok && !mbar_wait_warp(&S.sfull, n & 1)) ok = false;
     tc_fence_after();
-    if (w.first) {
+    if (w.first()) {
       seen = false;
       if (qw == 0) S.m[32 * half + lane] = 0.0f;
       named_bar(bar, 128);
@@ -606,7 +628,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
           l[4 * i + 3] *= al.w;
         }
       }
-      if (!w.first) {
+      if (!w.first()) {
         // the products of the units before are done: this unit's tile was
         // filled after them
 #pragma unroll 1
@@ -657,7 +679,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     if (ok && !mbar_wait_warp(&S.pvdone, n & 1)) ok = false;
     tc_fence_after();
     const int32_t h = w.g * kHT + 32 * half;          // first head of this half
-    const bool whole = w.i == w.n - 1 && w.u - u0 >= w.n - 1;
+    const bool whole = w.i == w.n - 1 && w.began_here();
     if (!ok) {
       // nothing to write
     } else if (whole) {
@@ -669,7 +691,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
         uint32_t o[32];
         tmem_ld_32x32b_x32(tmem + lanes + kOCol + e * kHT + 32 * half, o);
         tmem_ld_wait();
-        const int v = e * 128 + pos;
+        const int v = value_of(e, pos);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const float inv = S.alpha[32 * half + i];
@@ -680,7 +702,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     } else {
       // a row tile that began in an earlier CTA goes to slot 0, one that goes
       // on in the next to slot 1
-      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.u - u0 >= w.i ? 1 : 0);
+      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.began_here() ? 1 : 0);
       if (qw == 0) a.piece_lse[slot * kHT + 32 * half + lane] = lse2;
       float* dst = a.piece + slot * kPieceRow + (32 * half) * kD;
 #pragma unroll 1
@@ -688,7 +710,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
         uint32_t o[32];
         tmem_ld_32x32b_x32(tmem + lanes + kOCol + e * kHT + 32 * half, o);
         tmem_ld_wait();
-        const int v = e * 128 + pos;
+        const int v = value_of(e, pos);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (h + i < a.H) dst[i * kD + v] = __uint_as_float(o[i]) * S.alpha[32 * half + i];
@@ -716,21 +738,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
     mbar_init(&S.done, 1);
     fence_mbar_init();
   }
-  int64_t u0, u1;
   tc_fence_before();
-  plan(a, S, u0, u1);                                 // ends with a barrier of the CTA
+  plan(a, S);                                 // ends with a barrier of the CTA
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
-  if (u0 < u1) {
+  if (S.count > 0) {
     bool ok = true;
     if (warp < kSoftWarps) {
-      ok = run_softmax(a, S, tmem, u0, u1);
+      setmaxnreg_inc<kSoftRegs>();
+      ok = run_softmax(a, S, tmem);
     } else if (warp < kMmaWarp) {
-      ok = run_loaders<kFp8>(a, S, u0, u1);
-    } else if (lane == 0) {
-      ok = run_mma(a, S, tmem, u0, u1);
-      mma_commit(&S.done);                            // every product of the CTA
-      (void)mbar_wait_drain(&S.done, 0);
+      setmaxnreg_inc<kLoadRegs>();
+      ok = run_loaders<kFp8>(a, S);
+    } else {
+      setmaxnreg_dec<kMmaRegs>();
+      if (warp == kMmaWarp && lane == 0) {
+        ok = run_mma(a, S, tmem);
+        mma_commit(&S.done);                          // every product of the CTA
+        (void)mbar_wait_drain(&S.done, 0);
+      }
     }
     if (!ok && lane == 0 && a.err) atomicOr(a.err, QLI_DEVERR_TIMEOUT);
   }
