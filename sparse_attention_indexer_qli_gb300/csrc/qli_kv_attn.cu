@@ -16,18 +16,18 @@
 // A unit of work is (token, 64 heads, 128 positions). The units of a launch
 // are split evenly and contiguously over one CTA per SM; a row tile (token,
 // 64 heads) that lies across CTAs leaves normalised FP32 pieces and their LSE
-// in the workspace, joined by merge_pieces_kernel. Thirteen warps:
+// in the workspace, joined by merge_pieces_kernel. Twenty warps:
 //   0-7   softmax: S (lane = position, column = head) from TMEM, weights to
 //         shared memory, at the end of a row tile the output from TMEM
-//   8-11  loaders: the row tile's queries; per unit the 128 rows' codes, two
-//         128-value quarters of the tile in flight in registers, widened to
-//         FP16 and stored in the 128-byte-swizzled tile
-//   12    MMA issuer: S[128 positions, 64 heads] = K Q^T quarter by quarter as
+//   8-15  loaders: per unit the 128 rows' codes, two 128-value quarters of the
+//         tile in flight in registers, widened to FP16 and stored in the
+//         128-byte-swizzled tile
+//   17-19 the row tile's queries
+//   16    MMA issuer: S[128 positions, 64 heads] = K Q^T quarter by quarter as
 //         the tile fills, then O^T[128 values, 64 heads] += V^T P^T for each
 //         quarter, from the same tile read MN-major; a pair of quarters is
 //         handed back as soon as its products are done
-// TMEM: two S accumulators (even and odd 16-value steps) of 64 columns, four
-// O^T quarters of 64. Shared memory: the FP16 tile (128 KB), the queries
+// TMEM: S (64 columns) and four O^T quarters of 64. Shared memory: the FP16 tile (128 KB), the queries
 // (64 KB), the weights (16 KB).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,16 +45,17 @@ namespace {
 constexpr int kD = 512;
 constexpr int kHT = 64;                        // heads per row tile (MMA N)
 constexpr int kPos = 128;                      // positions per unit
-constexpr int kSoftWarps = 8, kLoadWarps = 4;
-constexpr int kLoadWarp0 = kSoftWarps, kMmaWarp = kSoftWarps + kLoadWarps;
-constexpr int kThreads = 512;                  // four warpgroups; warps 13-15 only plan
-constexpr int kSoftRegs = 152, kLoadRegs = 152, kMmaRegs = 56;   // sum over four groups: 4 * 128
-static_assert(2 * kSoftRegs + kLoadRegs + kMmaRegs <= 4 * 128, "registers of the CTA");
+constexpr int kSoftWarps = 8, kLoadWarps = 8;
+constexpr int kLoadWarp0 = kSoftWarps, kMmaWarp = kSoftWarps + kLoadWarps, kQueryWarps = 3;
+constexpr int kThreads = 640;                  // five warpgroups
+// Registers of the warpgroups' threads, within the CTA's 640 x 96.
+constexpr int kSoftRegs = 144, kLoadRegs = 72, kMmaRegs = 48;
+static_assert(2 * kSoftRegs + 2 * kLoadRegs + kMmaRegs <= 5 * 96, "registers of the CTA");
 constexpr int kRegion = kPos * 128;            // 64 values of every row of the tile
 constexpr int kQRegion = kHT * 128;            // 64 values of every query row
 constexpr int kChunkT = 2048;                  // tokens planned per launch
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSCol = 0, kOCol = 256;
+constexpr uint32_t kSCol = 0, kOCol = kHT;
 constexpr float kSlack = 8.0f, kShift = 6.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kPieceRow = kHT * kD;            // floats of a piece
@@ -66,13 +67,14 @@ struct Smem {
   int32_t tokV[kChunkT];                       // visible positions of the launch's tokens
   const uint8_t* row[2][kPos];                 // the rows' codes by unit parity
   float rs[2][kPos];                           // row scales by unit parity; -inf: no position
-  float sl2[kHT];                              // softmax scale in log2, times the query's power of two
+  float sl2[2][kHT];                           // by row tile parity: softmax scale in log2 over the
+                                               // queries' power of two
   float m[kHT], alpha[kHT];
   float part[2][4][32];                        // [head half][lane quarter][head]
   int32_t flag[2][2][4];                       // [unit parity][head half][lane quarter]
   int64_t warp_sum[kThreads / 32];
   int32_t count, start_t, start_g, start_i;    // the CTA's share: units, first token, row tile, unit
-  uint64_t full[4], empty[2], sfull, pready, pvdone, done;
+  uint64_t full[4], empty[2], qfull, qempty, sfull, pready, pvdone, done;
   uint32_t tmem_base;
 };
 constexpr int kSmemBytes = static_cast<int>(sizeof(Smem)) + 1024;
@@ -117,12 +119,12 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t n, bool a_mn, bool b_m
 // Shared-memory descriptor, 128-byte swizzle. K-major: sbo = bytes between
 // 8-row groups (lbo unused). MN-major: lbo = bytes between 64-value atoms
 // along M or N, sbo = bytes between 8-row groups along K. `off` bytes further
-// on is desc + (off >> 4): shared addresses stay within the 14 address bits.
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
-         (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
-         (static_cast<uint64_t>(2) << 61);
+// on is lo + (off >> 4): shared addresses stay within the 14 address bits.
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+__host__ __device__ constexpr uint32_t sdesc_hi(uint32_t sbo) {
+  return (sbo >> 4) | (1u << 14) | (2u << 29);
 }
 
 // Byte offset of 16-byte unit u of row r in a swizzled region of 128-byte rows.
@@ -136,11 +138,71 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y
                : "memory");
 }
 
+// Two FP32 numbers in one register pair, and the packed FP32 operations on
+// them (each half rounded as the scalar operation would be).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair_of(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 both(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // 2^x by the SFU's approximation (a few ulp; 2^-inf = +0).
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Waits, as a whole warp, for the phase with the given parity; false once it
+// has been probed 2^16 times (0.1 us each while the CTA is busy, 20 us when
+// nothing happens: some ms to a second or so). A loop of five instructions: the
+// roles' loops together have to stay within the instruction cache.
+#ifndef QLI_KV_ATTN_PROBES
+#define QLI_KV_ATTN_PROBES (1 << 16)
+#endif
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 i;\n\t"
+      "mov.u32 i, %3;\n"
+      "PROBE:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 i, i, 1;\n\t"
+      "setp.ne.u32 q, i, 0;\n\t"
+      "@q bra PROBE;\n"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "n"(QLI_KV_ATTN_PROBES)
+      : "memory");
+  return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ void named_bar(int id, int n) {
@@ -337,13 +399,14 @@ __device__ __forceinline__ float find_row(const Args& a, Smem& S, const Walk& w,
 
 // The row tile's queries as FP16 times a power of two per head that brings the
 // head's largest magnitude to [2^13, 2^14); rows past H are zero.
-__device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, int32_t g, int lw) {
+__device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, int32_t g,
+                                             uint32_t parity, int qw) {
   const int lane = threadIdx.x & 31;
-  constexpr int kRows = kHT / kLoadWarps, kBatch = 4;
+  constexpr int kBatch = 2;
   // lane l holds values 16l .. 16l + 15: unit l & 7 of regions 2 (l >> 3), + 1
   uint8_t* dst = S.q + (lane >> 3) * 2 * kQRegion;
 #pragma unroll 1
-  for (int r0 = lw * kRows; r0 < (lw + 1) * kRows; r0 += kBatch) {
+  for (int r0 = qw * kBatch; r0 < kHT; r0 += kBatch * kQueryWarps) {
     uint4 v[kBatch][2];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -373,24 +436,43 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         o[i] = pack_half2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-      *reinterpret_cast<uint4*>(dst + sw(r, lane & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(dst + kQRegion + sw(r, lane & 7)) = make_uint4(o[4], o[5], o[6], o[7]);
+      const uint32_t at = smem_u32(dst) + sw(r, lane & 7);
+      st_shared_v4(at, o[0], o[1], o[2], o[3]);
+      st_shared_v4(at + kQRegion, o[4], o[5], o[6], o[7]);
       if (lane == 0)
-        S.sl2[r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        S.sl2[parity][r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
   }
 }
 
-// A warp's 32 rows of one quarter of the tile: eight loads a lane, each warp
+__device__ __forceinline__ bool run_queries(const Args& a, Smem& S) {
+  const int qw = (threadIdx.x >> 5) - kMmaWarp - 1;
+  uint32_t seg = 0;
+  for (Walk w(a, S); w.valid(); w.next(a, S)) {
+    if (!w.first()) continue;
+    // the products with the previous row tile's queries are done, and the
+    // softmax is past its wait for them
+    if (!wait(&S.qempty, (seg & 1) ^ 1)) return false;
+    load_queries(a, S, w.t, w.g, seg & 1, qw);
+    ++seg;
+    fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&S.qfull);
+  }
+  return true;
+}
+
+// A warp's 16 rows of one quarter of the tile: four loads a lane, each warp
 // instruction 128 bytes of four rows.
+constexpr int kWarpRows = kPos / kLoadWarps, kSteps = kWarpRows / 4;
 struct Quarter {
-  uint4 v[8];
+  uint4 v[kSteps];
 };
 
 // rows: the lane's first row pointer (rows 4k apart follow); off: byte of the row.
 __device__ __forceinline__ void load_quarter(Quarter& b, const uint8_t* const* rows, int off) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) b.v[k] = __ldg(reinterpret_cast<const uint4*>(rows[4 * k] + off));
+  for (int k = 0; k < kSteps; ++k) b.v[k] = __ldg(reinterpret_cast<const uint4*>(rows[4 * k] + off));
 }
 
 // dst: the lane's unit of its first row in the quarter's first region. Rows
@@ -399,7 +481,7 @@ __device__ __forceinline__ void load_quarter(Quarter& b, const uint8_t* const* r
 template <bool kFp8>
 __device__ __forceinline__ void store_quarter(uint32_t even, uint32_t odd, const Quarter& b) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < kSteps; ++k) {
     uint32_t o[8];
     widen16<kFp8>(b.v[k], o);
     const uint32_t at = ((k & 1) ? odd : even) + k * 512;
@@ -410,20 +492,20 @@ __device__ __forceinline__ void store_quarter(uint32_t even, uint32_t odd, const
 
 template <bool kFp8>
 __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
-  const int lane = threadIdx.x & 31, lw = (threadIdx.x >> 5) - kLoadWarp0, r = 32 * lw + lane;
-  const int r0 = 32 * lw + (lane >> 3), off = (lane & 7) * 16;
+  const int lane = threadIdx.x & 31, lw = (threadIdx.x >> 5) - kLoadWarp0;
+  const int r = kWarpRows * lw + lane;                // lanes 0-15: the row looked up
+  const int r0 = kWarpRows * lw + (lane >> 3), off = (lane & 7) * 16;
   const uint32_t even = smem_u32(S.kv) + sw(r0, lane & 7), odd = even ^ 64u;
   bool bad = false, ok = true;
   Walk w(a, S);                                       // one unit ahead of the tile being filled
   int32_t bt = w.t, b = request_of(a.cu, a.B, a.T, a.t0 + bt);
-  float s = find_row(a, S, w, b, r, 0u, bad);
+  float s = 0.0f;
+  if (lane < kWarpRows) s = find_row(a, S, w, b, r, 0u, bad);
   __syncwarp();
   Quarter x, y;
   load_quarter(x, &S.row[0][r0], off);
   load_quarter(y, &S.row[0][r0], off + 128);
   for (uint32_t n = 0; w.valid(); ++n) {
-    const int32_t t = w.t, g = w.g;
-    const bool first = w.first();
     // the next unit's rows, whose loads go out during this one
     w.next(a, S);
     float s_next = -INFINITY;
@@ -432,29 +514,18 @@ __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
         bt = w.t;
         b = request_of(a.cu, a.B, a.T, a.t0 + bt);
       }
-      s_next = find_row(a, S, w, b, r, (n + 1) & 1, bad);
-    } else {
+      if (lane < kWarpRows) s_next = find_row(a, S, w, b, r, (n + 1) & 1, bad);
+    } else if (lane < kWarpRows) {
       S.row[(n + 1) & 1][r] = kZeroRow;
     }
     __syncwarp();
 #pragma unroll 1
     for (uint32_t pair = 0; pair < 2; ++pair) {
-      if (!mbar_wait_warp(&S.empty[pair], (n & 1) ^ 1)) {
+      if (!wait(&S.empty[pair], (n & 1) ^ 1)) {
         ok = false;
         break;
       }
-      if (pair == 0) {
-        if (first) {
-          // the products with the previous queries are done: the tile's second
-          // pair was handed back after them
-          if (!mbar_wait_warp(&S.empty[1], (n & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          load_queries(a, S, t, g, lw);
-        }
-        S.rs[n & 1][r] = s;
-      }
+      if (pair == 0 && lane < kWarpRows) S.rs[n & 1][r] = s;
       // this unit's second pair, or the next unit's first
       const uint8_t* const* rows = &S.row[(n + pair) & 1][r0];
       const int next = off + (pair ? 0 : 256);
@@ -477,61 +548,123 @@ __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
   return ok;
 }
 
-// ---- MMA issuer (one thread) --------------------------------------------------
-__device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem) {
+// ---- MMA issuer (one warp) ------------------------------------------------------
+// The whole warp runs the loop and an elected lane issues each batch of
+// products with constant descriptor steps, about ten instructions a product;
+// one thread's loop with 64-bit descriptors took 100-180 cycles a product,
+// where the tensor core takes 42.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
+// D (+)= A B^T from descriptors given as low and high words.
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                    uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, 1;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_first(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem_any) {
   constexpr uint32_t id_qk = idesc_f16(kHT, false, false), id_pv = idesc_f16(kHT, true, true);
-  const uint64_t k_desc = sdesc(smem_u32(S.kv), 16, 1024), q_desc = sdesc(smem_u32(S.q), 16, 1024);
-  const uint64_t v_desc = sdesc(smem_u32(S.kv), kRegion, 1024), p_desc = sdesc(smem_u32(S.p), 1024, 1024);
+  constexpr uint32_t hi = sdesc_hi(1024);
+  const uint32_t k_lo = sdesc_lo(smem_u32(S.kv), 16), q_lo = sdesc_lo(smem_u32(S.q), 16);
+  const uint32_t v_lo = sdesc_lo(smem_u32(S.kv), kRegion), p_lo = sdesc_lo(smem_u32(S.p), 1024);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
   bool ok = true;
-  uint32_t n = 0;
+  uint32_t n = 0, seg = 0;
   for (Walk w(a, S); w.valid(); w.next(a, S), ++n) {
+    const bool last = w.last();
+    if (w.first() && !wait(&S.qfull, seg++ & 1)) {
+      ok = false;
+      break;
+    }
 #pragma unroll 1
-    for (uint32_t e = 0; e < 4 && ok; ++e) {
-      if (!mbar_wait_bounded(&S.full[e], n & 1)) {
+    for (uint32_t e = 0; e < 4; ++e) {
+      if (!wait(&S.full[e], n & 1)) {
         ok = false;
         break;
       }
       tc_fence_after();
+      if (elect_one()) {
+        const uint32_t ke = k_lo + e * (2 * kRegion >> 4), qe = q_lo + e * (2 * kQRegion >> 4);
+        mma_first(tmem + kSCol, ke, qe, hi, id_qk, e);
 #pragma unroll
-      for (uint32_t k = 0; k < 8; ++k) {
-        const uint32_t reg = 2 * e + (k >> 2), off = (k & 3) * 32;
-        mma_f16_ss(tmem + kSCol + (k & 1) * kHT, k_desc + ((reg * kRegion + off) >> 4),
-                   q_desc + ((reg * kQRegion + off) >> 4), id_qk, (e | (k >> 1)) ? 1u : 0u);
+        for (uint32_t k = 1; k < 8; ++k)
+          mma(tmem + kSCol, ke + (((k >> 2) * kRegion + (k & 3) * 32) >> 4),
+              qe + (((k >> 2) * kQRegion + (k & 3) * 32) >> 4), hi, id_qk);
+        if (e == 3) {
+          mma_commit(&S.sfull);
+          if (last) mma_commit(&S.qempty);
+        }
       }
+      __syncwarp();
     }
     if (!ok) break;
-    const bool fresh = w.first();
-    mma_commit(&S.sfull);
-    if (!mbar_wait_bounded(&S.pready, n & 1)) {
+    const uint32_t more = w.first() ? 0u : 1u;
+    if (!wait(&S.pready, n & 1)) {
       ok = false;
       break;
     }
     tc_fence_after();
 #pragma unroll 1
     for (uint32_t pair = 0; pair < 2; ++pair) {
+      if (elect_one()) {
+        const uint32_t ve = v_lo + pair * (4 * kRegion >> 4), oe = tmem + kOCol + pair * (2 * kHT);
+        mma_first(oe, ve, p_lo, hi, id_pv, more);
+        mma_first(oe + kHT, ve + (2 * kRegion >> 4), p_lo, hi, id_pv, more);
 #pragma unroll
-      for (uint32_t k = 0; k < 8; ++k) {
-#pragma unroll
-        for (uint32_t f = 0; f < 2; ++f) {
-          const uint32_t e = 2 * pair + f;
-          mma_f16_ss(tmem + kOCol + e * kHT, v_desc + ((2 * e * kRegion + k * 2048) >> 4),
-                     p_desc + (k * 2048 >> 4), id_pv, (fresh && k == 0) ? 0u : 1u);
+        for (uint32_t k = 1; k < 8; ++k) {
+          mma(oe, ve + (k * 2048 >> 4), p_lo + (k * 2048 >> 4), hi, id_pv);
+          mma(oe + kHT, ve + ((2 * kRegion + k * 2048) >> 4), p_lo + (k * 2048 >> 4), hi, id_pv);
         }
+        mma_commit(&S.empty[pair]);
+        if (pair) mma_commit(&S.pvdone);
       }
-      mma_commit(&S.empty[pair]);
+      __syncwarp();
     }
-    mma_commit(&S.pvdone);
   }
-  return ok;
+  if (elect_one()) mma_commit(&S.done);               // every product of the CTA
+  __syncwarp();
+  return wait(&S.done, 0) && ok;
 }
 
 // ---- softmax ------------------------------------------------------------------
-// Combines 32 values a lane across the warp's 32 lanes: lane l gets value l's
-// result.
+// Combines 32 values a lane (as 16 pairs) across the warp's 32 lanes: lane l
+// gets value l's result.
 template <class F>
-__device__ __forceinline__ float across(float (&v)[32], int lane, F f) {
+__device__ __forceinline__ float across(const f32x2 (&x)[16], int lane, F f) {
+  float v[16];
+  {
+    const bool up = (lane & 16) != 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+    for (int i = 0; i < 8; ++i) {
+      const float2 lo = both(x[i]), hi = both(x[i + 8]);
+      v[2 * i] = f(up ? hi.x : lo.x, __shfl_xor_sync(0xffffffffu, up ? lo.x : hi.x, 16));
+      v[2 * i + 1] = f(up ? hi.y : lo.y, __shfl_xor_sync(0xffffffffu, up ? lo.y : hi.y, 16));
+    }
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
     const bool up = (lane & o) != 0;
 #pragma unroll
     for (int i = 0; i < o; ++i) {
@@ -548,52 +681,51 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
   const uint32_t lanes = static_cast<uint32_t>(32 * qw) << 16;
   const int pos = 32 * qw + lane, bar = 1 + half;
   float* part = S.part[half][0];
-  const float4* sl4 = reinterpret_cast<const float4*>(S.sl2 + 32 * half);
-  const float4* m4 = reinterpret_cast<const float4*>(S.m + 32 * half);
-  const float4* al4 = reinterpret_cast<const float4*>(S.alpha + 32 * half);
+  const f32x2* m2 = reinterpret_cast<const f32x2*>(S.m + 32 * half);
+  const f32x2* al2 = reinterpret_cast<const f32x2*>(S.alpha + 32 * half);
   bool ok = true, seen = false;
-  float l[32];
+  f32x2 l[16];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) l[i] = 0.0f;
-  uint32_t n = 0;
+  for (int i = 0; i < 16; ++i) l[i] = pair_of(0.0f, 0.0f);
+  uint32_t n = 0, seg = 0;
   // A wait that gives up clears `ok`; the warps still run through the same
   // named barriers, on whatever TMEM holds, and write no output.
   for (Walk w(a, S); w.valid(); w.next(a, S), ++n) {
-    if (ok && !mbar_wait_warp(&S.full[0], n & 1)) ok = false;     // the row scales are there
-    if (ok && !mbar_wait_warp(&S.sfull, n & 1)) ok = false;
+    if (w.first()) {                                  // the heads' factors
+      if (ok && !wait(&S.qfull, seg & 1)) ok = false;
+      ++seg;
+      // the queries after these wait for this warp too, so that it sees every
+      // phase of the barrier
+      if (lane == 0) mbar_arrive(&S.qempty);
+    }
+    if (ok && !wait(&S.full[0], n & 1)) ok = false;                  // the row scales
+    if (ok && !wait(&S.sfull, n & 1)) ok = false;
     tc_fence_after();
     if (w.first()) {
       seen = false;
       if (qw == 0) S.m[32 * half + lane] = 0.0f;
       named_bar(bar, 128);
     }
-    float x[32];
-    {
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(tmem + lanes + kSCol + 32 * half, r);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
-      tmem_ld_32x32b_x32(tmem + lanes + kSCol + kHT + 32 * half, r);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(r[i]);
-    }
+    uint32_t xr[32];
+    tmem_ld_32x32b_x32(tmem + lanes + kSCol + 32 * half, xr);
+    tmem_ld_wait();
     // no position here: y = -inf, p = 0. A row of zeros (scale 0) counts in the
     // normaliser only; the smallest scale keeps it from setting the reference.
     const float raw = S.rs[n & 1][pos];
     const bool valid = raw != -INFINITY;
     const float s = valid ? (raw == 0.0f ? 5.9604645e-8f : raw) : 0.0f;
     const float ls = valid ? log2f(s) : -INFINITY, inv_s = valid ? 1.0f / s : 0.0f;
+    const f32x2* sl2 = reinterpret_cast<const f32x2*>(S.sl2[(seg - 1) & 1] + 32 * half);
+    f32x2 x[16];
     float over = -INFINITY;
+    {
+      const f32x2 s2 = pair_of(s, s), ls2 = pair_of(ls, ls);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 c = sl4[i], m = m4[i];
-      const float cc[4] = {c.x, c.y, c.z, c.w}, mm[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[4 * i + k] = fmaf(x[4 * i + k] * cc[k], s, ls);
-        over = fmaxf(over, x[4 * i + k] - mm[k]);
+      for (int i = 0; i < 16; ++i) {
+        x[i] = fma2(mul2(pair_of(__uint_as_float(xr[2 * i]), __uint_as_float(xr[2 * i + 1])), sl2[i]),
+                    s2, ls2);
+        const float2 d = both(sub2(x[i], m2[i]));
+        over = fmaxf(over, fmaxf(d.x, d.y));
       }
     }
     const bool rises = __any_sync(0xffffffffu, over > kSlack);
@@ -604,10 +736,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     const int32_t flags = fl[0] | fl[1] | fl[2] | fl[3];
     if ((flags & 1) || ((flags & 2) && !seen)) {
       // move the references to the maxima so far
-      float y[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) y[i] = x[i];
-      part[qw * 32 + lane] = across(y, lane, [](float p, float q) { return fmaxf(p, q); });
+      part[qw * 32 + lane] = across(x, lane, [](float p, float q) { return fmaxf(p, q); });
       const float old = S.m[32 * half + lane];
       named_bar(bar, 128);
       float top = fmaxf(fmaxf(part[lane], part[32 + lane]), fmaxf(part[64 + lane], part[96 + lane]));
@@ -620,13 +749,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       named_bar(bar, 128);
       if (seen) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 al = al4[i];
-          l[4 * i] *= al.x;
-          l[4 * i + 1] *= al.y;
-          l[4 * i + 2] *= al.z;
-          l[4 * i + 3] *= al.w;
-        }
+        for (int i = 0; i < 16; ++i) l[i] = mul2(l[i], al2[i]);
       }
       if (!w.first()) {
         // the products of the units before are done: this unit's tile was
@@ -646,19 +769,18 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       }
       seen = true;
     }
+    const f32x2 is2 = pair_of(inv_s, inv_s), shift2 = pair_of(kShift, kShift);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 ma = m4[2 * i], mb = m4[2 * i + 1];
-      const float mm[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
-      float p[8];
+      uint32_t h[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        p[k] = ex2(x[8 * i + k] - (mm[k] - kShift));
-        l[8 * i + k] = fmaf(p[k], inv_s, l[8 * i + k]);
+      for (int k = 0; k < 4; ++k) {
+        const float2 d = both(add2(sub2(x[4 * i + k], m2[4 * i + k]), shift2));
+        const float2 p = make_float2(ex2(d.x), ex2(d.y));
+        l[4 * i + k] = fma2(pair_of(p.x, p.y), is2, l[4 * i + k]);
+        h[k] = pack_half2(p.x, p.y);
       }
-      *reinterpret_cast<uint4*>(&S.p[sw(pos, 4 * half + i)]) =
-          make_uint4(pack_half2(p[0], p[1]), pack_half2(p[2], p[3]), pack_half2(p[4], p[5]),
-                     pack_half2(p[6], p[7]));
+      *reinterpret_cast<uint4*>(&S.p[sw(pos, 4 * half + i)]) = make_uint4(h[0], h[1], h[2], h[3]);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -669,14 +791,14 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     // ---- the row tile's end in this CTA: totals, then the output
     part[qw * 32 + lane] = across(l, lane, [](float p, float q) { return p + q; });
 #pragma unroll
-    for (int i = 0; i < 32; ++i) l[i] = 0.0f;
+    for (int i = 0; i < 16; ++i) l[i] = pair_of(0.0f, 0.0f);
     named_bar(bar, 128);
     const float total = (part[lane] + part[32 + lane]) + (part[64 + lane] + part[96 + lane]);
     const float lse2 = total == 0.0f ? -INFINITY : S.m[32 * half + lane] - kShift + log2f(total);
     named_bar(bar, 128);
     if (qw == 0) S.alpha[32 * half + lane] = total == 0.0f ? 0.0f : 1.0f / total;
     named_bar(bar, 128);
-    if (ok && !mbar_wait_warp(&S.pvdone, n & 1)) ok = false;
+    if (ok && !wait(&S.pvdone, n & 1)) ok = false;
     tc_fence_after();
     const int32_t h = w.g * kHT + 32 * half;          // first head of this half
     const bool whole = w.i == w.n - 1 && w.began_here();
@@ -732,6 +854,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
   if (tid == 0) {
     for (int e = 0; e < 4; ++e) mbar_init(&S.full[e], kLoadWarps);
     for (int e = 0; e < 2; ++e) mbar_init(&S.empty[e], 1);
+    mbar_init(&S.qfull, kQueryWarps);
+    mbar_init(&S.qempty, 1 + kSoftWarps);
     mbar_init(&S.sfull, 1);
     mbar_init(&S.pready, kSoftWarps);
     mbar_init(&S.pvdone, 1);
@@ -748,15 +872,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
       setmaxnreg_inc<kSoftRegs>();
       ok = run_softmax(a, S, tmem);
     } else if (warp < kMmaWarp) {
-      setmaxnreg_inc<kLoadRegs>();
+      setmaxnreg_dec<kLoadRegs>();
       ok = run_loaders<kFp8>(a, S);
     } else {
       setmaxnreg_dec<kMmaRegs>();
-      if (warp == kMmaWarp && lane == 0) {
-        ok = run_mma(a, S, tmem);
-        mma_commit(&S.done);                          // every product of the CTA
-        (void)mbar_wait_drain(&S.done, 0);
-      }
+      ok = warp == kMmaWarp ? run_mma(a, S, tmem) : run_queries(a, S);
     }
     if (!ok && lane == 0 && a.err) atomicOr(a.err, QLI_DEVERR_TIMEOUT);
   }
