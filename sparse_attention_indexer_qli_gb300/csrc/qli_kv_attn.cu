@@ -25,8 +25,8 @@
 //   17-19 the row tile's queries
 //   16    MMA issuer: S[128 positions, 64 heads] = K Q^T quarter by quarter as
 //         the tile fills, then O^T[128 values, 64 heads] += V^T P^T for each
-//         quarter, from the same tile read MN-major; a pair of quarters is
-//         handed back as soon as its products are done
+//         quarter, from the same tile read MN-major; a quarter is handed back as
+//         soon as its products are done
 // TMEM: S (64 columns) and four O^T quarters of 64. Shared memory: the FP16 tile (128 KB), the queries
 // (64 KB), the weights (16 KB).
 #include <cuda_bf16.h>
@@ -66,15 +66,15 @@ struct Smem {
   uint8_t p[kPos * 128];                       // 1024-aligned
   int32_t tokV[kChunkT];                       // visible positions of the launch's tokens
   const uint8_t* row[2][kPos];                 // the rows' codes by unit parity
-  float rs[2][kPos];                           // row scales by unit parity; -inf: no position
+  float rs[2][kPos];                           // row scales by unit parity; 0: no position
   float sl2[2][kHT];                           // by row tile parity: softmax scale in log2 over the
                                                // queries' power of two
-  float m[kHT], alpha[kHT];
+  float m[kHT], alpha[kHT], delta[kHT];
   float part[2][4][32];                        // [head half][lane quarter][head]
-  int32_t flag[2][2][4];                       // [unit parity][head half][lane quarter]
+  alignas(16) int32_t flag[2][2][4];                       // [unit parity][head half][lane quarter]
   int64_t warp_sum[kThreads / 32];
   int32_t count, start_t, start_g, start_i;    // the CTA's share: units, first token, row tile, unit
-  uint64_t full[4], empty[2], qfull, qempty, sfull, pready, pvdone, done;
+  uint64_t full[4], empty[4], qfull, qempty, sfull, pready, pvdone, done;
   uint32_t tmem_base;
 };
 constexpr int kSmemBytes = static_cast<int>(sizeof(Smem)) + 1024;
@@ -203,6 +203,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity), "n"(QLI_KV_ATTN_PROBES)
       : "memory");
   return __all_sync(0xffffffffu, ok);
+}
+
+// log2 x likewise (log2 0 = -inf).
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ void named_bar(int id, int n) {
@@ -369,14 +376,16 @@ __device__ __forceinline__ int value_of(int e, int row) {
 // What rows without a position, and rows of zeros, are filled from.
 __device__ __align__(16) const uint8_t kZeroRow[kD] = {};
 
-// Row r of the walk's unit: its codes into S.row, its scale (-inf: no position
+// Row r of the walk's unit: its codes into S.row, its scale (0: no position
 // there). Positions past the table and pages outside the pool are skipped and
-// flagged. A row under a zero scale stands for zeros whatever its codes are.
+// flagged. A row under a zero scale stands for zeros whatever its codes are:
+// it counts in the normaliser only, under the smallest scale there is, so that
+// it does not set the reference. The codes are fetched into L2 a unit ahead.
 __device__ __forceinline__ float find_row(const Args& a, Smem& S, const Walk& w, int32_t b, int r,
                                           uint32_t parity, bool& bad) {
   const int32_t V = S.tokV[w.t], n = positions_of(a, V), e = w.i * kPos + r;
   const uint8_t* codes = kZeroRow;
-  float s = -INFINITY;
+  float s = 0.0f;
   int64_t j = -1;
   if (e < n) j = a.idx ? __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e) : V - n + e;
   if (j >= a.cap) {
@@ -388,9 +397,14 @@ __device__ __forceinline__ float find_row(const Args& a, Smem& S, const Walk& w,
     } else {
       const uint8_t* base = a.cache + static_cast<int64_t>(page) * a.page_stride;
       const int32_t row = static_cast<int32_t>(j) & (a.R - 1);
+      codes = base + a.kv_off + row * kD;
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(codes), "n"(kD));
       s = __half2float(__ushort_as_half(
           __ldg(reinterpret_cast<const uint16_t*>(base + a.sc_off + row * 2))));
-      if (s != 0.0f) codes = base + a.kv_off + row * kD;
+      if (s == 0.0f) {
+        s = 5.9604645e-8f;
+        codes = kZeroRow;
+      }
     }
   }
   S.row[parity][r] = codes;
@@ -508,7 +522,7 @@ __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
   for (uint32_t n = 0; w.valid(); ++n) {
     // the next unit's rows, whose loads go out during this one
     w.next(a, S);
-    float s_next = -INFINITY;
+    float s_next = 0.0f;
     if (w.valid()) {
       if (w.t != bt) {
         bt = w.t;
@@ -519,22 +533,27 @@ __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
       S.row[(n + 1) & 1][r] = kZeroRow;
     }
     __syncwarp();
+    const uint32_t parity = (n & 1) ^ 1;
 #pragma unroll 1
     for (uint32_t pair = 0; pair < 2; ++pair) {
-      if (!wait(&S.empty[pair], (n & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
-      if (pair == 0 && lane < kWarpRows) S.rs[n & 1][r] = s;
       // this unit's second pair, or the next unit's first
       const uint8_t* const* rows = &S.row[(n + pair) & 1][r0];
       const int next = off + (pair ? 0 : 256);
       const uint32_t base = pair * 4 * kRegion;
+      if (!wait(&S.empty[2 * pair], parity)) {
+        ok = false;
+        break;
+      }
+      if (pair == 0 && lane < kWarpRows) S.rs[n & 1][r] = s;
       store_quarter<kFp8>(even + base, odd + base, x);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.full[2 * pair]);
       load_quarter(x, rows, next);
+      if (!wait(&S.empty[2 * pair + 1], parity)) {
+        ok = false;
+        break;
+      }
       store_quarter<kFp8>(even + base + 2 * kRegion, odd + base + 2 * kRegion, y);
       fence_proxy_async_smem();
       __syncwarp();
@@ -627,18 +646,14 @@ __device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem_an
     }
     tc_fence_after();
 #pragma unroll 1
-    for (uint32_t pair = 0; pair < 2; ++pair) {
+    for (uint32_t e = 0; e < 4; ++e) {
       if (elect_one()) {
-        const uint32_t ve = v_lo + pair * (4 * kRegion >> 4), oe = tmem + kOCol + pair * (2 * kHT);
+        const uint32_t ve = v_lo + e * (2 * kRegion >> 4), oe = tmem + kOCol + e * kHT;
         mma_first(oe, ve, p_lo, hi, id_pv, more);
-        mma_first(oe + kHT, ve + (2 * kRegion >> 4), p_lo, hi, id_pv, more);
 #pragma unroll
-        for (uint32_t k = 1; k < 8; ++k) {
-          mma(oe, ve + (k * 2048 >> 4), p_lo + (k * 2048 >> 4), hi, id_pv);
-          mma(oe + kHT, ve + ((2 * kRegion + k * 2048) >> 4), p_lo + (k * 2048 >> 4), hi, id_pv);
-        }
-        mma_commit(&S.empty[pair]);
-        if (pair) mma_commit(&S.pvdone);
+        for (uint32_t k = 1; k < 8; ++k) mma(oe, ve + (k * 2048 >> 4), p_lo + (k * 2048 >> 4), hi, id_pv);
+        mma_commit(&S.empty[e]);
+        if (e == 3) mma_commit(&S.pvdone);
       }
       __syncwarp();
     }
@@ -681,7 +696,8 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
   const uint32_t lanes = static_cast<uint32_t>(32 * qw) << 16;
   const int pos = 32 * qw + lane, bar = 1 + half;
   float* part = S.part[half][0];
-  const f32x2* m2 = reinterpret_cast<const f32x2*>(S.m + 32 * half);
+  const float4* m4 = reinterpret_cast<const float4*>(S.m + 32 * half);
+  const f32x2* de2 = reinterpret_cast<const f32x2*>(S.delta + 32 * half);
   const f32x2* al2 = reinterpret_cast<const f32x2*>(S.alpha + 32 * half);
   bool ok = true, seen = false;
   f32x2 l[16];
@@ -701,57 +717,58 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     if (ok && !wait(&S.full[0], n & 1)) ok = false;                  // the row scales
     if (ok && !wait(&S.sfull, n & 1)) ok = false;
     tc_fence_after();
-    if (w.first()) {
-      seen = false;
-      if (qw == 0) S.m[32 * half + lane] = 0.0f;
-      named_bar(bar, 128);
-    }
+    if (w.first()) seen = false;
     uint32_t xr[32];
     tmem_ld_32x32b_x32(tmem + lanes + kSCol + 32 * half, xr);
     tmem_ld_wait();
-    // no position here: y = -inf, p = 0. A row of zeros (scale 0) counts in the
-    // normaliser only; the smallest scale keeps it from setting the reference.
-    const float raw = S.rs[n & 1][pos];
-    const bool valid = raw != -INFINITY;
-    const float s = valid ? (raw == 0.0f ? 5.9604645e-8f : raw) : 0.0f;
-    const float ls = valid ? log2f(s) : -INFINITY, inv_s = valid ? 1.0f / s : 0.0f;
-    const f32x2* sl2 = reinterpret_cast<const f32x2*>(S.sl2[(seg - 1) & 1] + 32 * half);
-    f32x2 x[16];
+    // d = y - M + kShift; no position here: -inf, weight 0. 1 / s is taken from
+    // the logarithm that d uses, so that p / s is free of its error.
+    const float s = S.rs[n & 1][pos];
+    const bool some = s != 0.0f;
+    const float ls = lg2(s), inv_s = some ? ex2(-ls) : 0.0f;
+    const float4* c4 = reinterpret_cast<const float4*>(S.sl2[(seg - 1) & 1] + 32 * half);
+    f32x2 d[16];
     float over = -INFINITY;
     {
-      const f32x2 s2 = pair_of(s, s), ls2 = pair_of(ls, ls);
+      const f32x2 s2 = pair_of(s, s), ls2 = pair_of(ls + kShift, ls + kShift);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        x[i] = fma2(mul2(pair_of(__uint_as_float(xr[2 * i]), __uint_as_float(xr[2 * i + 1])), sl2[i]),
-                    s2, ls2);
-        const float2 d = both(sub2(x[i], m2[i]));
-        over = fmaxf(over, fmaxf(d.x, d.y));
+      for (int i = 0; i < 8; ++i) {
+        const float4 c = c4[i], m = m4[i];
+        d[2 * i] = fma2(mul2(pair_of(__uint_as_float(xr[4 * i]), __uint_as_float(xr[4 * i + 1])),
+                             pair_of(c.x, c.y)),
+                        s2, sub2(ls2, pair_of(m.x, m.y)));
+        d[2 * i + 1] = fma2(mul2(pair_of(__uint_as_float(xr[4 * i + 2]), __uint_as_float(xr[4 * i + 3])),
+                                 pair_of(c.z, c.w)),
+                            s2, sub2(ls2, pair_of(m.z, m.w)));
+        const float2 u = both(d[2 * i]), v = both(d[2 * i + 1]);
+        over = fmaxf(over, fmaxf(fmaxf(u.x, u.y), fmaxf(v.x, v.y)));
       }
     }
-    const bool rises = __any_sync(0xffffffffu, over > kSlack);
-    const bool some = __any_sync(0xffffffffu, valid);
-    if (lane == 0) S.flag[n & 1][half][qw] = (rises ? 1 : 0) | (some ? 2 : 0);
+    const uint32_t mine = (__any_sync(0xffffffffu, over > kSlack + kShift) ? 1u : 0u) |
+                          (__any_sync(0xffffffffu, some) ? 2u : 0u);
+    if (lane == 0) S.flag[n & 1][half][qw] = static_cast<int32_t>(mine);
     named_bar(bar, 128);
-    const int32_t* fl = S.flag[n & 1][half];
-    const int32_t flags = fl[0] | fl[1] | fl[2] | fl[3];
+    const int4 fl = *reinterpret_cast<const int4*>(S.flag[n & 1][half]);
+    const int32_t flags = fl.x | fl.y | fl.z | fl.w;
     if ((flags & 1) || ((flags & 2) && !seen)) {
-      // move the references to the maxima so far
-      part[qw * 32 + lane] = across(x, lane, [](float p, float q) { return fmaxf(p, q); });
-      const float old = S.m[32 * half + lane];
+      // move references to the maxima so far: each head decides for itself, a
+      // non-finite one keeps its reference
+      part[qw * 32 + lane] = across(d, lane, [](float p, float q) { return fmaxf(p, q); });
       named_bar(bar, 128);
-      float top = fmaxf(fmaxf(part[lane], part[32 + lane]), fmaxf(part[64 + lane], part[96 + lane]));
-      // each head decides for itself; a non-finite one keeps its reference
-      if ((seen && !(top > old + kSlack)) || !(fabsf(top) < INFINITY)) top = old;
+      float up = fmaxf(fmaxf(part[lane], part[32 + lane]), fmaxf(part[64 + lane], part[96 + lane])) - kShift;
+      if ((seen && !(up > kSlack)) || !(fabsf(up) < INFINITY)) up = 0.0f;
       if (qw == 0) {
-        S.m[32 * half + lane] = top;
-        S.alpha[32 * half + lane] = seen ? ex2(old - top) : 1.0f;
+        S.m[32 * half + lane] += up;
+        S.delta[32 * half + lane] = up;
+        S.alpha[32 * half + lane] = seen ? ex2(-up) : 1.0f;
       }
       named_bar(bar, 128);
-      if (seen) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) l[i] = mul2(l[i], al2[i]);
+      for (int i = 0; i < 16; ++i) {
+        d[i] = sub2(d[i], de2[i]);
+        l[i] = mul2(l[i], al2[i]);
       }
-      if (!w.first()) {
+      if (seen) {
         // the products of the units before are done: this unit's tile was
         // filled after them
 #pragma unroll 1
@@ -769,16 +786,16 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       }
       seen = true;
     }
-    const f32x2 is2 = pair_of(inv_s, inv_s), shift2 = pair_of(kShift, kShift);
+    const f32x2 is2 = pair_of(inv_s, inv_s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t h[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 d = both(add2(sub2(x[4 * i + k], m2[4 * i + k]), shift2));
-        const float2 p = make_float2(ex2(d.x), ex2(d.y));
-        l[4 * i + k] = fma2(pair_of(p.x, p.y), is2, l[4 * i + k]);
-        h[k] = pack_half2(p.x, p.y);
+        const float2 v = both(d[4 * i + k]);
+        const float px = ex2(v.x), py = ex2(v.y);
+        l[4 * i + k] = fma2(pair_of(px, py), is2, l[4 * i + k]);
+        h[k] = pack_half2(px, py);
       }
       *reinterpret_cast<uint4*>(&S.p[sw(pos, 4 * half + i)]) = make_uint4(h[0], h[1], h[2], h[3]);
     }
@@ -796,7 +813,10 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     const float total = (part[lane] + part[32 + lane]) + (part[64 + lane] + part[96 + lane]);
     const float lse2 = total == 0.0f ? -INFINITY : S.m[32 * half + lane] - kShift + log2f(total);
     named_bar(bar, 128);
-    if (qw == 0) S.alpha[32 * half + lane] = total == 0.0f ? 0.0f : 1.0f / total;
+    if (qw == 0) {
+      S.alpha[32 * half + lane] = total == 0.0f ? 0.0f : 1.0f / total;
+      S.m[32 * half + lane] = 0.0f;
+    }
     named_bar(bar, 128);
     if (ok && !wait(&S.pvdone, n & 1)) ok = false;
     tc_fence_after();
@@ -852,8 +872,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
   pdl_trigger();
   if (warp == kMmaWarp) tmem_alloc(&S.tmem_base, kTmemCols);
   if (tid == 0) {
-    for (int e = 0; e < 4; ++e) mbar_init(&S.full[e], kLoadWarps);
-    for (int e = 0; e < 2; ++e) mbar_init(&S.empty[e], 1);
+    for (int h = 0; h < kHT; ++h) S.m[h] = 0.0f;
+    for (int e = 0; e < 4; ++e) {
+      mbar_init(&S.full[e], kLoadWarps);
+      mbar_init(&S.empty[e], 1);
+    }
     mbar_init(&S.qfull, kQueryWarps);
     mbar_init(&S.qempty, 1 + kSoftWarps);
     mbar_init(&S.sfull, 1);
