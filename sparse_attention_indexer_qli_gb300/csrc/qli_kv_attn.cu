@@ -13,22 +13,27 @@
 // head is one too (11 significand bits >= 8). So both contractions are
 // kind::f16 with exact products, and only p_j is rounded (2^-11).
 //
-// A unit of work is (token, 64 heads, 128 positions). The units of a launch
-// are split evenly and contiguously over one CTA per SM; a row tile (token,
-// 64 heads) that lies across CTAs leaves normalised FP32 pieces and their LSE
-// in the workspace, joined by merge_pieces_kernel. Twenty warps:
-//   0-7   softmax: S (lane = position, column = head) from TMEM, weights to
-//         shared memory, at the end of a row tile the output from TMEM
-//   8-15  loaders: per unit the 128 rows' codes, two 128-value quarters of the
-//         tile in flight in registers, widened to FP16 and stored in the
-//         128-byte-swizzled tile
+// A unit of work is (token, 64 heads, 64 positions). The units of a launch are
+// split evenly and contiguously over one CTA per SM; a row tile (token, 64
+// heads) that lies across CTAs leaves normalised FP32 pieces and their LSE in
+// the workspace, joined by merge_pieces_kernel. Twenty warps:
+//   0-7   softmax: S from TMEM, weights to shared memory, at the end of a row
+//         tile the output from TMEM
+//   8-15  loaders: a unit's 64 rows of codes in flight in registers, widened to
+//         FP16 and stored in one of two 128-byte-swizzled tiles
+//   16    MMA issuer: the scores of unit n + 1, then the values of unit n
 //   17-19 the row tile's queries
-//   16    MMA issuer: S[128 positions, 64 heads] = K Q^T quarter by quarter as
-//         the tile fills, then O^T[128 values, 64 heads] += V^T P^T for each
-//         quarter, from the same tile read MN-major; a quarter is handed back as
-//         soon as its products are done
-// TMEM: S (64 columns) and four O^T quarters of 64. Shared memory: the FP16 tile (128 KB), the queries
-// (64 KB), the weights (16 KB).
+// A tile's 128 rows are (half e of the 512 values, position), the queries are
+// stacked alike, so the scores are one product of M = 128, N = 128, K = 256
+// whose blocks e = e' are the halves' partial scores (the other two are
+// wasted: 1104 cycles for 64 positions, where M = 128 positions against N = 64
+// heads takes 832 but leaves no room for a second tile, so that products,
+// softmax and conversion would take turns). The softmax adds the halves
+// through shared memory. O^T[128 values, 64 heads] += V^T P^T for each quarter
+// of the values, from the same tile read MN-major.
+// TMEM: two S buffers of 128 columns, four O^T quarters of 64. Shared memory:
+// two FP16 tiles (128 KB), the queries (64 KB), the exchange (16 KB), the
+// weights (8 KB).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -44,37 +49,35 @@ namespace {
 
 constexpr int kD = 512;
 constexpr int kHT = 64;                        // heads per row tile (MMA N)
-constexpr int kPos = 128;                      // positions per unit
+constexpr int kPos = 64;                       // positions per unit
 constexpr int kSoftWarps = 8, kLoadWarps = 8;
 constexpr int kLoadWarp0 = kSoftWarps, kMmaWarp = kSoftWarps + kLoadWarps, kQueryWarps = 3;
-constexpr int kThreads = 640;                  // five warpgroups
-// Registers of the warpgroups' threads, within the CTA's 640 x 96.
-constexpr int kSoftRegs = 144, kLoadRegs = 72, kMmaRegs = 48;
-static_assert(2 * kSoftRegs + 2 * kLoadRegs + kMmaRegs <= 5 * 96, "registers of the CTA");
-constexpr int kRegion = kPos * 128;            // 64 values of every row of the tile
-constexpr int kQRegion = kHT * 128;            // 64 values of every query row
-constexpr int kChunkT = 2048;                  // tokens planned per launch
+constexpr int kThreads = 32 * (kMmaWarp + 1 + kQueryWarps);
+constexpr int kRegion = 128 * 128;             // 64 values of every row of a tile
+constexpr int kTile = 4 * kRegion;
+constexpr int kChunkT = 1024;                  // tokens planned per launch
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSCol = 0, kOCol = kHT;
+constexpr uint32_t kSCol = 0, kOCol = 256;
 constexpr float kSlack = 8.0f, kShift = 6.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kPieceRow = kHT * kD;            // floats of a piece
 
 struct Smem {
-  uint8_t kv[8 * kRegion];                     // 1024-aligned
-  uint8_t q[8 * kQRegion];                     // 1024-aligned
+  uint8_t kv[2][kTile];                        // 1024-aligned, by unit parity
+  uint8_t q[kTile];                            // 1024-aligned
   uint8_t p[kPos * 128];                       // 1024-aligned
+  float x[4][kPos][16];                        // partial scores a softmax warp gives to its partner
   int32_t tokV[kChunkT];                       // visible positions of the launch's tokens
   const uint8_t* row[2][kPos];                 // the rows' codes by unit parity
   float rs[2][kPos];                           // row scales by unit parity; 0: no position
   float sl2[2][kHT];                           // by row tile parity: softmax scale in log2 over the
                                                // queries' power of two
   float m[kHT], alpha[kHT], delta[kHT];
-  float part[2][4][32];                        // [head half][lane quarter][head]
-  alignas(16) int32_t flag[2][2][4];                       // [unit parity][head half][lane quarter]
-  int64_t warp_sum[kThreads / 32];
+  float part[2][4][16];                        // [32 heads][softmax warp of them][head]
+  alignas(16) int32_t flag[2][2][4];           // [unit parity][32 heads][warp]
+  int32_t warp_sum[kThreads / 32];
   int32_t count, start_t, start_g, start_i;    // the CTA's share: units, first token, row tile, unit
-  uint64_t full[4], empty[4], qfull, qempty, sfull, pready, pvdone, done;
+  uint64_t full[2], empty[2], sfull[2], sfree[2], qfull, qempty, pready, pvdone, done;
   uint32_t tmem_base;
 };
 constexpr int kSmemBytes = static_cast<int>(sizeof(Smem)) + 1024;
@@ -104,7 +107,7 @@ struct Args {
   int32_t t0, tc;              // tokens of this launch: t0 .. t0 + tc
   int32_t hg;                  // row tiles per token
   // workspace
-  int64_t* tok_start;          // [tc + 1] first unit of each token
+  int32_t* tok_start;          // [tc + 1] first unit of each token
   float* piece;                // [2 * CTAs][64][512]
   float* piece_lse;            // [2 * CTAs][64], log2
 };
@@ -205,6 +208,28 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, ok);
 }
 
+// 32 lanes x 8 consecutive 32-bit columns of TMEM.
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // log2 x likewise (log2 0 = -inf).
 __device__ __forceinline__ float lg2(float x) {
   float y;
@@ -214,16 +239,6 @@ __device__ __forceinline__ float lg2(float x) {
 
 __device__ __forceinline__ void named_bar(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-
-// The warpgroup's registers per thread (out of those the CTA was launched with).
-template <int kRegs>
-__device__ __forceinline__ void setmaxnreg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void setmaxnreg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // 16 codes to 16 FP16 values (exact), lowest byte first.
@@ -262,7 +277,13 @@ __device__ __forceinline__ int32_t units_of(const Args& a, int32_t V) {
   return n <= kPos ? 1 : (n - 1) / kPos + 1;
 }
 
-// A CTA's share, unit by unit (fewer than 2^31 of them).
+// First unit of CTA c of `ctas`, out of `total` (below 2^30).
+__device__ __forceinline__ int32_t share_begin(int32_t total, int32_t ctas, int32_t c) {
+  const int32_t each = total / ctas;
+  return each * c + min(c, total - each * ctas);
+}
+
+// A CTA's share, unit by unit.
 struct Walk {
   int32_t k, count;            // units behind, units of the share
   int32_t t, g, i, n;          // token (within the launch), row tile, unit of it, its units
@@ -297,80 +318,91 @@ __device__ __forceinline__ int32_t request_of(const int32_t* cu, int32_t B, int3
   return lo;
 }
 
-// Plans the launch: every token's visible positions and the CTA's first unit.
-// One pass over the tokens by the whole CTA.
+// Plans the launch: every token's visible positions and the CTA's share. Each
+// thread takes `per` consecutive tokens.
 __device__ __forceinline__ void plan(const Args& a, Smem& S) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the boundaries go through the (still unused) tile when they fit
-  int32_t* cu_s = reinterpret_cast<int32_t*>(S.kv);
-  const bool local = a.B <= static_cast<int32_t>(sizeof(S.kv) / 4);
+  const int32_t* cu = a.cu;
   if (!a.idx) {
-    if (local)
+    // the boundaries go through the (still unused) tile when they fit
+    int32_t* cu_s = reinterpret_cast<int32_t*>(S.kv);
+    if (a.B <= static_cast<int32_t>(sizeof(S.kv) / 4)) {
+#pragma unroll 1
       for (int b = tid; b < a.B; b += kThreads) cu_s[b] = __ldg(a.cu + b);
-    if (blockIdx.x == 0 && a.t0 == 0 && a.err) {
+      cu = cu_s;
+    }
+    __syncthreads();
+  }
+  const int per = (a.tc + kThreads - 1) / kThreads;
+  const int lo = min(a.tc, tid * per), hi = min(a.tc, lo + per);
+  int32_t mine = 0;
+#pragma unroll 1
+  for (int i = lo; i < hi; ++i) {
+    int32_t V = 0;
+    if (!a.idx) {
+      const int32_t t = a.t0 + i;
+      int32_t q0, q1, lk, res;
+      sanitize_request(a, request_of(cu, a.B, a.T, t), q0, q1, lk, res);
+      if (q0 <= t && t < q1) V = visible_count(lk, res, a.ratio, q1 - q0, t - q0);
+    }
+    S.tokV[i] = V;
+    mine += units_of(a, V);
+  }
+  mine *= a.hg;
+  int32_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) S.warp_sum[warp] = incl;
+  __syncthreads();
+  int32_t sums = lane < kThreads / 32 ? S.warp_sum[lane] : 0;
+  const int32_t own = __shfl_sync(0xffffffffu, sums, warp);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += y;
+  }
+  const int32_t total = __shfl_sync(0xffffffffu, sums, 31);
+  int32_t at = __shfl_sync(0xffffffffu, sums, warp) - own + incl - mine;
+  const int32_t ctas = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
+  const int32_t u0 = share_begin(total, ctas, c);
+  if (tid == 0) S.count = share_begin(total, ctas, c + 1) - u0;
+#pragma unroll 1
+  for (int i = lo; i < hi; ++i) {
+    const int32_t n = units_of(a, S.tokV[i]);
+    if (c == 0) a.tok_start[i] = at;
+    if (at <= u0 && u0 < at + n * a.hg) {
+      S.start_t = i;
+      S.start_g = (u0 - at) / n;
+      S.start_i = (u0 - at) % n;
+    }
+    at += n * a.hg;
+  }
+  if (c == 0) {
+    if (tid == 0) a.tok_start[a.tc] = total;
+    if (!a.idx && a.t0 == 0 && a.err) {
       uint32_t e = 0u;
+#pragma unroll 1
       for (int b = tid; b < a.B; b += kThreads) {
         int32_t q0, q1, lk, res;
         e |= sanitize_request(a, b, q0, q1, lk, res);
       }
       if (e) atomicOr(a.err, e);
     }
-    __syncthreads();
-    for (int i = tid; i < a.tc; i += kThreads) {
-      const int32_t t = a.t0 + i;
-      const int32_t b = request_of(local ? cu_s : a.cu, a.B, a.T, t);
-      int32_t q0, q1, lk, res;
-      sanitize_request(a, b, q0, q1, lk, res);
-      S.tokV[i] = q0 <= t && t < q1 ? visible_count(lk, res, a.ratio, q1 - q0, t - q0) : 0;
-    }
-  } else {
-    for (int i = tid; i < a.tc; i += kThreads) S.tokV[i] = 0;
   }
-  __syncthreads();
-  const int per = (a.tc + kThreads - 1) / kThreads;
-  const int lo = min(a.tc, tid * per), hi = min(a.tc, lo + per);
-  int64_t mine = 0;
-  for (int i = lo; i < hi; ++i) mine += units_of(a, S.tokV[i]);
-  mine *= a.hg;
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) S.warp_sum[warp] = incl;
-  __syncthreads();
-  int64_t before = 0, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int64_t v = S.warp_sum[w];
-    if (w < warp) before += v;
-    total += v;
-  }
-  int64_t at = before + incl - mine;
-  const int64_t u0 = total * blockIdx.x / gridDim.x;
-  const int64_t u1 = total * (blockIdx.x + 1) / gridDim.x;
-  if (tid == 0) S.count = static_cast<int32_t>(u1 - u0);
-  for (int i = lo; i < hi; ++i) {
-    const int64_t n = units_of(a, S.tokV[i]);
-    if (blockIdx.x == 0) a.tok_start[i] = at;
-    if (at <= u0 && u0 < at + n * a.hg) {
-      S.start_t = i;
-      S.start_g = static_cast<int32_t>((u0 - at) / n);
-      S.start_i = static_cast<int32_t>((u0 - at) % n);
-    }
-    at += n * a.hg;
-  }
-  if (blockIdx.x == 0 && tid == 0) a.tok_start[a.tc] = total;
   __syncthreads();
 }
 
 // ---- loaders ----------------------------------------------------------------
-// The order of a quarter's 128 values in the tile: 16-byte unit j of region
-// 2e + b holds values 128e + 16j + 8b .. + 7, so that a lane's 16 loaded codes
-// fill unit j of two regions and eight lanes cover all banks. The queries are
-// stored alike, and row 64b + 8j + x of O^T's quarter e is that value + x.
-__device__ __forceinline__ int value_of(int e, int row) {
-  return 128 * e + 16 * ((row >> 3) & 7) + 8 * (row >> 6) + (row & 7);
+// Quarter c = 2e + f of the values is in rows 64e .. 64e + 63 of regions 2f and
+// 2f + 1, in this order: 16-byte unit j of region 2f + b holds values
+// 128c + 16j + 8b .. + 7, so that a lane's 16 loaded codes fill unit j of two
+// regions and eight lanes cover all banks. The queries are stored alike, and
+// row 64b + 8j + x of O^T's quarter c is that value + x.
+__device__ __forceinline__ int value_of(int c, int row) {
+  return 128 * c + 16 * ((row >> 3) & 7) + 8 * (row >> 6) + (row & 7);
 }
 
 // What rows without a position, and rows of zeros, are filled from.
@@ -380,7 +412,7 @@ __device__ __align__(16) const uint8_t kZeroRow[kD] = {};
 // there). Positions past the table and pages outside the pool are skipped and
 // flagged. A row under a zero scale stands for zeros whatever its codes are:
 // it counts in the normaliser only, under the smallest scale there is, so that
-// it does not set the reference. The codes are fetched into L2 a unit ahead.
+// it does not set the reference. The codes are fetched into L2 on the way.
 __device__ __forceinline__ float find_row(const Args& a, Smem& S, const Walk& w, int32_t b, int r,
                                           uint32_t parity, bool& bad) {
   const int32_t V = S.tokV[w.t], n = positions_of(a, V), e = w.i * kPos + r;
@@ -417,8 +449,9 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
                                              uint32_t parity, int qw) {
   const int lane = threadIdx.x & 31;
   constexpr int kBatch = 2;
-  // lane l holds values 16l .. 16l + 15: unit l & 7 of regions 2 (l >> 3), + 1
-  uint8_t* dst = S.q + (lane >> 3) * 2 * kQRegion;
+  // lane l holds values 16l .. 16l + 15: unit l & 7 of quarter l >> 3
+  uint8_t* dst = S.q + ((lane >> 3) & 1) * 2 * kRegion;
+  const int e64 = (lane >> 4) * 64;
 #pragma unroll 1
   for (int r0 = qw * kBatch; r0 < kHT; r0 += kBatch * kQueryWarps) {
     uint4 v[kBatch][2];
@@ -450,9 +483,9 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         o[i] = pack_half2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-      const uint32_t at = smem_u32(dst) + sw(r, lane & 7);
+      const uint32_t at = smem_u32(dst) + sw(e64 + r, lane & 7);
       st_shared_v4(at, o[0], o[1], o[2], o[3]);
-      st_shared_v4(at + kQRegion, o[4], o[5], o[6], o[7]);
+      st_shared_v4(at + kRegion, o[4], o[5], o[6], o[7]);
       if (lane == 0)
         S.sl2[parity][r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
@@ -476,92 +509,63 @@ __device__ __forceinline__ bool run_queries(const Args& a, Smem& S) {
   return true;
 }
 
-// A warp's 16 rows of one quarter of the tile: four loads a lane, each warp
-// instruction 128 bytes of four rows.
-constexpr int kWarpRows = kPos / kLoadWarps, kSteps = kWarpRows / 4;
-struct Quarter {
-  uint4 v[kSteps];
-};
-
-// rows: the lane's first row pointer (rows 4k apart follow); off: byte of the row.
-__device__ __forceinline__ void load_quarter(Quarter& b, const uint8_t* const* rows, int off) {
-#pragma unroll
-  for (int k = 0; k < kSteps; ++k) b.v[k] = __ldg(reinterpret_cast<const uint4*>(rows[4 * k] + off));
-}
-
-// dst: the lane's unit of its first row in the quarter's first region. Rows
-// 4k apart are 512 bytes apart; the swizzle flips bit 2 of the unit between
-// even and odd k.
-template <bool kFp8>
-__device__ __forceinline__ void store_quarter(uint32_t even, uint32_t odd, const Quarter& b) {
-#pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    uint32_t o[8];
-    widen16<kFp8>(b.v[k], o);
-    const uint32_t at = ((k & 1) ? odd : even) + k * 512;
-    st_shared_v4(at, o[0], o[1], o[2], o[3]);
-    st_shared_v4(at + kRegion, o[4], o[5], o[6], o[7]);
-  }
-}
-
+// Iteration n stores unit n from registers, then loads unit n + 1 (32 KB in
+// flight on the SM while unit n is worked on), then looks up the rows of unit
+// n + 2. A warp has eight rows; a warp instruction loads one quarter of four.
 template <bool kFp8>
 __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
+  constexpr int kWarpRows = kPos / kLoadWarps;
   const int lane = threadIdx.x & 31, lw = (threadIdx.x >> 5) - kLoadWarp0;
-  const int r = kWarpRows * lw + lane;                // lanes 0-15: the row looked up
+  const int r = kWarpRows * lw + lane;                // lanes 0-7: the row looked up
   const int r0 = kWarpRows * lw + (lane >> 3), off = (lane & 7) * 16;
-  const uint32_t even = smem_u32(S.kv) + sw(r0, lane & 7), odd = even ^ 64u;
+  // rows 4 apart: 512 bytes on, and bit 2 of the swizzled unit flips
+  const uint32_t at0 = smem_u32(S.kv) + sw(r0, lane & 7), at1 = (at0 ^ 64u) + 512;
   bool bad = false, ok = true;
-  Walk w(a, S);                                       // one unit ahead of the tile being filled
-  int32_t bt = w.t, b = request_of(a.cu, a.B, a.T, a.t0 + bt);
-  float s = 0.0f;
-  if (lane < kWarpRows) s = find_row(a, S, w, b, r, 0u, bad);
-  __syncwarp();
-  Quarter x, y;
-  load_quarter(x, &S.row[0][r0], off);
-  load_quarter(y, &S.row[0][r0], off + 128);
-  for (uint32_t n = 0; w.valid(); ++n) {
-    // the next unit's rows, whose loads go out during this one
-    w.next(a, S);
-    float s_next = 0.0f;
+  Walk w(a, S);                                       // the unit looked up next
+  int32_t bt = -1, b = 0;
+  float s0 = 0.0f, s1 = 0.0f;                         // scales of units n and n + 1
+  uint4 x[2][4];
+#pragma unroll 1
+  for (int32_t n = -2; n < w.count; ++n) {
+    if (n >= 0) {
+      if (!wait(&S.empty[n & 1], ((n >> 1) & 1) ^ 1)) {
+        ok = false;
+        break;
+      }
+      if (lane < kWarpRows) S.rs[n & 1][r] = s0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[8];
+          widen16<kFp8>(x[k][c], o);
+          const uint32_t at = (k ? at1 : at0) + (n & 1) * kTile + (c & 1) * 2 * kRegion + (c >> 1) * 64 * 128;
+          st_shared_v4(at, o[0], o[1], o[2], o[3]);
+          st_shared_v4(at + kRegion, o[4], o[5], o[6], o[7]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.full[n & 1]);
+    }
+    if (n >= -1 && n + 1 < w.count) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint8_t* row = S.row[(n + 1) & 1][r0 + 4 * k] + off;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[k][c] = __ldg(reinterpret_cast<const uint4*>(row + c * 128));
+      }
+    }
+    s0 = s1;
     if (w.valid()) {
       if (w.t != bt) {
         bt = w.t;
         b = request_of(a.cu, a.B, a.T, a.t0 + bt);
       }
-      if (lane < kWarpRows) s_next = find_row(a, S, w, b, r, (n + 1) & 1, bad);
-    } else if (lane < kWarpRows) {
-      S.row[(n + 1) & 1][r] = kZeroRow;
+      if (lane < kWarpRows) s1 = find_row(a, S, w, b, r, n & 1, bad);
+      w.next(a, S);
     }
     __syncwarp();
-    const uint32_t parity = (n & 1) ^ 1;
-#pragma unroll 1
-    for (uint32_t pair = 0; pair < 2; ++pair) {
-      // this unit's second pair, or the next unit's first
-      const uint8_t* const* rows = &S.row[(n + pair) & 1][r0];
-      const int next = off + (pair ? 0 : 256);
-      const uint32_t base = pair * 4 * kRegion;
-      if (!wait(&S.empty[2 * pair], parity)) {
-        ok = false;
-        break;
-      }
-      if (pair == 0 && lane < kWarpRows) S.rs[n & 1][r] = s;
-      store_quarter<kFp8>(even + base, odd + base, x);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.full[2 * pair]);
-      load_quarter(x, rows, next);
-      if (!wait(&S.empty[2 * pair + 1], parity)) {
-        ok = false;
-        break;
-      }
-      store_quarter<kFp8>(even + base + 2 * kRegion, odd + base + 2 * kRegion, y);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.full[2 * pair + 1]);
-      load_quarter(y, rows, next + 128);
-    }
-    if (!ok) break;
-    s = s_next;
   }
   if (bad && a.err) atomicOr(a.err, QLI_DEVERR_PAGE);
   return ok;
@@ -604,59 +608,63 @@ __device__ __forceinline__ void mma_first(uint32_t d_tmem, uint32_t a_lo, uint32
 }
 
 __device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem_any) {
-  constexpr uint32_t id_qk = idesc_f16(kHT, false, false), id_pv = idesc_f16(kHT, true, true);
+  constexpr uint32_t id_qk = idesc_f16(128, false, false), id_pv = idesc_f16(kHT, true, true);
   constexpr uint32_t hi = sdesc_hi(1024);
   const uint32_t k_lo = sdesc_lo(smem_u32(S.kv), 16), q_lo = sdesc_lo(smem_u32(S.q), 16);
   const uint32_t v_lo = sdesc_lo(smem_u32(S.kv), kRegion), p_lo = sdesc_lo(smem_u32(S.p), 1024);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
   bool ok = true;
-  uint32_t n = 0, seg = 0;
-  for (Walk w(a, S); w.valid(); w.next(a, S), ++n) {
-    const bool last = w.last();
-    if (w.first() && !wait(&S.qfull, seg++ & 1)) {
-      ok = false;
-      break;
-    }
+  uint32_t seg = 0, more = 0;
+  Walk w(a, S);
 #pragma unroll 1
-    for (uint32_t e = 0; e < 4; ++e) {
-      if (!wait(&S.full[e], n & 1)) {
+  for (int32_t n = 0; n <= w.count; ++n) {
+    const uint32_t buf = n & 1, parity = (n >> 1) & 1;
+    const bool first = w.first();
+    if (n < w.count) {
+      // scores of unit n, while the softmax has unit n - 1
+      if ((first && !wait(&S.qfull, seg++ & 1)) || !wait(&S.full[buf], parity) ||
+          !wait(&S.sfree[buf], parity ^ 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool last = w.last();
+      if (elect_one()) {
+        const uint32_t ke = k_lo + buf * (kTile >> 4), se = tmem + kSCol + buf * 128;
+        mma_first(se, ke, q_lo, hi, id_qk, 0u);
+#pragma unroll
+        for (uint32_t k = 1; k < 16; ++k) {
+          const uint32_t step = ((k >> 2) * kRegion + (k & 3) * 32) >> 4;
+          mma(se, ke + step, q_lo + step, hi, id_qk);
+        }
+        mma_commit(&S.sfull[buf]);
+        if (last) mma_commit(&S.qempty);
+      }
+      __syncwarp();
+      w.next(a, S);
+    }
+    if (n > 0) {
+      // values of unit n - 1
+      if (!wait(&S.pready, (n - 1) & 1)) {
         ok = false;
         break;
       }
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t ke = k_lo + e * (2 * kRegion >> 4), qe = q_lo + e * (2 * kQRegion >> 4);
-        mma_first(tmem + kSCol, ke, qe, hi, id_qk, e);
 #pragma unroll
-        for (uint32_t k = 1; k < 8; ++k)
-          mma(tmem + kSCol, ke + (((k >> 2) * kRegion + (k & 3) * 32) >> 4),
-              qe + (((k >> 2) * kQRegion + (k & 3) * 32) >> 4), hi, id_qk);
-        if (e == 3) {
-          mma_commit(&S.sfull);
-          if (last) mma_commit(&S.qempty);
+        for (uint32_t c = 0; c < 4; ++c) {
+          const uint32_t ve = v_lo + (((buf ^ 1) * kTile + (c & 1) * 2 * kRegion + (c >> 1) * 64 * 128) >> 4);
+          const uint32_t oe = tmem + kOCol + c * kHT;
+          mma_first(oe, ve, p_lo, hi, id_pv, more);
+#pragma unroll
+          for (uint32_t k = 1; k < 4; ++k) mma(oe, ve + (k * 2048 >> 4), p_lo + (k * 2048 >> 4), hi, id_pv);
         }
+        mma_commit(&S.empty[buf ^ 1]);
+        mma_commit(&S.pvdone);
       }
       __syncwarp();
     }
-    if (!ok) break;
-    const uint32_t more = w.first() ? 0u : 1u;
-    if (!wait(&S.pready, n & 1)) {
-      ok = false;
-      break;
-    }
-    tc_fence_after();
-#pragma unroll 1
-    for (uint32_t e = 0; e < 4; ++e) {
-      if (elect_one()) {
-        const uint32_t ve = v_lo + e * (2 * kRegion >> 4), oe = tmem + kOCol + e * kHT;
-        mma_first(oe, ve, p_lo, hi, id_pv, more);
-#pragma unroll
-        for (uint32_t k = 1; k < 8; ++k) mma(oe, ve + (k * 2048 >> 4), p_lo + (k * 2048 >> 4), hi, id_pv);
-        mma_commit(&S.empty[e]);
-        if (e == 3) mma_commit(&S.pvdone);
-      }
-      __syncwarp();
-    }
+    more = first ? 0u : 1u;                           // for the values of unit n
   }
   if (elect_one()) mma_commit(&S.done);               // every product of the CTA
   __syncwarp();
@@ -664,123 +672,172 @@ __device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem_an
 }
 
 // ---- softmax ------------------------------------------------------------------
-// Combines 32 values a lane (as 16 pairs) across the warp's 32 lanes: lane l
-// gets value l's result.
+// Combines 16 values a lane (as 8 pairs) across the warp's 32 lanes: lanes 2i
+// and 2i + 1 get value i's result.
 template <class F>
-__device__ __forceinline__ float across(const f32x2 (&x)[16], int lane, F f) {
-  float v[16];
+__device__ __forceinline__ float across(const f32x2 (&x)[8], int lane, F f) {
+  float v[8];
   {
     const bool up = (lane & 16) != 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 lo = both(x[i]), hi = both(x[i + 8]);
+    for (int i = 0; i < 4; ++i) {
+      const float2 lo = both(x[i]), hi = both(x[i + 4]);
       v[2 * i] = f(up ? hi.x : lo.x, __shfl_xor_sync(0xffffffffu, up ? lo.x : hi.x, 16));
       v[2 * i + 1] = f(up ? hi.y : lo.y, __shfl_xor_sync(0xffffffffu, up ? lo.y : hi.y, 16));
     }
   }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
+  for (int o = 8; o > 1; o >>= 1) {
     const bool up = (lane & o) != 0;
 #pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+    for (int i = 0; i < o / 2; ++i) {
+      const float send = up ? v[i] : v[i + o / 2], keep = up ? v[i + o / 2] : v[i];
       v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, o));
     }
   }
-  return v[0];
+  return f(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
+__device__ __forceinline__ void store_value(uint16_t* at, float v) {
+  const __nv_bfloat16 y = __float2bfloat16_rn(v);
+  *at = *reinterpret_cast<const uint16_t*>(&y);
+}
+__device__ __forceinline__ void store_value(float* at, float v) { *at = v; }
+
+// O^T's row `pos` of each quarter times the heads' factors, for `nh` heads from
+// h0 on, head i at dst + i * stride.
+template <class T>
+__device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int pos, int32_t nh, T* dst,
+                                       int64_t stride) {
+#pragma unroll 1
+  for (int c = 0; c < 16; ++c) {
+    uint32_t o[8];
+    tmem_ld_x8(tmem + (c >> 2) * kHT + (c & 3) * 8, o);
+    tmem_ld_wait();
+    const int i0 = (c & 3) * 8;
+    T* at = dst + i0 * stride + value_of(c >> 2, pos);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i0 + i < nh) store_value(at, __uint_as_float(o[i]) * S.alpha[h0 + i0 + i]);
+      at += stride;
+    }
+  }
+}
+
+// Warp (qw, sub): TMEM lanes 32 qw .., that is half e = qw >> 1 of the values and
+// positions 32 (qw & 1) ..; of the 32 heads from 32 sub on it takes the 16 from
+// 16 e on, and gives its partial scores of the other 16 to warp (qw ^ 2, sub).
+// The four warps of a `sub` share a named barrier.
 __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tmem) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int qw = warp & 3, half = warp >> 2;          // TMEM lane quarter; heads 32 half ..
+  const int qw = warp & 3, sub = warp >> 2, e = qw >> 1;
   const uint32_t lanes = static_cast<uint32_t>(32 * qw) << 16;
-  const int pos = 32 * qw + lane, bar = 1 + half;
-  float* part = S.part[half][0];
-  const float4* m4 = reinterpret_cast<const float4*>(S.m + 32 * half);
-  const f32x2* de2 = reinterpret_cast<const f32x2*>(S.delta + 32 * half);
-  const f32x2* al2 = reinterpret_cast<const f32x2*>(S.alpha + 32 * half);
+  const int pos = 32 * (qw & 1) + lane, bar = 1 + sub, h0 = 32 * sub + 16 * e;
+  float* part = S.part[sub][0];
+  const f32x2* m2 = reinterpret_cast<const f32x2*>(S.m + h0);
+  const f32x2* de2 = reinterpret_cast<const f32x2*>(S.delta + h0);
+  const f32x2* al2 = reinterpret_cast<const f32x2*>(S.alpha + h0);
+  // 16-byte pieces of a position's 64 bytes, swizzled so that eight lanes cover all banks
+  float* give = S.x[2 * sub + e][pos];
+  const float* take = S.x[2 * sub + (e ^ 1)][pos];
+  const int swz = (lane >> 1) & 3;
   bool ok = true, seen = false;
-  f32x2 l[16];
+  f32x2 l[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) l[i] = pair_of(0.0f, 0.0f);
+  for (int i = 0; i < 8; ++i) l[i] = pair_of(0.0f, 0.0f);
   uint32_t n = 0, seg = 0;
   // A wait that gives up clears `ok`; the warps still run through the same
   // named barriers, on whatever TMEM holds, and write no output.
   for (Walk w(a, S); w.valid(); w.next(a, S), ++n) {
+    const uint32_t buf = n & 1, parity = (n >> 1) & 1;
     if (w.first()) {                                  // the heads' factors
       if (ok && !wait(&S.qfull, seg & 1)) ok = false;
       ++seg;
+      seen = false;
       // the queries after these wait for this warp too, so that it sees every
       // phase of the barrier
       if (lane == 0) mbar_arrive(&S.qempty);
     }
-    if (ok && !wait(&S.full[0], n & 1)) ok = false;                  // the row scales
-    if (ok && !wait(&S.sfull, n & 1)) ok = false;
+    if (ok && !wait(&S.sfull[buf], parity)) ok = false;
+    if (ok && !wait(&S.full[buf], parity)) ok = false;            // the row scales
     tc_fence_after();
-    if (w.first()) seen = false;
-    uint32_t xr[32];
-    tmem_ld_32x32b_x32(tmem + lanes + kSCol + 32 * half, xr);
-    tmem_ld_wait();
+    f32x2 d[8];
+    {
+      // the partner's block first: its values go out while the own ones arrive
+      uint32_t own[16], other[16];
+      const uint32_t at = tmem + lanes + kSCol + 128 * buf + 64 * e + 32 * sub;
+      tmem_ld_x16(at + 16 * (e ^ 1), other);
+      tmem_ld_x16(at + 16 * e, own);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(give + 4 * (i ^ swz)) =
+            make_uint4(other[4 * i], other[4 * i + 1], other[4 * i + 2], other[4 * i + 3]);
+      tc_fence_before();
+      named_bar(bar, 128);
+      if (lane == 0) mbar_arrive(&S.sfree[buf]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(take + 4 * (i ^ swz));
+        d[2 * i] = add2(pair_of(__uint_as_float(own[4 * i]), __uint_as_float(own[4 * i + 1])), pair_of(v.x, v.y));
+        d[2 * i + 1] =
+            add2(pair_of(__uint_as_float(own[4 * i + 2]), __uint_as_float(own[4 * i + 3])), pair_of(v.z, v.w));
+      }
+    }
     // d = y - M + kShift; no position here: -inf, weight 0. 1 / s is taken from
     // the logarithm that d uses, so that p / s is free of its error.
-    const float s = S.rs[n & 1][pos];
-    const bool some = s != 0.0f;
-    const float ls = lg2(s), inv_s = some ? ex2(-ls) : 0.0f;
-    const float4* c4 = reinterpret_cast<const float4*>(S.sl2[(seg - 1) & 1] + 32 * half);
-    f32x2 d[16];
+    const float s = S.rs[buf][pos];
+    const float ls = lg2(s), inv_s = s != 0.0f ? ex2(-ls) : 0.0f;
+    const f32x2* c2 = reinterpret_cast<const f32x2*>(S.sl2[(seg - 1) & 1] + h0);
     float over = -INFINITY;
     {
       const f32x2 s2 = pair_of(s, s), ls2 = pair_of(ls + kShift, ls + kShift);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float4 c = c4[i], m = m4[i];
-        d[2 * i] = fma2(mul2(pair_of(__uint_as_float(xr[4 * i]), __uint_as_float(xr[4 * i + 1])),
-                             pair_of(c.x, c.y)),
-                        s2, sub2(ls2, pair_of(m.x, m.y)));
-        d[2 * i + 1] = fma2(mul2(pair_of(__uint_as_float(xr[4 * i + 2]), __uint_as_float(xr[4 * i + 3])),
-                                 pair_of(c.z, c.w)),
-                            s2, sub2(ls2, pair_of(m.z, m.w)));
-        const float2 u = both(d[2 * i]), v = both(d[2 * i + 1]);
-        over = fmaxf(over, fmaxf(fmaxf(u.x, u.y), fmaxf(v.x, v.y)));
+        d[i] = fma2(mul2(d[i], c2[i]), s2, sub2(ls2, m2[i]));
+        const float2 u = both(d[i]);
+        over = fmaxf(over, fmaxf(u.x, u.y));
       }
     }
-    const uint32_t mine = (__any_sync(0xffffffffu, over > kSlack + kShift) ? 1u : 0u) |
-                          (__any_sync(0xffffffffu, some) ? 2u : 0u);
-    if (lane == 0) S.flag[n & 1][half][qw] = static_cast<int32_t>(mine);
+    // until something was seen, any position sets the references
+    const bool rises = __any_sync(0xffffffffu, over > (seen ? kSlack + kShift : -INFINITY));
+    if (lane == 0) S.flag[buf][sub][qw] = rises ? 1 : 0;
+    // the products of the units before are done: P and O^T may change
+    if (ok && n > 0 && !wait(&S.pvdone, (n - 1) & 1)) ok = false;
+    tc_fence_after();
     named_bar(bar, 128);
-    const int4 fl = *reinterpret_cast<const int4*>(S.flag[n & 1][half]);
-    const int32_t flags = fl.x | fl.y | fl.z | fl.w;
-    if ((flags & 1) || ((flags & 2) && !seen)) {
+    const int4 fl = *reinterpret_cast<const int4*>(S.flag[buf][sub]);
+    if ((fl.x | fl.y | fl.z | fl.w) != 0) {
       // move references to the maxima so far: each head decides for itself, a
       // non-finite one keeps its reference
-      part[qw * 32 + lane] = across(d, lane, [](float p, float q) { return fmaxf(p, q); });
+      const float top = across(d, lane, [](float p, float q) { return fmaxf(p, q); });
+      part[qw * 16 + (lane >> 1)] = top;
       named_bar(bar, 128);
-      float up = fmaxf(fmaxf(part[lane], part[32 + lane]), fmaxf(part[64 + lane], part[96 + lane])) - kShift;
+      const int at = (lane >> 4) * 32 + (lane & 15);
+      float up = fmaxf(part[at], part[at + 16]) - kShift;
       if ((seen && !(up > kSlack)) || !(fabsf(up) < INFINITY)) up = 0.0f;
       if (qw == 0) {
-        S.m[32 * half + lane] += up;
-        S.delta[32 * half + lane] = up;
-        S.alpha[32 * half + lane] = seen ? ex2(-up) : 1.0f;
+        S.m[32 * sub + lane] += up;
+        S.delta[32 * sub + lane] = up;
+        S.alpha[32 * sub + lane] = seen ? ex2(-up) : 1.0f;
       }
       named_bar(bar, 128);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 8; ++i) {
         d[i] = sub2(d[i], de2[i]);
         l[i] = mul2(l[i], al2[i]);
       }
       if (seen) {
-        // the products of the units before are done: this unit's tile was
-        // filled after them
 #pragma unroll 1
-        for (int e = 0; e < 4; ++e) {
-          uint32_t o[32];
-          const uint32_t at = tmem + lanes + kOCol + e * kHT + 32 * half;
-          tmem_ld_32x32b_x32(at, o);
+        for (int c = 0; c < 16; ++c) {
+          uint32_t o[8];
+          const uint32_t oe = tmem + lanes + kOCol + (c >> 2) * kHT + 32 * sub + (c & 3) * 8;
+          tmem_ld_x8(oe, o);
           tmem_ld_wait();
+          const float* al = S.alpha + 32 * sub + (c & 3) * 8;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            o[i] = __float_as_uint(__uint_as_float(o[i]) * S.alpha[32 * half + i]);
-          tmem_st_32x32b_x32(at, o);
+          for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al[i]);
+          tmem_st_x8(oe, o);
         }
         tmem_st_wait();
       }
@@ -788,7 +845,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     }
     const f32x2 is2 = pair_of(inv_s, inv_s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       uint32_t h[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -797,7 +854,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
         l[4 * i + k] = fma2(pair_of(px, py), is2, l[4 * i + k]);
         h[k] = pack_half2(px, py);
       }
-      *reinterpret_cast<uint4*>(&S.p[sw(pos, 4 * half + i)]) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(&S.p[sw(pos, h0 / 8 + i)]) = make_uint4(h[0], h[1], h[2], h[3]);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -806,57 +863,37 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     if (!w.last()) continue;
 
     // ---- the row tile's end in this CTA: totals, then the output
-    part[qw * 32 + lane] = across(l, lane, [](float p, float q) { return p + q; });
+    const float sum = across(l, lane, [](float p, float q) { return p + q; });
+    part[qw * 16 + (lane >> 1)] = sum;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) l[i] = pair_of(0.0f, 0.0f);
+    for (int i = 0; i < 8; ++i) l[i] = pair_of(0.0f, 0.0f);
     named_bar(bar, 128);
-    const float total = (part[lane] + part[32 + lane]) + (part[64 + lane] + part[96 + lane]);
-    const float lse2 = total == 0.0f ? -INFINITY : S.m[32 * half + lane] - kShift + log2f(total);
+    const int at = (lane >> 4) * 32 + (lane & 15);    // lane: head 32 sub + lane
+    const float total = part[at] + part[at + 16];
+    const float lse2 = total == 0.0f ? -INFINITY : S.m[32 * sub + lane] - kShift + log2f(total);
     named_bar(bar, 128);
     if (qw == 0) {
-      S.alpha[32 * half + lane] = total == 0.0f ? 0.0f : 1.0f / total;
-      S.m[32 * half + lane] = 0.0f;
+      S.alpha[32 * sub + lane] = total == 0.0f ? 0.0f : 1.0f / total;
+      S.m[32 * sub + lane] = 0.0f;
     }
     named_bar(bar, 128);
     if (ok && !wait(&S.pvdone, n & 1)) ok = false;
     tc_fence_after();
-    const int32_t h = w.g * kHT + 32 * half;          // first head of this half
-    const bool whole = w.i == w.n - 1 && w.began_here();
-    if (!ok) {
-      // nothing to write
-    } else if (whole) {
-      if (qw == 0 && h + lane < a.H && a.lse)
+    const int32_t h = w.g * kHT + 32 * sub;           // first head of this sub
+    const int32_t nh = ok ? min(32, a.H - h) : 0;     // heads to write
+    const uint32_t oe = tmem + lanes + kOCol + 32 * sub;
+    if (w.i == w.n - 1 && w.began_here()) {
+      if (qw == 0 && lane < nh && a.lse)
         a.lse[static_cast<int64_t>(a.t0 + w.t) * a.H + h + lane] = lse2 * kLn2;
       uint16_t* orow = a.out + static_cast<int64_t>(a.t0 + w.t) * a.o_st + h * a.o_sh;
-#pragma unroll 1
-      for (int e = 0; e < 4; ++e) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(tmem + lanes + kOCol + e * kHT + 32 * half, o);
-        tmem_ld_wait();
-        const int v = value_of(e, pos);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float inv = S.alpha[32 * half + i];
-          const __nv_bfloat16 y = __float2bfloat16_rn(__uint_as_float(o[i]) * inv);
-          if (h + i < a.H) orow[i * a.o_sh + v] = *reinterpret_cast<const uint16_t*>(&y);
-        }
-      }
+      output(S, oe, 32 * sub, 32 * qw + lane, nh, orow, a.o_sh);
     } else {
       // a row tile that began in an earlier CTA goes to slot 0, one that goes
       // on in the next to slot 1
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.began_here() ? 1 : 0);
-      if (qw == 0) a.piece_lse[slot * kHT + 32 * half + lane] = lse2;
-      float* dst = a.piece + slot * kPieceRow + (32 * half) * kD;
-#pragma unroll 1
-      for (int e = 0; e < 4; ++e) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(tmem + lanes + kOCol + e * kHT + 32 * half, o);
-        tmem_ld_wait();
-        const int v = value_of(e, pos);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (h + i < a.H) dst[i * kD + v] = __uint_as_float(o[i]) * S.alpha[32 * half + i];
-      }
+      if (qw == 0) a.piece_lse[slot * kHT + 32 * sub + lane] = lse2;
+      output(S, oe, 32 * sub, 32 * qw + lane, nh, a.piece + slot * kPieceRow + (32 * sub) * kD,
+             static_cast<int64_t>(kD));
     }
     named_bar(bar, 128);                              // the factors are read
   }
@@ -873,13 +910,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
   if (warp == kMmaWarp) tmem_alloc(&S.tmem_base, kTmemCols);
   if (tid == 0) {
     for (int h = 0; h < kHT; ++h) S.m[h] = 0.0f;
-    for (int e = 0; e < 4; ++e) {
-      mbar_init(&S.full[e], kLoadWarps);
-      mbar_init(&S.empty[e], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.full[i], kLoadWarps);
+      mbar_init(&S.empty[i], 1);
+      mbar_init(&S.sfull[i], 1);
+      mbar_init(&S.sfree[i], kSoftWarps);
     }
     mbar_init(&S.qfull, kQueryWarps);
     mbar_init(&S.qempty, 1 + kSoftWarps);
-    mbar_init(&S.sfull, 1);
     mbar_init(&S.pready, kSoftWarps);
     mbar_init(&S.pvdone, 1);
     mbar_init(&S.done, 1);
@@ -891,16 +929,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
   const uint32_t tmem = S.tmem_base;
   if (S.count > 0) {
     bool ok = true;
-    if (warp < kSoftWarps) {
-      setmaxnreg_inc<kSoftRegs>();
+    if (warp < kSoftWarps)
       ok = run_softmax(a, S, tmem);
-    } else if (warp < kMmaWarp) {
-      setmaxnreg_dec<kLoadRegs>();
+    else if (warp < kMmaWarp)
       ok = run_loaders<kFp8>(a, S);
-    } else {
-      setmaxnreg_dec<kMmaRegs>();
+    else
       ok = warp == kMmaWarp ? run_mma(a, S, tmem) : run_queries(a, S);
-    }
     if (!ok && lane == 0 && a.err) atomicOr(a.err, QLI_DEVERR_TIMEOUT);
   }
   tc_fence_before();
@@ -919,32 +953,28 @@ __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a
   pdl_wait();
   const int lane = threadIdx.x & 31, c = blockIdx.x + 1;
   const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-  const int64_t U = a.tok_start[a.tc];
-  const int64_t uc = U * c / ctas, ub = U * (c - 1) / ctas;
+  const int32_t U = a.tok_start[a.tc];
+  const int32_t uc = share_begin(U, ctas, c), ub = share_begin(U, ctas, c - 1);
   if (uc == ub || uc >= U) return;
   int32_t lo = 0, hi = a.tc - 1;
   while (lo < hi) {
     const int32_t mid = (lo + hi + 1) >> 1;
     if (a.tok_start[mid] <= uc) lo = mid; else hi = mid - 1;
   }
-  const int64_t base = a.tok_start[lo], n = (a.tok_start[lo + 1] - base) / a.hg;
-  const int32_t g = static_cast<int32_t>((uc - base) / n);
-  const int64_t start = base + g * n, end = start + n;
+  const int32_t base = a.tok_start[lo], n = (a.tok_start[lo + 1] - base) / a.hg;
+  const int32_t g = (uc - base) / n, start = base + g * n, end = start + n;
   const int32_t h = g * kHT + row;
   if (uc == start || ub > start || h >= a.H) return;   // not cut, or cut before
   // pieces: CTA c - 1's slot 1, then slot 0 of CTA c, c + 1, ... up to the end
+  // (a CTA with units has all its predecessors with units)
   int32_t last = c;
-  while (last + 1 < ctas && U * (last + 1) / ctas < end) ++last;
+#pragma unroll 1
+  while (last + 1 < ctas && share_begin(U, ctas, last + 1) < end) ++last;
   const int32_t count = last - c + 2;
   const auto slot = [&](int32_t k) -> int64_t {
     return k == 0 ? 2 * static_cast<int64_t>(c - 1) + 1 : 2 * static_cast<int64_t>(c - 1 + k);
   };
-  // a CTA without units left no piece
-  const auto lse_of = [&](int32_t k) -> float {
-    const int64_t cta = c - 1 + k;
-    if (U * cta / ctas == U * (cta + 1) / ctas) return -INFINITY;
-    return a.piece_lse[slot(k) * kHT + row];
-  };
+  const auto lse_of = [&](int32_t k) -> float { return a.piece_lse[slot(k) * kHT + row]; };
   float m = -INFINITY;
   for (int32_t k = lane; k < count; k += 32) m = fmaxf(m, lse_of(k));
 #pragma unroll
@@ -1080,7 +1110,7 @@ struct Layout {
 Layout layout_for(int sms) {
   Layout L{};
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  L.piece = up(sizeof(int64_t) * (kChunkT + 1));
+  L.piece = up(sizeof(int32_t) * (kChunkT + 1));
   L.lse = L.piece + up(sizeof(float) * 2 * static_cast<size_t>(sms) * kPieceRow);
   L.total = L.lse + up(sizeof(float) * 2 * static_cast<size_t>(sms) * kHT);
   return L;
@@ -1091,8 +1121,12 @@ cudaError_t launch(Args d, int sms, cudaStream_t s) {
   const auto kernel = kv_attn_kernel<kFp8>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kSmemBytes,
                                     g_smem_kv_attn[kFp8 ? 1 : 0]);
-  for (d.t0 = 0; e == cudaSuccess && d.t0 < d.T; d.t0 += kChunkT) {
-    d.tc = d.T - d.t0 < kChunkT ? d.T - d.t0 : kChunkT;
+  // tokens per launch: what one plan holds, and fewer than 2^30 units
+  const int64_t most = (d.idx ? static_cast<int64_t>(d.K) : d.cap < INT32_MAX ? d.cap : INT32_MAX) / kPos + 1;
+  const int64_t fit = (int64_t{1} << 30) / (most * d.hg);
+  const int32_t chunk = static_cast<int32_t>(fit < kChunkT ? fit : kChunkT);
+  for (d.t0 = 0; e == cudaSuccess && d.t0 < d.T; d.t0 += chunk) {
+    d.tc = d.T - d.t0 < chunk ? d.T - d.t0 : chunk;
     const int32_t ctas = ctas_for(d, d.tc, sms);
     kernel<<<static_cast<unsigned>(ctas), kThreads, kSmemBytes, s>>>(d);
     e = cudaGetLastError();
@@ -1135,7 +1169,7 @@ extern "C" qli_status qli_kv_attention(const qli_kv_attn_args* a, void* workspac
   if (!aligned(workspace, 256)) return QLI_ERR_ALIGNMENT;
   Args d = make_args(*a);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  d.tok_start = reinterpret_cast<int64_t*>(w);
+  d.tok_start = reinterpret_cast<int32_t*>(w);
   d.piece = reinterpret_cast<float*>(w + L.piece);
   d.piece_lse = reinterpret_cast<float*>(w + L.lse);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

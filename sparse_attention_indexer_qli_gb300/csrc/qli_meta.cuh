@@ -21,7 +21,7 @@ __device__ __forceinline__ int32_t visible_count(int32_t lk, int32_t res, int32_
   const int64_t S = static_cast<int64_t>(lk) * ratio + res;
   const int64_t seen = S - q_len + i + 1;   // raw tokens at or before the query
   if (seen <= 0) return 0;
-  const int64_t v = seen / ratio;
+  const int64_t v = ratio == 2 ? seen >> 1 : seen;   // the ratios there are: 1 and 2
   return static_cast<int32_t>(v < lk ? v : lk);
 }
 
