@@ -55,7 +55,7 @@ constexpr int kLoadWarp0 = kSoftWarps, kMmaWarp = kSoftWarps + kLoadWarps, kQuer
 constexpr int kThreads = 32 * (kMmaWarp + 1 + kQueryWarps);
 constexpr int kRegion = 128 * 128;             // 64 values of every row of a tile
 constexpr int kTile = 4 * kRegion;
-constexpr int kChunkT = 1024;                  // tokens planned per launch
+constexpr int kChunkT = kThreads;              // tokens planned per launch: one a thread
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 0, kOCol = 256;
 constexpr float kSlack = 8.0f, kShift = 6.0f;
@@ -67,8 +67,7 @@ struct Smem {
   uint8_t q[kTile];                            // 1024-aligned
   uint8_t p[kPos * 128];                       // 1024-aligned
   float x[4][kPos][16];                        // partial scores a softmax warp gives to its partner
-  int32_t tokV[kChunkT];                       // visible positions of the launch's tokens
-  const uint8_t* row[2][kPos];                 // the rows' codes by unit parity
+  int32_t tokV[kChunkT], tokB[kChunkT];        // visible positions and request of the launch's tokens
   float rs[2][kPos];                           // row scales by unit parity; 0: no position
   float sl2[2][kHT];                           // by row tile parity: softmax scale in log2 over the
                                                // queries' power of two
@@ -186,9 +185,7 @@ __device__ __forceinline__ float ex2(float x) {
 // has been probed 2^16 times (0.1 us each while the CTA is busy, 20 us when
 // nothing happens: some ms to a second or so). A loop of five instructions: the
 // roles' loops together have to stay within the instruction cache.
-#ifndef QLI_KV_ATTN_PROBES
-#define QLI_KV_ATTN_PROBES (1 << 16)
-#endif
+constexpr int kProbes = 1 << 16;
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -203,7 +200,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
       "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "n"(QLI_KV_ATTN_PROBES)
+      : "r"(smem_u32(bar)), "r"(parity), "n"(kProbes)
       : "memory");
   return __all_sync(0xffffffffu, ok);
 }
@@ -236,6 +233,20 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// One look at the phase, as a whole warp, without waiting in it.
+__device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok);
+}
+constexpr int kLooks = 1 << 22;                // some 0.1 us each
 
 __device__ __forceinline__ void named_bar(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
@@ -318,37 +329,32 @@ __device__ __forceinline__ int32_t request_of(const int32_t* cu, int32_t B, int3
   return lo;
 }
 
-// Plans the launch: every token's visible positions and the CTA's share. Each
-// thread takes `per` consecutive tokens.
+// Plans the launch: every token's request and visible positions, and the CTA's
+// share. A thread takes one token.
 __device__ __forceinline__ void plan(const Args& a, Smem& S) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the boundaries go through the (still unused) tiles when they fit
   const int32_t* cu = a.cu;
-  if (!a.idx) {
-    // the boundaries go through the (still unused) tile when they fit
-    int32_t* cu_s = reinterpret_cast<int32_t*>(S.kv);
-    if (a.B <= static_cast<int32_t>(sizeof(S.kv) / 4)) {
+  int32_t* cu_s = reinterpret_cast<int32_t*>(S.kv);
+  if (a.B <= static_cast<int32_t>(sizeof(S.kv) / 4)) {
 #pragma unroll 1
-      for (int b = tid; b < a.B; b += kThreads) cu_s[b] = __ldg(a.cu + b);
-      cu = cu_s;
-    }
-    __syncthreads();
+    for (int b = tid; b < a.B; b += kThreads) cu_s[b] = __ldg(a.cu + b);
+    cu = cu_s;
   }
-  const int per = (a.tc + kThreads - 1) / kThreads;
-  const int lo = min(a.tc, tid * per), hi = min(a.tc, lo + per);
-  int32_t mine = 0;
-#pragma unroll 1
-  for (int i = lo; i < hi; ++i) {
-    int32_t V = 0;
+  __syncthreads();
+  int32_t V = 0, units = 0;
+  if (tid < a.tc) {
+    const int32_t t = a.t0 + tid, b = request_of(cu, a.B, a.T, t);
     if (!a.idx) {
-      const int32_t t = a.t0 + i;
       int32_t q0, q1, lk, res;
-      sanitize_request(a, request_of(cu, a.B, a.T, t), q0, q1, lk, res);
+      sanitize_request(a, b, q0, q1, lk, res);
       if (q0 <= t && t < q1) V = visible_count(lk, res, a.ratio, q1 - q0, t - q0);
     }
-    S.tokV[i] = V;
-    mine += units_of(a, V);
+    S.tokV[tid] = V;
+    S.tokB[tid] = b;
+    units = units_of(a, V);
   }
-  mine *= a.hg;
+  const int32_t mine = units * a.hg;
   int32_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -365,22 +371,17 @@ __device__ __forceinline__ void plan(const Args& a, Smem& S) {
     if (lane >= o) sums += y;
   }
   const int32_t total = __shfl_sync(0xffffffffu, sums, 31);
-  int32_t at = __shfl_sync(0xffffffffu, sums, warp) - own + incl - mine;
+  const int32_t at = __shfl_sync(0xffffffffu, sums, warp) - own + incl - mine;
   const int32_t ctas = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
   const int32_t u0 = share_begin(total, ctas, c);
   if (tid == 0) S.count = share_begin(total, ctas, c + 1) - u0;
-#pragma unroll 1
-  for (int i = lo; i < hi; ++i) {
-    const int32_t n = units_of(a, S.tokV[i]);
-    if (c == 0) a.tok_start[i] = at;
-    if (at <= u0 && u0 < at + n * a.hg) {
-      S.start_t = i;
-      S.start_g = (u0 - at) / n;
-      S.start_i = (u0 - at) % n;
-    }
-    at += n * a.hg;
+  if (at <= u0 && u0 < at + mine) {
+    S.start_t = tid;
+    S.start_g = (u0 - at) / units;
+    S.start_i = (u0 - at) % units;
   }
   if (c == 0) {
+    if (tid < a.tc) a.tok_start[tid] = at;
     if (tid == 0) a.tok_start[a.tc] = total;
     if (!a.idx && a.t0 == 0 && a.err) {
       uint32_t e = 0u;
@@ -407,41 +408,6 @@ __device__ __forceinline__ int value_of(int c, int row) {
 
 // What rows without a position, and rows of zeros, are filled from.
 __device__ __align__(16) const uint8_t kZeroRow[kD] = {};
-
-// Row r of the walk's unit: its codes into S.row, its scale (0: no position
-// there). Positions past the table and pages outside the pool are skipped and
-// flagged. A row under a zero scale stands for zeros whatever its codes are:
-// it counts in the normaliser only, under the smallest scale there is, so that
-// it does not set the reference. The codes are fetched into L2 on the way.
-__device__ __forceinline__ float find_row(const Args& a, Smem& S, const Walk& w, int32_t b, int r,
-                                          uint32_t parity, bool& bad) {
-  const int32_t V = S.tokV[w.t], n = positions_of(a, V), e = w.i * kPos + r;
-  const uint8_t* codes = kZeroRow;
-  float s = 0.0f;
-  int64_t j = -1;
-  if (e < n) j = a.idx ? __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e) : V - n + e;
-  if (j >= a.cap) {
-    bad = true;
-  } else if (j >= 0) {
-    const int32_t page = __ldg(a.bt + static_cast<int64_t>(b) * a.bt_stride + (j >> a.log2R));
-    if (page < 0 || page >= a.num_pages) {
-      bad = true;
-    } else {
-      const uint8_t* base = a.cache + static_cast<int64_t>(page) * a.page_stride;
-      const int32_t row = static_cast<int32_t>(j) & (a.R - 1);
-      codes = base + a.kv_off + row * kD;
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(codes), "n"(kD));
-      s = __half2float(__ushort_as_half(
-          __ldg(reinterpret_cast<const uint16_t*>(base + a.sc_off + row * 2))));
-      if (s == 0.0f) {
-        s = 5.9604645e-8f;
-        codes = kZeroRow;
-      }
-    }
-  }
-  S.row[parity][r] = codes;
-  return s;
-}
 
 // The row tile's queries as FP16 times a power of two per head that brings the
 // head's largest magnitude to [2^13, 2^14); rows past H are zero.
@@ -509,30 +475,38 @@ __device__ __forceinline__ bool run_queries(const Args& a, Smem& S) {
   return true;
 }
 
-// Iteration n stores unit n from registers, then loads unit n + 1 (32 KB in
-// flight on the SM while unit n is worked on), then looks up the rows of unit
-// n + 2. A warp has eight rows; a warp instruction loads one quarter of four.
+// Iteration n stores unit n from registers, loads unit n + 1 (32 KB in flight
+// on the SM while unit n is worked on), and takes one step each of the lookup
+// of units n + 2 (page to codes and scale, the codes fetched into L2), n + 3
+// (position to page) and n + 4 (listed entry to position), so that no step
+// waits for the load of the one before. A warp has eight rows, looked up by its
+// lanes modulo eight; a warp instruction loads one quarter of four rows.
+// Positions past the table and pages outside the pool are skipped and flagged.
 template <bool kFp8>
 __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
   constexpr int kWarpRows = kPos / kLoadWarps;
   const int lane = threadIdx.x & 31, lw = (threadIdx.x >> 5) - kLoadWarp0;
-  const int r = kWarpRows * lw + lane;                // lanes 0-7: the row looked up
+  const int r = kWarpRows * lw + (lane & (kWarpRows - 1));    // the row looked up
   const int r0 = kWarpRows * lw + (lane >> 3), off = (lane & 7) * 16;
   // rows 4 apart: 512 bytes on, and bit 2 of the swizzled unit flips
   const uint32_t at0 = smem_u32(S.kv) + sw(r0, lane & 7), at1 = (at0 ^ 64u) + 512;
   bool bad = false, ok = true;
-  Walk w(a, S);                                       // the unit looked up next
-  int32_t bt = -1, b = 0;
-  float s0 = 0.0f, s1 = 0.0f;                         // scales of units n and n + 1
+  Walk w(a, S);                                       // unit n + 4
+  int32_t j4 = -1, b4 = 0;                            // position, request
+  int32_t j3 = -1, page3 = -1;                        // position, page
+  const uint8_t* codes2 = kZeroRow;                   // codes and scale
+  uint16_t s2 = 0;
+  bool live2 = false;
+  float s1 = 0.0f;                                    // scale for the softmax (0: no position)
   uint4 x[2][4];
 #pragma unroll 1
-  for (int32_t n = -2; n < w.count; ++n) {
+  for (int32_t n = -4; n < w.count; ++n) {
     if (n >= 0) {
       if (!wait(&S.empty[n & 1], ((n >> 1) & 1) ^ 1)) {
         ok = false;
         break;
       }
-      if (lane < kWarpRows) S.rs[n & 1][r] = s0;
+      if (lane < kWarpRows) S.rs[n & 1][r] = s1;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -548,24 +522,45 @@ __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.full[n & 1]);
     }
-    if (n >= -1 && n + 1 < w.count) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint8_t* row = S.row[(n + 1) & 1][r0 + 4 * k] + off;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[k][c] = __ldg(reinterpret_cast<const uint4*>(row + c * 128));
-      }
+    // unit n + 1. A row under a zero scale stands for zeros whatever its codes
+    // are: it counts in the normaliser only, under the smallest scale there
+    // is, so that it does not set the reference.
+    s1 = live2 ? __half2float(__ushort_as_half(s2)) : 0.0f;
+    if (live2 && s1 == 0.0f) {
+      s1 = 5.9604645e-8f;
+      codes2 = kZeroRow;
     }
-    s0 = s1;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint8_t* row =
+          reinterpret_cast<const uint8_t*>(__shfl_sync(
+              0xffffffffu, reinterpret_cast<uintptr_t>(codes2), 4 * k + (lane >> 3))) + off;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[k][c] = __ldg(reinterpret_cast<const uint4*>(row + c * 128));
+    }
+    // unit n + 2
+    codes2 = kZeroRow;
+    live2 = j3 >= 0 && page3 >= 0 && page3 < a.num_pages;
+    bad |= j3 >= 0 && !live2;
+    if (live2) {
+      const uint8_t* base = a.cache + static_cast<int64_t>(page3) * a.page_stride;
+      const int32_t row = j3 & (a.R - 1);
+      codes2 = base + a.kv_off + row * kD;
+      s2 = __ldg(reinterpret_cast<const uint16_t*>(base + a.sc_off + row * 2));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(codes2 + (lane >> 3) * 128));
+    }
+    // unit n + 3
+    bad |= j4 >= a.cap;
+    j3 = j4 < a.cap ? j4 : -1;
+    if (j3 >= 0) page3 = __ldg(a.bt + static_cast<int64_t>(b4) * a.bt_stride + (j3 >> a.log2R));
+    // unit n + 4
+    j4 = -1;
     if (w.valid()) {
-      if (w.t != bt) {
-        bt = w.t;
-        b = request_of(a.cu, a.B, a.T, a.t0 + bt);
-      }
-      if (lane < kWarpRows) s1 = find_row(a, S, w, b, r, n & 1, bad);
+      const int32_t V = S.tokV[w.t], m = positions_of(a, V), e = w.i * kPos + r;
+      b4 = S.tokB[w.t];
+      if (e < m) j4 = a.idx ? __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e) : V - m + e;
       w.next(a, S);
     }
-    __syncwarp();
   }
   if (bad && a.err) atomicOr(a.err, QLI_DEVERR_PAGE);
   return ok;
@@ -613,59 +608,59 @@ __device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem_an
   const uint32_t k_lo = sdesc_lo(smem_u32(S.kv), 16), q_lo = sdesc_lo(smem_u32(S.q), 16);
   const uint32_t v_lo = sdesc_lo(smem_u32(S.kv), kRegion), p_lo = sdesc_lo(smem_u32(S.p), 1024);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
-  bool ok = true;
-  uint32_t seg = 0, more = 0;
-  Walk w(a, S);
-#pragma unroll 1
-  for (int32_t n = 0; n <= w.count; ++n) {
-    const uint32_t buf = n & 1, parity = (n >> 1) & 1;
+  uint32_t seg = 0;
+  int32_t nq = 0, np = 0;                             // units whose scores, values come next
+  uint32_t fresh = 0;                                 // bit 0, 1: unit nq - 1, nq - 2 starts a row tile
+  Walk w(a, S);                                       // unit nq
+  // whichever is ready first: the scores of unit nq, or the values of unit np
+  int32_t looks = 0;
+  while (np < w.count && looks < kLooks) {
+    ++looks;
+    const uint32_t qb = nq & 1, qparity = (nq >> 1) & 1;
     const bool first = w.first();
-    if (n < w.count) {
-      // scores of unit n, while the softmax has unit n - 1
-      if ((first && !wait(&S.qfull, seg++ & 1)) || !wait(&S.full[buf], parity) ||
-          !wait(&S.sfree[buf], parity ^ 1)) {
-        ok = false;
-        break;
-      }
+    if (nq < w.count && ready(&S.full[qb], qparity) && ready(&S.sfree[qb], qparity ^ 1) &&
+        (!first || ready(&S.qfull, seg & 1))) {
       tc_fence_after();
       const bool last = w.last();
       if (elect_one()) {
-        const uint32_t ke = k_lo + buf * (kTile >> 4), se = tmem + kSCol + buf * 128;
+        const uint32_t ke = k_lo + qb * (kTile >> 4), se = tmem + kSCol + qb * 128;
         mma_first(se, ke, q_lo, hi, id_qk, 0u);
 #pragma unroll
         for (uint32_t k = 1; k < 16; ++k) {
           const uint32_t step = ((k >> 2) * kRegion + (k & 3) * 32) >> 4;
           mma(se, ke + step, q_lo + step, hi, id_qk);
         }
-        mma_commit(&S.sfull[buf]);
+        mma_commit(&S.sfull[qb]);
         if (last) mma_commit(&S.qempty);
       }
       __syncwarp();
+      seg += first ? 1 : 0;
+      fresh = (fresh << 1) | (first ? 1u : 0u);
+      ++nq;
       w.next(a, S);
+      looks = 0;
     }
-    if (n > 0) {
-      // values of unit n - 1
-      if (!wait(&S.pready, (n - 1) & 1)) {
-        ok = false;
-        break;
-      }
+    if (np < nq && ready(&S.pready, np & 1)) {
       tc_fence_after();
       if (elect_one()) {
+        const uint32_t more = ((fresh >> (nq - 1 - np)) & 1u) ^ 1u;
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {
-          const uint32_t ve = v_lo + (((buf ^ 1) * kTile + (c & 1) * 2 * kRegion + (c >> 1) * 64 * 128) >> 4);
+          const uint32_t ve = v_lo + (((np & 1) * kTile + (c & 1) * 2 * kRegion + (c >> 1) * 64 * 128) >> 4);
           const uint32_t oe = tmem + kOCol + c * kHT;
           mma_first(oe, ve, p_lo, hi, id_pv, more);
 #pragma unroll
           for (uint32_t k = 1; k < 4; ++k) mma(oe, ve + (k * 2048 >> 4), p_lo + (k * 2048 >> 4), hi, id_pv);
         }
-        mma_commit(&S.empty[buf ^ 1]);
+        mma_commit(&S.empty[np & 1]);
         mma_commit(&S.pvdone);
       }
       __syncwarp();
+      ++np;
+      looks = 0;
     }
-    more = first ? 0u : 1u;                           // for the values of unit n
   }
+  const bool ok = np == w.count;
   if (elect_one()) mma_commit(&S.done);               // every product of the CTA
   __syncwarp();
   return wait(&S.done, 0) && ok;
