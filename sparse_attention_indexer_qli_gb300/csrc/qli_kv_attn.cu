@@ -22,7 +22,8 @@
 //   8-15  loaders: a unit's 64 rows of codes in flight in registers, widened to
 //         FP16 and stored in one of two 128-byte-swizzled tiles
 //   16    MMA issuer: the scores of unit n + 1, then the values of unit n
-//   17-19 the row tile's queries
+//   17    the units' rows: pages, scales, fetches into L2, up to four units ahead
+//   18-19 the row tile's queries
 // A tile's 128 rows are (half e of the 512 values, position), the queries are
 // stacked alike, so the scores are one product of M = 128, N = 128, K = 256
 // whose blocks e = e' are the halves' partial scores (the other two are
@@ -51,11 +52,13 @@ constexpr int kD = 512;
 constexpr int kHT = 64;                        // heads per row tile (MMA N)
 constexpr int kPos = 64;                       // positions per unit
 constexpr int kSoftWarps = 8, kLoadWarps = 8;
-constexpr int kLoadWarp0 = kSoftWarps, kMmaWarp = kSoftWarps + kLoadWarps, kQueryWarps = 3;
-constexpr int kThreads = 32 * (kMmaWarp + 1 + kQueryWarps);
+constexpr int kLoadWarp0 = kSoftWarps, kMmaWarp = kSoftWarps + kLoadWarps;
+constexpr int kRowWarp = kMmaWarp + 1, kQueryWarp0 = kMmaWarp + 2, kQueryWarps = 2;
+constexpr int kThreads = 32 * (kQueryWarp0 + kQueryWarps);
+constexpr int kSlots = 4;                      // units whose rows are looked up ahead
 constexpr int kRegion = 128 * 128;             // 64 values of every row of a tile
 constexpr int kTile = 4 * kRegion;
-constexpr int kChunkT = kThreads;              // tokens planned per launch: one a thread
+constexpr int kChunkT = 512;                   // tokens planned per launch, one a thread
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 0, kOCol = 256;
 constexpr float kSlack = 8.0f, kShift = 6.0f;
@@ -68,15 +71,15 @@ struct Smem {
   uint8_t p[kPos * 128];                       // 1024-aligned
   float x[4][kPos][16];                        // partial scores a softmax warp gives to its partner
   int32_t tokV[kChunkT], tokB[kChunkT];        // visible positions and request of the launch's tokens
-  float rs[2][kPos];                           // row scales by unit parity; 0: no position
+  const uint8_t* row[kSlots][kPos];            // the rows' codes, by unit modulo kSlots
+  float rs[kSlots][kPos];                      // and scales; 0: no position
   float sl2[2][kHT];                           // by row tile parity: softmax scale in log2 over the
                                                // queries' power of two
   float m[kHT], alpha[kHT], delta[kHT];
   float part[2][4][16];                        // [32 heads][softmax warp of them][head]
-  alignas(16) int32_t flag[2][2][4];           // [unit parity][32 heads][warp]
   int32_t warp_sum[kThreads / 32];
   int32_t count, start_t, start_g, start_i;    // the CTA's share: units, first token, row tile, unit
-  uint64_t full[2], empty[2], sfull[2], sfree[2], qfull, qempty, pready, pvdone, done;
+  uint64_t full[2], empty[2], sfull[2], sfree[2], rowfull[kSlots], rowfree[kSlots], qfull, qempty, pready, pvdone, done;
   uint32_t tmem_base;
 };
 constexpr int kSmemBytes = static_cast<int>(sizeof(Smem)) + 1024;
@@ -252,11 +255,29 @@ __device__ __forceinline__ void named_bar(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
+// The same, and whether any of the n threads has p.
+__device__ __forceinline__ bool named_bar_any(int id, int n, bool p) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(n), "r"(static_cast<uint32_t>(p))
+      : "memory");
+  return any != 0;
+}
+
 // 16 codes to 16 FP16 values (exact), lowest byte first.
 template <bool kFp8>
 __device__ __forceinline__ void widen16(const uint4 v, uint32_t (&o)[8]) {
   if constexpr (kFp8) {
-    e4m3x16_to_f16x16(v, o);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+          "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+          : "=r"(o[2 * k]), "=r"(o[2 * k + 1])
+          : "r"(w[k]));
   } else {
     // 0x64xx is the FP16 number 1024 + xx; the code plus 128 is xx
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -459,7 +480,7 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
 }
 
 __device__ __forceinline__ bool run_queries(const Args& a, Smem& S) {
-  const int qw = (threadIdx.x >> 5) - kMmaWarp - 1;
+  const int qw = (threadIdx.x >> 5) - kQueryWarp0;
   uint32_t seg = 0;
   for (Walk w(a, S); w.valid(); w.next(a, S)) {
     if (!w.first()) continue;
@@ -475,38 +496,90 @@ __device__ __forceinline__ bool run_queries(const Args& a, Smem& S) {
   return true;
 }
 
-// Iteration n stores unit n from registers, loads unit n + 1 (32 KB in flight
-// on the SM while unit n is worked on), and takes one step each of the lookup
-// of units n + 2 (page to codes and scale, the codes fetched into L2), n + 3
-// (position to page) and n + 4 (listed entry to position), so that no step
-// waits for the load of the one before. A warp has eight rows, looked up by its
-// lanes modulo eight; a warp instruction loads one quarter of four rows.
+// The rows of the units: iteration m publishes unit m and takes one step each of
+// the lookup of units m + 1 (page to codes and scale, the codes fetched into
+// L2), m + 2 (position to page) and m + 3 (listed entry to position), so that no
+// step waits for the load of the one before. Lane l has rows l and l + 32.
 // Positions past the table and pages outside the pool are skipped and flagged.
+__device__ __forceinline__ bool run_rows(const Args& a, Smem& S) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  Walk w(a, S);                                       // unit m + 3
+  int32_t j3[2] = {-1, -1}, b3 = 0;                   // position, request
+  int32_t j2[2] = {-1, -1}, page2[2] = {-1, -1};      // position, page
+  const uint8_t* codes1[2] = {kZeroRow, kZeroRow};    // codes and scale
+  uint16_t s1[2] = {0, 0};
+  bool live1[2] = {false, false};
+#pragma unroll 1
+  for (int32_t m = -3; m < w.count; ++m) {
+    if (m >= 0) {
+      const uint32_t slot = m & (kSlots - 1);
+      if (!wait(&S.rowfree[slot], ((m / kSlots) & 1) ^ 1)) return false;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        // a row under a zero scale stands for zeros whatever its codes are: it
+        // counts in the normaliser only, under the smallest scale there is, so
+        // that it does not set the reference
+        const float s = __half2float(__ushort_as_half(s1[k]));
+        const bool zero = live1[k] && s == 0.0f;
+        S.row[slot][lane + 32 * k] = zero ? kZeroRow : codes1[k];
+        S.rs[slot][lane + 32 * k] = live1[k] ? (zero ? 5.9604645e-8f : s) : 0.0f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.rowfull[slot]);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      // unit m + 1
+      codes1[k] = kZeroRow;
+      live1[k] = j2[k] >= 0 && page2[k] >= 0 && page2[k] < a.num_pages;
+      bad |= j2[k] >= 0 && !live1[k];
+      if (live1[k]) {
+        const uint8_t* base = a.cache + static_cast<int64_t>(page2[k]) * a.page_stride;
+        const int32_t row = j2[k] & (a.R - 1);
+        codes1[k] = base + a.kv_off + row * kD;
+        s1[k] = __ldg(reinterpret_cast<const uint16_t*>(base + a.sc_off + row * 2));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(codes1[k] + c * 128));
+      }
+      // unit m + 2
+      bad |= j3[k] >= a.cap;
+      j2[k] = j3[k] < a.cap ? j3[k] : -1;
+      if (j2[k] >= 0)
+        page2[k] = __ldg(a.bt + static_cast<int64_t>(b3) * a.bt_stride + (j2[k] >> a.log2R));
+    }
+    // unit m + 3
+    j3[0] = j3[1] = -1;
+    if (w.valid()) {
+      const int32_t V = S.tokV[w.t], n = positions_of(a, V);
+      b3 = S.tokB[w.t];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int32_t e = w.i * kPos + lane + 32 * k;
+        if (e < n) j3[k] = a.idx ? __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e) : V - n + e;
+      }
+      w.next(a, S);
+    }
+  }
+  if (bad && a.err) atomicOr(a.err, QLI_DEVERR_PAGE);
+  return true;
+}
+
+// Iteration n stores unit n from registers, then loads unit n + 1 (32 KB in
+// flight on the SM while unit n is worked on). A warp has eight rows; a warp
+// instruction loads one quarter of four.
 template <bool kFp8>
-__device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
-  constexpr int kWarpRows = kPos / kLoadWarps;
+__device__ __forceinline__ bool run_loaders(Smem& S) {
   const int lane = threadIdx.x & 31, lw = (threadIdx.x >> 5) - kLoadWarp0;
-  const int r = kWarpRows * lw + (lane & (kWarpRows - 1));    // the row looked up
-  const int r0 = kWarpRows * lw + (lane >> 3), off = (lane & 7) * 16;
+  const int r0 = kPos / kLoadWarps * lw + (lane >> 3), off = (lane & 7) * 16;
   // rows 4 apart: 512 bytes on, and bit 2 of the swizzled unit flips
   const uint32_t at0 = smem_u32(S.kv) + sw(r0, lane & 7), at1 = (at0 ^ 64u) + 512;
-  bool bad = false, ok = true;
-  Walk w(a, S);                                       // unit n + 4
-  int32_t j4 = -1, b4 = 0;                            // position, request
-  int32_t j3 = -1, page3 = -1;                        // position, page
-  const uint8_t* codes2 = kZeroRow;                   // codes and scale
-  uint16_t s2 = 0;
-  bool live2 = false;
-  float s1 = 0.0f;                                    // scale for the softmax (0: no position)
+  const int32_t count = S.count;
   uint4 x[2][4];
 #pragma unroll 1
-  for (int32_t n = -4; n < w.count; ++n) {
+  for (int32_t n = -1; n < count; ++n) {
     if (n >= 0) {
-      if (!wait(&S.empty[n & 1], ((n >> 1) & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
-      if (lane < kWarpRows) S.rs[n & 1][r] = s1;
+      if (!wait(&S.empty[n & 1], ((n >> 1) & 1) ^ 1)) return false;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -522,48 +595,20 @@ __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.full[n & 1]);
     }
-    // unit n + 1. A row under a zero scale stands for zeros whatever its codes
-    // are: it counts in the normaliser only, under the smallest scale there
-    // is, so that it does not set the reference.
-    s1 = live2 ? __half2float(__ushort_as_half(s2)) : 0.0f;
-    if (live2 && s1 == 0.0f) {
-      s1 = 5.9604645e-8f;
-      codes2 = kZeroRow;
-    }
+    if (n + 1 < count) {
+      const uint32_t slot = (n + 1) & (kSlots - 1);
+      if (!wait(&S.rowfull[slot], ((n + 1) / kSlots) & 1)) return false;
+      const uint8_t* r[2] = {S.row[slot][r0] + off, S.row[slot][r0 + 4] + off};
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint8_t* row =
-          reinterpret_cast<const uint8_t*>(__shfl_sync(
-              0xffffffffu, reinterpret_cast<uintptr_t>(codes2), 4 * k + (lane >> 3))) + off;
+      for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[k][c] = __ldg(reinterpret_cast<const uint4*>(row + c * 128));
-    }
-    // unit n + 2
-    codes2 = kZeroRow;
-    live2 = j3 >= 0 && page3 >= 0 && page3 < a.num_pages;
-    bad |= j3 >= 0 && !live2;
-    if (live2) {
-      const uint8_t* base = a.cache + static_cast<int64_t>(page3) * a.page_stride;
-      const int32_t row = j3 & (a.R - 1);
-      codes2 = base + a.kv_off + row * kD;
-      s2 = __ldg(reinterpret_cast<const uint16_t*>(base + a.sc_off + row * 2));
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(codes2 + (lane >> 3) * 128));
-    }
-    // unit n + 3
-    bad |= j4 >= a.cap;
-    j3 = j4 < a.cap ? j4 : -1;
-    if (j3 >= 0) page3 = __ldg(a.bt + static_cast<int64_t>(b4) * a.bt_stride + (j3 >> a.log2R));
-    // unit n + 4
-    j4 = -1;
-    if (w.valid()) {
-      const int32_t V = S.tokV[w.t], m = positions_of(a, V), e = w.i * kPos + r;
-      b4 = S.tokB[w.t];
-      if (e < m) j4 = a.idx ? __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e) : V - m + e;
-      w.next(a, S);
+        for (int c = 0; c < 4; ++c) x[k][c] = __ldg(reinterpret_cast<const uint4*>(r[k] + c * 128));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.rowfree[slot]);
     }
   }
-  if (bad && a.err) atomicOr(a.err, QLI_DEVERR_PAGE);
-  return ok;
+  return true;
 }
 
 // ---- MMA issuer (one warp) ------------------------------------------------------
@@ -753,8 +798,11 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       // phase of the barrier
       if (lane == 0) mbar_arrive(&S.qempty);
     }
+    const uint32_t slot = n & (kSlots - 1);
+    if (ok && !wait(&S.rowfull[slot], (n / kSlots) & 1)) ok = false;
+    const float s = S.rs[slot][pos];
+    const float ls = lg2(s), inv_s = s != 0.0f ? ex2(-ls) : 0.0f;
     if (ok && !wait(&S.sfull[buf], parity)) ok = false;
-    if (ok && !wait(&S.full[buf], parity)) ok = false;            // the row scales
     tc_fence_after();
     f32x2 d[8];
     {
@@ -769,7 +817,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
         *reinterpret_cast<uint4*>(give + 4 * (i ^ swz)) =
             make_uint4(other[4 * i], other[4 * i + 1], other[4 * i + 2], other[4 * i + 3]);
       tc_fence_before();
-      named_bar(bar, 128);
+      named_bar(3 + 2 * sub + (qw & 1), 64);         // the two partners
       if (lane == 0) mbar_arrive(&S.sfree[buf]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -781,8 +829,6 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     }
     // d = y - M + kShift; no position here: -inf, weight 0. 1 / s is taken from
     // the logarithm that d uses, so that p / s is free of its error.
-    const float s = S.rs[buf][pos];
-    const float ls = lg2(s), inv_s = s != 0.0f ? ex2(-ls) : 0.0f;
     const f32x2* c2 = reinterpret_cast<const f32x2*>(S.sl2[(seg - 1) & 1] + h0);
     float over = -INFINITY;
     {
@@ -795,14 +841,11 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       }
     }
     // until something was seen, any position sets the references
-    const bool rises = __any_sync(0xffffffffu, over > (seen ? kSlack + kShift : -INFINITY));
-    if (lane == 0) S.flag[buf][sub][qw] = rises ? 1 : 0;
+    const bool rises = over > (seen ? kSlack + kShift : -INFINITY);
     // the products of the units before are done: P and O^T may change
     if (ok && n > 0 && !wait(&S.pvdone, (n - 1) & 1)) ok = false;
     tc_fence_after();
-    named_bar(bar, 128);
-    const int4 fl = *reinterpret_cast<const int4*>(S.flag[buf][sub]);
-    if ((fl.x | fl.y | fl.z | fl.w) != 0) {
+    if (named_bar_any(bar, 128, rises)) {
       // move references to the maxima so far: each head decides for itself, a
       // non-finite one keeps its reference
       const float top = across(d, lane, [](float p, float q) { return fmaxf(p, q); });
@@ -854,7 +897,10 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&S.pready);
+    if (lane == 0) {
+      mbar_arrive(&S.pready);
+      mbar_arrive(&S.rowfree[slot]);
+    }
     if (!w.last()) continue;
 
     // ---- the row tile's end in this CTA: totals, then the output
@@ -911,6 +957,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
       mbar_init(&S.sfull[i], 1);
       mbar_init(&S.sfree[i], kSoftWarps);
     }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&S.rowfull[i], 1);
+      mbar_init(&S.rowfree[i], kLoadWarps + kSoftWarps);
+    }
     mbar_init(&S.qfull, kQueryWarps);
     mbar_init(&S.qempty, 1 + kSoftWarps);
     mbar_init(&S.pready, kSoftWarps);
@@ -927,9 +977,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
     if (warp < kSoftWarps)
       ok = run_softmax(a, S, tmem);
     else if (warp < kMmaWarp)
-      ok = run_loaders<kFp8>(a, S);
+      ok = run_loaders<kFp8>(S);
     else
-      ok = warp == kMmaWarp ? run_mma(a, S, tmem) : run_queries(a, S);
+      ok = warp == kMmaWarp ? run_mma(a, S, tmem) : warp == kRowWarp ? run_rows(a, S) : run_queries(a, S);
     if (!ok && lane == 0 && a.err) atomicOr(a.err, QLI_DEVERR_TIMEOUT);
   }
   tc_fence_before();
