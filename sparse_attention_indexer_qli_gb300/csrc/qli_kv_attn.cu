@@ -55,6 +55,10 @@ constexpr int kSoftWarps = 8, kLoadWarps = 8;
 constexpr int kLoadWarp0 = kSoftWarps, kMmaWarp = kSoftWarps + kLoadWarps;
 constexpr int kRowWarp = kMmaWarp + 1, kQueryWarp0 = kMmaWarp + 2, kQueryWarps = 2;
 constexpr int kThreads = 32 * (kQueryWarp0 + kQueryWarps);
+// Registers of the warpgroups' threads, within the CTA's 640 x 96. A spill in a
+// role's loop costs an L2 round trip: the streamed codes leave L1 to nothing else.
+constexpr int kSoftRegs = 120, kLoadRegs = 72;
+static_assert(2 * kSoftRegs + 2 * kLoadRegs + 96 <= 5 * 96, "registers of the CTA");
 constexpr int kSlots = 4;                      // units whose rows are looked up ahead
 constexpr int kRegion = 128 * 128;             // 64 values of every row of a tile
 constexpr int kTile = 4 * kRegion;
@@ -79,7 +83,8 @@ struct Smem {
   float part[2][4][16];                        // [32 heads][softmax warp of them][head]
   int32_t warp_sum[kThreads / 32];
   int32_t count, start_t, start_g, start_i;    // the CTA's share: units, first token, row tile, unit
-  uint64_t full[2], empty[2], sfull[2], sfree[2], rowfull[kSlots], rowfree[kSlots], qfull, qempty, pready, pvdone, done;
+  // tiles by unit parity and pair of regions
+  uint64_t full[2][2], empty[2][2], sfull[2], sfree[2], rowfull[kSlots], rowfree[kSlots], qfull, qempty, pready, pvdone, done;
   uint32_t tmem_base;
 };
 constexpr int kSmemBytes = static_cast<int>(sizeof(Smem)) + 1024;
@@ -265,6 +270,16 @@ __device__ __forceinline__ bool named_bar_any(int id, int n, bool p) {
       : "r"(id), "r"(n), "r"(static_cast<uint32_t>(p))
       : "memory");
   return any != 0;
+}
+
+// The warpgroup's registers per thread.
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // 16 codes to 16 FP16 values (exact), lowest byte first.
@@ -565,8 +580,9 @@ __device__ __forceinline__ bool run_rows(const Args& a, Smem& S) {
   return true;
 }
 
-// Iteration n stores unit n from registers, then loads unit n + 1 (32 KB in
-// flight on the SM while unit n is worked on). A warp has eight rows; a warp
+// Iteration n stores unit n from registers, one pair of regions after the
+// other as they come free, then loads unit n + 1 (32 KB in flight on the SM
+// while unit n is worked on). A warp has eight rows; a warp
 // instruction loads one quarter of four.
 template <bool kFp8>
 __device__ __forceinline__ bool run_loaders(Smem& S) {
@@ -579,21 +595,25 @@ __device__ __forceinline__ bool run_loaders(Smem& S) {
 #pragma unroll 1
   for (int32_t n = -1; n < count; ++n) {
     if (n >= 0) {
-      if (!wait(&S.empty[n & 1], ((n >> 1) & 1) ^ 1)) return false;
+      const int buf = n & 1;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int f = 0; f < 2; ++f) {
+        if (!wait(&S.empty[buf][f], ((n >> 1) & 1) ^ 1)) return false;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[8];
-          widen16<kFp8>(x[k][c], o);
-          const uint32_t at = (k ? at1 : at0) + (n & 1) * kTile + (c & 1) * 2 * kRegion + (c >> 1) * 64 * 128;
-          st_shared_v4(at, o[0], o[1], o[2], o[3]);
-          st_shared_v4(at + kRegion, o[4], o[5], o[6], o[7]);
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t o[8];
+            widen16<kFp8>(x[k][2 * e + f], o);
+            const uint32_t at = (k ? at1 : at0) + buf * kTile + f * 2 * kRegion + e * 64 * 128;
+            st_shared_v4(at, o[0], o[1], o[2], o[3]);
+            st_shared_v4(at + kRegion, o[4], o[5], o[6], o[7]);
+          }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.full[buf][f]);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.full[n & 1]);
     }
     if (n + 1 < count) {
       const uint32_t slot = (n + 1) & (kSlots - 1);
@@ -655,54 +675,68 @@ __device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem_an
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
   uint32_t seg = 0;
   int32_t nq = 0, np = 0;                             // units whose scores, values come next
-  uint32_t fresh = 0;                                 // bit 0, 1: unit nq - 1, nq - 2 starts a row tile
+  uint32_t part = 0;                                  // which half of unit nq's score products
+  uint32_t fresh = 0;                                 // bit i: unit nq - 1 - i starts a row tile
   Walk w(a, S);                                       // unit nq
-  // whichever is ready first: the scores of unit nq, or the values of unit np
+  // whichever is ready first: the values of unit np, or half of the score
+  // products of unit nq (those on the first or second pair of regions)
   int32_t looks = 0;
+#pragma unroll 1
   while (np < w.count && looks < kLooks) {
     ++looks;
-    const uint32_t qb = nq & 1, qparity = (nq >> 1) & 1;
-    const bool first = w.first();
-    if (nq < w.count && ready(&S.full[qb], qparity) && ready(&S.sfree[qb], qparity ^ 1) &&
-        (!first || ready(&S.qfull, seg & 1))) {
-      tc_fence_after();
-      const bool last = w.last();
-      if (elect_one()) {
-        const uint32_t ke = k_lo + qb * (kTile >> 4), se = tmem + kSCol + qb * 128;
-        mma_first(se, ke, q_lo, hi, id_qk, 0u);
-#pragma unroll
-        for (uint32_t k = 1; k < 16; ++k) {
-          const uint32_t step = ((k >> 2) * kRegion + (k & 3) * 32) >> 4;
-          mma(se, ke + step, q_lo + step, hi, id_qk);
-        }
-        mma_commit(&S.sfull[qb]);
-        if (last) mma_commit(&S.qempty);
-      }
-      __syncwarp();
-      seg += first ? 1 : 0;
-      fresh = (fresh << 1) | (first ? 1u : 0u);
-      ++nq;
-      w.next(a, S);
-      looks = 0;
-    }
     if (np < nq && ready(&S.pready, np & 1)) {
       tc_fence_after();
       if (elect_one()) {
         const uint32_t more = ((fresh >> (nq - 1 - np)) & 1u) ^ 1u;
+        const uint32_t tile = v_lo + (np & 1) * (kTile >> 4);
 #pragma unroll
-        for (uint32_t c = 0; c < 4; ++c) {
-          const uint32_t ve = v_lo + (((np & 1) * kTile + (c & 1) * 2 * kRegion + (c >> 1) * 64 * 128) >> 4);
-          const uint32_t oe = tmem + kOCol + c * kHT;
-          mma_first(oe, ve, p_lo, hi, id_pv, more);
+        for (uint32_t f = 0; f < 2; ++f) {
 #pragma unroll
-          for (uint32_t k = 1; k < 4; ++k) mma(oe, ve + (k * 2048 >> 4), p_lo + (k * 2048 >> 4), hi, id_pv);
+          for (uint32_t e = 0; e < 2; ++e) {
+            const uint32_t ve = tile + ((f * 2 * kRegion + e * 64 * 128) >> 4);
+            const uint32_t oe = tmem + kOCol + (2 * e + f) * kHT;
+            mma_first(oe, ve, p_lo, hi, id_pv, more);
+#pragma unroll
+            for (uint32_t k = 1; k < 4; ++k)
+              mma(oe, ve + (k * 2048 >> 4), p_lo + (k * 2048 >> 4), hi, id_pv);
+          }
+          mma_commit(&S.empty[np & 1][f]);
         }
-        mma_commit(&S.empty[np & 1]);
         mma_commit(&S.pvdone);
       }
       __syncwarp();
       ++np;
       looks = 0;
+    }
+    const uint32_t buf = nq & 1, parity = (nq >> 1) & 1;
+    if (nq < w.count && ready(&S.full[buf][part], parity) &&
+        (part || (ready(&S.sfree[buf], parity ^ 1) && (!w.first() || ready(&S.qfull, seg & 1))))) {
+      tc_fence_after();
+      const bool last = w.last();
+      if (elect_one()) {
+        const uint32_t step = part * (2 * kRegion >> 4), ke = k_lo + buf * (kTile >> 4) + step;
+        const uint32_t qe = q_lo + step, se = tmem + kSCol + buf * 128;
+        mma_first(se, ke, qe, hi, id_qk, part);
+#pragma unroll
+        for (uint32_t k = 1; k < 8; ++k) {
+          const uint32_t on = ((k >> 2) * kRegion + (k & 3) * 32) >> 4;
+          mma(se, ke + on, qe + on, hi, id_qk);
+        }
+        if (part) {
+          mma_commit(&S.sfull[buf]);
+          if (last) mma_commit(&S.qempty);
+        }
+      }
+      __syncwarp();
+      looks = 0;
+      if (part) {
+        const uint32_t first = w.first() ? 1u : 0u;
+        seg += first;
+        fresh = (fresh << 1) | first;
+        ++nq;
+        w.next(a, S);
+      }
+      part ^= 1;
     }
   }
   const bool ok = np == w.count;
@@ -774,7 +808,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
   const uint32_t lanes = static_cast<uint32_t>(32 * qw) << 16;
   const int pos = 32 * (qw & 1) + lane, bar = 1 + sub, h0 = 32 * sub + 16 * e;
   float* part = S.part[sub][0];
-  const f32x2* m2 = reinterpret_cast<const f32x2*>(S.m + h0);
+  const float4* m4 = reinterpret_cast<const float4*>(S.m + h0);
   const f32x2* de2 = reinterpret_cast<const f32x2*>(S.delta + h0);
   const f32x2* al2 = reinterpret_cast<const f32x2*>(S.alpha + h0);
   // 16-byte pieces of a position's 64 bytes, swizzled so that eight lanes cover all banks
@@ -800,8 +834,24 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     }
     const uint32_t slot = n & (kSlots - 1);
     if (ok && !wait(&S.rowfull[slot], (n / kSlots) & 1)) ok = false;
+    // d = y - M + kShift = (partial sums) * cs + es; no position here: -inf,
+    // weight 0. 1 / s is taken from the logarithm that d uses, so that p / s is
+    // free of its error.
     const float s = S.rs[slot][pos];
     const float ls = lg2(s), inv_s = s != 0.0f ? ex2(-ls) : 0.0f;
+    f32x2 cs[8], es[8];
+    {
+      const float4* c4 = reinterpret_cast<const float4*>(S.sl2[(seg - 1) & 1] + h0);
+      const f32x2 s2 = pair_of(s, s), ls2 = pair_of(ls + kShift, ls + kShift);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 c = c4[i], m = m4[i];
+        cs[2 * i] = mul2(pair_of(c.x, c.y), s2);
+        cs[2 * i + 1] = mul2(pair_of(c.z, c.w), s2);
+        es[2 * i] = sub2(ls2, pair_of(m.x, m.y));
+        es[2 * i + 1] = sub2(ls2, pair_of(m.z, m.w));
+      }
+    }
     if (ok && !wait(&S.sfull[buf], parity)) ok = false;
     tc_fence_after();
     f32x2 d[8];
@@ -827,18 +877,12 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
             add2(pair_of(__uint_as_float(own[4 * i + 2]), __uint_as_float(own[4 * i + 3])), pair_of(v.z, v.w));
       }
     }
-    // d = y - M + kShift; no position here: -inf, weight 0. 1 / s is taken from
-    // the logarithm that d uses, so that p / s is free of its error.
-    const f32x2* c2 = reinterpret_cast<const f32x2*>(S.sl2[(seg - 1) & 1] + h0);
     float over = -INFINITY;
-    {
-      const f32x2 s2 = pair_of(s, s), ls2 = pair_of(ls + kShift, ls + kShift);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        d[i] = fma2(mul2(d[i], c2[i]), s2, sub2(ls2, m2[i]));
-        const float2 u = both(d[i]);
-        over = fmaxf(over, fmaxf(u.x, u.y));
-      }
+    for (int i = 0; i < 8; ++i) {
+      d[i] = fma2(d[i], cs[i], es[i]);
+      const float2 u = both(d[i]);
+      over = fmaxf(over, fmaxf(u.x, u.y));
     }
     // until something was seen, any position sets the references
     const bool rises = over > (seen ? kSlack + kShift : -INFINITY);
@@ -881,7 +925,6 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       }
       seen = true;
     }
-    const f32x2 is2 = pair_of(inv_s, inv_s);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t h[4];
@@ -889,7 +932,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       for (int k = 0; k < 4; ++k) {
         const float2 v = both(d[4 * i + k]);
         const float px = ex2(v.x), py = ex2(v.y);
-        l[4 * i + k] = fma2(pair_of(px, py), is2, l[4 * i + k]);
+        d[4 * i + k] = pair_of(px, py);
         h[k] = pack_half2(px, py);
       }
       *reinterpret_cast<uint4*>(&S.p[sw(pos, h0 / 8 + i)]) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -901,6 +944,9 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       mbar_arrive(&S.pready);
       mbar_arrive(&S.rowfree[slot]);
     }
+    const f32x2 is2 = pair_of(inv_s, inv_s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l[i] = fma2(d[i], is2, l[i]);
     if (!w.last()) continue;
 
     // ---- the row tile's end in this CTA: totals, then the output
@@ -952,8 +998,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
   if (tid == 0) {
     for (int h = 0; h < kHT; ++h) S.m[h] = 0.0f;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.full[i], kLoadWarps);
-      mbar_init(&S.empty[i], 1);
+      for (int f = 0; f < 2; ++f) {
+        mbar_init(&S.full[i][f], kLoadWarps);
+        mbar_init(&S.empty[i][f], 1);
+      }
       mbar_init(&S.sfull[i], 1);
       mbar_init(&S.sfree[i], kSoftWarps);
     }
@@ -974,12 +1022,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
   const uint32_t tmem = S.tmem_base;
   if (S.count > 0) {
     bool ok = true;
-    if (warp < kSoftWarps)
+    if (warp < kSoftWarps) {
+      more_registers<kSoftRegs>();
       ok = run_softmax(a, S, tmem);
-    else if (warp < kMmaWarp)
+    } else if (warp < kMmaWarp) {
+      fewer_registers<kLoadRegs>();
       ok = run_loaders<kFp8>(S);
-    else
+    } else {
       ok = warp == kMmaWarp ? run_mma(a, S, tmem) : warp == kRowWarp ? run_rows(a, S) : run_queries(a, S);
+    }
     if (!ok && lane == 0 && a.err) atomicOr(a.err, QLI_DEVERR_TIMEOUT);
   }
   tc_fence_before();
