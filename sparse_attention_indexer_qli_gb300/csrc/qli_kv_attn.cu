@@ -20,10 +20,11 @@
 //   0-7   softmax: S from TMEM, weights to shared memory, at the end of a row
 //         tile the output from TMEM
 //   8-15  loaders: a unit's 64 rows of codes in flight in registers, widened to
-//         FP16 and stored in one of two 128-byte-swizzled tiles
-//   16    MMA issuer: the scores of unit n + 1, then the values of unit n
-//   17    the units' rows: pages, scales, fetches into L2, up to four units ahead
-//   18-19 the row tile's queries
+//         FP16 and stored in one of two 128-byte-swizzled tiles; at the start
+//         of a row tile its queries
+//   16    issues the score products, 17 the value products: each waits for its
+//         own operands, and the tensor core takes what is there
+//   18    the units' rows: pages, scales, fetches into L2, up to four units ahead
 // A tile's 128 rows are (half e of the 512 values, position), the queries are
 // stacked alike, so the scores are one product of M = 128, N = 128, K = 256
 // whose blocks e = e' are the halves' partial scores (the other two are
@@ -52,13 +53,13 @@ constexpr int kD = 512;
 constexpr int kHT = 64;                        // heads per row tile (MMA N)
 constexpr int kPos = 64;                       // positions per unit
 constexpr int kSoftWarps = 8, kLoadWarps = 8;
-constexpr int kLoadWarp0 = kSoftWarps, kMmaWarp = kSoftWarps + kLoadWarps;
-constexpr int kRowWarp = kMmaWarp + 1, kQueryWarp0 = kMmaWarp + 2, kQueryWarps = 2;
-constexpr int kThreads = 32 * (kQueryWarp0 + kQueryWarps);
+constexpr int kLoadWarp0 = kSoftWarps, kScoreWarp = kSoftWarps + kLoadWarps;
+constexpr int kValueWarp = kScoreWarp + 1, kRowWarp = kScoreWarp + 2;
+constexpr int kThreads = 640;                  // five warpgroups, the last warp idle
 // Registers of the warpgroups' threads, within the CTA's 640 x 96. A spill in a
 // role's loop costs an L2 round trip: the streamed codes leave L1 to nothing else.
-constexpr int kSoftRegs = 120, kLoadRegs = 72;
-static_assert(2 * kSoftRegs + 2 * kLoadRegs + 96 <= 5 * 96, "registers of the CTA");
+constexpr int kSoftRegs = 112, kLoadRegs = 96, kIssueRegs = 64;
+static_assert(2 * kSoftRegs + 2 * kLoadRegs + kIssueRegs <= 5 * 96, "registers of the CTA");
 constexpr int kSlots = 4;                      // units whose rows are looked up ahead
 constexpr int kRegion = 128 * 128;             // 64 values of every row of a tile
 constexpr int kTile = 4 * kRegion;
@@ -213,7 +214,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, ok);
 }
 
-// 32 lanes x 8 consecutive 32-bit columns of TMEM.
+// 32 lanes x 8 or 16 consecutive 32-bit columns of TMEM.
 __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
@@ -229,10 +230,13 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 // log2 x likewise (log2 0 = -inf).
@@ -241,20 +245,6 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-// One look at the phase, as a whole warp, without waiting in it.
-__device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return __all_sync(0xffffffffu, ok);
-}
-constexpr int kLooks = 1 << 22;                // some 0.1 us each
 
 __device__ __forceinline__ void named_bar(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
@@ -448,14 +438,14 @@ __device__ __align__(16) const uint8_t kZeroRow[kD] = {};
 // The row tile's queries as FP16 times a power of two per head that brings the
 // head's largest magnitude to [2^13, 2^14); rows past H are zero.
 __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, int32_t g,
-                                             uint32_t parity, int qw) {
+                                             uint32_t parity, int lw) {
   const int lane = threadIdx.x & 31;
-  constexpr int kBatch = 2;
+  constexpr int kRows = kHT / kLoadWarps, kBatch = 4;
   // lane l holds values 16l .. 16l + 15: unit l & 7 of quarter l >> 3
-  uint8_t* dst = S.q + ((lane >> 3) & 1) * 2 * kRegion;
+  const uint32_t dst = smem_u32(S.q) + ((lane >> 3) & 1) * 2 * kRegion;
   const int e64 = (lane >> 4) * 64;
 #pragma unroll 1
-  for (int r0 = qw * kBatch; r0 < kHT; r0 += kBatch * kQueryWarps) {
+  for (int r0 = lw * kRows; r0 < (lw + 1) * kRows; r0 += kBatch) {
     uint4 v[kBatch][2];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -471,8 +461,8 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int r = r0 + k;
-      const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
-                             v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+      uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                       v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
       // magnitudes compare as integers (NaN above all)
       uint32_t top = 0u;
 #pragma unroll
@@ -481,34 +471,16 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
       top = __reduce_max_sync(0xffffffffu, top);
       const int e = min(100, 13 - (static_cast<int>(top >> 23) - 127));
       const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      uint32_t o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        o[i] = pack_half2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-      const uint32_t at = smem_u32(dst) + sw(e64 + r, lane & 7);
-      st_shared_v4(at, o[0], o[1], o[2], o[3]);
-      st_shared_v4(at + kRegion, o[4], o[5], o[6], o[7]);
+        w[i] = pack_half2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+      const uint32_t at = dst + sw(e64 + r, lane & 7);
+      st_shared_v4(at, w[0], w[1], w[2], w[3]);
+      st_shared_v4(at + kRegion, w[4], w[5], w[6], w[7]);
       if (lane == 0)
         S.sl2[parity][r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
   }
-}
-
-__device__ __forceinline__ bool run_queries(const Args& a, Smem& S) {
-  const int qw = (threadIdx.x >> 5) - kQueryWarp0;
-  uint32_t seg = 0;
-  for (Walk w(a, S); w.valid(); w.next(a, S)) {
-    if (!w.first()) continue;
-    // the products with the previous row tile's queries are done, and the
-    // softmax is past its wait for them
-    if (!wait(&S.qempty, (seg & 1) ^ 1)) return false;
-    load_queries(a, S, w.t, w.g, seg & 1, qw);
-    ++seg;
-    fence_proxy_async_smem();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&S.qfull);
-  }
-  return true;
 }
 
 // The rows of the units: iteration m publishes unit m and takes one step each of
@@ -568,6 +540,13 @@ __device__ __forceinline__ bool run_rows(const Args& a, Smem& S) {
     if (w.valid()) {
       const int32_t V = S.tokV[w.t], n = positions_of(a, V);
       b3 = S.tokB[w.t];
+      if (w.first()) {
+        // the row tile's queries, into L2
+#pragma unroll 1
+        for (int h = w.g * kHT + (lane >> 3); h < min(a.H, (w.g + 1) * kHT); h += 4)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(
+              a.q + static_cast<int64_t>(a.t0 + w.t) * a.q_st + h * a.q_sh + (lane & 7) * 64));
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int32_t e = w.i * kPos + lane + 32 * k;
@@ -585,17 +564,29 @@ __device__ __forceinline__ bool run_rows(const Args& a, Smem& S) {
 // while unit n is worked on). A warp has eight rows; a warp
 // instruction loads one quarter of four.
 template <bool kFp8>
-__device__ __forceinline__ bool run_loaders(Smem& S) {
+__device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
   const int lane = threadIdx.x & 31, lw = (threadIdx.x >> 5) - kLoadWarp0;
   const int r0 = kPos / kLoadWarps * lw + (lane >> 3), off = (lane & 7) * 16;
   // rows 4 apart: 512 bytes on, and bit 2 of the swizzled unit flips
   const uint32_t at0 = smem_u32(S.kv) + sw(r0, lane & 7), at1 = (at0 ^ 64u) + 512;
-  const int32_t count = S.count;
+  uint32_t seg = 0;
+  Walk w(a, S);                                       // unit n
   uint4 x[2][4];
 #pragma unroll 1
-  for (int32_t n = -1; n < count; ++n) {
+  for (int32_t n = -1; n < w.count; ++n) {
     if (n >= 0) {
       const int buf = n & 1;
+      if (w.first()) {
+        // the products with the previous row tile's queries are done, and the
+        // softmax is past its wait for them
+        if (!wait(&S.qempty, (seg & 1) ^ 1)) return false;
+        load_queries(a, S, w.t, w.g, seg & 1, lw);
+        ++seg;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.qfull);
+      }
+      w.next(a, S);
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         if (!wait(&S.empty[buf][f], ((n >> 1) & 1) ^ 1)) return false;
@@ -615,7 +606,7 @@ __device__ __forceinline__ bool run_loaders(Smem& S) {
         if (lane == 0) mbar_arrive(&S.full[buf][f]);
       }
     }
-    if (n + 1 < count) {
+    if (n + 1 < w.count) {
       const uint32_t slot = (n + 1) & (kSlots - 1);
       if (!wait(&S.rowfull[slot], ((n + 1) / kSlots) & 1)) return false;
       const uint8_t* r[2] = {S.row[slot][r0] + off, S.row[slot][r0 + 4] + off};
@@ -631,11 +622,10 @@ __device__ __forceinline__ bool run_loaders(Smem& S) {
   return true;
 }
 
-// ---- MMA issuer (one warp) ------------------------------------------------------
+// ---- products (a warp for the scores, one for the values) -------------------------
 // The whole warp runs the loop and an elected lane issues each batch of
 // products with constant descriptor steps, about ten instructions a product;
-// one thread's loop with 64-bit descriptors took 100-180 cycles a product,
-// where the tensor core takes 42.
+// one thread's loop with 64-bit descriptors took 100-180 cycles a product.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
   asm volatile(
@@ -667,82 +657,78 @@ __device__ __forceinline__ void mma_first(uint32_t d_tmem, uint32_t a_lo, uint32
       : "memory");
 }
 
-__device__ __forceinline__ bool run_mma(const Args& a, Smem& S, uint32_t tmem_any) {
-  constexpr uint32_t id_qk = idesc_f16(128, false, false), id_pv = idesc_f16(kHT, true, true);
-  constexpr uint32_t hi = sdesc_hi(1024);
+// At the end each warp waits for the products of both.
+__device__ __forceinline__ bool drain(Smem& S) {
+  if (elect_one()) mma_commit(&S.done);
+  __syncwarp();
+  return wait(&S.done, 0);
+}
+
+__device__ __forceinline__ bool run_scores(const Args& a, Smem& S, uint32_t tmem_any) {
+  constexpr uint32_t id = idesc_f16(128, false, false), hi = sdesc_hi(1024);
   const uint32_t k_lo = sdesc_lo(smem_u32(S.kv), 16), q_lo = sdesc_lo(smem_u32(S.q), 16);
-  const uint32_t v_lo = sdesc_lo(smem_u32(S.kv), kRegion), p_lo = sdesc_lo(smem_u32(S.p), 1024);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
-  uint32_t seg = 0;
-  int32_t nq = 0, np = 0;                             // units whose scores, values come next
-  uint32_t part = 0;                                  // which half of unit nq's score products
-  uint32_t fresh = 0;                                 // bit i: unit nq - 1 - i starts a row tile
-  Walk w(a, S);                                       // unit nq
-  // whichever is ready first: the values of unit np, or half of the score
-  // products of unit nq (those on the first or second pair of regions)
-  int32_t looks = 0;
+  bool ok = true;
+  uint32_t n = 0, seg = 0;
 #pragma unroll 1
-  while (np < w.count && looks < kLooks) {
-    ++looks;
-    if (np < nq && ready(&S.pready, np & 1)) {
+  for (Walk w(a, S); ok && w.valid(); w.next(a, S), ++n) {
+    const uint32_t buf = n & 1, parity = (n >> 1) & 1;
+    const bool last = w.last();
+    if (w.first()) ok = wait(&S.qfull, seg++ & 1);
+    ok = ok && wait(&S.sfree[buf], parity ^ 1);
+#pragma unroll 1
+    for (uint32_t f = 0; f < 2 && ok; ++f) {
+      ok = wait(&S.full[buf][f], parity);
       tc_fence_after();
-      if (elect_one()) {
-        const uint32_t more = ((fresh >> (nq - 1 - np)) & 1u) ^ 1u;
-        const uint32_t tile = v_lo + (np & 1) * (kTile >> 4);
-#pragma unroll
-        for (uint32_t f = 0; f < 2; ++f) {
-#pragma unroll
-          for (uint32_t e = 0; e < 2; ++e) {
-            const uint32_t ve = tile + ((f * 2 * kRegion + e * 64 * 128) >> 4);
-            const uint32_t oe = tmem + kOCol + (2 * e + f) * kHT;
-            mma_first(oe, ve, p_lo, hi, id_pv, more);
-#pragma unroll
-            for (uint32_t k = 1; k < 4; ++k)
-              mma(oe, ve + (k * 2048 >> 4), p_lo + (k * 2048 >> 4), hi, id_pv);
-          }
-          mma_commit(&S.empty[np & 1][f]);
-        }
-        mma_commit(&S.pvdone);
-      }
-      __syncwarp();
-      ++np;
-      looks = 0;
-    }
-    const uint32_t buf = nq & 1, parity = (nq >> 1) & 1;
-    if (nq < w.count && ready(&S.full[buf][part], parity) &&
-        (part || (ready(&S.sfree[buf], parity ^ 1) && (!w.first() || ready(&S.qfull, seg & 1))))) {
-      tc_fence_after();
-      const bool last = w.last();
-      if (elect_one()) {
-        const uint32_t step = part * (2 * kRegion >> 4), ke = k_lo + buf * (kTile >> 4) + step;
+      if (ok && elect_one()) {
+        const uint32_t step = f * (2 * kRegion >> 4), ke = k_lo + buf * (kTile >> 4) + step;
         const uint32_t qe = q_lo + step, se = tmem + kSCol + buf * 128;
-        mma_first(se, ke, qe, hi, id_qk, part);
+        mma_first(se, ke, qe, hi, id, f);
 #pragma unroll
         for (uint32_t k = 1; k < 8; ++k) {
           const uint32_t on = ((k >> 2) * kRegion + (k & 3) * 32) >> 4;
-          mma(se, ke + on, qe + on, hi, id_qk);
+          mma(se, ke + on, qe + on, hi, id);
         }
-        if (part) {
+        if (f) {
           mma_commit(&S.sfull[buf]);
           if (last) mma_commit(&S.qempty);
         }
       }
       __syncwarp();
-      looks = 0;
-      if (part) {
-        const uint32_t first = w.first() ? 1u : 0u;
-        seg += first;
-        fresh = (fresh << 1) | first;
-        ++nq;
-        w.next(a, S);
-      }
-      part ^= 1;
     }
   }
-  const bool ok = np == w.count;
-  if (elect_one()) mma_commit(&S.done);               // every product of the CTA
-  __syncwarp();
-  return wait(&S.done, 0) && ok;
+  return drain(S) && ok;
+}
+
+__device__ __forceinline__ bool run_values(const Args& a, Smem& S, uint32_t tmem_any) {
+  constexpr uint32_t id = idesc_f16(kHT, true, true), hi = sdesc_hi(1024);
+  const uint32_t v_lo = sdesc_lo(smem_u32(S.kv), kRegion), p_lo = sdesc_lo(smem_u32(S.p), 1024);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
+  bool ok = true;
+  uint32_t n = 0;
+#pragma unroll 1
+  for (Walk w(a, S); ok && w.valid(); w.next(a, S), ++n) {
+    const uint32_t more = w.first() ? 0u : 1u, tile = v_lo + (n & 1) * (kTile >> 4);
+    ok = wait(&S.pready, n & 1);
+    tc_fence_after();
+    if (ok && elect_one()) {
+#pragma unroll
+      for (uint32_t f = 0; f < 2; ++f) {
+#pragma unroll
+        for (uint32_t e = 0; e < 2; ++e) {
+          const uint32_t ve = tile + ((f * 2 * kRegion + e * 64 * 128) >> 4);
+          const uint32_t oe = tmem + kOCol + (2 * e + f) * kHT;
+          mma_first(oe, ve, p_lo, hi, id, more);
+#pragma unroll
+          for (uint32_t k = 1; k < 4; ++k) mma(oe, ve + (k * 2048 >> 4), p_lo + (k * 2048 >> 4), hi, id);
+        }
+        mma_commit(&S.empty[n & 1][f]);
+      }
+      mma_commit(&S.pvdone);
+    }
+    __syncwarp();
+  }
+  return drain(S) && ok;
 }
 
 // ---- softmax ------------------------------------------------------------------
@@ -910,16 +896,21 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
         l[i] = mul2(l[i], al2[i]);
       }
       if (seen) {
+        // 16 heads at a time, those whose reference moved
 #pragma unroll 1
-        for (int c = 0; c < 16; ++c) {
-          uint32_t o[8];
-          const uint32_t oe = tmem + lanes + kOCol + (c >> 2) * kHT + 32 * sub + (c & 3) * 8;
-          tmem_ld_x8(oe, o);
-          tmem_ld_wait();
-          const float* al = S.alpha + 32 * sub + (c & 3) * 8;
+        for (int g = 0; g < 2; ++g) {
+          const float* al = S.alpha + 32 * sub + 16 * g;
+          if (!__any_sync(0xffffffffu, al[lane & 15] != 1.0f)) continue;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[16];
+            const uint32_t oe = tmem + lanes + kOCol + c * kHT + 32 * sub + 16 * g;
+            tmem_ld_x16(oe, o);
+            tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al[i]);
-          tmem_st_x8(oe, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al[i]);
+            tmem_st_x16(oe, o);
+          }
         }
         tmem_st_wait();
       }
@@ -994,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
-  if (warp == kMmaWarp) tmem_alloc(&S.tmem_base, kTmemCols);
+  if (warp == kScoreWarp) tmem_alloc(&S.tmem_base, kTmemCols);
   if (tid == 0) {
     for (int h = 0; h < kHT; ++h) S.m[h] = 0.0f;
     for (int i = 0; i < 2; ++i) {
@@ -1009,11 +1000,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
       mbar_init(&S.rowfull[i], 1);
       mbar_init(&S.rowfree[i], kLoadWarps + kSoftWarps);
     }
-    mbar_init(&S.qfull, kQueryWarps);
+    mbar_init(&S.qfull, kLoadWarps);
     mbar_init(&S.qempty, 1 + kSoftWarps);
     mbar_init(&S.pready, kSoftWarps);
     mbar_init(&S.pvdone, 1);
-    mbar_init(&S.done, 1);
+    mbar_init(&S.done, 2);
     fence_mbar_init();
   }
   tc_fence_before();
@@ -1025,18 +1016,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
     if (warp < kSoftWarps) {
       more_registers<kSoftRegs>();
       ok = run_softmax(a, S, tmem);
-    } else if (warp < kMmaWarp) {
+    } else if (warp < kScoreWarp) {
       fewer_registers<kLoadRegs>();
-      ok = run_loaders<kFp8>(S);
+      ok = run_loaders<kFp8>(a, S);
     } else {
-      ok = warp == kMmaWarp ? run_mma(a, S, tmem) : warp == kRowWarp ? run_rows(a, S) : run_queries(a, S);
+      fewer_registers<kIssueRegs>();
+      if (warp == kScoreWarp) ok = run_scores(a, S, tmem);
+      if (warp == kValueWarp) ok = run_values(a, S, tmem);
+      if (warp == kRowWarp) ok = run_rows(a, S);
     }
     if (!ok && lane == 0 && a.err) atomicOr(a.err, QLI_DEVERR_TIMEOUT);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 // ---- joining the pieces ---------------------------------------------------------
