@@ -58,7 +58,7 @@ constexpr int kValueWarp = kScoreWarp + 1, kRowWarp = kScoreWarp + 2;
 constexpr int kThreads = 640;                  // five warpgroups, the last warp idle
 // Registers of the warpgroups' threads, within the CTA's 640 x 96. A spill in a
 // role's loop costs an L2 round trip: the streamed codes leave L1 to nothing else.
-constexpr int kSoftRegs = 112, kLoadRegs = 96, kIssueRegs = 64;
+constexpr int kSoftRegs = 112, kLoadRegs = 104, kIssueRegs = 48;
 static_assert(2 * kSoftRegs + 2 * kLoadRegs + kIssueRegs <= 5 * 96, "registers of the CTA");
 constexpr int kSlots = 4;                      // units whose rows are looked up ahead
 constexpr int kRegion = 128 * 128;             // 64 values of every row of a tile
@@ -214,13 +214,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, ok);
 }
 
-// 32 lanes x 8 or 16 consecutive 32-bit columns of TMEM.
-__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                 "=r"(r[7])
-               : "r"(taddr));
-}
+// 32 lanes x 16 consecutive 32-bit columns of TMEM.
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -570,23 +564,12 @@ __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
   // rows 4 apart: 512 bytes on, and bit 2 of the swizzled unit flips
   const uint32_t at0 = smem_u32(S.kv) + sw(r0, lane & 7), at1 = (at0 ^ 64u) + 512;
   uint32_t seg = 0;
-  Walk w(a, S);                                       // unit n
+  Walk w(a, S);                                       // unit n + 1
   uint4 x[2][4];
 #pragma unroll 1
   for (int32_t n = -1; n < w.count; ++n) {
     if (n >= 0) {
       const int buf = n & 1;
-      if (w.first()) {
-        // the products with the previous row tile's queries are done, and the
-        // softmax is past its wait for them
-        if (!wait(&S.qempty, (seg & 1) ^ 1)) return false;
-        load_queries(a, S, w.t, w.g, seg & 1, lw);
-        ++seg;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.qfull);
-      }
-      w.next(a, S);
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         if (!wait(&S.empty[buf][f], ((n >> 1) & 1) ^ 1)) return false;
@@ -606,18 +589,34 @@ __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
         if (lane == 0) mbar_arrive(&S.full[buf][f]);
       }
     }
-    if (n + 1 < w.count) {
-      const uint32_t slot = (n + 1) & (kSlots - 1);
-      if (!wait(&S.rowfull[slot], ((n + 1) / kSlots) & 1)) return false;
-      const uint8_t* r[2] = {S.row[slot][r0] + off, S.row[slot][r0 + 4] + off};
+    if (n + 1 == w.count) break;
+    // unit n + 1: its codes, and at the start of a row tile its queries; the
+    // codes first, but at the very start, where their rows are not known yet
+#pragma unroll 1
+    for (int step = 0; step < 2; ++step) {
+      if ((step == 0) == (n >= 0)) {
+        const uint32_t slot = (n + 1) & (kSlots - 1);
+        if (!wait(&S.rowfull[slot], ((n + 1) / kSlots) & 1)) return false;
+        const uint8_t* r[2] = {S.row[slot][r0] + off, S.row[slot][r0 + 4] + off};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[k][c] = __ldg(reinterpret_cast<const uint4*>(r[k] + c * 128));
+          for (int c = 0; c < 4; ++c) x[k][c] = __ldg(reinterpret_cast<const uint4*>(r[k] + c * 128));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.rowfree[slot]);
+      } else if (w.first()) {
+        // the products with the previous row tile's queries are done, and the
+        // softmax is past its wait for them
+        if (!wait(&S.qempty, (seg & 1) ^ 1)) return false;
+        load_queries(a, S, w.t, w.g, seg & 1, lw);
+        ++seg;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.qfull);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.rowfree[slot]);
     }
+    w.next(a, S);
   }
   return true;
 }
@@ -770,14 +769,14 @@ template <class T>
 __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int pos, int32_t nh, T* dst,
                                        int64_t stride) {
 #pragma unroll 1
-  for (int c = 0; c < 16; ++c) {
-    uint32_t o[8];
-    tmem_ld_x8(tmem + (c >> 2) * kHT + (c & 3) * 8, o);
+  for (int c = 0; c < 8; ++c) {
+    uint32_t o[16];
+    tmem_ld_x16(tmem + (c >> 1) * kHT + (c & 1) * 16, o);
     tmem_ld_wait();
-    const int i0 = (c & 3) * 8;
-    T* at = dst + i0 * stride + value_of(c >> 2, pos);
+    const int i0 = (c & 1) * 16;
+    T* at = dst + i0 * stride + value_of(c >> 1, pos);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       if (i0 + i < nh) store_value(at, __uint_as_float(o[i]) * S.alpha[h0 + i0 + i]);
       at += stride;
     }
@@ -1017,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
       more_registers<kSoftRegs>();
       ok = run_softmax(a, S, tmem);
     } else if (warp < kScoreWarp) {
-      fewer_registers<kLoadRegs>();
+      more_registers<kLoadRegs>();
       ok = run_loaders<kFp8>(a, S);
     } else {
       fewer_registers<kIssueRegs>();
