@@ -7,7 +7,9 @@ fallback: a missing library or a non-CUDA tensor raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from ctypes import c_int32, c_int64, c_size_t, c_uint32, c_void_p
 from typing import Optional
 
@@ -102,6 +104,21 @@ class MergeArgs(ctypes.Structure):
     ]
 
 
+def _packer(mirror):
+    """A struct.Struct of the fields of `mirror` (scalars and pointers as ints, in
+    the native layout): packing one call's arguments takes a fraction of what
+    setting a ctypes structure does."""
+    codes = {c_void_p: "P", c_int64: "q", c_int32: "i", ctypes.c_float: "f"}
+    fmt = "@"
+    for _, t in mirror._fields_:
+        n = getattr(t, "_length_", 0)
+        fmt += codes[t._type_] * n if n else codes[t]
+    return struct.Struct(fmt + "0q")
+
+
+_pack_kv_attn = _packer(KVAttnArgs).pack
+_pack_merge = _packer(MergeArgs).pack
+
 EXPORTS = ["qli_validate", "qli_workspace_size", "qli_run", "qli_run_stage", "qli_launch_count",
            "qli_scores_layout", "qli_read_device_error", "qli_status_string", "qli_abi_version",
            "qli_args_size", "qli_run_static", "qli_read_static_device_error",
@@ -159,10 +176,10 @@ def lib(path: Optional[str] = None) -> ctypes.CDLL:
                                c_int32, c_int64, c_int64, c_int32, c_void_p, c_void_p]
     L.qli_read_kv.argtypes = [c_void_p, c_int64, c_int64, c_int32, c_int64, c_int64, c_int32,
                               c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p]
-    L.qli_kv_attention.argtypes = [ctypes.POINTER(KVAttnArgs), c_void_p, c_size_t, c_void_p]
-    L.qli_kv_attention_workspace_size.argtypes = [ctypes.POINTER(KVAttnArgs),
-                                                  ctypes.POINTER(c_size_t)]
-    L.qli_merge_attention.argtypes = [ctypes.POINTER(MergeArgs), c_void_p]
+    # the structures may also come packed, as bytes
+    L.qli_kv_attention.argtypes = [c_void_p, c_void_p, c_size_t, c_void_p]
+    L.qli_kv_attention_workspace_size.argtypes = [c_void_p, ctypes.POINTER(c_size_t)]
+    L.qli_merge_attention.argtypes = [c_void_p, c_void_p]
     for name in ("qli_write_kv", "qli_read_kv", "qli_kv_attention",
                  "qli_kv_attention_workspace_size", "qli_merge_attention"):
         getattr(L, name).restype = c_int32
@@ -314,9 +331,11 @@ class Call:
         return int(w.value)
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device=None) -> Optional[int]:
+    """The raw stream: the given one, or the current one (of device index
+    `device`, which spares looking the current device up)."""
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
+    s = torch.cuda.current_stream(device) if stream is None else stream
     return s.cuda_stream
 
 
@@ -427,6 +446,18 @@ def sparse_attention(q, cu_seqlens_q, cache, block_table, indices, *, rows_per_p
 
 
 
+def _check_cuda(name, t, dtype):
+    """_require_cuda for a tensor that has to be there, the good case first."""
+    try:
+        if t.is_cuda and t.dtype is dtype:
+            return
+    except AttributeError:
+        pass
+    if t is None:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    _require_cuda(name, t, dtype)
+
+
 def write_kv(kv, slot_mapping, cache, *, rows_per_page: int, page_stride: int, kv_offset: int,
              kv_scale_offset: int, err_word=None, stream=None, quant_mode=QUANT_INT8):
     """qli_write_kv: quantises the rows of kv [n, 512] (BF16, CUDA, unit stride
@@ -435,10 +466,11 @@ def write_kv(kv, slot_mapping, cache, *, rows_per_page: int, page_stride: int, k
     CUDA) at slot_mapping [n] (int64: page * rows_per_page + row; negative =
     skip)."""
     import torch
-    _require_cuda("kv", kv, torch.bfloat16)
-    _require_cuda("slot_mapping", slot_mapping, torch.int64)
-    _require_cuda("cache", cache, torch.uint8)
-    _require_cuda("err_word", err_word, torch.int32)
+    _check_cuda("kv", kv, torch.bfloat16)
+    _check_cuda("slot_mapping", slot_mapping, torch.int64)
+    _check_cuda("cache", cache, torch.uint8)
+    if err_word is not None:
+        _check_cuda("err_word", err_word, torch.int32)
     if kv.dim() != 2 or kv.shape[1] != 512 or kv.stride(1) != 1:
         raise ValueError("kv must be [n, 512] with unit stride in the last dim")
     if not cache.is_contiguous() or not slot_mapping.is_contiguous():
@@ -446,11 +478,11 @@ def write_kv(kv, slot_mapping, cache, *, rows_per_page: int, page_stride: int, k
     n = kv.shape[0]
     if slot_mapping.numel() != n:
         raise ValueError("one slot per row")
-    _check(lib().qli_write_kv(kv.data_ptr(), kv.stride(0) if n > 1 else 512, n,
-                              slot_mapping.data_ptr(), cache.data_ptr(),
-                              cache.numel() // page_stride, page_stride, rows_per_page, kv_offset,
-                              kv_scale_offset, quant_mode, _ptr(err_word), _stream(stream)),
-           "qli_write_kv")
+    _check((_lib or lib()).qli_write_kv(
+        kv.data_ptr(), kv.stride(0) if n > 1 else 512, n, slot_mapping.data_ptr(),
+        cache.data_ptr(), cache.numel() // page_stride, page_stride, rows_per_page, kv_offset,
+        kv_scale_offset, quant_mode, _ptr(err_word), _stream(stream, cache.get_device())),
+        "qli_write_kv")
 
 
 def read_kv(cache, slots, *, rows_per_page: int, page_stride: int, kv_offset: int,
@@ -458,21 +490,24 @@ def read_kv(cache, slots, *, rows_per_page: int, page_stride: int, kv_offset: in
     """qli_read_kv: the rows named by slots [n] (int64: page * rows_per_page +
     row; negative = zeros) of the page pool `cache` as BF16 [n, 512]."""
     import torch
-    _require_cuda("cache", cache, torch.uint8)
-    _require_cuda("slots", slots, torch.int64)
-    _require_cuda("err_word", err_word, torch.int32)
+    _check_cuda("cache", cache, torch.uint8)
+    _check_cuda("slots", slots, torch.int64)
+    if err_word is not None:
+        _check_cuda("err_word", err_word, torch.int32)
     if not cache.is_contiguous() or not slots.is_contiguous():
         raise ValueError("cache and slots must be contiguous")
     n = slots.numel()
     if out is None:
         out = torch.empty((n, 512), dtype=torch.bfloat16, device=cache.device)
-    _require_cuda("out", out, torch.bfloat16)
-    if out.dim() != 2 or tuple(out.shape) != (n, 512) or out.stride(1) != 1:
-        raise ValueError("out must be [n, 512] with unit stride in the last dim")
-    _check(lib().qli_read_kv(cache.data_ptr(), cache.numel() // page_stride, page_stride,
-                             rows_per_page, kv_offset, kv_scale_offset, quant_mode,
-                             slots.data_ptr(), n, out.data_ptr(), out.stride(0) if n > 1 else 512,
-                             _ptr(err_word), _stream(stream)), "qli_read_kv")
+    else:
+        _check_cuda("out", out, torch.bfloat16)
+        if out.shape != (n, 512) or out.stride(1) != 1:
+            raise ValueError("out must be [n, 512] with unit stride in the last dim")
+    _check((_lib or lib()).qli_read_kv(
+        cache.data_ptr(), cache.numel() // page_stride, page_stride, rows_per_page, kv_offset,
+        kv_scale_offset, quant_mode, slots.data_ptr(), n, out.data_ptr(),
+        out.stride(0) if n > 1 else 512, _ptr(err_word), _stream(stream, cache.get_device())),
+        "qli_read_kv")
     return out
 
 
@@ -482,27 +517,39 @@ def _attn_outputs(q_shape, device, out, lse):
     T, H, D = q_shape
     if out is None:
         out = torch.empty((T, H, D), dtype=torch.bfloat16, device=device)
+    else:
+        _check_cuda("out", out, torch.bfloat16)
+        if out.shape != q_shape or out.stride(2) != 1:
+            raise ValueError("out must be [T, H, 512] with unit stride in the last dim")
     if lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=device)
-    _require_cuda("out", out, torch.bfloat16)
-    _require_cuda("lse", lse, torch.float32)
-    if tuple(out.shape) != (T, H, D) or out.stride(2) != 1:
-        raise ValueError("out must be [T, H, 512] with unit stride in the last dim")
-    if tuple(lse.shape) != (T, H) or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous [T, H] tensor")
+    else:
+        _check_cuda("lse", lse, torch.float32)
+        if lse.shape != (T, H) or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous [T, H] tensor")
     return out, lse
 
 
-def kv_attention_workspace_bytes(T: int, H: int) -> int:
-    """Bytes of device workspace kv_attention needs for T tokens of H heads on
-    the current device."""
-    # the size comes from T and H alone; the other arguments are only checked
-    a = KVAttnArgs(256, H * 512, 512, T, H, 512, 256, 1, 256, 128 * 514, 1, 128, QUANT_INT8, 0,
-                   128 * 512, 256, 1, 1, 256, None, None, 1, 0, 1.0, 256, H * 512, 512, None, None)
+@functools.lru_cache(maxsize=None)
+def _workspace_bytes(some: bool, device: int) -> int:
+    # the size depends on the device's SM count and on there being tokens; the
+    # other arguments are only checked
+    import torch
+    a = KVAttnArgs(256, 512, 512, int(some), 1, 512, 256, 1, 256, 128 * 514, 1, 128, QUANT_INT8, 0,
+                   128 * 512, 256, 1, 1, 256, None, None, 1, 0, 1.0, 256, 512, 512, None, None)
     n = c_size_t(0)
-    _check(lib().qli_kv_attention_workspace_size(ctypes.byref(a), ctypes.byref(n)),
-           "qli_kv_attention_workspace_size")
+    with torch.cuda.device(device):
+        _check(lib().qli_kv_attention_workspace_size(ctypes.byref(a), ctypes.byref(n)),
+               "qli_kv_attention_workspace_size")
     return int(n.value)
+
+
+def kv_attention_workspace_bytes(T: int, H: int, device=None) -> int:
+    """Bytes of device workspace kv_attention needs for T tokens of H heads on
+    `device` (default: the current one)."""
+    import torch
+    device = torch.cuda.current_device() if device is None else torch.device(device).index
+    return _workspace_bytes(T > 0 and H > 0, device)
 
 
 def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, page_stride: int,
@@ -513,53 +560,67 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
     8-bit KV rows read through block_table from the page pool `cache`: over the
     positions of indices [T, 1, K] (int32, -1 skipped), or without indices over
     the positions k_lens, residual and ratio make visible to each token (the
-    last `window` of them if window > 0). workspace: a 256-byte
-    aligned uint8 tensor of at least kv_attention_workspace_bytes(T, H) bytes,
-    allocated when not given. Returns
-    (out [T, H, 512] BF16, lse [T, H] float32)."""
+    last `window` of them if window > 0). workspace: a 256-byte aligned uint8
+    tensor of at least kv_attention_workspace_bytes(T, H) bytes, allocated when
+    not given. Returns (out [T, H, 512] BF16, lse [T, H] float32)."""
     import torch
-    _require_cuda("q", q, torch.bfloat16)
-    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("block_table", block_table),
-                    ("indices", indices), ("k_lens", k_lens), ("residual", residual),
-                    ("err_word", err_word)):
-        _require_cuda(name, t, torch.int32)
-    _require_cuda("cache", cache, torch.uint8)
+    _check_cuda("q", q, torch.bfloat16)
+    int32 = torch.int32
+    _check_cuda("cu_seqlens_q", cu_seqlens_q, int32)
+    _check_cuda("block_table", block_table, int32)
+    _check_cuda("cache", cache, torch.uint8)
     if q.dim() != 3 or q.stride(2) != 1:
         raise ValueError("q must be [T, H, 512] with unit stride in the last dim")
     if not cache.is_contiguous() or not cu_seqlens_q.is_contiguous():
         raise ValueError("cache and cu_seqlens_q must be contiguous")
     if block_table.dim() != 2 or block_table.stride(1) != 1:
         raise ValueError("block_table must be [B, bt_stride] row-major")
-    T, H, D = q.shape
+    shape = q.shape
+    T, H, D = shape
     B = cu_seqlens_q.numel() - 1
     if block_table.shape[0] < B:
         raise ValueError("block_table needs a row per request")
-    K = 0
+    K, idx = 0, 0
     if indices is not None:
+        _check_cuda("indices", indices, int32)
         if indices.dim() != 3 or indices.shape[0] != T or indices.shape[1] != 1 \
                 or not indices.is_contiguous():
             raise ValueError("indices must be a contiguous [T, 1, K] tensor")
-        K = indices.shape[2]
+        K, idx = indices.shape[2], indices.data_ptr()
     elif k_lens is None:
         raise ValueError("either indices or k_lens must be given")
-    for name, t in (("k_lens", k_lens), ("residual", residual)):
-        if t is not None and (t.numel() != B or not t.is_contiguous()):
-            raise ValueError("%s must be a contiguous [B] tensor" % name)
-    out, lse = _attn_outputs(q.shape, q.device, out, lse)
-    a = KVAttnArgs(q.data_ptr(), q.stride(0), q.stride(1), T, H, D, cu_seqlens_q.data_ptr(), B,
-                   cache.data_ptr(), page_stride, cache.numel() // page_stride, rows_per_page,
-                   quant_mode, kv_offset, kv_scale_offset, block_table.data_ptr(),
-                   block_table.stride(0), K, _ptr(indices), _ptr(k_lens), _ptr(residual), ratio,
-                   window, scale, out.data_ptr(), out.stride(0), out.stride(1), lse.data_ptr(),
-                   _ptr(err_word))
+    lens, res, err = 0, 0, 0
+    if k_lens is not None:
+        _check_cuda("k_lens", k_lens, int32)
+        if k_lens.numel() != B or not k_lens.is_contiguous():
+            raise ValueError("k_lens must be a contiguous [B] tensor")
+        lens = k_lens.data_ptr()
+    if residual is not None:
+        _check_cuda("residual", residual, int32)
+        if residual.numel() != B or not residual.is_contiguous():
+            raise ValueError("residual must be a contiguous [B] tensor")
+        res = residual.data_ptr()
+    if err_word is not None:
+        _check_cuda("err_word", err_word, int32)
+        err = err_word.data_ptr()
+    device = q.device
+    out, lse = _attn_outputs(shape, device, out, lse)
+    q_t, q_h, _ = q.stride()
+    o_t, o_h, _ = out.stride()
+    a = _pack_kv_attn(q.data_ptr(), q_t, q_h, T, H, D, cu_seqlens_q.data_ptr(), B,
+                      cache.data_ptr(), page_stride, cache.numel() // page_stride, rows_per_page,
+                      quant_mode, kv_offset, kv_scale_offset, block_table.data_ptr(),
+                      block_table.stride(0), K, idx, lens, res, ratio, window, scale,
+                      out.data_ptr(), o_t, o_h, lse.data_ptr(), err)
     if workspace is None:
-        workspace = torch.empty(max(256, kv_attention_workspace_bytes(T, H)), dtype=torch.uint8,
-                                device=q.device)
+        workspace = torch.empty(max(256, _workspace_bytes(T > 0 and H > 0, device.index)),
+                                dtype=torch.uint8, device=device)
         if stream is not None:
             workspace.record_stream(stream)
-    _require_cuda("workspace", workspace, torch.uint8)
-    _check(lib().qli_kv_attention(ctypes.byref(a), workspace.data_ptr(), workspace.numel(),
-                                  _stream(stream)), "qli_kv_attention")
+    else:
+        _check_cuda("workspace", workspace, torch.uint8)
+    _check((_lib or lib()).qli_kv_attention(a, workspace.data_ptr(), workspace.numel(),
+                                            _stream(stream, device.index)), "qli_kv_attention")
     return out, lse
 
 
@@ -577,21 +638,22 @@ def merge_attention(outs, lses, *, out=None, lse=None, stream=None):
         raise TypeError("outs must be bfloat16 or float32")
     if len(shape) != 3:
         raise ValueError("outs must be [T, H, 512]")
-    a = MergeArgs()
-    for i, (o, l) in enumerate(zip(outs, lses)):
-        _require_cuda("outs[%d]" % i, o, dtype)
-        _require_cuda("lses[%d]" % i, l, torch.float32)
+    ptrs, st, sh, lptrs = [0] * MERGE_MAX, [0] * MERGE_MAX, [0] * MERGE_MAX, [0] * MERGE_MAX
+    for i in range(n):
+        o, l = outs[i], lses[i]
+        _check_cuda("outs", o, dtype)
+        _check_cuda("lses", l, torch.float32)
         if o.shape != shape or o.stride(2) != 1:
             raise ValueError("outs must share one [T, H, 512] shape with unit stride in the last dim")
         if l.shape != shape[:2] or not l.is_contiguous():
             raise ValueError("lses must be contiguous [T, H] tensors")
-        a.part_out[i] = o.data_ptr()
-        a.part_stride_t[i], a.part_stride_h[i] = o.stride(0), o.stride(1)
-        a.part_lse[i] = l.data_ptr()
+        ptrs[i], lptrs[i] = o.data_ptr(), l.data_ptr()
+        st[i], sh[i], _ = o.stride()
     out, lse = _attn_outputs(shape, outs[0].device, out, lse)
-    a.parts, a.parts_f32 = n, int(dtype == torch.float32)
-    a.T, a.H, a.D = shape
-    a.out, a.out_stride_t, a.out_stride_h = out.data_ptr(), out.stride(0), out.stride(1)
-    a.lse = lse.data_ptr()
-    _check(lib().qli_merge_attention(ctypes.byref(a), _stream(stream)), "qli_merge_attention")
+    o_t, o_h, _ = out.stride()
+    T, H, D = shape
+    a = _pack_merge(*ptrs, *st, *sh, *lptrs, n, int(dtype == torch.float32), T, H, D,
+                    out.data_ptr(), o_t, o_h, lse.data_ptr())
+    _check((_lib or lib()).qli_merge_attention(a, _stream(stream, out.get_device())),
+           "qli_merge_attention")
     return out, lse
