@@ -24,7 +24,7 @@
 //         of a row tile its queries
 //   16    issues the score products, 17 the value products: each waits for its
 //         own operands, and the tensor core takes what is there
-//   18    the units' rows: pages, scales, fetches into L2, up to four units ahead
+//   18-19 the units' rows: pages, scales, fetches into L2, up to four units ahead
 // A tile's 128 rows are (half e of the 512 values, position), the queries are
 // stacked alike, so the scores are one product of M = 128, N = 128, K = 256
 // whose blocks e = e' are the halves' partial scores (the other two are
@@ -54,8 +54,8 @@ constexpr int kHT = 64;                        // heads per row tile (MMA N)
 constexpr int kPos = 64;                       // positions per unit
 constexpr int kSoftWarps = 8, kLoadWarps = 8;
 constexpr int kLoadWarp0 = kSoftWarps, kScoreWarp = kSoftWarps + kLoadWarps;
-constexpr int kValueWarp = kScoreWarp + 1, kRowWarp = kScoreWarp + 2;
-constexpr int kThreads = 640;                  // five warpgroups, the last warp idle
+constexpr int kValueWarp = kScoreWarp + 1, kRowWarp0 = kScoreWarp + 2, kRowWarps = 2;
+constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
 // Registers of the warpgroups' threads, within the CTA's 640 x 96. A spill in a
 // role's loop costs an L2 round trip: the streamed codes leave L1 to nothing else.
 constexpr int kSoftRegs = 112, kLoadRegs = 104, kIssueRegs = 48;
@@ -115,7 +115,8 @@ struct Args {
   int32_t t0, tc;              // tokens of this launch: t0 .. t0 + tc
   int32_t hg;                  // row tiles per token
   // workspace
-  int32_t* tok_start;          // [tc + 1] first unit of each token
+  int4* cut;                   // [CTAs] the row tile that goes on in the next CTA: token, row tile,
+                               // first unit past it (token -1: none)
   float* piece;                // [2 * CTAs][64][512]
   float* piece_lse;            // [2 * CTAs][64], log2
 };
@@ -394,15 +395,22 @@ __device__ __forceinline__ void plan(const Args& a, Smem& S) {
   const int32_t at = __shfl_sync(0xffffffffu, sums, warp) - own + incl - mine;
   const int32_t ctas = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
   const int32_t u0 = share_begin(total, ctas, c);
-  if (tid == 0) S.count = share_begin(total, ctas, c + 1) - u0;
+  const int32_t u1 = share_begin(total, ctas, c + 1);
   if (at <= u0 && u0 < at + mine) {
     S.start_t = tid;
     S.start_g = (u0 - at) / units;
     S.start_i = (u0 - at) % units;
   }
+  if (tid == 0) S.count = u1 - u0;
+  if (u1 <= u0) {
+    if (tid == 0) a.cut[c] = make_int4(-1, 0, 0, 0);
+  } else if (at <= u1 - 1 && u1 - 1 < at + mine) {
+    // the row tile of the share's last unit: cut if it goes on, and the first
+    // cut of it if it began here
+    const int32_t g = (u1 - 1 - at) / units, first = at + g * units, end = first + units;
+    a.cut[c] = make_int4(end > u1 && first >= u0 ? tid : -1, g, end, total);
+  }
   if (c == 0) {
-    if (tid < a.tc) a.tok_start[tid] = at;
-    if (tid == 0) a.tok_start[a.tc] = total;
     if (!a.idx && a.t0 == 0 && a.err) {
       uint32_t e = 0u;
 #pragma unroll 1
@@ -477,74 +485,63 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
   }
 }
 
-// The rows of the units: iteration m publishes unit m and takes one step each of
-// the lookup of units m + 1 (page to codes and scale, the codes fetched into
-// L2), m + 2 (position to page) and m + 3 (listed entry to position), so that no
-// step waits for the load of the one before. Lane l has rows l and l + 32.
-// Positions past the table and pages outside the pool are skipped and flagged.
+// The rows of the units, one a lane: iteration m publishes unit m and takes one
+// step each of the lookup of units m + 1 (page to codes and scale, the codes
+// fetched into L2), m + 2 (position to page) and m + 3 (listed entry to
+// position), so that no step waits for the load of the one before. Positions
+// past the table and pages outside the pool are skipped and flagged.
 __device__ __forceinline__ bool run_rows(const Args& a, Smem& S) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, r = threadIdx.x - 32 * kRowWarp0;
   bool bad = false;
   Walk w(a, S);                                       // unit m + 3
-  int32_t j3[2] = {-1, -1}, b3 = 0;                   // position, request
-  int32_t j2[2] = {-1, -1}, page2[2] = {-1, -1};      // position, page
-  const uint8_t* codes1[2] = {kZeroRow, kZeroRow};    // codes and scale
-  uint16_t s1[2] = {0, 0};
-  bool live1[2] = {false, false};
+  int32_t j3 = -1, b3 = 0;                            // position, request
+  int32_t j2 = -1, page2 = -1;                        // position, page
+  const uint8_t* codes1 = kZeroRow;                   // codes and scale
+  uint16_t s1 = 0;
+  bool live1 = false;
 #pragma unroll 1
   for (int32_t m = -3; m < w.count; ++m) {
     if (m >= 0) {
       const uint32_t slot = m & (kSlots - 1);
       if (!wait(&S.rowfree[slot], ((m / kSlots) & 1) ^ 1)) return false;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        // a row under a zero scale stands for zeros whatever its codes are: it
-        // counts in the normaliser only, under the smallest scale there is, so
-        // that it does not set the reference
-        const float s = __half2float(__ushort_as_half(s1[k]));
-        const bool zero = live1[k] && s == 0.0f;
-        S.row[slot][lane + 32 * k] = zero ? kZeroRow : codes1[k];
-        S.rs[slot][lane + 32 * k] = live1[k] ? (zero ? 5.9604645e-8f : s) : 0.0f;
-      }
+      // a row under a zero scale stands for zeros whatever its codes are: it
+      // counts in the normaliser only, under the smallest scale there is, so
+      // that it does not set the reference
+      const float s = __half2float(__ushort_as_half(s1));
+      const bool zero = live1 && s == 0.0f;
+      S.row[slot][r] = zero ? kZeroRow : codes1;
+      S.rs[slot][r] = live1 ? (zero ? 5.9604645e-8f : s) : 0.0f;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.rowfull[slot]);
     }
+    // unit m + 1
+    codes1 = kZeroRow;
+    live1 = j2 >= 0 && page2 >= 0 && page2 < a.num_pages;
+    bad |= j2 >= 0 && !live1;
+    if (live1) {
+      const uint8_t* base = a.cache + static_cast<int64_t>(page2) * a.page_stride;
+      const int32_t row = j2 & (a.R - 1);
+      codes1 = base + a.kv_off + row * kD;
+      s1 = __ldg(reinterpret_cast<const uint16_t*>(base + a.sc_off + row * 2));
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      // unit m + 1
-      codes1[k] = kZeroRow;
-      live1[k] = j2[k] >= 0 && page2[k] >= 0 && page2[k] < a.num_pages;
-      bad |= j2[k] >= 0 && !live1[k];
-      if (live1[k]) {
-        const uint8_t* base = a.cache + static_cast<int64_t>(page2[k]) * a.page_stride;
-        const int32_t row = j2[k] & (a.R - 1);
-        codes1[k] = base + a.kv_off + row * kD;
-        s1[k] = __ldg(reinterpret_cast<const uint16_t*>(base + a.sc_off + row * 2));
-#pragma unroll
-        for (int c = 0; c < 4; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(codes1[k] + c * 128));
-      }
-      // unit m + 2
-      bad |= j3[k] >= a.cap;
-      j2[k] = j3[k] < a.cap ? j3[k] : -1;
-      if (j2[k] >= 0)
-        page2[k] = __ldg(a.bt + static_cast<int64_t>(b3) * a.bt_stride + (j2[k] >> a.log2R));
+      for (int c = 0; c < 4; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(codes1 + c * 128));
     }
+    // unit m + 2
+    bad |= j3 >= a.cap;
+    j2 = j3 < a.cap ? j3 : -1;
+    if (j2 >= 0) page2 = __ldg(a.bt + static_cast<int64_t>(b3) * a.bt_stride + (j2 >> a.log2R));
     // unit m + 3
-    j3[0] = j3[1] = -1;
+    j3 = -1;
     if (w.valid()) {
-      const int32_t V = S.tokV[w.t], n = positions_of(a, V);
+      const int32_t V = S.tokV[w.t], n = positions_of(a, V), e = w.i * kPos + r;
       b3 = S.tokB[w.t];
+      if (e < n) j3 = a.idx ? __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e) : V - n + e;
       if (w.first()) {
-        // the row tile's queries, into L2
+        // the row tile's queries, into L2: head r, 128 bytes at a time
+        const int h = w.g * kHT + r;
+        const uint16_t* q = a.q + static_cast<int64_t>(a.t0 + w.t) * a.q_st + h * a.q_sh;
 #pragma unroll 1
-        for (int h = w.g * kHT + (lane >> 3); h < min(a.H, (w.g + 1) * kHT); h += 4)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(
-              a.q + static_cast<int64_t>(a.t0 + w.t) * a.q_st + h * a.q_sh + (lane & 7) * 64));
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int32_t e = w.i * kPos + lane + 32 * k;
-        if (e < n) j3[k] = a.idx ? __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e) : V - n + e;
+        for (int c = 0; c < 8 && h < a.H; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + c * 64));
       }
       w.next(a, S);
     }
@@ -764,7 +761,9 @@ __device__ __forceinline__ void store_value(uint16_t* at, float v) {
 __device__ __forceinline__ void store_value(float* at, float v) { *at = v; }
 
 // O^T's row `pos` of each quarter times the heads' factors, for `nh` heads from
-// h0 on, head i at dst + i * stride.
+// h0 on, head i at dst + i * stride: BF16 in the order of the values (a warp
+// stores to one 128-byte line), FP32 pieces in the order of the rows (likewise;
+// merge_pieces_kernel reorders).
 template <class T>
 __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int pos, int32_t nh, T* dst,
                                        int64_t stride) {
@@ -773,11 +772,20 @@ __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int
     uint32_t o[16];
     tmem_ld_x16(tmem + (c >> 1) * kHT + (c & 1) * 16, o);
     tmem_ld_wait();
+    // the factors before the stores, which the compiler has to keep in order
     const int i0 = (c & 1) * 16;
-    T* at = dst + i0 * stride + value_of(c >> 1, pos);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 al = *reinterpret_cast<const float4*>(S.alpha + h0 + i0 + 4 * i);
+      o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * al.x);
+      o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * al.y);
+      o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * al.z);
+      o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * al.w);
+    }
+    T* at = dst + i0 * stride + (sizeof(T) == 2 ? value_of(c >> 1, pos) : 128 * (c >> 1) + pos);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      if (i0 + i < nh) store_value(at, __uint_as_float(o[i]) * S.alpha[h0 + i0 + i]);
+      if (i0 + i < nh) store_value(at, __uint_as_float(o[i]));
       at += stride;
     }
   }
@@ -996,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
       mbar_init(&S.sfree[i], kSoftWarps);
     }
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&S.rowfull[i], 1);
+      mbar_init(&S.rowfull[i], kRowWarps);
       mbar_init(&S.rowfree[i], kLoadWarps + kSoftWarps);
     }
     mbar_init(&S.qfull, kLoadWarps);
@@ -1022,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
       fewer_registers<kIssueRegs>();
       if (warp == kScoreWarp) ok = run_scores(a, S, tmem);
       if (warp == kValueWarp) ok = run_values(a, S, tmem);
-      if (warp == kRowWarp) ok = run_rows(a, S);
+      if (warp >= kRowWarp0) ok = run_rows(a, S);
     }
     if (!ok && lane == 0 && a.err) atomicOr(a.err, QLI_DEVERR_TIMEOUT);
   }
@@ -1033,8 +1041,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
 }
 
 // ---- joining the pieces ---------------------------------------------------------
-// Block (c, k): the row tile that boundary c (between CTA c - 1 and CTA c) is
-// the first to cut, rows 8k .. 8k+7 of it, a warp per row.
+// Block (c - 1, k): the row tile that began in CTA c - 1 and goes on in CTA c, if
+// there is one; rows 8k .. 8k+7 of it, a warp per row.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = kJoinThreads / 32;
 
@@ -1042,68 +1050,69 @@ __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a
   pdl_wait();
   const int lane = threadIdx.x & 31, c = blockIdx.x + 1;
   const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-  const int32_t U = a.tok_start[a.tc];
-  const int32_t uc = share_begin(U, ctas, c), ub = share_begin(U, ctas, c - 1);
-  if (uc == ub || uc >= U) return;
-  int32_t lo = 0, hi = a.tc - 1;
-  while (lo < hi) {
-    const int32_t mid = (lo + hi + 1) >> 1;
-    if (a.tok_start[mid] <= uc) lo = mid; else hi = mid - 1;
-  }
-  const int32_t base = a.tok_start[lo], n = (a.tok_start[lo + 1] - base) / a.hg;
-  const int32_t g = (uc - base) / n, start = base + g * n, end = start + n;
-  const int32_t h = g * kHT + row;
-  if (uc == start || ub > start || h >= a.H) return;   // not cut, or cut before
+  const int4 tile = __ldcg(a.cut + c - 1);
+  const int32_t h = tile.y * kHT + row;
+  if (tile.x < 0 || h >= a.H) return;
   // pieces: CTA c - 1's slot 1, then slot 0 of CTA c, c + 1, ... up to the end
   // (a CTA with units has all its predecessors with units)
-  int32_t last = c;
+  int32_t count = 2;
 #pragma unroll 1
-  while (last + 1 < ctas && share_begin(U, ctas, last + 1) < end) ++last;
-  const int32_t count = last - c + 2;
+  while (c + count - 1 < ctas && share_begin(tile.w, ctas, c + count - 1) < tile.z) ++count;
   const auto slot = [&](int32_t k) -> int64_t {
     return k == 0 ? 2 * static_cast<int64_t>(c - 1) + 1 : 2 * static_cast<int64_t>(c - 1 + k);
   };
-  const auto lse_of = [&](int32_t k) -> float { return a.piece_lse[slot(k) * kHT + row]; };
-  float m = -INFINITY;
-  for (int32_t k = lane; k < count; k += 32) m = fmaxf(m, lse_of(k));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const auto lse_of = [&](int32_t k) -> float {
+    return k < count ? __ldcg(a.piece_lse + slot(k) * kHT + row) : -INFINITY;
+  };
+  const float first = lse_of(lane);
+  float m = first;
+#pragma unroll 1
+  for (int32_t k = lane + 32; k < count; k += 32) m = fmaxf(m, lse_of(k));
   float acc[16], total = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-  for (int32_t k0 = 0; k0 < count; k0 += 32) {
-    const float mine = k0 + lane < count ? lse_of(k0 + lane) : -INFINITY;
+  const float4* src = reinterpret_cast<const float4*>(a.piece + static_cast<int64_t>(row) * kD) + lane;
+  constexpr int kBatch = 4;                           // pieces whose loads are in flight together
+#pragma unroll 1
+  for (int32_t k0 = 0; k0 < count; k0 += kBatch) {
+    float4 v[kBatch][4];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[k][i] = k0 + k < count ? __ldcg(src + slot(k0 + k) * (kPieceRow / 4) + 32 * i)
+                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    if (k0 == 0) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    const float mine = k0 < 32 ? first : lse_of(k0 - k0 % 32 + lane);
     const float wk = mine == -INFINITY ? 0.0f : ex2(mine - m);
-    const int32_t some = min(32, count - k0);
-#pragma unroll 4
-    for (int32_t k = 0; k < some; ++k) {
-      const float w = __shfl_sync(0xffffffffu, wk, k);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float w = __shfl_sync(0xffffffffu, wk, (k0 + k) & 31);
       if (w == 0.0f) continue;
       total += w;
-      const float4* src = reinterpret_cast<const float4*>(
-          a.piece + slot(k0 + k) * kPieceRow + static_cast<int64_t>(row) * kD);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 v = src[(i >> 1) * 64 + 2 * lane + (i & 1)];
-        acc[4 * i] = fmaf(w, v.x, acc[4 * i]);
-        acc[4 * i + 1] = fmaf(w, v.y, acc[4 * i + 1]);
-        acc[4 * i + 2] = fmaf(w, v.z, acc[4 * i + 2]);
-        acc[4 * i + 3] = fmaf(w, v.w, acc[4 * i + 3]);
+        acc[4 * i] = fmaf(w, v[k][i].x, acc[4 * i]);
+        acc[4 * i + 1] = fmaf(w, v[k][i].y, acc[4 * i + 1]);
+        acc[4 * i + 2] = fmaf(w, v[k][i].z, acc[4 * i + 2]);
+        acc[4 * i + 3] = fmaf(w, v[k][i].w, acc[4 * i + 3]);
       }
     }
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  const int64_t t = a.t0 + lo;
-  uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.o_st + h * a.o_sh) + lane;
+  const int64_t t = a.t0 + tile.x;
+  // the lane's rows 4l .. 4l + 3 of each quarter are four values in a row
+  uint16_t* dst = a.out + t * a.o_st + h * a.o_sh;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 y = __floats2bfloat162_rn(acc[8 * i + 2 * k] * inv, acc[8 * i + 2 * k + 1] * inv);
-      w[k] = *reinterpret_cast<const uint32_t*>(&y);
-    }
-    dst[32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
+    *reinterpret_cast<uint2*>(dst + value_of(i, 4 * lane)) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
   if (lane == 0 && a.lse)
     a.lse[t * a.H + h] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
@@ -1192,14 +1201,14 @@ int32_t ctas_for(const Args& d, int32_t tc, int sms) {
   return static_cast<int32_t>(units < sms ? units : sms);
 }
 
-// Workspace: the tokens' first units, then two pieces and their LSE per SM.
+// Workspace, per SM: the row tile it cuts, two pieces and their LSE.
 struct Layout {
   size_t piece, lse, total;
 };
 Layout layout_for(int sms) {
   Layout L{};
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  L.piece = up(sizeof(int32_t) * (kChunkT + 1));
+  L.piece = up(sizeof(int4) * static_cast<size_t>(sms));
   L.lse = L.piece + up(sizeof(float) * 2 * static_cast<size_t>(sms) * kPieceRow);
   L.total = L.lse + up(sizeof(float) * 2 * static_cast<size_t>(sms) * kHT);
   return L;
@@ -1258,7 +1267,7 @@ extern "C" qli_status qli_kv_attention(const qli_kv_attn_args* a, void* workspac
   if (!aligned(workspace, 256)) return QLI_ERR_ALIGNMENT;
   Args d = make_args(*a);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  d.tok_start = reinterpret_cast<int32_t*>(w);
+  d.cut = reinterpret_cast<int4*>(w);
   d.piece = reinterpret_cast<float*>(w + L.piece);
   d.piece_lse = reinterpret_cast<float*>(w + L.lse);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
