@@ -53,25 +53,52 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4 v, float* x) {
   }
 }
 
-// Eight codes of FP32 values under the scale sf (y = RN(1 / sf)).
+// Eight codes of BF16 pairs under the scale sf (y = RN(1 / sf)); the same codes
+// as code_of and e4m3x2_of give value by value. INT8: adding 1.5 * 2^23 rounds
+// the quotient to an integer, ties to even, in the low bits (it is below 1.5 *
+// 127 but under the largest scale, where `huge` clamps it first), two are
+// clamped at a time as 16-bit halves. E4M3: the quotient's sign is x's; the
+// correction step gives +0 for a negative x far below s, so the signs are taken
+// from x (the top bytes of its BF16 halves).
 template <bool kFp8>
-__device__ __forceinline__ uint2 codes8(const float* x, float sf, float y) {
-  uint32_t lo = 0u, hi = 0u;
-  if constexpr (kFp8) {
-    // the quotient's sign is x's (a negative x far below s keeps its -0)
-    float c[8];
+__device__ __forceinline__ uint2 codes8(const uint4 v, float sf, float y, bool huge) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t out[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = copysignf(quotient(x[i], sf, y), x[i]);
-    lo = e4m3x2_of(c[0], c[1]) | (e4m3x2_of(c[2], c[3]) << 16);
-    hi = e4m3x2_of(c[4], c[5]) | (e4m3x2_of(c[6], c[7]) << 16);
-  } else {
+  for (int i = 0; i < 2; ++i) {
+    float q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      lo |= code_byte(x[i], sf, y) << (8 * i);
-      hi |= code_byte(x[4 + i], sf, y) << (8 * i);
+    for (int k = 0; k < 2; ++k) {
+      q[2 * k] = quotient(__uint_as_float(w[2 * i + k] << 16), sf, y);
+      q[2 * k + 1] = quotient(__uint_as_float(w[2 * i + k] & 0xffff0000u), sf, y);
+    }
+    if constexpr (kFp8) {
+      const uint32_t c = e4m3x2_of(q[0], q[1]) | (e4m3x2_of(q[2], q[3]) << 16);
+      const uint32_t sign = __byte_perm(w[2 * i], w[2 * i + 1], 0x7531);
+      out[i] = (c & 0x7f7f7f7fu) | (sign & 0x80808080u);
+    } else {
+      uint32_t n[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (huge) q[k] = fminf(fmaxf(q[k], -127.0f), 127.0f);
+        n[k] = __float_as_uint(__fadd_rn(q[k], 12582912.0f));
+      }
+      const uint32_t lo = __vmins2(__vmaxs2(__byte_perm(n[0], n[1], 0x5410), 0xff81ff81u), 0x007f007fu);
+      const uint32_t hi = __vmins2(__vmaxs2(__byte_perm(n[2], n[3], 0x5410), 0xff81ff81u), 0x007f007fu);
+      out[i] = __byte_perm(lo, hi, 0x6420);
     }
   }
-  return make_uint2(lo, hi);
+  return make_uint2(out[0], out[1]);
+}
+
+// The largest magnitude of a row's BF16 values (a lane has two times eight),
+// compared as integers: NaN is above all.
+__device__ __forceinline__ float row_amax(const uint4 a, const uint4 b) {
+  constexpr uint32_t k = 0x7fff7fffu;
+  uint32_t m = __vmaxu2(__vmaxu2(__vmaxu2(a.x & k, a.y & k), __vmaxu2(a.z & k, a.w & k)),
+                        __vmaxu2(__vmaxu2(b.x & k, b.y & k), __vmaxu2(b.z & k, b.w & k)));
+  m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
+  return __uint_as_float(m << 16);
 }
 
 // ---- writer -----------------------------------------------------------------
@@ -102,21 +129,13 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const uint16_t* __re
     }
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      float f[16];
-      bf16x8_to_f32(v[d][0], f);
-      bf16x8_to_f32(v[d][1], f + 8);
-      float m = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      uint16_t sb = scale_bits_of<kFp8>(m);
+      uint16_t sb = scale_bits_of<kFp8>(row_amax(v[d][0], v[d][1]));
       const float sf = __half2float(__ushort_as_half(sb));
       uint2 c0 = make_uint2(0u, 0u), c1 = c0;
       if (sf != 0.0f) {
         const float y = __frcp_rn(sf);
-        c0 = codes8<kFp8>(f, sf, y);
-        c1 = codes8<kFp8>(f + 8, sf, y);
+        c0 = codes8<kFp8>(v[d][0], sf, y, sb == 0x7bffu);
+        c1 = codes8<kFp8>(v[d][1], sf, y, sb == 0x7bffu);
       } else {
         sb = 0u;
       }
