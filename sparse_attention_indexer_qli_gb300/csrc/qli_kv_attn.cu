@@ -114,6 +114,7 @@ struct Args {
   uint32_t* err;
   int32_t t0, tc;              // tokens of this launch: t0 .. t0 + tc
   int32_t hg;                  // row tiles per token
+  int32_t whole;               // 1: CTA c has row tile c, whole; 0: even shares
   // workspace
   int4* cut;                   // [CTAs] the row tile that goes on in the next CTA: token, row tile,
                                // first unit past it (token -1: none)
@@ -350,6 +351,18 @@ __device__ __forceinline__ int32_t request_of(const int32_t* cu, int32_t B, int3
   return lo;
 }
 
+// Flags requests with bad metadata, once a call.
+__device__ __forceinline__ void flag_requests(const Args& a, int tid) {
+  if (a.idx || a.t0 != 0 || !a.err) return;
+  uint32_t e = 0u;
+#pragma unroll 1
+  for (int b = tid; b < a.B; b += kThreads) {
+    int32_t q0, q1, lk, res;
+    e |= sanitize_request(a, b, q0, q1, lk, res);
+  }
+  if (e) atomicOr(a.err, e);
+}
+
 // Plans the launch: every token's request and visible positions, and the CTA's
 // share. A thread takes one token.
 __device__ __forceinline__ void plan(const Args& a, Smem& S) {
@@ -374,6 +387,18 @@ __device__ __forceinline__ void plan(const Args& a, Smem& S) {
     S.tokV[tid] = V;
     S.tokB[tid] = b;
     units = units_of(a, V);
+  }
+  if (a.whole) {
+    __syncthreads();
+    if (tid == 0) {
+      S.start_t = static_cast<int32_t>(blockIdx.x) / a.hg;
+      S.start_g = static_cast<int32_t>(blockIdx.x) % a.hg;
+      S.start_i = 0;
+      S.count = units_of(a, S.tokV[S.start_t]);
+    }
+    if (blockIdx.x == 0) flag_requests(a, tid);
+    __syncthreads();
+    return;
   }
   const int32_t mine = units * a.hg;
   int32_t incl = mine;
@@ -410,17 +435,7 @@ __device__ __forceinline__ void plan(const Args& a, Smem& S) {
     const int32_t g = (u1 - 1 - at) / units, first = at + g * units, end = first + units;
     a.cut[c] = make_int4(end > u1 && first >= u0 ? tid : -1, g, end, total);
   }
-  if (c == 0) {
-    if (!a.idx && a.t0 == 0 && a.err) {
-      uint32_t e = 0u;
-#pragma unroll 1
-      for (int b = tid; b < a.B; b += kThreads) {
-        int32_t q0, q1, lk, res;
-        e |= sanitize_request(a, b, q0, q1, lk, res);
-      }
-      if (e) atomicOr(a.err, e);
-    }
-  }
+  if (c == 0) flag_requests(a, tid);
   __syncthreads();
 }
 
@@ -754,39 +769,35 @@ __device__ __forceinline__ float across(const f32x2 (&x)[8], int lane, F f) {
   return f(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-__device__ __forceinline__ void store_value(uint16_t* at, float v) {
-  const __nv_bfloat16 y = __float2bfloat16_rn(v);
-  *at = *reinterpret_cast<const uint16_t*>(&y);
-}
-__device__ __forceinline__ void store_value(float* at, float v) { *at = v; }
-
-// O^T's row `pos` of each quarter times the heads' factors, for `nh` heads from
-// h0 on, head i at dst + i * stride: BF16 in the order of the values (a warp
-// stores to one 128-byte line), FP32 pieces in the order of the rows (likewise;
+// O^T's row `pos` of each quarter times the heads' factors, the 32 heads from h0
+// on. BF16 outputs (kOut), of the first `nh` heads: head i at dst + i * stride,
+// in the order of the values (a warp stores to one 128-byte line). FP32 pieces:
+// head i at dst + i * kD, in the order of the rows (likewise;
 // merge_pieces_kernel reorders).
-template <class T>
+template <bool kOut, class T>
 __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int pos, int32_t nh, T* dst,
                                        int64_t stride) {
 #pragma unroll 1
   for (int c = 0; c < 8; ++c) {
-    uint32_t o[16];
-    tmem_ld_x16(tmem + (c >> 1) * kHT + (c & 1) * 16, o);
-    tmem_ld_wait();
-    // the factors before the stores, which the compiler has to keep in order
     const int i0 = (c & 1) * 16;
+    uint32_t o[16];
+    tmem_ld_x16(tmem + (c >> 1) * kHT + i0, o);
+    float al[16];                                     // before the stores, which loads may not pass
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 al = *reinterpret_cast<const float4*>(S.alpha + h0 + i0 + 4 * i);
-      o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * al.x);
-      o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * al.y);
-      o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * al.z);
-      o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * al.w);
-    }
-    T* at = dst + i0 * stride + (sizeof(T) == 2 ? value_of(c >> 1, pos) : 128 * (c >> 1) + pos);
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(al + 4 * i) =
+        *reinterpret_cast<const float4*>(S.alpha + h0 + i0 + 4 * i);
+    tmem_ld_wait();
+    T* at = dst + i0 * stride + (kOut ? value_of(c >> 1, pos) : 128 * (c >> 1) + pos);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      if (i0 + i < nh) store_value(at, __uint_as_float(o[i]));
-      at += stride;
+      const float v = __uint_as_float(o[i]) * al[i];
+      if constexpr (kOut) {
+        const __nv_bfloat16 y = __float2bfloat16_rn(v);
+        if (i0 + i < nh) *at = *reinterpret_cast<const uint16_t*>(&y);
+        at += stride;
+      } else {
+        at[i * kD] = v;
+      }
     }
   }
 }
@@ -971,14 +982,14 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       if (qw == 0 && lane < nh && a.lse)
         a.lse[static_cast<int64_t>(a.t0 + w.t) * a.H + h + lane] = lse2 * kLn2;
       uint16_t* orow = a.out + static_cast<int64_t>(a.t0 + w.t) * a.o_st + h * a.o_sh;
-      output(S, oe, 32 * sub, 32 * qw + lane, nh, orow, a.o_sh);
+      output<true>(S, oe, 32 * sub, 32 * qw + lane, nh, orow, a.o_sh);
     } else {
       // a row tile that began in an earlier CTA goes to slot 0, one that goes
       // on in the next to slot 1
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.began_here() ? 1 : 0);
       if (qw == 0) a.piece_lse[slot * kHT + 32 * sub + lane] = lse2;
-      output(S, oe, 32 * sub, 32 * qw + lane, nh, a.piece + slot * kPieceRow + (32 * sub) * kD,
-             static_cast<int64_t>(kD));
+      output<false>(S, oe, 32 * sub, 32 * qw + lane, 32, a.piece + slot * kPieceRow + (32 * sub) * kD,
+                    static_cast<int64_t>(kD));
     }
     named_bar(bar, 128);                              // the factors are read
   }
@@ -993,8 +1004,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   if (warp == kScoreWarp) tmem_alloc(&S.tmem_base, kTmemCols);
+  if (tid < kHT) S.m[tid] = 0.0f;
   if (tid == 0) {
-    for (int h = 0; h < kHT; ++h) S.m[h] = 0.0f;
     for (int i = 0; i < 2; ++i) {
       for (int f = 0; f < 2; ++f) {
         mbar_init(&S.full[i][f], kLoadWarps);
@@ -1193,13 +1204,17 @@ Args make_args(const qli_kv_attn_args& a) {
   return d;
 }
 
-// CTAs of a launch over tc tokens: one per SM, and no more than there can be
-// units (known on the host for lists only).
-int32_t ctas_for(const Args& d, int32_t tc, int sms) {
-  if (d.idx == nullptr) return sms;
-  const int64_t units = static_cast<int64_t>(tc) * d.hg * ((static_cast<int64_t>(d.K) - 1) / kPos + 1);
-  return static_cast<int32_t>(units < sms ? units : sms);
+// Most units a row tile can have.
+int64_t most_units(const Args& d) {
+  int64_t n = d.idx ? static_cast<int64_t>(d.K) : d.cap < INT32_MAX ? d.cap : INT32_MAX;
+  if (!d.idx && d.window > 0 && d.window < n) n = d.window;
+  return n <= kPos ? 1 : (n - 1) / kPos + 1;
 }
+
+// Row tiles of at most this many units are not cut while there is an SM for
+// each. 64 tokens over a window of 128 positions (two units): 21.6 us cut and
+// joined, 19.6 us whole.
+constexpr int kWholeUnits = 2;
 
 // Workspace, per SM: the row tile it cuts, two pieces and their LSE.
 struct Layout {
@@ -1220,15 +1235,18 @@ cudaError_t launch(Args d, int sms, cudaStream_t s) {
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kSmemBytes,
                                     g_smem_kv_attn[kFp8 ? 1 : 0]);
   // tokens per launch: what one plan holds, and fewer than 2^30 units
-  const int64_t most = (d.idx ? static_cast<int64_t>(d.K) : d.cap < INT32_MAX ? d.cap : INT32_MAX) / kPos + 1;
-  const int64_t fit = (int64_t{1} << 30) / (most * d.hg);
+  const int64_t most = most_units(d), fit = (int64_t{1} << 30) / (most * d.hg);
   const int32_t chunk = static_cast<int32_t>(fit < kChunkT ? fit : kChunkT);
   for (d.t0 = 0; e == cudaSuccess && d.t0 < d.T; d.t0 += chunk) {
     d.tc = d.T - d.t0 < chunk ? d.T - d.t0 : chunk;
-    const int32_t ctas = ctas_for(d, d.tc, sms);
+    const int64_t tiles = static_cast<int64_t>(d.tc) * d.hg;
+    d.whole = most <= kWholeUnits && tiles <= sms ? 1 : 0;
+    // one CTA per SM, and no more than there can be units
+    const int64_t units = tiles * most;
+    const int32_t ctas = static_cast<int32_t>(d.whole ? tiles : units < sms ? units : sms);
     kernel<<<static_cast<unsigned>(ctas), kThreads, kSmemBytes, s>>>(d);
     e = cudaGetLastError();
-    if (e == cudaSuccess && ctas > 1)
+    if (e == cudaSuccess && ctas > 1 && !d.whole)
       e = launch_pdl(merge_pieces_kernel,
                      dim3(static_cast<unsigned>(ctas - 1),
                           static_cast<unsigned>(((d.H < kHT ? d.H : kHT) + kJoinRows - 1) / kJoinRows)),
