@@ -25,17 +25,13 @@
 //   16    issues the score products, 17 the value products: each waits for its
 //         own operands, and the tensor core takes what is there
 //   18-19 the units' rows: pages, scales, fetches into L2, up to four units ahead
-// A tile's 128 rows are (half e of the 512 values, position), the queries are
-// stacked alike, so the scores are one product of M = 128, N = 128, K = 256
-// whose blocks e = e' are the halves' partial scores (the other two are
-// wasted: 1104 cycles for 64 positions, where M = 128 positions against N = 64
-// heads takes 832 but leaves no room for a second tile, so that products,
-// softmax and conversion would take turns). The softmax adds the halves
-// through shared memory. O^T[128 values, 64 heads] += V^T P^T for each quarter
-// of the values, from the same tile read MN-major.
-// TMEM: two S buffers of 128 columns, four O^T quarters of 64. Shared memory:
-// two FP16 tiles (128 KB), the queries (64 KB), the exchange (16 KB), the
-// weights (8 KB).
+// The scores are S[64 positions, 64 heads] = K Q^T as M = 64 products (36 cycles
+// each, against 52 with M = 128, whose tile would leave no room for a second
+// one, so that products, softmax and conversion would take turns); the values
+// O^T[128 values, 64 heads] += V^T P^T for each quarter of the values, from the
+// same tile read MN-major.
+// TMEM: two S buffers of 64 columns, four O^T quarters of 64. Shared memory:
+// two FP16 tiles (128 KB), the queries (64 KB), two buffers of weights (16 KB).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -58,11 +54,11 @@ constexpr int kValueWarp = kScoreWarp + 1, kRowWarp0 = kScoreWarp + 2, kRowWarps
 constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
 // Registers of the warpgroups' threads, within the CTA's 640 x 96. A spill in a
 // role's loop costs an L2 round trip: the streamed codes leave L1 to nothing else.
-constexpr int kSoftRegs = 112, kLoadRegs = 104, kIssueRegs = 48;
+constexpr int kSoftRegs = 104, kLoadRegs = 104, kIssueRegs = 64;
 static_assert(2 * kSoftRegs + 2 * kLoadRegs + kIssueRegs <= 5 * 96, "registers of the CTA");
 constexpr int kSlots = 4;                      // units whose rows are looked up ahead
-constexpr int kRegion = 128 * 128;             // 64 values of every row of a tile
-constexpr int kTile = 4 * kRegion;
+constexpr int kRegion = kPos * 128;            // 64 values of every row of a tile (or query)
+constexpr int kTile = 8 * kRegion;
 constexpr int kChunkT = 512;                   // tokens planned per launch, one a thread
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 0, kOCol = 256;
@@ -73,19 +69,18 @@ constexpr int kPieceRow = kHT * kD;            // floats of a piece
 struct Smem {
   uint8_t kv[2][kTile];                        // 1024-aligned, by unit parity
   uint8_t q[kTile];                            // 1024-aligned
-  uint8_t p[kPos * 128];                       // 1024-aligned
-  float x[4][kPos][16];                        // partial scores a softmax warp gives to its partner
+  uint8_t p[2][kPos * 128];                    // 1024-aligned, by unit parity
   int32_t tokV[kChunkT], tokB[kChunkT];        // visible positions and request of the launch's tokens
   const uint8_t* row[kSlots][kPos];            // the rows' codes, by unit modulo kSlots
   float rs[kSlots][kPos];                      // and scales; 0: no position
   float sl2[2][kHT];                           // by row tile parity: softmax scale in log2 over the
                                                // queries' power of two
   float m[kHT], alpha[kHT], delta[kHT];
-  float part[2][4][16];                        // [32 heads][softmax warp of them][head]
+  float part[2][4][32];                        // [32 heads][softmax warp of them][head]
   int32_t warp_sum[kThreads / 32];
   int32_t count, start_t, start_g, start_i;    // the CTA's share: units, first token, row tile, unit
-  // tiles by unit parity and pair of regions
-  uint64_t full[2][2], empty[2][2], sfull[2], sfree[2], rowfull[kSlots], rowfree[kSlots], qfull, qempty, pready, pvdone, done;
+  // tiles by unit parity and half of the values
+  uint64_t full[2][2], empty[2][2], sfull[2], sfree[2], rowfull[kSlots], rowfree[kSlots], qfull, qempty, pready, done;
   uint32_t tmem_base;
 };
 constexpr int kSmemBytes = static_cast<int>(sizeof(Smem)) + 1024;
@@ -122,11 +117,11 @@ struct Args {
   float* piece_lse;            // [2 * CTAs][64], log2
 };
 
-// Instruction descriptor, kind::f16 with FP16 A and B, FP32 D, M = 128, N = n;
+// Instruction descriptor, kind::f16 with FP16 A and B, FP32 D, M = m, N = n;
 // a_mn / b_mn select MN-major operands.
-__host__ __device__ constexpr uint32_t idesc_f16(uint32_t n, bool a_mn, bool b_mn) {
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) |
-         ((128u >> 4) << 24);
+         ((m >> 4) << 24);
 }
 
 // Shared-memory descriptor, 128-byte swizzle. K-major: sbo = bytes between
@@ -169,11 +164,6 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) {
   f32x2 r;
   asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -183,6 +173,10 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
+}
+
+__device__ __forceinline__ void st_shared(uint32_t at, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
 }
 
 // 2^x by the SFU's approximation (a few ulp; 2^-inf = +0).
@@ -220,6 +214,18 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// The first 16 of the warp's 32 lanes x 32 columns: lane t gets, of the i-th
+// eight columns, 2 (t & 3) and the next, of rows t / 4 (r[4i], r[4i + 1]) and
+// t / 4 + 8 (r[4i + 2], r[4i + 3]).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
@@ -440,11 +446,11 @@ __device__ __forceinline__ void plan(const Args& a, Smem& S) {
 }
 
 // ---- loaders ----------------------------------------------------------------
-// Quarter c = 2e + f of the values is in rows 64e .. 64e + 63 of regions 2f and
-// 2f + 1, in this order: 16-byte unit j of region 2f + b holds values
-// 128c + 16j + 8b .. + 7, so that a lane's 16 loaded codes fill unit j of two
-// regions and eight lanes cover all banks. The queries are stored alike, and
-// row 64b + 8j + x of O^T's quarter c is that value + x.
+// Quarter c of the values is in regions 2c and 2c + 1, in this order: 16-byte
+// unit j of region 2c + b holds values 128c + 16j + 8b .. + 7, so that a lane's 16
+// loaded codes fill unit j of two regions and eight lanes cover all banks. The
+// queries are stored alike, and row 64b + 8j + x of O^T's quarter c is that
+// value + x.
 __device__ __forceinline__ int value_of(int c, int row) {
   return 128 * c + 16 * ((row >> 3) & 7) + 8 * (row >> 6) + (row & 7);
 }
@@ -459,8 +465,7 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
   const int lane = threadIdx.x & 31;
   constexpr int kRows = kHT / kLoadWarps, kBatch = 4;
   // lane l holds values 16l .. 16l + 15: unit l & 7 of quarter l >> 3
-  const uint32_t dst = smem_u32(S.q) + ((lane >> 3) & 1) * 2 * kRegion;
-  const int e64 = (lane >> 4) * 64;
+  const uint32_t dst = smem_u32(S.q) + (lane >> 3) * 2 * kRegion;
 #pragma unroll 1
   for (int r0 = lw * kRows; r0 < (lw + 1) * kRows; r0 += kBatch) {
     uint4 v[kBatch][2];
@@ -491,7 +496,7 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         w[i] = pack_half2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-      const uint32_t at = dst + sw(e64 + r, lane & 7);
+      const uint32_t at = dst + sw(r, lane & 7);
       st_shared_v4(at, w[0], w[1], w[2], w[3]);
       st_shared_v4(at + kRegion, w[4], w[5], w[6], w[7]);
       if (lane == 0)
@@ -565,7 +570,7 @@ __device__ __forceinline__ bool run_rows(const Args& a, Smem& S) {
   return true;
 }
 
-// Iteration n stores unit n from registers, one pair of regions after the
+// Iteration n stores unit n from registers, one half of the values after the
 // other as they come free, then loads unit n + 1 (32 KB in flight on the SM
 // while unit n is worked on). A warp has eight rows; a warp
 // instruction loads one quarter of four.
@@ -588,10 +593,10 @@ __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int c = 2 * f; c < 2 * f + 2; ++c) {
             uint32_t o[8];
-            widen16<kFp8>(x[k][2 * e + f], o);
-            const uint32_t at = (k ? at1 : at0) + buf * kTile + f * 2 * kRegion + e * 64 * 128;
+            widen16<kFp8>(x[k][c], o);
+            const uint32_t at = (k ? at1 : at0) + buf * kTile + c * 2 * kRegion;
             st_shared_v4(at, o[0], o[1], o[2], o[3]);
             st_shared_v4(at + kRegion, o[4], o[5], o[6], o[7]);
           }
@@ -676,7 +681,7 @@ __device__ __forceinline__ bool drain(Smem& S) {
 }
 
 __device__ __forceinline__ bool run_scores(const Args& a, Smem& S, uint32_t tmem_any) {
-  constexpr uint32_t id = idesc_f16(128, false, false), hi = sdesc_hi(1024);
+  constexpr uint32_t id = idesc_f16(kPos, kHT, false, false), hi = sdesc_hi(1024);
   const uint32_t k_lo = sdesc_lo(smem_u32(S.kv), 16), q_lo = sdesc_lo(smem_u32(S.q), 16);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
   bool ok = true;
@@ -692,11 +697,11 @@ __device__ __forceinline__ bool run_scores(const Args& a, Smem& S, uint32_t tmem
       ok = wait(&S.full[buf][f], parity);
       tc_fence_after();
       if (ok && elect_one()) {
-        const uint32_t step = f * (2 * kRegion >> 4), ke = k_lo + buf * (kTile >> 4) + step;
-        const uint32_t qe = q_lo + step, se = tmem + kSCol + buf * 128;
+        const uint32_t step = f * (4 * kRegion >> 4), ke = k_lo + buf * (kTile >> 4) + step;
+        const uint32_t qe = q_lo + step, se = tmem + kSCol + buf * kHT;
         mma_first(se, ke, qe, hi, id, f);
 #pragma unroll
-        for (uint32_t k = 1; k < 8; ++k) {
+        for (uint32_t k = 1; k < 16; ++k) {
           const uint32_t on = ((k >> 2) * kRegion + (k & 3) * 32) >> 4;
           mma(se, ke + on, qe + on, hi, id);
         }
@@ -712,7 +717,7 @@ __device__ __forceinline__ bool run_scores(const Args& a, Smem& S, uint32_t tmem
 }
 
 __device__ __forceinline__ bool run_values(const Args& a, Smem& S, uint32_t tmem_any) {
-  constexpr uint32_t id = idesc_f16(kHT, true, true), hi = sdesc_hi(1024);
+  constexpr uint32_t id = idesc_f16(128, kHT, true, true), hi = sdesc_hi(1024);
   const uint32_t v_lo = sdesc_lo(smem_u32(S.kv), kRegion), p_lo = sdesc_lo(smem_u32(S.p), 1024);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
   bool ok = true;
@@ -720,22 +725,21 @@ __device__ __forceinline__ bool run_values(const Args& a, Smem& S, uint32_t tmem
 #pragma unroll 1
   for (Walk w(a, S); ok && w.valid(); w.next(a, S), ++n) {
     const uint32_t more = w.first() ? 0u : 1u, tile = v_lo + (n & 1) * (kTile >> 4);
+    const uint32_t pe = p_lo + (n & 1) * (kPos * 128 >> 4);
     ok = wait(&S.pready, n & 1);
     tc_fence_after();
     if (ok && elect_one()) {
 #pragma unroll
       for (uint32_t f = 0; f < 2; ++f) {
 #pragma unroll
-        for (uint32_t e = 0; e < 2; ++e) {
-          const uint32_t ve = tile + ((f * 2 * kRegion + e * 64 * 128) >> 4);
-          const uint32_t oe = tmem + kOCol + (2 * e + f) * kHT;
-          mma_first(oe, ve, p_lo, hi, id, more);
+        for (uint32_t c = 2 * f; c < 2 * f + 2; ++c) {
+          const uint32_t ve = tile + c * (2 * kRegion >> 4), oe = tmem + kOCol + c * kHT;
+          mma_first(oe, ve, pe, hi, id, more);
 #pragma unroll
-          for (uint32_t k = 1; k < 4; ++k) mma(oe, ve + (k * 2048 >> 4), p_lo + (k * 2048 >> 4), hi, id);
+          for (uint32_t k = 1; k < 4; ++k) mma(oe, ve + (k * 2048 >> 4), pe + (k * 2048 >> 4), hi, id);
         }
         mma_commit(&S.empty[n & 1][f]);
       }
-      mma_commit(&S.pvdone);
     }
     __syncwarp();
   }
@@ -743,30 +747,33 @@ __device__ __forceinline__ bool run_values(const Args& a, Smem& S, uint32_t tmem
 }
 
 // ---- softmax ------------------------------------------------------------------
-// Combines 16 values a lane (as 8 pairs) across the warp's 32 lanes: lanes 2i
-// and 2i + 1 get value i's result.
+// Combines 8 values a lane (pair i: heads 8i + 2 (lane & 3) and the next) across
+// the eight lanes that share lane & 3; the lane gets the one of head_of(lane).
 template <class F>
-__device__ __forceinline__ float across(const f32x2 (&x)[8], int lane, F f) {
-  float v[8];
+__device__ __forceinline__ float across(const f32x2 (&x)[4], int lane, F f) {
+  float v[4];
   {
     const bool up = (lane & 16) != 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 lo = both(x[i]), hi = both(x[i + 4]);
+    for (int i = 0; i < 2; ++i) {
+      const float2 lo = both(x[i]), hi = both(x[i + 2]);
       v[2 * i] = f(up ? hi.x : lo.x, __shfl_xor_sync(0xffffffffu, up ? lo.x : hi.x, 16));
       v[2 * i + 1] = f(up ? hi.y : lo.y, __shfl_xor_sync(0xffffffffu, up ? lo.y : hi.y, 16));
     }
   }
 #pragma unroll
-  for (int o = 8; o > 1; o >>= 1) {
+  for (int o = 8; o > 2; o >>= 1) {
     const bool up = (lane & o) != 0;
 #pragma unroll
-    for (int i = 0; i < o / 2; ++i) {
-      const float send = up ? v[i] : v[i + o / 2], keep = up ? v[i + o / 2] : v[i];
+    for (int i = 0; i < o / 4; ++i) {
+      const float send = up ? v[i] : v[i + o / 4], keep = up ? v[i + o / 4] : v[i];
       v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, o));
     }
   }
-  return f(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+  return v[0];
+}
+__device__ __forceinline__ int head_of(int lane) {
+  return 8 * (lane >> 3) + 2 * (lane & 3) + ((lane >> 2) & 1);
 }
 
 // O^T's row `pos` of each quarter times the heads' factors, the 32 heads from h0
@@ -802,27 +809,26 @@ __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int
   }
 }
 
-// Warp (qw, sub): TMEM lanes 32 qw .., that is half e = qw >> 1 of the values and
-// positions 32 (qw & 1) ..; of the 32 heads from 32 sub on it takes the 16 from
-// 16 e on, and gives its partial scores of the other 16 to warp (qw ^ 2, sub).
-// The four warps of a `sub` share a named barrier.
+// Warp (qw, sub) has positions 16 qw .. 16 qw + 15 (M = 64 scores lie in the first
+// 16 of every 32 TMEM lanes) of the 32 heads from 32 sub on; a lane has two
+// positions, lane / 4 and 8 further, of four pairs of heads. The four warps of a
+// `sub` share a named barrier.
 __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tmem) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int qw = warp & 3, sub = warp >> 2, e = qw >> 1;
+  const int qw = warp & 3, sub = warp >> 2, bar = 1 + sub;
   const uint32_t lanes = static_cast<uint32_t>(32 * qw) << 16;
-  const int pos = 32 * (qw & 1) + lane, bar = 1 + sub, h0 = 32 * sub + 16 * e;
+  const int pos = 16 * qw + (lane >> 2), h0 = 32 * sub + 2 * (lane & 3);
   float* part = S.part[sub][0];
-  const float4* m4 = reinterpret_cast<const float4*>(S.m + h0);
+  // pair i: heads h0 + 8i, h0 + 8i + 1
+  const f32x2* m2 = reinterpret_cast<const f32x2*>(S.m + h0);
   const f32x2* de2 = reinterpret_cast<const f32x2*>(S.delta + h0);
   const f32x2* al2 = reinterpret_cast<const f32x2*>(S.alpha + h0);
-  // 16-byte pieces of a position's 64 bytes, swizzled so that eight lanes cover all banks
-  float* give = S.x[2 * sub + e][pos];
-  const float* take = S.x[2 * sub + (e ^ 1)][pos];
-  const int swz = (lane >> 1) & 3;
+  // the lane's word of unit 4 sub of its first position; unit 4 sub + i flips bits 4, 5
+  const uint32_t p_at = smem_u32(S.p) + sw(pos, 4 * sub) + 4 * (lane & 3);
   bool ok = true, seen = false;
-  f32x2 l[8];
+  f32x2 l[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) l[i] = pair_of(0.0f, 0.0f);
+  for (int i = 0; i < 4; ++i) l[i] = pair_of(0.0f, 0.0f);
   uint32_t n = 0, seg = 0;
   // A wait that gives up clears `ok`; the warps still run through the same
   // named barriers, on whatever TMEM holds, and write no output.
@@ -838,69 +844,59 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     }
     const uint32_t slot = n & (kSlots - 1);
     if (ok && !wait(&S.rowfull[slot], (n / kSlots) & 1)) ok = false;
-    // d = y - M + kShift = (partial sums) * cs + es; no position here: -inf,
-    // weight 0. 1 / s is taken from the logarithm that d uses, so that p / s is
-    // free of its error.
-    const float s = S.rs[slot][pos];
-    const float ls = lg2(s), inv_s = s != 0.0f ? ex2(-ls) : 0.0f;
-    f32x2 cs[8], es[8];
-    {
-      const float4* c4 = reinterpret_cast<const float4*>(S.sl2[(seg - 1) & 1] + h0);
+    // d = y - M + kShift = score * cs + es; no position here: -inf, weight 0.
+    // 1 / s is taken from the logarithm that d uses, so that p / s is free of
+    // its error.
+    f32x2 cs[2][4], es[2][4], inv2[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float s = S.rs[slot][pos + 8 * k], ls = lg2(s), inv_s = s != 0.0f ? ex2(-ls) : 0.0f;
+      const f32x2* c2 = reinterpret_cast<const f32x2*>(S.sl2[(seg - 1) & 1] + h0);
       const f32x2 s2 = pair_of(s, s), ls2 = pair_of(ls + kShift, ls + kShift);
+      inv2[k] = pair_of(inv_s, inv_s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 c = c4[i], m = m4[i];
-        cs[2 * i] = mul2(pair_of(c.x, c.y), s2);
-        cs[2 * i + 1] = mul2(pair_of(c.z, c.w), s2);
-        es[2 * i] = sub2(ls2, pair_of(m.x, m.y));
-        es[2 * i + 1] = sub2(ls2, pair_of(m.z, m.w));
+        cs[k][i] = mul2(c2[4 * i], s2);
+        es[k][i] = sub2(ls2, m2[4 * i]);
       }
     }
     if (ok && !wait(&S.sfull[buf], parity)) ok = false;
     tc_fence_after();
-    f32x2 d[8];
+    f32x2 d[2][4];
+    float over = -INFINITY;
     {
-      // the partner's block first: its values go out while the own ones arrive
-      uint32_t own[16], other[16];
-      const uint32_t at = tmem + lanes + kSCol + 128 * buf + 64 * e + 32 * sub;
-      tmem_ld_x16(at + 16 * (e ^ 1), other);
-      tmem_ld_x16(at + 16 * e, own);
+      uint32_t r[16];
+      tmem_ld_16x256b_x4(tmem + lanes + kSCol + kHT * buf + 32 * sub, r);
       tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(give + 4 * (i ^ swz)) =
-            make_uint4(other[4 * i], other[4 * i + 1], other[4 * i + 2], other[4 * i + 3]);
       tc_fence_before();
-      named_bar(3 + 2 * sub + (qw & 1), 64);         // the two partners
       if (lane == 0) mbar_arrive(&S.sfree[buf]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(take + 4 * (i ^ swz));
-        d[2 * i] = add2(pair_of(__uint_as_float(own[4 * i]), __uint_as_float(own[4 * i + 1])), pair_of(v.x, v.y));
-        d[2 * i + 1] =
-            add2(pair_of(__uint_as_float(own[4 * i + 2]), __uint_as_float(own[4 * i + 3])), pair_of(v.z, v.w));
-      }
-    }
-    float over = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      d[i] = fma2(d[i], cs[i], es[i]);
-      const float2 u = both(d[i]);
-      over = fmaxf(over, fmaxf(u.x, u.y));
+        for (int k = 0; k < 2; ++k) {
+          d[k][i] = fma2(pair_of(__uint_as_float(r[4 * i + 2 * k]), __uint_as_float(r[4 * i + 2 * k + 1])),
+                         cs[k][i], es[k][i]);
+          const float2 u = both(d[k][i]);
+          over = fmaxf(over, fmaxf(u.x, u.y));
+        }
+      }
     }
     // until something was seen, any position sets the references
     const bool rises = over > (seen ? kSlack + kShift : -INFINITY);
-    // the products of the units before are done: P and O^T may change
-    if (ok && n > 0 && !wait(&S.pvdone, (n - 1) & 1)) ok = false;
-    tc_fence_after();
+    // the weights of the unit before last have been used
+    if (ok && !wait(&S.empty[buf][1], parity ^ 1)) ok = false;
     if (named_bar_any(bar, 128, rises)) {
       // move references to the maxima so far: each head decides for itself, a
       // non-finite one keeps its reference
-      const float top = across(d, lane, [](float p, float q) { return fmaxf(p, q); });
-      part[qw * 16 + (lane >> 1)] = top;
+      f32x2 t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = both(d[0][i]), v = both(d[1][i]);
+        t[i] = pair_of(fmaxf(u.x, v.x), fmaxf(u.y, v.y));
+      }
+      part[qw * 32 + head_of(lane)] = across(t, lane, [](float p, float q) { return fmaxf(p, q); });
       named_bar(bar, 128);
-      const int at = (lane >> 4) * 32 + (lane & 15);
-      float up = fmaxf(part[at], part[at + 16]) - kShift;
+      float up = fmaxf(fmaxf(part[lane], part[32 + lane]), fmaxf(part[64 + lane], part[96 + lane])) - kShift;
       if ((seen && !(up > kSlack)) || !(fabsf(up) < INFINITY)) up = 0.0f;
       if (qw == 0) {
         S.m[32 * sub + lane] += up;
@@ -909,11 +905,15 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       }
       named_bar(bar, 128);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        d[i] = sub2(d[i], de2[i]);
-        l[i] = mul2(l[i], al2[i]);
+      for (int i = 0; i < 4; ++i) {
+        d[0][i] = sub2(d[0][i], de2[4 * i]);
+        d[1][i] = sub2(d[1][i], de2[4 * i]);
+        l[i] = mul2(l[i], al2[4 * i]);
       }
       if (seen) {
+        // the products of the units before are done
+        if (ok && !wait(&S.empty[buf ^ 1][1], ((n - 1) >> 1) & 1)) ok = false;
+        tc_fence_after();
         // 16 heads at a time, those whose reference moved
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {
@@ -935,16 +935,14 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       seen = true;
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t h[4];
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 v = both(d[4 * i + k]);
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = both(d[k][i]);
         const float px = ex2(v.x), py = ex2(v.y);
-        d[4 * i + k] = pair_of(px, py);
-        h[k] = pack_half2(px, py);
+        d[k][i] = pair_of(px, py);
+        st_shared((p_at ^ (i << 4)) + buf * (kPos * 128) + k * 1024, pack_half2(px, py));
       }
-      *reinterpret_cast<uint4*>(&S.p[sw(pos, h0 / 8 + i)]) = make_uint4(h[0], h[1], h[2], h[3]);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -953,19 +951,17 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       mbar_arrive(&S.pready);
       mbar_arrive(&S.rowfree[slot]);
     }
-    const f32x2 is2 = pair_of(inv_s, inv_s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l[i] = fma2(d[i], is2, l[i]);
+    for (int i = 0; i < 4; ++i) l[i] = fma2(d[1][i], inv2[1], fma2(d[0][i], inv2[0], l[i]));
     if (!w.last()) continue;
 
     // ---- the row tile's end in this CTA: totals, then the output
-    const float sum = across(l, lane, [](float p, float q) { return p + q; });
-    part[qw * 16 + (lane >> 1)] = sum;
+    part[qw * 32 + head_of(lane)] = across(l, lane, [](float p, float q) { return p + q; });
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l[i] = pair_of(0.0f, 0.0f);
+    for (int i = 0; i < 4; ++i) l[i] = pair_of(0.0f, 0.0f);
     named_bar(bar, 128);
-    const int at = (lane >> 4) * 32 + (lane & 15);    // lane: head 32 sub + lane
-    const float total = part[at] + part[at + 16];
+    // lane: head 32 sub + lane
+    const float total = (part[lane] + part[32 + lane]) + (part[64 + lane] + part[96 + lane]);
     const float lse2 = total == 0.0f ? -INFINITY : S.m[32 * sub + lane] - kShift + log2f(total);
     named_bar(bar, 128);
     if (qw == 0) {
@@ -973,7 +969,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       S.m[32 * sub + lane] = 0.0f;
     }
     named_bar(bar, 128);
-    if (ok && !wait(&S.pvdone, n & 1)) ok = false;
+    if (ok && !wait(&S.empty[buf][1], parity)) ok = false;
     tc_fence_after();
     const int32_t h = w.g * kHT + 32 * sub;           // first head of this sub
     const int32_t nh = ok ? min(32, a.H - h) : 0;     // heads to write
@@ -986,9 +982,9 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     } else {
       // a row tile that began in an earlier CTA goes to slot 0, one that goes
       // on in the next to slot 1
-      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.began_here() ? 1 : 0);
-      if (qw == 0) a.piece_lse[slot * kHT + 32 * sub + lane] = lse2;
-      output<false>(S, oe, 32 * sub, 32 * qw + lane, 32, a.piece + slot * kPieceRow + (32 * sub) * kD,
+      const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (w.began_here() ? 1 : 0);
+      if (qw == 0) a.piece_lse[piece * kHT + 32 * sub + lane] = lse2;
+      output<false>(S, oe, 32 * sub, 32 * qw + lane, 32, a.piece + piece * kPieceRow + (32 * sub) * kD,
                     static_cast<int64_t>(kD));
     }
     named_bar(bar, 128);                              // the factors are read
@@ -1021,7 +1017,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
     mbar_init(&S.qfull, kLoadWarps);
     mbar_init(&S.qempty, 1 + kSoftWarps);
     mbar_init(&S.pready, kSoftWarps);
-    mbar_init(&S.pvdone, 1);
     mbar_init(&S.done, 2);
     fence_mbar_init();
   }
