@@ -379,7 +379,7 @@ qli_status qli_read_kv(const uint8_t *cache, int64_t num_pages, int64_t page_str
  * A block-table entry outside the pool skips its positions and is flagged.
  * Rows no token attends to may hold anything. Scales must not be negative.
  * The codes are multiplied as they are on the tensor cores (FP16, exact), q as
- * FP16 times a power of two per head (exact unless a value is below 2^-24 of
+ * FP16 times a power of two per head (exact unless a value is below 2^-30 of
  * the head's largest), sums are FP32, and the weights times the row scales are
  * rounded to FP16: out agrees with the definition to about 2^-11 of the largest
  * value attended to, besides its own rounding. */
@@ -411,8 +411,8 @@ typedef struct qli_kv_attn_args {
     uint32_t *err_word;          /* device word or NULL: QLI_DEVERR_* bits are OR'ed in */
 } qli_kv_attn_args;
 
-/* Bytes of device workspace qli_kv_attention needs (from T, H and the device's
- * SM count; no device memory is read). */
+/* Bytes of device workspace qli_kv_attention needs (from the device's SM count
+ * alone; no device memory is read). */
 qli_status qli_kv_attention_workspace_size(const qli_kv_attn_args *a, size_t *bytes);
 
 /* Queues the attention on `stream`. `workspace`: 256-byte aligned device memory
