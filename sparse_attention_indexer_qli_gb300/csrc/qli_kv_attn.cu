@@ -94,8 +94,9 @@ struct Smem {
   float part[2][4][32];                        // [32 heads][softmax warp of them][head]
   int32_t warp_sum[kThreads / 32];
   int32_t count, start_t, start_g, start_i;    // the CTA's share: units, first token, row tile, unit
-  // tiles by unit parity and half of the values
-  uint64_t full[2][2], empty[2][2], sfull[2], sfree[2], rowfull[kSlots], rowfree[kSlots], qfull, qempty, pready, done;
+  // tiles by unit parity and half of the values. What the softmax warps arrive
+  // on is by unit parity too: four of them may be a unit ahead of the others.
+  uint64_t full[2][2], empty[2][2], sfull[2], sfree[2], rowfull[kSlots], rowfree[kSlots], qfull, qempty, pready[2], done;
   uint32_t tmem_base;
 };
 constexpr int kSmemBytes = static_cast<int>(sizeof(Smem)) + 1024;
@@ -813,7 +814,7 @@ __device__ __forceinline__ bool run_values(const Args& a, Smem& S, uint32_t tmem
   for (Walk w(a, S); ok && w.valid(); w.next(a, S), ++n) {
     const uint32_t more = w.first() ? 0u : 1u, tile = v_lo + (n & 1) * (kTile >> 4);
     const uint32_t pe = p_lo + (n & 1) * (kPos * 128 >> 4);
-    ok = wait(&S.pready, n & 1);
+    ok = wait(&S.pready[n & 1], (n >> 1) & 1);
     tc_fence_after();
     if (ok && elect_one()) {
 #pragma unroll
@@ -1036,7 +1037,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&S.pready);
+      mbar_arrive(&S.pready[buf]);
       mbar_arrive(&S.rowfree[slot]);
     }
 #pragma unroll
@@ -1098,6 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
       }
       mbar_init(&S.sfull[i], 1);
       mbar_init(&S.sfree[i], kSoftWarps);
+      mbar_init(&S.pready[i], kSoftWarps);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&S.rowfull[i], kRowWarps);
@@ -1105,7 +1107,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
     }
     mbar_init(&S.qfull, kLoadWarps);
     mbar_init(&S.qempty, 1 + kSoftWarps);
-    mbar_init(&S.pready, kSoftWarps);
     mbar_init(&S.done, 2);
     fence_mbar_init();
   }
