@@ -33,16 +33,21 @@
 // TMEM: two S buffers of 64 columns, four O^T quarters of 64. Shared memory:
 // two FP16 tiles (128 KB), the queries (64 KB), two buffers of weights (16 KB).
 //
-// What bounds it. The tensor core needs 1.98k cycles a unit (32 score products of
-// 36 cycles, 16 value products of 52); in a long run a unit takes 3.1k, the chain
-// of the codes' arrival, their widening and storing (64 KB of FP16 out of 32 KB of
-// codes, eight warps), and the hand-over of the two tiles. Around a CTA's units
-// lie about 8k cycles up to its first rows (planning, dependent lookups, cold
-// instructions) and 4.1k for each output or piece. Measured on one GB300: 1021
-// tokens over some 8K positions each, 64 heads, INT8: 1.33 ms, 0.76 PFLOP/s; 12
-// tokens over 64K positions, E4M3: 148 us, 2.6 TB/s and 0.67 PFLOP/s; 64 tokens
-// over 2048 listed positions, E4M3: 49 us, 1.4 TB/s; one token over 512 listed
-// positions: 17 us, nearly all of it fixed cost.
+// What bounds it. In a long run a unit takes about 3.1k cycles, of which the path
+// between shared memory, L1 and the rest, 128 bytes a clock, is taken up in nearly
+// all: the products read 224 KB (1792 cycles; alone they take 1984, 32 score
+// products of 36 and 16 value products of 52), the tile's stores and the codes'
+// loads are 96 KB (768), the rest lookups, weights and barriers. Copies of the
+// kernel without half of the stores are 0.22k cycles a unit faster, without the
+// loads 0.24k, with half the score products 0.26k, without the exponentials 0.03k;
+// loads issued a half earlier, conversion before the wait and weights stored before
+// the vote changed nothing or lost. Around a CTA's units lie 7k cycles up to its
+// first rows (planning, dependent lookups, cold instructions), and 4.1k for each
+// output or piece of 64 heads. Measured on one GB300: 1021 tokens over some 8K
+// positions each, 64 heads, INT8: 1.34 ms, 0.75 PFLOP/s; 12 tokens over 64K
+// positions, E4M3: 150 us, 2.6 TB/s and 0.67 PFLOP/s; 64 tokens over 2048 listed
+// positions, E4M3: 49 us, 1.5 TB/s; one token over 512 listed positions: 15 us,
+// nearly all of it fixed cost.
 // 64 positions a unit: with 128 a tile's 128 KB leave room for one only, and
 // conversion, products and softmax take turns (the first case 2.01 ms against
 // 1.85 when the two were compared).
