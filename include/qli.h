@@ -417,7 +417,8 @@ qli_status qli_kv_attention_workspace_size(const qli_kv_attn_args *a, size_t *by
 
 /* Queues the attention on `stream`. `workspace`: 256-byte aligned device memory
  * of at least that size, contents irrelevant on entry, the caller's until the
- * queued work is done; calls that share one run in order on one stream.
+ * queued work is done. A call queues several kernels: calls that share one run
+ * on one stream, and one host thread after the other queues them.
  * Allocates nothing, never synchronises; nothing is launched on a non-OK
  * status. The result does not depend on timing: the same call gives the same
  * bits. */

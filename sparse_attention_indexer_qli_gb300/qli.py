@@ -10,6 +10,7 @@ import ctypes
 import functools
 import os
 import struct
+import threading
 from ctypes import c_int32, c_int64, c_size_t, c_uint32, c_void_p
 from typing import Optional
 
@@ -552,16 +553,31 @@ def kv_attention_workspace_bytes(T: int, H: int, device=None) -> int:
     return _workspace_bytes(T > 0 and H > 0, device)
 
 
-@functools.lru_cache(maxsize=None)
+class _Kept(threading.local):
+    """Each host thread's workspaces, by device index."""
+
+    def __init__(self):
+        self.workspace = {}
+
+
+_kept = _Kept()
+
+
 def _default_stream_workspace(device: int):
-    """The workspace of the calls on `device`'s default stream that give none
-    (about 40 MB): one for all, since that stream runs them in order, is never
-    destroyed and cannot be captured into a graph. Allocating one for each call
-    took 7 of the 20 us that a small call takes the host."""
-    import torch
-    with torch.cuda.stream(torch.cuda.default_stream(device)):
-        return torch.empty(_workspace_bytes(True, device), dtype=torch.uint8,
-                           device=torch.device("cuda", device))
+    """This thread's workspace for its calls on `device`'s default stream that
+    give none (about 40 MB). That stream runs a thread's calls in order, is never
+    destroyed and cannot be captured into a graph. A call is several kernels,
+    though, and those of two threads' calls may be queued interleaved, so no two
+    threads share one. Allocating one for each call took 7 of the 20 us that a
+    small call takes the host."""
+    workspace = _kept.workspace.get(device)
+    if workspace is None:
+        import torch
+        with torch.cuda.stream(torch.cuda.default_stream(device)):
+            workspace = torch.empty(_workspace_bytes(True, device), dtype=torch.uint8,
+                                    device=torch.device("cuda", device))
+        _kept.workspace[device] = workspace
+    return workspace
 
 
 def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, page_stride: int,
@@ -573,8 +589,10 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
     positions of indices [T, 1, K] (int32, -1 skipped), or without indices over
     the positions k_lens, residual and ratio make visible to each token (the
     last `window` of them if window > 0). workspace: a 256-byte aligned uint8
-    tensor of at least kv_attention_workspace_bytes(T, H) bytes, allocated when
-    not given (on the default stream once per device). Returns (out [T, H, 512] BF16, lse [T, H] float32)."""
+    tensor of at least kv_attention_workspace_bytes(T, H) bytes, which no call of
+    another host thread or stream uses meanwhile; allocated when not given (on the
+    default stream once per host thread and device). Returns (out [T, H, 512]
+    BF16, lse [T, H] float32)."""
     import torch
     _check_cuda("q", q, torch.bfloat16)
     int32 = torch.int32

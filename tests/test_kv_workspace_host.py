@@ -1,0 +1,44 @@
+"""Who shares the workspace that kv_attention keeps for the default stream: one
+call is several kernels, so two host threads that queue calls on that stream side
+by side may queue them interleaved, and must not write to one block."""
+import threading
+
+from fake_cuda import DEVICE, attention_inputs, fake  # noqa: F401
+from sparse_attention_indexer_qli_gb300 import qli
+
+
+def _in_threads(n, f):
+    """f(i) in n threads that are all alive until the last has run."""
+    out, all_ran = [None] * n, threading.Barrier(n)
+
+    def body(i):
+        out[i] = f(i)
+        all_ran.wait(10)
+
+    threads = [threading.Thread(target=body, args=(i,)) for i in range(n)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return out
+
+
+def test_host_threads_do_not_share_a_workspace(fake):  # noqa: F811
+    def calls(i):
+        for _ in range(3):
+            qli.kv_attention(**attention_inputs(T=1 + i))
+
+    _in_threads(3, calls)
+    used = {}
+    for name, (a, workspace, n, stream) in fake.lib.calls:
+        assert name == "kv_attention" and stream == 0 and n >= 4096
+        used.setdefault(a.T, set()).add(workspace)
+    # a thread keeps its own, and no other has it
+    assert sorted(used) == [1, 2, 3] and all(len(w) == 1 for w in used.values())
+    assert len(set.union(*used.values())) == 3
+
+
+def test_a_thread_keeps_one_per_device(fake):  # noqa: F811
+    kept = _in_threads(1, lambda i: [qli._default_stream_workspace(d) for d in (DEVICE, DEVICE + 1, DEVICE)])[0]
+    assert kept[0] is kept[2] and kept[0] is not kept[1]
+    assert all(stream is fake.default for stream, _ in fake.made)
