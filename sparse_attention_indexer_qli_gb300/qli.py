@@ -340,6 +340,22 @@ def _stream(stream, device=None) -> Optional[int]:
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream, result=True):
+    """torch.empty for a kernel on `stream` (None: the current one), out of that
+    stream's memory: a block of the current stream's may still be in use by work
+    pending there. A result may be used and dropped on the current stream, once
+    that has waited for `stream`."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result and here.cuda_stream != stream.cuda_stream:
+        t.record_stream(here)
+    return t
+
+
 def run(*args, workspace=None, stream=None, **kw):
     """One indexer call. Returns (indices [T,1,K] int32, candidates [T,1,C] int32 or None)."""
     c = Call(*args, **kw)
@@ -499,7 +515,7 @@ def read_kv(cache, slots, *, rows_per_page: int, page_stride: int, kv_offset: in
         raise ValueError("cache and slots must be contiguous")
     n = slots.numel()
     if out is None:
-        out = torch.empty((n, 512), dtype=torch.bfloat16, device=cache.device)
+        out = _empty((n, 512), torch.bfloat16, cache.device, stream)
     else:
         _check_cuda("out", out, torch.bfloat16)
         if out.shape != (n, 512) or out.stride(1) != 1:
@@ -512,18 +528,18 @@ def read_kv(cache, slots, *, rows_per_page: int, page_stride: int, kv_offset: in
     return out
 
 
-def _attn_outputs(q_shape, device, out, lse):
-    """Output tensors of an attention over q [T, H, 512], made or checked."""
+def _attn_outputs(q_shape, device, out, lse, stream):
+    """Output tensors of an attention over q [T, H, 512] on `stream`, made or checked."""
     import torch
     T, H, D = q_shape
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=device)
+        out = _empty((T, H, D), torch.bfloat16, device, stream)
     else:
         _check_cuda("out", out, torch.bfloat16)
         if out.shape != q_shape or out.stride(2) != 1:
             raise ValueError("out must be [T, H, 512] with unit stride in the last dim")
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=device)
+        lse = _empty((T, H), torch.float32, device, stream)
     else:
         _check_cuda("lse", lse, torch.float32)
         if lse.shape != (T, H) or not lse.is_contiguous():
@@ -634,7 +650,7 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
         _check_cuda("err_word", err_word, int32)
         err = err_word.data_ptr()
     device = q.device
-    out, lse = _attn_outputs(shape, device, out, lse)
+    out, lse = _attn_outputs(shape, device, out, lse, stream)
     q_t, q_h, _ = q.stride()
     o_t, o_h, _ = out.stride()
     a = _pack_kv_attn(q.data_ptr(), q_t, q_h, T, H, D, cu_seqlens_q.data_ptr(), B,
@@ -648,10 +664,8 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
     elif raw == 0:
         workspace = _default_stream_workspace(device.index)
     else:
-        workspace = torch.empty(max(256, _workspace_bytes(T > 0 and H > 0, device.index)),
-                                dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _empty(max(256, _workspace_bytes(T > 0 and H > 0, device.index)), torch.uint8,
+                           device, stream, result=False)
     _check((_lib or lib()).qli_kv_attention(a, workspace.data_ptr(), workspace.numel(), raw),
            "qli_kv_attention")
     return out, lse
@@ -682,7 +696,7 @@ def merge_attention(outs, lses, *, out=None, lse=None, stream=None):
             raise ValueError("lses must be contiguous [T, H] tensors")
         ptrs[i], lptrs[i] = o.data_ptr(), l.data_ptr()
         st[i], sh[i], _ = o.stride()
-    out, lse = _attn_outputs(shape, outs[0].device, out, lse)
+    out, lse = _attn_outputs(shape, outs[0].device, out, lse, stream)
     o_t, o_h, _ = out.stride()
     T, H, D = shape
     a = _pack_merge(*ptrs, *st, *sh, *lptrs, n, int(dtype == torch.float32), T, H, D,
