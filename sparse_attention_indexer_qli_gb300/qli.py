@@ -358,8 +358,18 @@ def _empty(shape, dtype, device, stream, result=True):
 
 def run(*args, workspace=None, stream=None, **kw):
     """One indexer call. Returns (indices [T,1,K] int32, candidates [T,1,C] int32 or None)."""
-    c = Call(*args, **kw)
-    ws = c.alloc_workspace() if workspace is None else workspace
+    import torch
+    if stream is None:
+        c = Call(*args, **kw)
+        return c.run(c.alloc_workspace() if workspace is None else workspace)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):                   # memory for `stream`: see _empty
+        c = Call(*args, **kw)
+        ws = c.alloc_workspace() if workspace is None else workspace
+    if here.cuda_stream != stream.cuda_stream:
+        for name, t in (("indices_out", c.indices), ("cand_out", c.cand)):
+            if t is not None and kw.get(name) is None:
+                t.record_stream(here)
     return c.run(ws, stream)
 
 
@@ -375,9 +385,9 @@ def quantize_q(x, q_out=None, scale_out=None, stream=None, quant_mode=QUANT_INT8
         raise TypeError("x must hold 16-bit BF16 patterns with 128 values per row")
     rows = x.numel() // 128
     if q_out is None:
-        q_out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        q_out = _empty(x.shape, torch.int8, x.device, stream)
     if scale_out is None:
-        scale_out = torch.empty(x.shape[:-1], dtype=torch.int16, device=x.device)
+        scale_out = _empty(x.shape[:-1], torch.int16, x.device, stream)
     _require_cuda("q_out", q_out, torch.int8)
     name = "qli_quantize_q_fp8" if quant_mode == QUANT_FP8 else "qli_quantize_q"
     _check(getattr(lib(), name)(_ptr(x), rows, _ptr(q_out), _ptr(scale_out), _stream(stream)),
@@ -390,8 +400,11 @@ def check_quant_rounding(stream=None):
     the quantisers' division against IEEE FP32 division over every BF16 x and
     every positive finite FP16 scale."""
     import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):               # made and read there too
+            return check_quant_rounding()
     counts = torch.empty(2, dtype=torch.int64, device="cuda")
-    _check(lib().qli_check_quant_rounding(_ptr(counts), _stream(stream)),
+    _check(lib().qli_check_quant_rounding(_ptr(counts), _stream(None)),
            "qli_check_quant_rounding")
     return tuple(int(v) for v in counts.cpu())
 
@@ -441,9 +454,9 @@ def sparse_attention(q, cu_seqlens_q, cache, block_table, indices, *, rows_per_p
         raise ValueError("block_table must be [B, bt_stride] row-major")
     T, H, D = q.shape
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, H, D), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = _empty((T, H), torch.float32, q.device, stream)
     _require_cuda("out", out, torch.bfloat16)
     _require_cuda("lse", lse, torch.float32)
     if out.stride(2) != 1 or not lse.is_contiguous():

@@ -75,6 +75,22 @@ class FakeLib:
     def qli_read_kv(self, *args):
         return self._note("read_kv", *args)
 
+    def qli_workspace_size(self, a, n):
+        n._obj.value = 4096
+        return 0
+
+    def qli_run(self, a, workspace, n, stream):
+        return self._note("run", workspace, n, stream)
+
+    def qli_sparse_attention(self, a, stream):
+        return self._note("sparse_attention", stream)
+
+    def qli_quantize_q(self, *args):
+        return self._note("quantize_q", *args)
+
+    def qli_check_quant_rounding(self, counts, stream):
+        return self._note("check_quant_rounding", counts, stream)
+
     def qli_status_string(self, status):
         return b"status %d" % status
 
