@@ -476,16 +476,32 @@ def sparse_attention(q, cu_seqlens_q, cache, block_table, indices, *, rows_per_p
 
 
 
-def _check_cuda(name, t, dtype):
-    """_require_cuda for a tensor that has to be there, the good case first."""
+def _first_cuda(name, t, dtype) -> int:
+    """Checks a call's first tensor and returns the index of its device, which has
+    to be the current one: that is where the library launches."""
+    import torch
+    if t is None:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    _require_cuda(name, t, dtype)
+    device, current = t.get_device(), torch.cuda.current_device()
+    if device != current:
+        raise ValueError("%s is on CUDA device %d, the current device is %d" % (name, device, current))
+    return device
+
+
+def _check_cuda(name, t, dtype, device):
+    """_require_cuda for a tensor that has to be there, on the call's device, the
+    good case first."""
     try:
-        if t.is_cuda and t.dtype is dtype:
+        if t.get_device() == device and t.dtype is dtype:
             return
     except AttributeError:
         pass
     if t is None:
         raise TypeError("%s must be a CUDA tensor" % name)
     _require_cuda(name, t, dtype)
+    raise ValueError("%s is on CUDA device %d, the call's other tensors on device %d"
+                     % (name, t.get_device(), device))
 
 
 def write_kv(kv, slot_mapping, cache, *, rows_per_page: int, page_stride: int, kv_offset: int,
@@ -496,11 +512,11 @@ def write_kv(kv, slot_mapping, cache, *, rows_per_page: int, page_stride: int, k
     CUDA) at slot_mapping [n] (int64: page * rows_per_page + row; negative =
     skip)."""
     import torch
-    _check_cuda("kv", kv, torch.bfloat16)
-    _check_cuda("slot_mapping", slot_mapping, torch.int64)
-    _check_cuda("cache", cache, torch.uint8)
+    device = _first_cuda("kv", kv, torch.bfloat16)
+    _check_cuda("slot_mapping", slot_mapping, torch.int64, device)
+    _check_cuda("cache", cache, torch.uint8, device)
     if err_word is not None:
-        _check_cuda("err_word", err_word, torch.int32)
+        _check_cuda("err_word", err_word, torch.int32, device)
     if kv.dim() != 2 or kv.shape[1] != 512 or kv.stride(1) != 1:
         raise ValueError("kv must be [n, 512] with unit stride in the last dim")
     if not cache.is_contiguous() or not slot_mapping.is_contiguous():
@@ -511,7 +527,7 @@ def write_kv(kv, slot_mapping, cache, *, rows_per_page: int, page_stride: int, k
     _check((_lib or lib()).qli_write_kv(
         kv.data_ptr(), kv.stride(0) if n > 1 else 512, n, slot_mapping.data_ptr(),
         cache.data_ptr(), cache.numel() // page_stride, page_stride, rows_per_page, kv_offset,
-        kv_scale_offset, quant_mode, _ptr(err_word), _stream(stream, cache.get_device())),
+        kv_scale_offset, quant_mode, _ptr(err_word), _stream(stream, device)),
         "qli_write_kv")
 
 
@@ -520,41 +536,42 @@ def read_kv(cache, slots, *, rows_per_page: int, page_stride: int, kv_offset: in
     """qli_read_kv: the rows named by slots [n] (int64: page * rows_per_page +
     row; negative = zeros) of the page pool `cache` as BF16 [n, 512]."""
     import torch
-    _check_cuda("cache", cache, torch.uint8)
-    _check_cuda("slots", slots, torch.int64)
+    device = _first_cuda("cache", cache, torch.uint8)
+    _check_cuda("slots", slots, torch.int64, device)
     if err_word is not None:
-        _check_cuda("err_word", err_word, torch.int32)
+        _check_cuda("err_word", err_word, torch.int32, device)
     if not cache.is_contiguous() or not slots.is_contiguous():
         raise ValueError("cache and slots must be contiguous")
     n = slots.numel()
     if out is None:
         out = _empty((n, 512), torch.bfloat16, cache.device, stream)
     else:
-        _check_cuda("out", out, torch.bfloat16)
+        _check_cuda("out", out, torch.bfloat16, device)
         if out.shape != (n, 512) or out.stride(1) != 1:
             raise ValueError("out must be [n, 512] with unit stride in the last dim")
     _check((_lib or lib()).qli_read_kv(
         cache.data_ptr(), cache.numel() // page_stride, page_stride, rows_per_page, kv_offset,
         kv_scale_offset, quant_mode, slots.data_ptr(), n, out.data_ptr(),
-        out.stride(0) if n > 1 else 512, _ptr(err_word), _stream(stream, cache.get_device())),
+        out.stride(0) if n > 1 else 512, _ptr(err_word), _stream(stream, device)),
         "qli_read_kv")
     return out
 
 
 def _attn_outputs(q_shape, device, out, lse, stream):
-    """Output tensors of an attention over q [T, H, 512] on `stream`, made or checked."""
+    """Output tensors of an attention over q [T, H, 512] on the device of that index
+    and on `stream`, made or checked."""
     import torch
     T, H, D = q_shape
     if out is None:
-        out = _empty((T, H, D), torch.bfloat16, device, stream)
+        out = _empty((T, H, D), torch.bfloat16, torch.device("cuda", device), stream)
     else:
-        _check_cuda("out", out, torch.bfloat16)
+        _check_cuda("out", out, torch.bfloat16, device)
         if out.shape != q_shape or out.stride(2) != 1:
             raise ValueError("out must be [T, H, 512] with unit stride in the last dim")
     if lse is None:
-        lse = _empty((T, H), torch.float32, device, stream)
+        lse = _empty((T, H), torch.float32, torch.device("cuda", device), stream)
     else:
-        _check_cuda("lse", lse, torch.float32)
+        _check_cuda("lse", lse, torch.float32, device)
         if lse.shape != (T, H) or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous [T, H] tensor")
     return out, lse
@@ -578,8 +595,10 @@ def kv_attention_workspace_bytes(T: int, H: int, device=None) -> int:
     """Bytes of device workspace kv_attention needs for T tokens of H heads on
     `device` (default: the current one)."""
     import torch
-    device = torch.cuda.current_device() if device is None else torch.device(device).index
-    return _workspace_bytes(T > 0 and H > 0, device)
+    index = None if device is None else torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    return _workspace_bytes(T > 0 and H > 0, index)
 
 
 class _Kept(threading.local):
@@ -623,11 +642,11 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
     default stream once per host thread and device). Returns (out [T, H, 512]
     BF16, lse [T, H] float32)."""
     import torch
-    _check_cuda("q", q, torch.bfloat16)
+    device = _first_cuda("q", q, torch.bfloat16)
     int32 = torch.int32
-    _check_cuda("cu_seqlens_q", cu_seqlens_q, int32)
-    _check_cuda("block_table", block_table, int32)
-    _check_cuda("cache", cache, torch.uint8)
+    _check_cuda("cu_seqlens_q", cu_seqlens_q, int32, device)
+    _check_cuda("block_table", block_table, int32, device)
+    _check_cuda("cache", cache, torch.uint8, device)
     if q.dim() != 3 or q.stride(2) != 1:
         raise ValueError("q must be [T, H, 512] with unit stride in the last dim")
     if not cache.is_contiguous() or not cu_seqlens_q.is_contiguous():
@@ -641,7 +660,7 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
         raise ValueError("block_table needs a row per request")
     K, idx = 0, 0
     if indices is not None:
-        _check_cuda("indices", indices, int32)
+        _check_cuda("indices", indices, int32, device)
         if indices.dim() != 3 or indices.shape[0] != T or indices.shape[1] != 1 \
                 or not indices.is_contiguous():
             raise ValueError("indices must be a contiguous [T, 1, K] tensor")
@@ -650,19 +669,18 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
         raise ValueError("either indices or k_lens must be given")
     lens, res, err = 0, 0, 0
     if k_lens is not None:
-        _check_cuda("k_lens", k_lens, int32)
+        _check_cuda("k_lens", k_lens, int32, device)
         if k_lens.numel() != B or not k_lens.is_contiguous():
             raise ValueError("k_lens must be a contiguous [B] tensor")
         lens = k_lens.data_ptr()
     if residual is not None:
-        _check_cuda("residual", residual, int32)
+        _check_cuda("residual", residual, int32, device)
         if residual.numel() != B or not residual.is_contiguous():
             raise ValueError("residual must be a contiguous [B] tensor")
         res = residual.data_ptr()
     if err_word is not None:
-        _check_cuda("err_word", err_word, int32)
+        _check_cuda("err_word", err_word, int32, device)
         err = err_word.data_ptr()
-    device = q.device
     out, lse = _attn_outputs(shape, device, out, lse, stream)
     q_t, q_h, _ = q.stride()
     o_t, o_h, _ = out.stride()
@@ -671,14 +689,14 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
                       quant_mode, kv_offset, kv_scale_offset, block_table.data_ptr(),
                       block_table.stride(0), K, idx, lens, res, ratio, window, scale,
                       out.data_ptr(), o_t, o_h, lse.data_ptr(), err)
-    raw = _stream(stream, device.index)
+    raw = _stream(stream, device)
     if workspace is not None:
-        _check_cuda("workspace", workspace, torch.uint8)
+        _check_cuda("workspace", workspace, torch.uint8, device)
     elif raw == 0:
-        workspace = _default_stream_workspace(device.index)
+        workspace = _default_stream_workspace(device)
     else:
-        workspace = _empty(max(256, _workspace_bytes(T > 0 and H > 0, device.index)), torch.uint8,
-                           device, stream, result=False)
+        workspace = _empty(max(256, _workspace_bytes(T > 0 and H > 0, device)), torch.uint8,
+                           q.device, stream, result=False)
     _check((_lib or lib()).qli_kv_attention(a, workspace.data_ptr(), workspace.numel(), raw),
            "qli_kv_attention")
     return out, lse
@@ -699,21 +717,22 @@ def merge_attention(outs, lses, *, out=None, lse=None, stream=None):
     if len(shape) != 3:
         raise ValueError("outs must be [T, H, 512]")
     ptrs, st, sh, lptrs = [0] * MERGE_MAX, [0] * MERGE_MAX, [0] * MERGE_MAX, [0] * MERGE_MAX
+    device = _first_cuda("outs", outs[0], dtype)
     for i in range(n):
         o, l = outs[i], lses[i]
-        _check_cuda("outs", o, dtype)
-        _check_cuda("lses", l, torch.float32)
+        _check_cuda("outs", o, dtype, device)
+        _check_cuda("lses", l, torch.float32, device)
         if o.shape != shape or o.stride(2) != 1:
             raise ValueError("outs must share one [T, H, 512] shape with unit stride in the last dim")
         if l.shape != shape[:2] or not l.is_contiguous():
             raise ValueError("lses must be contiguous [T, H] tensors")
         ptrs[i], lptrs[i] = o.data_ptr(), l.data_ptr()
         st[i], sh[i], _ = o.stride()
-    out, lse = _attn_outputs(shape, outs[0].device, out, lse, stream)
+    out, lse = _attn_outputs(shape, device, out, lse, stream)
     o_t, o_h, _ = out.stride()
     T, H, D = shape
     a = _pack_merge(*ptrs, *st, *sh, *lptrs, n, int(dtype == torch.float32), T, H, D,
                     out.data_ptr(), o_t, o_h, lse.data_ptr())
-    _check((_lib or lib()).qli_merge_attention(a, _stream(stream, out.get_device())),
+    _check((_lib or lib()).qli_merge_attention(a, _stream(stream, device)),
            "qli_merge_attention")
     return out, lse
