@@ -390,13 +390,15 @@ typedef struct qli_kv_attn_args {
     int32_t T, H, D;             /* tokens, heads (1..128), values per row (512) */
     const int32_t *cu_seqlens_q; /* [B+1] raw query boundaries */
     int32_t B;
+    int32_t bt_width;            /* page IDs of a block_table row that may be read; 0: bt_stride */
     const uint8_t *cache;        /* page pool; page p at cache + p * page_stride */
     int64_t page_stride, num_pages;
     int32_t rows_per_page;       /* 64 or 128 */
     int32_t quant_mode;          /* QLI_QUANT_INT8 or QLI_QUANT_FP8 */
     int64_t kv_offset;           /* bytes to row 0's codes (multiple of 16) */
     int64_t kv_scale_offset;     /* bytes to row 0's scale (multiple of 2) */
-    const int32_t *block_table;  /* [B, bt_stride] page IDs */
+    const int32_t *block_table;  /* page IDs: entry i of request b at block_table[b*bt_stride + i],
+                                    i < bt_width */
     int32_t bt_stride;
     int32_t K;                   /* entries per token (>= 1) when indices is given */
     const int32_t *indices;      /* [T, 1, K] positions, or NULL: every visible position */

@@ -115,7 +115,7 @@ struct Args {
   const int32_t* k_lens;
   const int32_t* residual;
   int32_t ratio, window;
-  int64_t cap;                 // bt_stride * R
+  int64_t cap;                 // positions a block-table row holds
   const uint8_t* cache;
   int64_t page_stride, num_pages, kv_off, sc_off;
   int32_t R, log2R;
@@ -1244,7 +1244,7 @@ qli_status validate(const qli_kv_attn_args* a) {
   if (a->q == nullptr || a->cu_seqlens_q == nullptr || a->cache == nullptr ||
       a->block_table == nullptr || a->out == nullptr)
     return QLI_ERR_INVALID_ARG;
-  if (a->bt_stride < 1 || a->num_pages < 1 || a->page_stride <= 0 || a->kv_offset < 0 ||
+  if (a->bt_stride < 1 || a->bt_width < 0 || a->num_pages < 1 || a->page_stride <= 0 || a->kv_offset < 0 ||
       a->kv_scale_offset < 0 ||
       a->kv_offset + static_cast<int64_t>(a->rows_per_page) * kD > a->page_stride ||
       a->kv_scale_offset + static_cast<int64_t>(a->rows_per_page) * 2 > a->page_stride)
@@ -1274,7 +1274,7 @@ Args make_args(const qli_kv_attn_args& a) {
   d.residual = a.residual;
   d.ratio = a.ratio;
   d.window = a.window;
-  d.cap = static_cast<int64_t>(a.bt_stride) * a.rows_per_page;
+  d.cap = static_cast<int64_t>(a.bt_width ? a.bt_width : a.bt_stride) * a.rows_per_page;
   d.cache = a.cache;
   d.page_stride = a.page_stride;
   d.num_pages = a.num_pages;

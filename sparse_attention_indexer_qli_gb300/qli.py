@@ -77,7 +77,7 @@ class KVAttnArgs(ctypes.Structure):
     _fields_ = [
         ("q", c_void_p), ("q_stride_t", c_int64), ("q_stride_h", c_int64),
         ("T", c_int32), ("H", c_int32), ("D", c_int32),
-        ("cu_seqlens_q", c_void_p), ("B", c_int32),
+        ("cu_seqlens_q", c_void_p), ("B", c_int32), ("bt_width", c_int32),
         ("cache", c_void_p), ("page_stride", c_int64), ("num_pages", c_int64),
         ("rows_per_page", c_int32), ("quant_mode", c_int32),
         ("kv_offset", c_int64), ("kv_scale_offset", c_int64),
@@ -582,7 +582,7 @@ def _workspace_bytes(some: bool, device: int) -> int:
     # the size depends on the device's SM count and on there being tokens; the
     # other arguments are only checked
     import torch
-    a = KVAttnArgs(256, 512, 512, int(some), 1, 512, 256, 1, 256, 128 * 514, 1, 128, QUANT_INT8, 0,
+    a = KVAttnArgs(256, 512, 512, int(some), 1, 512, 256, 1, 1, 256, 128 * 514, 1, 128, QUANT_INT8, 0,
                    128 * 512, 256, 1, 1, 256, None, None, 1, 0, 1.0, 256, 512, 512, None, None)
     n = c_size_t(0)
     with torch.cuda.device(device):
@@ -651,12 +651,19 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
         raise ValueError("q must be [T, H, 512] with unit stride in the last dim")
     if not cache.is_contiguous() or not cu_seqlens_q.is_contiguous():
         raise ValueError("cache and cu_seqlens_q must be contiguous")
-    if block_table.dim() != 2 or block_table.stride(1) != 1:
-        raise ValueError("block_table must be [B, bt_stride] row-major")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, pages of a request]")
+    rows, width = block_table.shape
+    # the strides of a dimension of size one may be any number
+    pitch, step = block_table.stride()
+    if step != 1 and width > 1:
+        raise ValueError("block_table must have unit stride in the last dim")
+    if rows == 1:
+        pitch = width
     shape = q.shape
     T, H, D = shape
     B = cu_seqlens_q.numel() - 1
-    if block_table.shape[0] < B:
+    if rows < B:
         raise ValueError("block_table needs a row per request")
     K, idx = 0, 0
     if indices is not None:
@@ -685,9 +692,9 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
     q_t, q_h, _ = q.stride()
     o_t, o_h, _ = out.stride()
     a = _pack_kv_attn(q.data_ptr(), q_t, q_h, T, H, D, cu_seqlens_q.data_ptr(), B,
-                      cache.data_ptr(), page_stride, cache.numel() // page_stride, rows_per_page,
+                      width, cache.data_ptr(), page_stride, cache.numel() // page_stride, rows_per_page,
                       quant_mode, kv_offset, kv_scale_offset, block_table.data_ptr(),
-                      block_table.stride(0), K, idx, lens, res, ratio, window, scale,
+                      pitch, K, idx, lens, res, ratio, window, scale,
                       out.data_ptr(), o_t, o_h, lse.data_ptr(), err)
     raw = _stream(stream, device)
     if workspace is not None:
