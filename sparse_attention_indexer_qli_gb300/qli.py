@@ -577,6 +577,13 @@ def _attn_outputs(q_shape, device, out, lse, stream):
     return out, lse
 
 
+def _strides(t, T, H, one):
+    """Strides of t [T, H, 512] along tokens and heads; `one` along a dimension of
+    size one, whose own may be any number."""
+    st, sh, _ = t.stride()
+    return st if T > 1 else one, sh if H > 1 else one
+
+
 @functools.lru_cache(maxsize=None)
 def _workspace_bytes(some: bool, device: int) -> int:
     # the size depends on the device's SM count and on there being tokens; the
@@ -689,8 +696,8 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
         _check_cuda("err_word", err_word, int32, device)
         err = err_word.data_ptr()
     out, lse = _attn_outputs(shape, device, out, lse, stream)
-    q_t, q_h, _ = q.stride()
-    o_t, o_h, _ = out.stride()
+    q_t, q_h = _strides(q, T, H, 512)
+    o_t, o_h = _strides(out, T, H, 512)
     a = _pack_kv_attn(q.data_ptr(), q_t, q_h, T, H, D, cu_seqlens_q.data_ptr(), B,
                       width, cache.data_ptr(), page_stride, cache.numel() // page_stride, rows_per_page,
                       quant_mode, kv_offset, kv_scale_offset, block_table.data_ptr(),
@@ -723,6 +730,7 @@ def merge_attention(outs, lses, *, out=None, lse=None, stream=None):
         raise TypeError("outs must be bfloat16 or float32")
     if len(shape) != 3:
         raise ValueError("outs must be [T, H, 512]")
+    T, H, D = shape
     ptrs, st, sh, lptrs = [0] * MERGE_MAX, [0] * MERGE_MAX, [0] * MERGE_MAX, [0] * MERGE_MAX
     device = _first_cuda("outs", outs[0], dtype)
     for i in range(n):
@@ -734,10 +742,9 @@ def merge_attention(outs, lses, *, out=None, lse=None, stream=None):
         if l.shape != shape[:2] or not l.is_contiguous():
             raise ValueError("lses must be contiguous [T, H] tensors")
         ptrs[i], lptrs[i] = o.data_ptr(), l.data_ptr()
-        st[i], sh[i], _ = o.stride()
+        st[i], sh[i] = _strides(o, T, H, 0)
     out, lse = _attn_outputs(shape, device, out, lse, stream)
-    o_t, o_h, _ = out.stride()
-    T, H, D = shape
+    o_t, o_h = _strides(out, T, H, 512)
     a = _pack_merge(*ptrs, *st, *sh, *lptrs, n, int(dtype == torch.float32), T, H, D,
                     out.data_ptr(), o_t, o_h, lse.data_ptr())
     _check((_lib or lib()).qli_merge_attention(a, _stream(stream, device)),
