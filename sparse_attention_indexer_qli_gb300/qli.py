@@ -706,6 +706,8 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
     raw = _stream(stream, device)
     if workspace is not None:
         _check_cuda("workspace", workspace, torch.uint8, device)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
     elif raw == 0:
         workspace = _default_stream_workspace(device)
     else:

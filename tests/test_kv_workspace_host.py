@@ -3,7 +3,10 @@ call is several kernels, so two host threads that queue calls on that stream sid
 by side may queue them interleaved, and must not write to one block."""
 import threading
 
-from fake_cuda import DEVICE, attention_inputs, fake  # noqa: F401
+import pytest
+import torch
+
+from fake_cuda import DEVICE, attention_inputs, fake, on_gpu  # noqa: F401
 from sparse_attention_indexer_qli_gb300 import qli
 
 
@@ -42,3 +45,13 @@ def test_a_thread_keeps_one_per_device(fake):  # noqa: F811
     kept = _in_threads(1, lambda i: [qli._default_stream_workspace(d) for d in (DEVICE, DEVICE + 1, DEVICE)])[0]
     assert kept[0] is kept[2] and kept[0] is not kept[1]
     assert all(stream is fake.default for stream, _ in fake.made)
+
+
+def test_a_workspace_has_to_be_as_long_as_it_says(fake):  # noqa: F811
+    short = torch.zeros(1, dtype=torch.uint8)
+    for ws in (short.expand(1 << 30), torch.zeros(8192, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            qli.kv_attention(workspace=on_gpu(ws), **attention_inputs())
+    assert not fake.lib.calls
+    qli.kv_attention(workspace=on_gpu(torch.zeros(8192, dtype=torch.uint8)[256:]), **attention_inputs())
+    assert fake.lib.calls[0][1][2] == 8192 - 256
