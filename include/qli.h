@@ -369,7 +369,7 @@ qli_status qli_read_kv(const uint8_t *cache, int64_t num_pages, int64_t page_str
  *     kv_j = code_j * scale_j,   z_j = scale * sum_d q[t, h, d] * kv_j[d]
  *     out[t, h, :] = BF16( sum_j exp(z_j - m) kv_j / sum_j exp(z_j - m) ),
  *     lse[t, h] = m + ln(sum_j exp(z_j - m)),    m = max_j z_j;
- * an empty J gives out = 0 and lse = -inf.
+ * an empty J gives out = 0 and lse = -inf, whatever q holds there.
  *  - With `indices`: J(t) = the entries >= 0 of indices[t, 0, :], as for
  *    qli_sparse_attention (a position listed twice counts twice; a listed
  *    position past the block table is skipped and flagged).

@@ -873,10 +873,11 @@ __device__ __forceinline__ int head_of(int lane) {
 // on. BF16 outputs (kOut), of the first `nh` heads: head i at dst + i * stride,
 // in the order of the values (a warp stores to one 128-byte line). FP32 pieces,
 // of at least those: head i at dst + i * kD, in the order of the rows (likewise;
-// merge_pieces_kernel reorders).
+// merge_pieces_kernel reorders). A row tile without positions (`none`) gives zeros
+// whatever a query that is not finite has left in the accumulators.
 template <bool kOut, class T>
-__device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int pos, int32_t nh, T* dst,
-                                       int64_t stride) {
+__device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int pos, int32_t nh, bool none,
+                                       T* dst, int64_t stride) {
 #pragma unroll 1
   for (int c = 0; c < 8; ++c) {
     const int i0 = (c & 1) * 16;
@@ -891,7 +892,7 @@ __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int
     T* at = dst + i0 * stride + (kOut ? value_of(c >> 1, pos) : 128 * (c >> 1) + pos);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float v = __uint_as_float(o[i]) * al[i];
+      const float v = none ? 0.0f : __uint_as_float(o[i]) * al[i];
       if constexpr (kOut) {
         const __nv_bfloat16 y = __float2bfloat16_rn(v);
         if (i0 + i < nh) *at = *reinterpret_cast<const uint16_t*>(&y);
@@ -919,7 +920,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
   const f32x2* al2 = reinterpret_cast<const f32x2*>(S.alpha + h0);
   // the lane's word of unit 4 sub of its first position; unit 4 sub + i flips bits 4, 5
   const uint32_t p_at = smem_u32(S.p) + sw(pos, 4 * sub) + 4 * (lane & 3);
-  bool ok = true, seen = false;
+  bool ok = true, seen = false, live = false;          // live: one of the lane's positions is there
   f32x2 l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) l[i] = pair_of(0.0f, 0.0f);
@@ -931,7 +932,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     if (w.first()) {                                  // the heads' factors
       if (ok && !wait(&S.qfull, seg & 1)) ok = false;
       ++seg;
-      seen = false;
+      seen = live = false;
       // the queries after these wait for this warp too, so that it sees every
       // phase of the barrier
       if (lane == 0) mbar_arrive(&S.qempty);
@@ -945,6 +946,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const float s = S.rs[slot][pos + 8 * k], ls = lg2(s), inv_s = s != 0.0f ? ex2(-ls) : 0.0f;
+      live |= s != 0.0f;
       const f32x2* c2 = reinterpret_cast<const f32x2*>(S.sl2[(seg - 1) & 1] + h0);
       const f32x2 s2 = pair_of(s, s), ls2 = pair_of(ls + kShift, ls + kShift);
       inv2[k] = pair_of(inv_s, inv_s);
@@ -1050,12 +1052,16 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     if (!w.last()) continue;
 
     // ---- the row tile's end in this CTA: totals, then the output
-    part[qw * 32 + head_of(lane)] = across(l, lane, [](float p, float q) { return p + q; });
+    // A query that is not finite makes NaN weights of rows without a position too:
+    // a warp that has no position adds nothing.
+    const float mine = across(l, lane, [](float p, float q) { return p + q; });
+    part[qw * 32 + head_of(lane)] = __any_sync(0xffffffffu, live) ? mine : 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) l[i] = pair_of(0.0f, 0.0f);
     named_bar(bar, 128);
     // lane: head 32 sub + lane
     const float total = (part[lane] + part[32 + lane]) + (part[64 + lane] + part[96 + lane]);
+    const bool none = __all_sync(0xffffffffu, total == 0.0f);
     const float lse2 = total == 0.0f ? -INFINITY : S.m[32 * sub + lane] - kShift + log2f(total);
     named_bar(bar, 128);
     if (qw == 0) {
@@ -1072,13 +1078,13 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       if (qw == 0 && lane < nh && a.lse)
         a.lse[static_cast<int64_t>(a.t0 + w.t) * a.H + h + lane] = lse2 * kLn2;
       uint16_t* orow = a.out + static_cast<int64_t>(a.t0 + w.t) * a.o_st + h * a.o_sh;
-      output<true>(S, oe, 32 * sub, 32 * qw + lane, nh, orow, a.o_sh);
+      output<true>(S, oe, 32 * sub, 32 * qw + lane, nh, none, orow, a.o_sh);
     } else {
       // a row tile that began in an earlier CTA goes to slot 0, one that goes
       // on in the next to slot 1
       const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (w.began_here() ? 1 : 0);
       if (qw == 0) a.piece_lse[piece * kHT + 32 * sub + lane] = lse2;
-      output<false>(S, oe, 32 * sub, 32 * qw + lane, nh, a.piece + piece * kPieceRow + (32 * sub) * kD,
+      output<false>(S, oe, 32 * sub, 32 * qw + lane, nh, none, a.piece + piece * kPieceRow + (32 * sub) * kD,
                     static_cast<int64_t>(kD));
     }
     named_bar(bar, 128);                              // the factors are read
