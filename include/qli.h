@@ -423,7 +423,8 @@ qli_status qli_kv_attention_workspace_size(const qli_kv_attn_args *a, size_t *by
  * on one stream, and one host thread after the other queues them.
  * Allocates nothing, never synchronises; nothing is launched on a non-OK
  * status. The result does not depend on timing: the same call gives the same
- * bits. */
+ * bits. Where an on-chip wait gave up (QLI_DEVERR_TIMEOUT), the outputs that were
+ * not finished are NaN. */
 qli_status qli_kv_attention(const qli_kv_attn_args *a, void *workspace, size_t workspace_bytes,
                             void *stream);
 

@@ -212,7 +212,11 @@ __device__ __forceinline__ float ex2(float x) {
 // has been probed 2^16 times (0.1 us each while the CTA is busy, 20 us when
 // nothing happens: some ms to a second or so). A loop of five instructions: the
 // roles' loops together have to stay within the instruction cache.
+#ifdef QLI_TEST_STALL_EPILOGUE
+constexpr int kProbes = 1 << 13;               // a test build, in which CTA 1 waits for what never comes
+#else
 constexpr int kProbes = 1 << 16;
+#endif
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -814,6 +818,9 @@ __device__ __forceinline__ bool run_values(const Args& a, Smem& S, uint32_t tmem
   const uint32_t v_lo = sdesc_lo(smem_u32(S.kv), kRegion), p_lo = sdesc_lo(smem_u32(S.p), 1024);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
   bool ok = true;
+#ifdef QLI_TEST_STALL_EPILOGUE
+  ok = blockIdx.x != 1;
+#endif
   uint32_t n = 0;
 #pragma unroll 1
   for (Walk w(a, S); ok && w.valid(); w.next(a, S), ++n) {
@@ -925,8 +932,12 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
 #pragma unroll
   for (int i = 0; i < 4; ++i) l[i] = pair_of(0.0f, 0.0f);
   uint32_t n = 0, seg = 0;
-  // A wait that gives up clears `ok`; the warps still run through the same
-  // named barriers, on whatever TMEM holds, and write no output.
+  // A wait that gives up clears `ok`. The warp still runs through the named
+  // barriers, on whatever TMEM holds, but arrives nowhere else, so that nobody
+  // goes on with what it should have made and the units after this one end in
+  // waits that give up too. What it adds to a normaliser is NaN, and so are its
+  // outputs: a row tile that was not finished does not look like a result, in
+  // `out` or, by way of its piece, in a join.
   for (Walk w(a, S); w.valid(); w.next(a, S), ++n) {
     const uint32_t buf = n & 1, parity = (n >> 1) & 1;
     if (w.first()) {                                  // the heads' factors
@@ -935,7 +946,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       seen = live = false;
       // the queries after these wait for this warp too, so that it sees every
       // phase of the barrier
-      if (lane == 0) mbar_arrive(&S.qempty);
+      if (lane == 0 && ok) mbar_arrive(&S.qempty);
     }
     const uint32_t slot = n & (kSlots - 1);
     if (ok && !wait(&S.rowfull[slot], (n / kSlots) & 1)) ok = false;
@@ -965,7 +976,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       tmem_ld_16x256b_x4(tmem + lanes + kSCol + kHT * buf + 32 * sub, r);
       tmem_ld_wait();
       tc_fence_before();
-      if (lane == 0) mbar_arrive(&S.sfree[buf]);
+      if (lane == 0 && ok) mbar_arrive(&S.sfree[buf]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -1043,7 +1054,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) {
+    if (lane == 0 && ok) {
       mbar_arrive(&S.pready[buf]);
       mbar_arrive(&S.rowfree[slot]);
     }
@@ -1055,14 +1066,14 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     // A query that is not finite makes NaN weights of rows without a position too:
     // a warp that has no position adds nothing.
     const float mine = across(l, lane, [](float p, float q) { return p + q; });
-    part[qw * 32 + head_of(lane)] = __any_sync(0xffffffffu, live) ? mine : 0.0f;
+    part[qw * 32 + head_of(lane)] = !ok ? NAN : __any_sync(0xffffffffu, live) ? mine : 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) l[i] = pair_of(0.0f, 0.0f);
     named_bar(bar, 128);
     // lane: head 32 sub + lane
     const float total = (part[lane] + part[32 + lane]) + (part[64 + lane] + part[96 + lane]);
     const bool none = __all_sync(0xffffffffu, total == 0.0f);
-    const float lse2 = total == 0.0f ? -INFINITY : S.m[32 * sub + lane] - kShift + log2f(total);
+    float lse2 = total == 0.0f ? -INFINITY : S.m[32 * sub + lane] - kShift + log2f(total);
     named_bar(bar, 128);
     if (qw == 0) {
       S.alpha[32 * sub + lane] = total == 0.0f ? 0.0f : 1.0f / total;
@@ -1070,9 +1081,14 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     }
     named_bar(bar, 128);
     if (ok && !wait(&S.empty[buf][1], parity)) ok = false;
+    if (!ok) {
+      lse2 = NAN;
+      S.alpha[32 * sub + lane] = NAN;
+      __syncwarp();
+    }
     tc_fence_after();
     const int32_t h = w.g * a.ht + 32 * sub;          // first head of this sub
-    const int32_t nh = ok ? min(min(32, a.ht - 32 * sub), a.H - h) : 0;  // heads to write
+    const int32_t nh = min(min(32, a.ht - 32 * sub), a.H - h);  // heads to write
     const uint32_t oe = tmem + lanes + kOCol + 32 * sub;
     if (w.i == w.n - 1 && w.began_here()) {
       if (qw == 0 && lane < nh && a.lse)
