@@ -6,8 +6,8 @@ step, as a serving loop makes it for a batch of requests with one new token each
 
   1. the new tokens' KV rows and index-K rows are quantised into their slots;
   2. the indexer scores every visible position and picks the best;
-  3. each token attends over the picked positions, and over a window of the
-     latest ones; positions in both count twice, as two stages do;
+  3. each token attends over a window of the latest positions, and over the
+     picked ones before the window, so that none counts twice;
   4. the two stages are merged by their log-sum-exps;
   5. the rows of one request's window are read back, for example to hand the
      request over to another cache.
@@ -100,6 +100,8 @@ def decode_step(pool: Pool, topk: int, window: int):
                          scales.view(torch.float16), ratio=1, rows_per_page=pool.R,
                          page_stride=L["page_stride"], k_offset=L["k_offset"],
                          scale_offset=L["scale_offset"], topk=topk, quant_mode=pool.quant_mode)
+    # the window's positions are the other stage's
+    indices.masked_fill_(indices >= (pool.lengths - window)[:, None, None], -1)
     # the two stages over the KV rows, and their merge
     q, scale = pool.random(B, HEADS, D), 1.0 / math.sqrt(D)
     picked = qli.kv_attention(q, cu, pool.cache, pool.block_table, indices=indices, scale=scale,
