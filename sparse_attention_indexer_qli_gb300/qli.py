@@ -332,11 +332,9 @@ class Call:
         return int(w.value)
 
 
-def _stream(stream, device=None) -> Optional[int]:
-    """The raw stream: the given one, or the current one (of device index
-    `device`, which spares looking the current device up)."""
+def _stream(stream) -> Optional[int]:
     import torch
-    s = torch.cuda.current_stream(device) if stream is None else stream
+    s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
 
 
@@ -476,17 +474,20 @@ def sparse_attention(q, cu_seqlens_q, cache, block_table, indices, *, rows_per_p
 
 
 
-def _first_cuda(name, t, dtype) -> int:
+def _first_cuda(name, t, dtype, current_device) -> int:
     """Checks a call's first tensor and returns the index of its device, which has
-    to be the current one: that is where the library launches."""
-    import torch
+    to be the current one (asked for once there is a CUDA tensor): that is where
+    the library launches. The good case first."""
+    try:
+        device = t.get_device()
+        if device >= 0 and t.dtype is dtype and device == current_device():
+            return device
+    except AttributeError:
+        pass
     if t is None:
         raise TypeError("%s must be a CUDA tensor" % name)
     _require_cuda(name, t, dtype)
-    device, current = t.get_device(), torch.cuda.current_device()
-    if device != current:
-        raise ValueError("%s is on CUDA device %d, the current device is %d" % (name, device, current))
-    return device
+    raise ValueError("%s is on CUDA device %d, the current device is %d" % (name, device, current_device()))
 
 
 def _check_cuda(name, t, dtype, device):
@@ -512,11 +513,13 @@ def write_kv(kv, slot_mapping, cache, *, rows_per_page: int, page_stride: int, k
     CUDA) at slot_mapping [n] (int64: page * rows_per_page + row; negative =
     skip)."""
     import torch
-    device = _first_cuda("kv", kv, torch.bfloat16)
+    device = _first_cuda("kv", kv, torch.bfloat16, torch.cuda.current_device)
     _check_cuda("slot_mapping", slot_mapping, torch.int64, device)
     _check_cuda("cache", cache, torch.uint8, device)
+    err = None
     if err_word is not None:
         _check_cuda("err_word", err_word, torch.int32, device)
+        err = err_word.data_ptr()
     if kv.dim() != 2 or kv.shape[1] != 512 or kv.stride(1) != 1:
         raise ValueError("kv must be [n, 512] with unit stride in the last dim")
     if not cache.is_contiguous() or not slot_mapping.is_contiguous():
@@ -524,11 +527,11 @@ def write_kv(kv, slot_mapping, cache, *, rows_per_page: int, page_stride: int, k
     n = kv.shape[0]
     if slot_mapping.numel() != n:
         raise ValueError("one slot per row")
+    raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
     _check((_lib or lib()).qli_write_kv(
         kv.data_ptr(), kv.stride(0) if n > 1 else 512, n, slot_mapping.data_ptr(),
         cache.data_ptr(), cache.numel() // page_stride, page_stride, rows_per_page, kv_offset,
-        kv_scale_offset, quant_mode, _ptr(err_word), _stream(stream, device)),
-        "qli_write_kv")
+        kv_scale_offset, quant_mode, err, raw), "qli_write_kv")
 
 
 def read_kv(cache, slots, *, rows_per_page: int, page_stride: int, kv_offset: int,
@@ -536,10 +539,12 @@ def read_kv(cache, slots, *, rows_per_page: int, page_stride: int, kv_offset: in
     """qli_read_kv: the rows named by slots [n] (int64: page * rows_per_page +
     row; negative = zeros) of the page pool `cache` as BF16 [n, 512]."""
     import torch
-    device = _first_cuda("cache", cache, torch.uint8)
+    device = _first_cuda("cache", cache, torch.uint8, torch.cuda.current_device)
     _check_cuda("slots", slots, torch.int64, device)
+    err = None
     if err_word is not None:
         _check_cuda("err_word", err_word, torch.int32, device)
+        err = err_word.data_ptr()
     if not cache.is_contiguous() or not slots.is_contiguous():
         raise ValueError("cache and slots must be contiguous")
     n = slots.numel()
@@ -549,11 +554,11 @@ def read_kv(cache, slots, *, rows_per_page: int, page_stride: int, kv_offset: in
         _check_cuda("out", out, torch.bfloat16, device)
         if out.shape != (n, 512) or out.stride(1) != 1:
             raise ValueError("out must be [n, 512] with unit stride in the last dim")
+    raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
     _check((_lib or lib()).qli_read_kv(
         cache.data_ptr(), cache.numel() // page_stride, page_stride, rows_per_page, kv_offset,
         kv_scale_offset, quant_mode, slots.data_ptr(), n, out.data_ptr(),
-        out.stride(0) if n > 1 else 512, _ptr(err_word), _stream(stream, device)),
-        "qli_read_kv")
+        out.stride(0) if n > 1 else 512, err, raw), "qli_read_kv")
     return out
 
 
@@ -575,13 +580,6 @@ def _attn_outputs(q_shape, device, out, lse, stream):
         if lse.shape != (T, H) or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous [T, H] tensor")
     return out, lse
-
-
-def _strides(t, T, H, one):
-    """Strides of t [T, H, 512] along tokens and heads; `one` along a dimension of
-    size one, whose own may be any number."""
-    st, sh, _ = t.stride()
-    return st if T > 1 else one, sh if H > 1 else one
 
 
 @functools.lru_cache(maxsize=None)
@@ -649,7 +647,7 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
     default stream once per host thread and device). Returns (out [T, H, 512]
     BF16, lse [T, H] float32)."""
     import torch
-    device = _first_cuda("q", q, torch.bfloat16)
+    device = _first_cuda("q", q, torch.bfloat16, torch.cuda.current_device)
     int32 = torch.int32
     _check_cuda("cu_seqlens_q", cu_seqlens_q, int32, device)
     _check_cuda("block_table", block_table, int32, device)
@@ -661,11 +659,10 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, pages of a request]")
     rows, width = block_table.shape
-    # the strides of a dimension of size one may be any number
     pitch, step = block_table.stride()
     if step != 1 and width > 1:
         raise ValueError("block_table must have unit stride in the last dim")
-    if rows == 1:
+    if rows == 1:                                     # its pitch may be any number
         pitch = width
     shape = q.shape
     T, H, D = shape
@@ -696,14 +693,19 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
         _check_cuda("err_word", err_word, int32, device)
         err = err_word.data_ptr()
     out, lse = _attn_outputs(shape, device, out, lse, stream)
-    q_t, q_h = _strides(q, T, H, 512)
-    o_t, o_h = _strides(out, T, H, 512)
+    q_t, q_h, _ = q.stride()
+    o_t, o_h, _ = out.stride()
+    # the strides of a dimension of size one may be any number
+    if T == 1:
+        q_t = o_t = 512
+    if H == 1:
+        q_h = o_h = 512
     a = _pack_kv_attn(q.data_ptr(), q_t, q_h, T, H, D, cu_seqlens_q.data_ptr(), B,
                       width, cache.data_ptr(), page_stride, cache.numel() // page_stride, rows_per_page,
                       quant_mode, kv_offset, kv_scale_offset, block_table.data_ptr(),
                       pitch, K, idx, lens, res, ratio, window, scale,
                       out.data_ptr(), o_t, o_h, lse.data_ptr(), err)
-    raw = _stream(stream, device)
+    raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
     if workspace is not None:
         _check_cuda("workspace", workspace, torch.uint8, device)
         if not workspace.is_contiguous():
@@ -734,21 +736,27 @@ def merge_attention(outs, lses, *, out=None, lse=None, stream=None):
         raise ValueError("outs must be [T, H, 512]")
     T, H, D = shape
     ptrs, st, sh, lptrs = [0] * MERGE_MAX, [0] * MERGE_MAX, [0] * MERGE_MAX, [0] * MERGE_MAX
-    device = _first_cuda("outs", outs[0], dtype)
+    device = _first_cuda("outs", outs[0], dtype, torch.cuda.current_device)
     for i in range(n):
         o, l = outs[i], lses[i]
-        _check_cuda("outs", o, dtype, device)
+        if i > 0:
+            _check_cuda("outs", o, dtype, device)
         _check_cuda("lses", l, torch.float32, device)
         if o.shape != shape or o.stride(2) != 1:
             raise ValueError("outs must share one [T, H, 512] shape with unit stride in the last dim")
         if l.shape != shape[:2] or not l.is_contiguous():
             raise ValueError("lses must be contiguous [T, H] tensors")
         ptrs[i], lptrs[i] = o.data_ptr(), l.data_ptr()
-        st[i], sh[i] = _strides(o, T, H, 0)
+        st[i], sh[i], _ = o.stride()
     out, lse = _attn_outputs(shape, device, out, lse, stream)
-    o_t, o_h = _strides(out, T, H, 512)
+    o_t, o_h, _ = out.stride()
+    # the strides of a dimension of size one may be any number
+    if T == 1:
+        st, o_t = [0] * MERGE_MAX, 512
+    if H == 1:
+        sh, o_h = [0] * MERGE_MAX, 512
     a = _pack_merge(*ptrs, *st, *sh, *lptrs, n, int(dtype == torch.float32), T, H, D,
                     out.data_ptr(), o_t, o_h, lse.data_ptr())
-    _check((_lib or lib()).qli_merge_attention(a, _stream(stream, device)),
-           "qli_merge_attention")
+    raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    _check((_lib or lib()).qli_merge_attention(a, raw), "qli_merge_attention")
     return out, lse
