@@ -676,6 +676,8 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
                 or not indices.is_contiguous():
             raise ValueError("indices must be a contiguous [T, 1, K] tensor")
         K, idx = indices.shape[2], indices.data_ptr()
+        if K < 1 and T > 0:
+            raise ValueError("indices must have an entry for each token")
     elif k_lens is None:
         raise ValueError("either indices or k_lens must be given")
     lens, res, err = 0, 0, 0
