@@ -33,17 +33,21 @@
 // TMEM: two S buffers of 64 columns, four O^T quarters of 64. Shared memory:
 // two FP16 tiles (128 KB), the queries (64 KB), two buffers of weights (16 KB).
 //
-// What bounds it. In a long run a unit takes about 3.1k cycles, of which the path
-// between shared memory, L1 and the rest, 128 bytes a clock, is taken up in nearly
-// all: the products read 224 KB (1792 cycles; alone they take 1984, 32 score
-// products of 36 and 16 value products of 52), the tile's stores and the codes'
-// loads are 96 KB (768), the rest lookups, weights and barriers. Copies of the
-// kernel without half of the stores are 0.22k cycles a unit faster, without the
-// loads 0.24k, with half the score products 0.26k, without the exponentials 0.03k;
-// loads issued a half earlier, conversion before the wait and weights stored before
-// the vote changed nothing or lost. Around a CTA's units lie 7k cycles up to its
-// first rows (planning, dependent lookups, cold instructions), and 4.1k for each
-// output or piece of 64 heads. Measured on one GB300: 1021 tokens over some 8K
+// What bounds it. In a long run a unit takes about 3.1k cycles, most of them on the
+// path between shared memory, L1 and the rest, 128 bytes a clock. Counted over a call
+// of 64 tokens over 8192 positions (ncu, 3.5k cycles a unit with the start and the
+// outputs): the products' operands 1792 wavefronts a unit (224 KB; issued alone they
+// take 1984 cycles, 32 score products of 36 and 16 value products of 52), loads and
+// stores 1417 (the tile's stores and the codes' loads are 768, the rest weights,
+// factors, lookups, pieces and outputs) and 411 more in conflicts between the two.
+// It is not all: copies of the kernel without half of the stores are 0.22k cycles a
+// unit faster, without the loads 0.24k, with half the score products 0.26k (of 0.58k
+// that these take to issue), without the exponentials 0.03k; loads issued a half
+// earlier, conversion before the wait and weights stored before the vote changed
+// nothing or lost. Around a CTA's units lie 7k cycles up to its first rows (planning,
+// dependent lookups, cold instructions), and 4.1k for each output or piece of 64 heads
+// (a piece's 128 KB leave the SM at 32 bytes a clock; an output is half as long, in
+// stores of 2 bytes). Measured on one GB300: 1021 tokens over some 8K
 // positions each, 64 heads, INT8: 1.34 ms, 0.75 PFLOP/s; 12 tokens over 64K
 // positions, E4M3: 150 us, 2.6 TB/s and 0.67 PFLOP/s; 64 tokens over 2048 listed
 // positions, E4M3: 49 us, 1.5 TB/s; one token over 512 listed positions: 15 us,
