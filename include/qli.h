@@ -428,6 +428,19 @@ qli_status qli_kv_attention_workspace_size(const qli_kv_attn_args *a, size_t *by
 qli_status qli_kv_attention(const qli_kv_attn_args *a, void *workspace, size_t workspace_bytes,
                             void *stream);
 
+/* The same attention for drafted tokens: a request's tokens of the call are the
+ * nodes of a tree and have its last positions, node i the position k_lens -
+ * (number of nodes) + i. Token t sees all positions before the nodes and the nodes
+ * i whose bit i % 64 of tree_mask[t * mask_words + i / 64] is set (as a rule the node
+ * itself and its ancestors); nodes from 64 * mask_words on are not seen, bits from
+ * the number of nodes on mean nothing. window > 0: the last `window` of the
+ * positions it sees. A request of fewer positions than tokens is flagged
+ * (QLI_DEVERR_KLEN) and its tokens see none. Without indices and residual, with
+ * ratio 1; otherwise arguments, workspace and results as for qli_kv_attention. */
+qli_status qli_kv_tree_attention(const qli_kv_attn_args *a, const uint64_t *tree_mask,
+                                 int32_t mask_words, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
 /* sizeof(qli_kv_attn_args) the library was built with. */
 int64_t qli_kv_attn_args_size(void);
 
@@ -454,6 +467,113 @@ qli_status qli_merge_attention(const qli_merge_args *a, void *stream);
 
 /* sizeof(qli_merge_args) the library was built with. */
 int64_t qli_merge_args_size(void);
+
+/* ---- Rotation of positions, queries and cache rows ------------------------------
+ * The steps between a layer's projections and the calls above. The blog (section
+ * 四) rotates the output's tail back in place after the attention; the pages give
+ * neither the frequencies nor the norms, so both are arguments. */
+
+/* Pair i of a row at position p, values (a, b), becomes
+ *     magnitude * (a cos t - b sin t, b cos t + a sin t),  t = 2 pi p turns[i] / 2^64;
+ * the angle is reduced exactly for every int32 position, negative ones among them.
+ * The pairs are values (offset + 2i, offset + 2i + 1) of the row (interleaved) or
+ * (offset + i, offset + pairs + i) (half); the other values stay. A host structure. */
+#define QLI_ROTARY_PAIRS 64
+enum { QLI_ROTARY_INTERLEAVED = 0, QLI_ROTARY_HALF = 1 };
+typedef struct qli_rotary {
+    int32_t pairs;               /* 8..64, a multiple of 8 */
+    int32_t layout;              /* QLI_ROTARY_INTERLEAVED or QLI_ROTARY_HALF */
+    int32_t offset;              /* first rotated value, a multiple of 8 */
+    float magnitude;             /* finite */
+    uint64_t turns[QLI_ROTARY_PAIRS]; /* turns per position, in units of 2^-64 (modulo 1) */
+} qli_rotary;
+
+/* Rotates x [T, H, D] (BF16) by its tokens' positions into out; with `inverse`
+ * undoes that rotation (angles negated, divided by the magnitude). out may be x,
+ * with the same strides: then only the rotated values are read and written.
+ * Otherwise out and x do not overlap and the other values are copied. FP32
+ * arithmetic, one rounding. One kernel on `stream`; asynchronous. */
+typedef struct qli_rotate_args {
+    const uint16_t *x;           /* (t, h, d) at x[t*x_stride_t + h*x_stride_h + d]; 16-byte aligned,
+                                    strides in elements, multiples of 8; 0 broadcasts */
+    int64_t x_stride_t, x_stride_h;
+    int32_t T, H, D;             /* D: a multiple of 8, at least 16; T * H below 2^31 */
+    int32_t inverse;
+    const int32_t *positions;    /* [T] */
+    uint16_t *out;               /* likewise; rows that do not overlap */
+    int64_t out_stride_t, out_stride_h;
+} qli_rotate_args;
+qli_status qli_rotate(const qli_rotate_args *a, const qli_rotary *rotary, void *stream);
+
+/* What is done to a row of `width` values before it is rounded: the norm
+ *     rms:   y = x / sqrt(mean(x^2) + eps) * weight
+ *     layer: y = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * weight + bias
+ * and the rotation, in FP32 (squares are summed in FP32: magnitudes below 2^59).
+ * A host structure; weight and bias are device pointers. */
+enum { QLI_NORM_NONE = 0, QLI_NORM_RMS = 1, QLI_NORM_LAYER = 2 };
+typedef struct qli_row_prep {
+    int32_t width;
+    int32_t norm;                /* QLI_NORM_* */
+    float eps;                   /* finite, not negative */
+    int32_t reserved;
+    const float *weight;         /* [width], 16-byte aligned, or NULL: 1; NULL without a norm */
+    const float *bias;           /* [width], 16-byte aligned, or NULL: 0; layer norm only */
+    qli_rotary rotary;           /* pairs 0: no rotation */
+} qli_row_prep;
+
+/* Norm and rotation of queries x [T, H, width] (BF16) in one pass, rounded once:
+ * to BF16 (quant_mode 0; width 64, 128, 256 or 512) or, for the indexer's queries
+ * (width 128), to the codes and scales of qli_quantize_q (QLI_QUANT_INT8) or
+ * qli_quantize_q_fp8 (QLI_QUANT_FP8), taken of the FP32 values. BF16 results may
+ * replace x (same pointer and strides). One kernel on `stream`; asynchronous. */
+typedef struct qli_prepare_args {
+    const uint16_t *x;           /* as in qli_rotate_args */
+    int64_t x_stride_t, x_stride_h;
+    int32_t T, H;
+    const int32_t *positions;    /* [T], or NULL without a rotation */
+    void *out;                   /* BF16 or codes [T, H, width]: strides in elements, multiples of 16 bytes;
+                                    16-byte aligned; rows that do not overlap */
+    int64_t out_stride_t, out_stride_h;
+    uint16_t *scale_out;         /* [T, H] FP16 scales of codes */
+    int32_t quant_mode;          /* 0, QLI_QUANT_INT8 or QLI_QUANT_FP8 */
+    int32_t reserved;
+} qli_prepare_args;
+qli_status qli_prepare_q(const qli_prepare_args *a, const qli_row_prep *prep, void *stream);
+
+/* Norm and rotation of n new cache rows on their way into their page slots: KV rows
+ * of 512 values (BF16, as qli_sparse_attention reads them, or the 8-bit rows of
+ * qli_write_kv) and index K rows of 128 (the 8-bit rows of qli_write_index_k), the
+ * codes taken of the FP32 values. Either kind may be left out (NULL). Slots,
+ * padding, distinctness and err_word as for qli_write_kv; the parts of a page that
+ * are written must not overlap. One kernel on `stream`; asynchronous. */
+typedef struct qli_append_args {
+    const uint16_t *kv;          /* row i: 512 BF16 values at kv + i * kv_stride (elements, a multiple
+                                    of 8, at least 512), 16-byte aligned; or NULL */
+    int64_t kv_stride;
+    const uint16_t *index_k;     /* row i: 128 BF16 values at index_k + i * index_stride; or NULL */
+    int64_t index_stride;
+    int64_t n;                   /* below 2^31 */
+    const int32_t *positions;    /* [n], or NULL without a rotation */
+    const int64_t *slot_mapping; /* [n]: page * rows_per_page + row; negative: padding */
+    uint8_t *cache;
+    int64_t num_pages, page_stride;
+    int32_t rows_per_page;       /* 64 or 128 */
+    int32_t kv_mode;             /* 0: BF16 rows of 1024 bytes; QLI_QUANT_INT8 or QLI_QUANT_FP8 */
+    int32_t quant_mode;          /* of the index K: QLI_QUANT_INT8 or QLI_QUANT_FP8 */
+    int32_t reserved;
+    int64_t kv_offset, kv_scale_offset;   /* the latter unused with BF16 rows */
+    int64_t k_offset, scale_offset;
+    uint32_t *err_word;
+} qli_append_args;
+qli_status qli_append_kv(const qli_append_args *a, const qli_row_prep *kv_prep,
+                         const qli_row_prep *index_prep, void *stream);
+
+/* sizeof of the structures the library was built with. */
+int64_t qli_rotary_size(void);
+int64_t qli_row_prep_size(void);
+int64_t qli_rotate_args_size(void);
+int64_t qli_prepare_args_size(void);
+int64_t qli_append_args_size(void);
 
 /* Human-readable name of a status. Never NULL. */
 const char *qli_status_string(qli_status s);

@@ -95,6 +95,7 @@ struct Smem {
   uint8_t q[kTile];                            // 1024-aligned
   uint8_t p[2][kPos * 128];                    // 1024-aligned, by unit parity
   int32_t tokV[kChunkT], tokB[kChunkT];        // visible positions and request of the launch's tokens
+  int32_t treeP[kChunkT], treeR[kChunkT], treeN[kChunkT];  // drafted trees: see Tree
   const uint8_t* row[kSlots][kPos];            // the rows' codes, by unit modulo kSlots
   float rs[kSlots][kPos];                      // and scales; 0: no position
   float sl2[2][kHT];                           // by row tile parity: softmax scale in log2 over the
@@ -127,6 +128,8 @@ struct Args {
   int32_t bt_stride;
   const int32_t* idx;
   int32_t K;
+  const uint64_t* mask;        // drafted trees: [T][words], nodes that a token sees
+  int32_t words;
   float scale;
   uint16_t* out;
   int64_t o_st, o_sh;
@@ -388,6 +391,7 @@ __device__ __forceinline__ int32_t request_of(const int32_t* cu, int32_t B, int3
 }
 
 // Flags requests with bad metadata, once a call.
+template <bool kTree>
 __device__ __forceinline__ void flag_requests(const Args& a, int tid) {
   if (a.idx || a.t0 != 0 || !a.err) return;
   uint32_t e = 0u;
@@ -395,6 +399,7 @@ __device__ __forceinline__ void flag_requests(const Args& a, int tid) {
   for (int b = tid; b < a.B; b += kThreads) {
     int32_t q0, q1, lk, res;
     e |= sanitize_request(a, b, q0, q1, lk, res);
+    if (kTree && lk < q1 - q0) e |= QLI_DEVERR_KLEN;
   }
   if (e) atomicOr(a.err, e);
 }
@@ -408,6 +413,51 @@ struct Requests {
 };
 constexpr int kRequestsInSmem = 10000;
 static_assert((3 * kRequestsInSmem + 1) * 4 <= 2 * kTile, "the requests fit in the tiles");
+
+// Drafted trees. A request's last `nodes` positions (its tokens of the call) are
+// behind a prefix of P; a token sees the prefix and the nodes whose bits are set in
+// its mask, `seen` of them, in this order, and with a window the last n of these.
+// Its position e of n has the rank e + (seen - n) after the prefix's end: below 0
+// it is that far before the end, else the mask's set bit of that rank. So a unit
+// holds no position that the token does not see.
+__device__ __forceinline__ uint64_t tree_word(const Args& a, int32_t t, int32_t w, int32_t nodes) {
+  const int32_t left = nodes - 64 * w;
+  const uint64_t m = __ldg(reinterpret_cast<const unsigned long long*>(a.mask) + static_cast<int64_t>(t) * a.words + w);
+  return left >= 64 ? m : left <= 0 ? 0u : m & ((uint64_t{1} << left) - 1);
+}
+// Positions that token t sees (n above) behind a prefix of P; seen - n.
+__device__ __forceinline__ int32_t tree_count(const Args& a, int32_t t, int32_t P, int32_t nodes, int32_t& rank0) {
+  int32_t seen = 0;
+#pragma unroll 1
+  for (int32_t w = 0; w < a.words && 64 * w < nodes; ++w) seen += __popcll(tree_word(a, t, w, nodes));
+  const int32_t n = a.window > 0 ? min(P + seen, a.window) : P + seen;
+  rank0 = seen - n;
+  return n;
+}
+// The set bit of that rank (from 0) in token t's mask; -1: there is none.
+__device__ __forceinline__ int32_t tree_node(const Args& a, int32_t t, int32_t nodes, int32_t rank) {
+#pragma unroll 1
+  for (int32_t w = 0; w < a.words && 64 * w < nodes; ++w) {
+    uint64_t m = tree_word(a, t, w, nodes);
+    const int32_t c = __popcll(m);
+    if (rank >= c) {
+      rank -= c;
+      continue;
+    }
+    int32_t at = 64 * w;
+#pragma unroll 1
+    for (int s = 32; s > 0; s >>= 1) {
+      const int32_t low = __popcll(m & ((uint64_t{1} << s) - 1));
+      if (rank >= low) {
+        rank -= low;
+        m >>= s;
+        at += s;
+      }
+    }
+    return at;
+  }
+  return -1;
+}
 
 // What a thread loads before the CTA has set itself up, so that the latencies
 // overlap: its request's metadata, and in listed mode (where the CTA's share
@@ -449,6 +499,7 @@ __device__ __forceinline__ void record_cut(const Args& a, int32_t t, int32_t g, 
 
 // Plans the launch: every token's request and visible positions, and the CTA's
 // share. A thread takes one token.
+template <bool kTree>
 __device__ __forceinline__ void plan(const Args& a, Smem& S, const Early& early) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Requests req{a.cu, a.k_lens, a.residual, a.T, a.B, a.ratio, a.cap};
@@ -473,13 +524,22 @@ __device__ __forceinline__ void plan(const Args& a, Smem& S, const Early& early)
     if (!a.idx) {
       int32_t q0, q1, lk, res;
       sanitize_request(req, b, q0, q1, lk, res);
-      if (q0 <= t && t < q1) V = visible_count(lk, res, a.ratio, q1 - q0, t - q0);
+      if constexpr (kTree) {
+        const int32_t nodes = q1 - q0, P = lk - nodes;
+        int32_t rank0 = 0;
+        if (q0 <= t && t < q1 && P >= 0) V = tree_count(a, t, P, nodes, rank0);
+        S.treeP[tid] = P;
+        S.treeR[tid] = rank0;
+        S.treeN[tid] = nodes;
+      } else {
+        if (q0 <= t && t < q1) V = visible_count(lk, res, a.ratio, q1 - q0, t - q0);
+      }
     }
     S.tokV[tid] = V;
     S.tokB[tid] = b;
     units = units_of(a, V);
   }
-  if (blockIdx.x == 0) flag_requests(a, tid);
+  if (blockIdx.x == 0) flag_requests<kTree>(a, tid);
   if (a.whole) {
     __syncthreads();
     if (tid == 0) {
@@ -610,6 +670,7 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
 // position; `entry` is the first unit's), so that no step waits for the load of the
 // one before. Positions
 // past the table and pages outside the pool are skipped and flagged.
+template <bool kTree>
 __device__ __forceinline__ bool run_rows(const Args& a, Smem& S, int32_t entry) {
   const int lane = threadIdx.x & 31, r = threadIdx.x - 32 * kRowWarp0;
   bool bad = false;
@@ -655,8 +716,12 @@ __device__ __forceinline__ bool run_rows(const Args& a, Smem& S, int32_t entry) 
     if (w.valid()) {
       const int32_t V = S.tokV[w.t], n = positions_of(a, V), e = w.i * kPos + r;
       b3 = S.tokB[w.t];
-      if (e < n)
+      if constexpr (kTree) {
+        const int32_t rank = S.treeR[w.t] + e;
+        if (e < n) j3 = S.treeP[w.t] + (rank < 0 ? rank : tree_node(a, a.t0 + w.t, S.treeN[w.t], rank));
+      } else if (e < n) {
         j3 = !a.idx ? V - n + e : m == -3 ? entry : __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e);
+      }
       if (w.first()) {
         // the row tile's queries, into L2: head r, 128 bytes at a time
         const int h = w.g * a.ht + r, end = r < a.ht ? a.H : 0;
@@ -1112,7 +1177,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
   return ok;
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
   extern __shared__ uint8_t smem_raw[];
   Smem& S = *reinterpret_cast<Smem*>(
@@ -1142,7 +1207,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
     fence_mbar_init();
   }
   tc_fence_before();
-  plan(a, S, early);                          // ends with a barrier of the CTA
+  plan<kTree>(a, S, early);                          // ends with a barrier of the CTA
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   if (S.count > 0) {
@@ -1157,7 +1222,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
       fewer_registers<kIssueRegs>();
       if (warp == kScoreWarp) ok = run_scores(a, S, tmem);
       if (warp == kValueWarp) ok = run_values(a, S, tmem);
-      if (warp >= kRowWarp0) ok = run_rows(a, S, early.entry);
+      if (warp >= kRowWarp0) ok = run_rows<kTree>(a, S, early.entry);
     }
     if (!ok && lane == 0 && a.err) atomicOr(a.err, QLI_DEVERR_TIMEOUT);
   }
@@ -1247,7 +1312,7 @@ __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a
     a.lse[t * a.H + h] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
 }
 
-std::atomic<uint64_t> g_smem_kv_attn[2];
+std::atomic<uint64_t> g_smem_kv_attn[4];
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
@@ -1358,11 +1423,11 @@ Layout layout_for(int sms) {
   return L;
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kTree>
 cudaError_t launch(Args d, int sms, cudaStream_t s) {
-  const auto kernel = kv_attn_kernel<kFp8>;
+  const auto kernel = kv_attn_kernel<kFp8, kTree>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kSmemBytes,
-                                    g_smem_kv_attn[kFp8 ? 1 : 0]);
+                                    g_smem_kv_attn[(kTree ? 2 : 0) + (kFp8 ? 1 : 0)]);
   const int64_t most = most_units(d);
   d.ht = heads_per_tile(d, most, sms);
   d.hg = (d.H + d.ht - 1) / d.ht;
@@ -1403,11 +1468,20 @@ extern "C" qli_status qli_kv_attention_workspace_size(const qli_kv_attn_args* a,
   return st;
 }
 
-extern "C" qli_status qli_kv_attention(const qli_kv_attn_args* a, void* workspace,
-                                       size_t workspace_bytes, void* stream) {
+namespace {
+
+template <bool kTree>
+qli_status attend(const qli_kv_attn_args* a, const uint64_t* mask, int32_t words, void* workspace,
+                  size_t workspace_bytes, void* stream) {
   using namespace qli::kvattn;
   qli_status st = validate(a);
   if (st != QLI_OK) return st;
+  if (kTree) {
+    if (a->indices != nullptr || words < 1) return QLI_ERR_INVALID_ARG;
+    if (a->ratio != 1) return QLI_ERR_UNSUPPORTED;
+    if (a->T > 0 && mask == nullptr) return QLI_ERR_INVALID_ARG;
+    if (!aligned(mask, 8)) return QLI_ERR_ALIGNMENT;
+  }
   if (a->T == 0) return QLI_OK;
   int sms = 0;
   st = qli::device_sms(&sms);
@@ -1420,9 +1494,25 @@ extern "C" qli_status qli_kv_attention(const qli_kv_attn_args* a, void* workspac
   d.cut = reinterpret_cast<int4*>(w);
   d.piece = reinterpret_cast<float*>(w + L.piece);
   d.piece_lse = reinterpret_cast<float*>(w + L.lse);
+  d.mask = mask;
+  d.words = words;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->quant_mode == QLI_QUANT_FP8 ? launch<true>(d, sms, s) : launch<false>(d, sms, s);
+  const cudaError_t e =
+      a->quant_mode == QLI_QUANT_FP8 ? launch<true, kTree>(d, sms, s) : launch<false, kTree>(d, sms, s);
   return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" qli_status qli_kv_attention(const qli_kv_attn_args* a, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  return attend<false>(a, nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+extern "C" qli_status qli_kv_tree_attention(const qli_kv_attn_args* a, const uint64_t* tree_mask,
+                                            int32_t mask_words, void* workspace, size_t workspace_bytes,
+                                            void* stream) {
+  return attend<true>(a, tree_mask, mask_words, workspace, workspace_bytes, stream);
 }
 
 extern "C" int64_t qli_kv_attn_args_size(void) {

@@ -8,10 +8,11 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import struct
 import threading
-from ctypes import c_int32, c_int64, c_size_t, c_uint32, c_void_p
+from ctypes import c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -105,6 +106,56 @@ class MergeArgs(ctypes.Structure):
     ]
 
 
+ROTARY_PAIRS = 64
+ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}
+NORMS = {None: 0, "rms": 1, "layer": 2}
+KV_BF16 = 0              # kv_mode of append_kv: rows of 1024 bytes
+
+
+class RotaryArgs(ctypes.Structure):
+    """Mirror of `qli_rotary` (field order and types as in include/qli.h)."""
+    _fields_ = [("pairs", c_int32), ("layout", c_int32), ("offset", c_int32),
+                ("magnitude", ctypes.c_float), ("turns", c_uint64 * ROTARY_PAIRS)]
+
+
+class RowPrepArgs(ctypes.Structure):
+    """Mirror of `qli_row_prep` (field order and types as in include/qli.h)."""
+    _fields_ = [("width", c_int32), ("norm", c_int32), ("eps", ctypes.c_float), ("reserved", c_int32),
+                ("weight", c_void_p), ("bias", c_void_p), ("rotary", RotaryArgs)]
+
+
+class RotateArgs(ctypes.Structure):
+    """Mirror of `qli_rotate_args` (field order and types as in include/qli.h)."""
+    _fields_ = [
+        ("x", c_void_p), ("x_stride_t", c_int64), ("x_stride_h", c_int64),
+        ("T", c_int32), ("H", c_int32), ("D", c_int32), ("inverse", c_int32),
+        ("positions", c_void_p),
+        ("out", c_void_p), ("out_stride_t", c_int64), ("out_stride_h", c_int64),
+    ]
+
+
+class PrepareArgs(ctypes.Structure):
+    """Mirror of `qli_prepare_args` (field order and types as in include/qli.h)."""
+    _fields_ = [
+        ("x", c_void_p), ("x_stride_t", c_int64), ("x_stride_h", c_int64),
+        ("T", c_int32), ("H", c_int32), ("positions", c_void_p),
+        ("out", c_void_p), ("out_stride_t", c_int64), ("out_stride_h", c_int64),
+        ("scale_out", c_void_p), ("quant_mode", c_int32), ("reserved", c_int32),
+    ]
+
+
+class AppendArgs(ctypes.Structure):
+    """Mirror of `qli_append_args` (field order and types as in include/qli.h)."""
+    _fields_ = [
+        ("kv", c_void_p), ("kv_stride", c_int64), ("index_k", c_void_p), ("index_stride", c_int64),
+        ("n", c_int64), ("positions", c_void_p), ("slot_mapping", c_void_p),
+        ("cache", c_void_p), ("num_pages", c_int64), ("page_stride", c_int64),
+        ("rows_per_page", c_int32), ("kv_mode", c_int32), ("quant_mode", c_int32), ("reserved", c_int32),
+        ("kv_offset", c_int64), ("kv_scale_offset", c_int64), ("k_offset", c_int64), ("scale_offset", c_int64),
+        ("err_word", c_void_p),
+    ]
+
+
 def _packer(mirror):
     """A struct.Struct of the fields of `mirror` (scalars and pointers as ints, in
     the native layout): packing one call's arguments takes a fraction of what
@@ -119,6 +170,9 @@ def _packer(mirror):
 
 _pack_kv_attn = _packer(KVAttnArgs).pack
 _pack_merge = _packer(MergeArgs).pack
+_pack_rotate = _packer(RotateArgs).pack
+_pack_prepare = _packer(PrepareArgs).pack
+_pack_append = _packer(AppendArgs).pack
 
 EXPORTS = ["qli_validate", "qli_workspace_size", "qli_run", "qli_run_stage", "qli_launch_count",
            "qli_scores_layout", "qli_read_device_error", "qli_status_string", "qli_abi_version",
@@ -127,7 +181,9 @@ EXPORTS = ["qli_validate", "qli_workspace_size", "qli_run", "qli_run_stage", "ql
            "qli_check_quant_rounding",
            "qli_sparse_attention", "qli_attn_args_size",
            "qli_write_kv", "qli_read_kv", "qli_kv_attention", "qli_kv_attention_workspace_size",
-           "qli_kv_attn_args_size", "qli_merge_attention", "qli_merge_args_size"]
+           "qli_kv_attn_args_size", "qli_merge_attention", "qli_merge_args_size",
+           "qli_kv_tree_attention", "qli_rotate", "qli_prepare_q", "qli_append_kv", "qli_rotary_size", "qli_row_prep_size",
+           "qli_rotate_args_size", "qli_prepare_args_size", "qli_append_args_size"]
 
 _lib = None
 
@@ -179,12 +235,20 @@ def lib(path: Optional[str] = None) -> ctypes.CDLL:
                               c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p]
     # the structures may also come packed, as bytes
     L.qli_kv_attention.argtypes = [c_void_p, c_void_p, c_size_t, c_void_p]
+    L.qli_kv_tree_attention.argtypes = [c_void_p, c_void_p, c_int32, c_void_p, c_size_t, c_void_p]
     L.qli_kv_attention_workspace_size.argtypes = [c_void_p, ctypes.POINTER(c_size_t)]
     L.qli_merge_attention.argtypes = [c_void_p, c_void_p]
+    L.qli_rotate.argtypes = [c_void_p, c_void_p, c_void_p]
+    L.qli_prepare_q.argtypes = [c_void_p, c_void_p, c_void_p]
+    L.qli_append_kv.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p]
     for name in ("qli_write_kv", "qli_read_kv", "qli_kv_attention",
-                 "qli_kv_attention_workspace_size", "qli_merge_attention"):
+                 "qli_kv_attention_workspace_size", "qli_merge_attention",
+                 "qli_rotate", "qli_prepare_q", "qli_append_kv", "qli_kv_tree_attention"):
         getattr(L, name).restype = c_int32
-    for name, mirror in (("qli_kv_attn_args", KVAttnArgs), ("qli_merge_args", MergeArgs)):
+    for name, mirror in (("qli_kv_attn_args", KVAttnArgs), ("qli_merge_args", MergeArgs),
+                         ("qli_rotary", RotaryArgs), ("qli_row_prep", RowPrepArgs),
+                         ("qli_rotate_args", RotateArgs), ("qli_prepare_args", PrepareArgs),
+                         ("qli_append_args", AppendArgs)):
         size = getattr(L, name + "_size")
         size.restype = c_int64
         if size() != ctypes.sizeof(mirror):
@@ -646,6 +710,38 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
     another host thread or stream uses meanwhile; allocated when not given (on the
     default stream once per host thread and device). Returns (out [T, H, 512]
     BF16, lse [T, H] float32)."""
+    return _kv_attention(q, cu_seqlens_q, cache, block_table, rows_per_page, page_stride, kv_offset,
+                         kv_scale_offset, scale, indices, k_lens, residual, ratio, window, None, out, lse,
+                         workspace, err_word, stream, quant_mode)
+
+
+def kv_tree_attention(q, cu_seqlens_q, cache, block_table, *, k_lens, tree_mask, rows_per_page: int,
+                      page_stride: int, kv_offset: int, kv_scale_offset: int, scale: float,
+                      window: int = 0, out=None, lse=None, workspace=None, err_word=None, stream=None,
+                      quant_mode=QUANT_INT8):
+    """qli_kv_tree_attention: kv_attention for drafted tokens. A request's tokens are
+    the nodes of a tree; their rows are its last positions (k_lens [B] counts them).
+    Token t sees every position before them and the nodes i with bit i % 64 of word
+    i // 64 set in tree_mask [T, words] (int64; [T] for up to 64 nodes), as a rule
+    itself and its ancestors; with window > 0 the last `window` of these. Everything
+    else as for kv_attention."""
+    import torch
+    device = _first_cuda("q", q, torch.bfloat16, torch.cuda.current_device)
+    _check_cuda("tree_mask", tree_mask, torch.int64, device)
+    if tree_mask.dim() not in (1, 2) or tree_mask.shape[0] != q.shape[0] or not tree_mask.is_contiguous() \
+            or tree_mask.dim() == 2 and tree_mask.shape[1] < 1:
+        raise ValueError("tree_mask must be contiguous [T, words] or [T]")
+    if k_lens is None:
+        raise ValueError("k_lens must be given")
+    return _kv_attention(q, cu_seqlens_q, cache, block_table, rows_per_page, page_stride, kv_offset,
+                         kv_scale_offset, scale, None, k_lens, None, 1, window, tree_mask, out, lse,
+                         workspace, err_word, stream, quant_mode)
+
+
+def _kv_attention(q, cu_seqlens_q, cache, block_table, rows_per_page, page_stride, kv_offset,
+                  kv_scale_offset, scale, indices, k_lens, residual, ratio, window, tree_mask, out, lse,
+                  workspace, err_word, stream, quant_mode):
+    """kv_attention, or with tree_mask kv_tree_attention."""
     import torch
     device = _first_cuda("q", q, torch.bfloat16, torch.cuda.current_device)
     int32 = torch.int32
@@ -717,8 +813,13 @@ def kv_attention(q, cu_seqlens_q, cache, block_table, *, rows_per_page: int, pag
     else:
         workspace = _empty(max(256, _workspace_bytes(T > 0 and H > 0, device)), torch.uint8,
                            q.device, stream, result=False)
-    _check((_lib or lib()).qli_kv_attention(a, workspace.data_ptr(), workspace.numel(), raw),
-           "qli_kv_attention")
+    if tree_mask is None:
+        _check((_lib or lib()).qli_kv_attention(a, workspace.data_ptr(), workspace.numel(), raw),
+               "qli_kv_attention")
+    else:
+        _check((_lib or lib()).qli_kv_tree_attention(
+            a, tree_mask.data_ptr(), 1 if tree_mask.dim() == 1 else tree_mask.shape[1], workspace.data_ptr(),
+            workspace.numel(), raw), "qli_kv_tree_attention")
     return out, lse
 
 
@@ -762,3 +863,227 @@ def merge_attention(outs, lses, *, out=None, lse=None, stream=None):
     raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
     _check((_lib or lib()).qli_merge_attention(a, raw), "qli_merge_attention")
     return out, lse
+
+
+class Rotary:
+    """A rotation of positions: pair i of a row at position p turns by p * f_i radians
+    and is multiplied by `magnitude`. The pairs are neighbouring values of the `dim`
+    rotated ones (layout "interleaved") or dim / 2 apart ("half"); dim is a multiple
+    of 16, at most 128.
+
+    f_i = base^(-2i / dim), or `frequencies` (dim / 2 of them). For contexts `factor`
+    times as long as the frequencies were made for, all are divided by it (position
+    interpolation: Chen et al. 2023), or with `trained`, the positions of the original
+    context, by parts (YaRN: Peng et al. 2023): a pair that turns fewer than ramp[0]
+    times over them is divided, one that turns more than ramp[1] times stays, those
+    between are blended linearly. A plan without device memory, made once for a model."""
+
+    def __init__(self, dim: int, *, base: float = 10000.0, layout: str = "interleaved",
+                 factor: float = 1.0, trained: Optional[int] = None, ramp=(1.0, 32.0),
+                 magnitude: float = 1.0, frequencies=None):
+        if dim < 16 or dim > 2 * ROTARY_PAIRS or dim % 16:
+            raise ValueError("dim must be a multiple of 16 up to %d" % (2 * ROTARY_PAIRS))
+        if layout not in ROTARY_LAYOUTS:
+            raise ValueError("layout must be one of %s" % sorted(ROTARY_LAYOUTS))
+        if not math.isfinite(magnitude) or magnitude <= 0:
+            raise ValueError("magnitude must be positive")
+        if frequencies is None:
+            if not math.isfinite(base) or base <= 0:
+                raise ValueError("base must be positive")
+            f = [float(base) ** (-2.0 * i / dim) for i in range(dim // 2)]
+        else:
+            f = [float(v) for v in frequencies]
+            if len(f) != dim // 2 or not all(math.isfinite(v) for v in f):
+                raise ValueError("frequencies must be dim / 2 finite numbers")
+        if not math.isfinite(factor) or factor <= 0:
+            raise ValueError("factor must be positive")
+        if trained is not None:
+            low, high = ramp
+            if not trained > 0 or not low < high:
+                raise ValueError("trained must be positive and ramp rise")
+            turned = [trained * abs(v) / (2 * math.pi) for v in f]
+            keep = [min(1.0, max(0.0, (t - low) / (high - low))) for t in turned]
+        else:
+            keep = [0.0] * len(f)
+        self.dim, self.layout, self.magnitude = dim, layout, float(magnitude)
+        self.frequencies = f if factor == 1.0 else [v * (k + (1.0 - k) / factor) for v, k in zip(f, keep)]
+        self._turns = [round(math.ldexp(v / (2 * math.pi), 64)) % (1 << 64) for v in self.frequencies]
+        self._packed = {}
+
+    def args(self, offset: int) -> RotaryArgs:
+        """The library's structure for rows whose rotated values start at `offset`."""
+        return RotaryArgs(self.dim // 2, ROTARY_LAYOUTS[self.layout], offset, self.magnitude,
+                          (c_uint64 * ROTARY_PAIRS)(*self._turns))
+
+    def packed(self, offset: int) -> bytes:
+        if offset not in self._packed:
+            self._packed[offset] = bytes(self.args(offset))
+        return self._packed[offset]
+
+
+class RowPrep:
+    """What prepare_q and append_kv do to a row of `width` values before it is
+    rounded: the norm (None, "rms" or "layer", with float32 CUDA weight and, for
+    "layer", bias [width], both optional), then the rotation of the values from
+    `offset` on (None: none). A plan made once with a layer's weights; it keeps
+    them alive."""
+
+    def __init__(self, width: int, *, norm: Optional[str] = None, weight=None, bias=None,
+                 eps: float = 1e-6, rotary: Optional[Rotary] = None, offset: int = 0):
+        import torch
+        if norm not in NORMS:
+            raise ValueError("norm must be None, 'rms' or 'layer'")
+        if weight is not None and norm is None or bias is not None and norm != "layer":
+            raise ValueError("weight needs a norm and bias the layer norm")
+        self.device = None
+        for name, t in (("weight", weight), ("bias", bias)):
+            if t is None:
+                continue
+            if self.device is None:
+                _require_cuda(name, t, torch.float32)
+                self.device = t.get_device()
+            _check_cuda(name, t, torch.float32, self.device)
+            if t.shape != (width,) or not t.is_contiguous():
+                raise ValueError("%s must be contiguous [%d]" % (name, width))
+        self.width, self.rotary, self.weight, self.bias = width, rotary, weight, bias
+        self.packed = bytes(RowPrepArgs(width, NORMS[norm], eps, 0, _ptr(weight), _ptr(bias),
+                                        rotary.args(offset) if rotary is not None else RotaryArgs()))
+
+
+def _positions(positions, n, device):
+    """The address of a call's positions [n]."""
+    import torch
+    _check_cuda("positions", positions, torch.int32, device)
+    if positions.numel() != n or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous [%d] tensor" % n)
+    return positions.data_ptr()
+
+
+def _row_strides(t, T, H, D):
+    """Strides of t [T, H, D] over its tokens and heads; those of a dimension of size
+    one may be any number."""
+    st, sh, _ = t.stride()
+    return (st if T > 1 else H * D), (sh if H > 1 else D)
+
+
+def _row_output(name, out, dtype, shape, device, stream):
+    import torch
+    if out is None:
+        return _empty(shape, dtype, torch.device("cuda", device), stream)
+    _check_cuda(name, out, dtype, device)
+    if out.shape != shape or out.stride(-1) != 1:
+        raise ValueError("%s must be %s with unit stride in the last dim" % (name, list(shape)))
+    return out
+
+
+def rotate(x, positions, rotary: Rotary, *, offset: int = 0, inverse: bool = False, out=None,
+           stream=None):
+    """qli_rotate: x [T, H, D] (BF16, CUDA, unit stride in D) with the rotary.dim
+    values from `offset` on (a multiple of 8) of every head rotated by its token's
+    position in positions [T] (int32); inverse=True undoes that. out=x rotates in
+    place. Returns out [T, H, D]."""
+    import torch
+    device = _first_cuda("x", x, torch.bfloat16, torch.cuda.current_device)
+    if x.dim() != 3 or x.stride(2) != 1:
+        raise ValueError("x must be [T, H, D] with unit stride in the last dim")
+    T, H, D = x.shape
+    pos = _positions(positions, T, device)
+    out = _row_output("out", out, torch.bfloat16, x.shape, device, stream)
+    raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    a = _pack_rotate(x.data_ptr(), *_row_strides(x, T, H, D), T, H, D, int(inverse), pos,
+                     out.data_ptr(), *_row_strides(out, T, H, D))
+    _check((_lib or lib()).qli_rotate(a, rotary.packed(offset), raw), "qli_rotate")
+    return out
+
+
+def prepare_q(x, positions, prep: RowPrep, *, out=None, scale_out=None, stream=None,
+              quant_mode=None):
+    """qli_prepare_q: the norm and rotation of `prep` on every row of x [T, H, width]
+    (BF16, CUDA, unit stride in the last dim; width 64, 128, 256 or 512) at its
+    token's position in positions [T] (int32; None without a rotation). Returns out
+    [T, H, width] BF16 (out=x in place), or with quant_mode (rows of 128) the codes
+    int8 [T, H, 128] and FP16 scale bits int16 [T, H], as quantize_q does."""
+    import torch
+    device = _first_cuda("x", x, torch.bfloat16, torch.cuda.current_device)
+    if x.dim() != 3 or x.stride(2) != 1 or x.shape[2] != prep.width:
+        raise ValueError("x must be [T, H, %d] with unit stride in the last dim" % prep.width)
+    if prep.device is not None and prep.device != device:
+        raise ValueError("the weights of prep are on CUDA device %d, x on device %d" % (prep.device, device))
+    T, H, D = x.shape
+    if positions is not None:
+        pos = _positions(positions, T, device)
+    elif prep.rotary is None:
+        pos = 0
+    else:
+        raise ValueError("a rotation needs positions")
+    sc = 0
+    if quant_mode is None:
+        if scale_out is not None:
+            raise ValueError("scale_out needs a quant_mode")
+        out = _row_output("out", out, torch.bfloat16, x.shape, device, stream)
+    else:
+        if quant_mode not in (QUANT_INT8, QUANT_FP8):
+            raise ValueError("quant_mode must be QUANT_INT8 or QUANT_FP8")
+        out = _row_output("out", out, torch.int8, x.shape, device, stream)
+        scale_out = _row_output("scale_out", scale_out, torch.int16, x.shape[:2], device, stream)
+        if not scale_out.is_contiguous():
+            raise ValueError("scale_out must be contiguous [T, H]")
+        sc = scale_out.data_ptr()
+    raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    a = _pack_prepare(x.data_ptr(), *_row_strides(x, T, H, D), T, H, pos, out.data_ptr(),
+                      *_row_strides(out, T, H, D), sc, quant_mode or 0, 0)
+    _check((_lib or lib()).qli_prepare_q(a, prep.packed, raw), "qli_prepare_q")
+    return out if quant_mode is None else (out, scale_out)
+
+
+def append_kv(kv, index_k, positions, slot_mapping, cache, *, rows_per_page: int, page_stride: int,
+              kv_prep: Optional[RowPrep] = None, index_prep: Optional[RowPrep] = None,
+              kv_offset: int = 0, kv_scale_offset: int = 0, k_offset: int = 0, scale_offset: int = 0,
+              kv_mode: int = QUANT_INT8, err_word=None, stream=None, quant_mode: int = QUANT_INT8):
+    """qli_append_kv: the norm and rotation of kv_prep on the rows of kv [n, 512] and
+    of index_prep on those of index_k [n, 128] (BF16, CUDA, unit stride in the last
+    dim; either may be None), at positions [n] (int32; None without a rotation),
+    written into the page pool `cache` (uint8, CUDA) at slot_mapping [n] (int64: page
+    * rows_per_page + row; negative = skip): KV rows in kv_mode (KV_BF16, QUANT_INT8
+    or QUANT_FP8), index K rows in quant_mode (QUANT_INT8 or QUANT_FP8)."""
+    import torch
+    first, name = (kv, "kv") if kv is not None else (index_k, "index_k")
+    device = _first_cuda(name, first, torch.bfloat16, torch.cuda.current_device)
+    _check_cuda("slot_mapping", slot_mapping, torch.int64, device)
+    _check_cuda("cache", cache, torch.uint8, device)
+    err = 0
+    if err_word is not None:
+        _check_cuda("err_word", err_word, torch.int32, device)
+        err = err_word.data_ptr()
+    if not cache.is_contiguous() or not slot_mapping.is_contiguous():
+        raise ValueError("cache and slot_mapping must be contiguous")
+    n, turns, at = slot_mapping.numel(), False, []
+    for name, x, prep, width in (("kv", kv, kv_prep, 512), ("index_k", index_k, index_prep, 128)):
+        if x is None:
+            at += [0, width]
+            continue
+        _check_cuda(name, x, torch.bfloat16, device)
+        if x.dim() != 2 or x.shape[1] != width or x.stride(1) != 1:
+            raise ValueError("%s must be [n, %d] with unit stride in the last dim" % (name, width))
+        if x.shape[0] != n:
+            raise ValueError("one slot per row")
+        if prep is None or prep.width != width:
+            raise ValueError("%s needs a RowPrep of width %d" % (name, width))
+        if prep.device is not None and prep.device != device:
+            raise ValueError("the weights of %s's RowPrep are on CUDA device %d, the call's tensors on device %d"
+                             % (name, prep.device, device))
+        turns |= prep.rotary is not None
+        at += [x.data_ptr(), x.stride(0) if n > 1 else width]
+    if positions is not None:
+        pos = _positions(positions, n, device)
+    elif turns:
+        raise ValueError("a rotation needs positions")
+    else:
+        pos = 0
+    a = _pack_append(*at, n, pos, slot_mapping.data_ptr(), cache.data_ptr(), cache.numel() // page_stride,
+                     page_stride, rows_per_page, kv_mode, quant_mode, 0, kv_offset, kv_scale_offset,
+                     k_offset, scale_offset, err)
+    raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    _check((_lib or lib()).qli_append_kv(a, kv_prep.packed if kv is not None else None,
+                                         index_prep.packed if index_k is not None else None, raw),
+           "qli_append_kv")
