@@ -12,7 +12,7 @@
 // Statistics and products are FP32. The angle is exact before it becomes FP32:
 // f_i is a whole number of 2^-64 turns, so p f_i modulo 2^64 is the fraction of a
 // turn whatever the position (an FP32 product would be 0.06 rad off at 10^6), and
-// its top 32 bits go to sincospif.
+// its top 32 bits are exact in 2^-32 turns.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -32,6 +32,7 @@ constexpr int kKvRow = 512, kIndexRow = 128;
 // A rotation: pairs of a row's values from unit `o8` on (units are 8 values).
 struct Turn {
   int32_t pairs, half, o8;
+  uint32_t per_pair;                       // 2^32 / pairs, rounded up
   float cos_scale, sin_scale;              // the magnitude; sin's sign is the direction
   uint64_t turns[QLI_ROTARY_PAIRS];
 };
@@ -43,47 +44,130 @@ struct Prep {
   Turn turn;
 };
 
+// Cosine and sine of 2^-32 `frac` turns. Within an eighth of a turn of the nearest
+// quarter, |t| <= pi / 4, the Taylor series up to t^9 and t^10 leave 2^-29 and 2^-30;
+// what is off is the rounding of t and of the sums, about 2^-24 together.
+__device__ __forceinline__ void turn_of(uint32_t frac, float& c, float& s) {
+  const uint32_t quarter = (frac + 0x20000000u) >> 30;
+  const float t = static_cast<float>(static_cast<int32_t>(frac - (quarter << 30))) *
+                  1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float t2 = t * t;
+  float p = fmaf(t2, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  p = fmaf(p, t2, 1.0f / 120.0f);
+  p = fmaf(p, t2, -1.0f / 6.0f);
+  const float sin_t = fmaf(p * t2, t, t);
+  float q = fmaf(t2, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  q = fmaf(q, t2, -1.0f / 720.0f);
+  q = fmaf(q, t2, 1.0f / 24.0f);
+  q = fmaf(q, t2, -0.5f);
+  const float cos_t = fmaf(q, t2, 1.0f);
+  const float a = quarter & 1u ? sin_t : cos_t, b = quarter & 1u ? cos_t : sin_t;
+  c = (quarter + 1u) & 2u ? -a : a;
+  s = quarter & 2u ? -b : b;
+}
+
 // (cos, sin) times the magnitude of the tokens t0 .. t0 + n, by token and pair.
 __device__ __forceinline__ void fill_table(float2* table, const Turn& w, const int32_t* positions,
                                            int32_t t0, int32_t n) {
 #pragma unroll 1
-  for (int32_t i = threadIdx.x; i < n * w.pairs; i += kThreads) {
-    const int32_t t = i / w.pairs, p = i - t * w.pairs;
-    const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(__ldg(positions + t0 + t))) * w.turns[p];
+  for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(n * w.pairs); i += kThreads) {
+    const uint32_t t = __umulhi(i, w.per_pair), p = i - t * w.pairs;
+    // by its generic address: lanes that index the constant bank apart take turns
+    uint64_t f;
+    asm volatile("ld.u64 %0, [%1];" : "=l"(f) : "l"(w.turns + p));
+    const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(__ldg(positions + t0 + t))) * f;
     float s, c;
-    // 2^-31: half turns, as sincospif takes them
-    sincospif(static_cast<float>(static_cast<int32_t>(frac >> 32)) * 4.656612873077393e-10f, &s, &c);
+    turn_of(static_cast<uint32_t>(frac >> 32), c, s);
     table[i] = make_float2(c * w.cos_scale, s * w.sin_scale);
   }
 }
 
-__device__ __forceinline__ void unpack8(const uint4 v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+// Two FP32 numbers in one register pair, and the packed operations on them.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair_of(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 both(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+// Eight values of a row, in pairs of neighbours.
+struct Unit {
+  f32x2 p[4];
+};
+
+__device__ __forceinline__ Unit unpack8(const uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  Unit u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u.p[i] = pair_of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  return u;
+}
+
+__device__ __forceinline__ uint4 pack8(const Unit& u) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    const float2 x = both(u.p[i]);
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x.x, x.y);
     w[i] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Four entries of the table.
+__device__ __forceinline__ void load4(const float2* cs, float2 (&t)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(cs)[i];
+    t[2 * i] = make_float2(v.x, v.y);
+    t[2 * i + 1] = make_float2(v.z, v.w);
+  }
+}
+
 // Four neighbouring pairs in one unit.
-__device__ __forceinline__ void turn_neighbours(float (&x)[8], const float2* cs) {
+__device__ __forceinline__ void turn_neighbours(Unit& u, const float2* cs) {
+  float2 t[4];
+  load4(cs, t);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = x[2 * i], b = x[2 * i + 1];
-    const float2 t = cs[i];
-    x[2 * i] = a * t.x - b * t.y;
-    x[2 * i + 1] = b * t.x + a * t.y;
+    const float2 v = both(u.p[i]);
+    u.p[i] = fma2(pair_of(-v.y, v.x), pair_of(t[i].y, t[i].y), mul2(u.p[i], pair_of(t[i].x, t[i].x)));
+  }
+}
+
+// Eight values and the eight that are their pairs' other halves (`w`), by their own
+// eight entries: a cos + sign w sin, the sign -1 for first halves and 1 for second.
+__device__ __forceinline__ void turn_half(Unit& u, const Unit& w, const float2* cs, float sign) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float2 t[4];
+    load4(cs + 4 * k, t);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x2 c = pair_of(t[2 * i].x, t[2 * i + 1].x), s = pair_of(t[2 * i].y, t[2 * i + 1].y);
+      f32x2& a = u.p[2 * k + i];
+      a = fma2(mul2(w.p[2 * k + i], pair_of(sign, sign)), s, mul2(a, c));
+    }
   }
 }
 
@@ -97,43 +181,61 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// The lane's values of a weight or bias vector: out of L1, which holds them for every
+// row; kept in registers they would cost more warps than they save loads.
 template <int G>
-__device__ __forceinline__ void normalise(float (&v)[2][8], const Prep& p, int l) {
-  if (p.norm == QLI_NORM_NONE) return;
-  constexpr float kInv = 1.0f / (16 * G);
-  if (p.norm == QLI_NORM_LAYER) {
-    float s = 0.0f;
+__device__ __forceinline__ Unit vector_of(const float* from, int at) {
+  Unit u;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += v[i >> 3][i & 7];
-    const float mean = row_sum<G>(s) * kInv;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] -= mean;
+  for (int i = 0; i < 2; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(from) + 2 * at + i);
+    u.p[2 * i] = pair_of(v.x, v.y);
+    u.p[2 * i + 1] = pair_of(v.z, v.w);
   }
-  float s = 0.0f;
+  return u;
+}
+
+template <int G, int kNorm>
+__device__ __forceinline__ void normalise(Unit (&v)[2], const Prep& p, int l) {
+  constexpr float kInv = 1.0f / (16 * G);
+  if constexpr (kNorm == QLI_NORM_LAYER) {
+    f32x2 s = add2(v[0].p[0], v[1].p[0]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s = fmaf(v[i >> 3][i & 7], v[i >> 3][i & 7], s);
-  const float r = rsqrtf(row_sum<G>(s) * kInv + p.eps);
+    for (int i = 1; i < 4; ++i) s = add2(s, add2(v[0].p[i], v[1].p[i]));
+    const float2 e = both(s);
+    const float mean = row_sum<G>(e.x + e.y) * -kInv;
+    const f32x2 m = pair_of(mean, mean);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i >> 2].p[i & 3] = add2(v[i >> 2].p[i & 3], m);
+  }
+  f32x2 s = mul2(v[0].p[0], v[0].p[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s = fma2(v[i >> 2].p[i & 3], v[i >> 2].p[i & 3], s);
+  const float2 e = both(s);
+  const float r = rsqrtf(fmaf(row_sum<G>(e.x + e.y), kInv, p.eps));
+  const f32x2 r2 = pair_of(r, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i >> 2].p[i & 3] = mul2(v[i >> 2].p[i & 3], r2);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    float w[8], b[8];
+    if (p.weight) {
+      const Unit w = vector_of<G>(p.weight, l + k * G);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = 2 * (l + k * G) + i;
-      const float4 one = make_float4(1.0f, 1.0f, 1.0f, 1.0f), zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      *reinterpret_cast<float4*>(w + 4 * i) = p.weight ? __ldg(reinterpret_cast<const float4*>(p.weight) + at) : one;
-      *reinterpret_cast<float4*>(b + 4 * i) = p.bias ? __ldg(reinterpret_cast<const float4*>(p.bias) + at) : zero;
+      for (int i = 0; i < 4; ++i) v[k].p[i] = mul2(v[k].p[i], w.p[i]);
     }
+    if (kNorm == QLI_NORM_LAYER && p.bias) {
+      const Unit b = vector_of<G>(p.bias, l + k * G);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[k][i] = fmaf(v[k][i] * r, w[i], b[i]);
+      for (int i = 0; i < 4; ++i) v[k].p[i] = add2(v[k].p[i], b.p[i]);
+    }
   }
 }
 
 // `cs`: the row's token in the table.
-template <int G>
-__device__ __forceinline__ void turn_row(float (&v)[2][8], const Turn& w, const float2* cs, int l) {
-  if (w.pairs == 0) return;
+template <int G, bool kHalf>
+__device__ __forceinline__ void turn_row(Unit (&v)[2], const Turn& w, const float2* cs, int l) {
   const int r8 = w.pairs / 4;
-  if (!w.half) {
+  if constexpr (!kHalf) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int u = l + k * G - w.o8;
@@ -145,39 +247,46 @@ __device__ __forceinline__ void turn_row(float (&v)[2][8], const Turn& w, const 
   // unit; the slots that hold part of the rotation are the same for every lane
   const int h8 = r8 / 2;
   const bool slot0 = w.o8 < G, slot1 = w.o8 + r8 > G;
-  float other[2][8];
+  const auto partner = [&](int u) { return u < 0 || u >= r8 ? l : (u < h8 ? u + h8 : u - h8) + w.o8; };
+  const auto turn = [&](Unit& x, const Unit& y, int u) {
+    if (u >= 0 && u < r8) turn_half(x, y, cs + 8 * (u < h8 ? u : u - h8), u < h8 ? -1.0f : 1.0f);
+  };
+  Unit other[2];
+  if (slot0 && slot1) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (!(k ? slot1 : slot0)) continue;
-    const int u = l + k * G - w.o8;
-    const int from = u < 0 || u >= r8 ? l : (u < h8 ? u + h8 : u - h8) + w.o8;
+    for (int k = 0; k < 2; ++k) {
+      const int from = partner(l + k * G - w.o8);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = slot0 ? __shfl_sync(0xffffffffu, v[0][i], from & (G - 1), G) : 0.0f;
-      const float b = slot1 ? __shfl_sync(0xffffffffu, v[1][i], from & (G - 1), G) : 0.0f;
-      other[k][i] = from < G ? a : b;
+      for (int i = 0; i < 4; ++i) {
+        const f32x2 a = __shfl_sync(0xffffffffu, v[0].p[i], from & (G - 1), G);
+        const f32x2 b = __shfl_sync(0xffffffffu, v[1].p[i], from & (G - 1), G);
+        other[k].p[i] = from < G ? a : b;
+      }
     }
+    turn(v[0], other[0], l - w.o8);
+    turn(v[1], other[1], l + G - w.o8);
+    return;
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int u = l + k * G - w.o8;
-    if (u < 0 || u >= r8) continue;
-    const bool first = u < h8;
-    const float2* t = cs + 8 * (first ? u : u - h8);
+    if (k ? !slot1 : !slot0) continue;
+    const int u = l + k * G - w.o8, from = partner(u) & (G - 1);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 c = t[i];
-      v[k][i] = first ? v[k][i] * c.x - other[k][i] * c.y : v[k][i] * c.x + other[k][i] * c.y;
-    }
+    for (int i = 0; i < 4; ++i) other[k].p[i] = __shfl_sync(0xffffffffu, v[k].p[i], from, G);
+    turn(v[k], other[k], u);
   }
 }
 
-// The row's codes and the FP16 bits of its scale: s = FP16(max |x| / Q), code(x / s).
+// The row's codes and the FP16 bits of its scale: s = FP16(max |x| / Q), code(x / s),
+// the quotient as the other writers take it (qli_codes.cuh), two at a time.
 template <int G, bool kFp8>
-__device__ __forceinline__ uint16_t quantise(const float (&v)[2][8], uint2 (&codes)[2]) {
+__device__ __forceinline__ uint16_t quantise(const Unit (&v)[2], uint2 (&codes)[2]) {
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i >> 3][i & 7]));
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = both(v[i >> 2].p[i & 3]);
+    m = fmaxf(fmaxf(m, fabsf(x.x)), fabsf(x.y));
+  }
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const uint16_t sb = scale_bits_of<kFp8>(m);
@@ -185,6 +294,9 @@ __device__ __forceinline__ uint16_t quantise(const float (&v)[2][8], uint2 (&cod
   codes[0] = codes[1] = make_uint2(0u, 0u);
   if (sf == 0.0f) return 0u;
   const float y = __frcp_rn(sf);
+  const f32x2 y2 = pair_of(y, y), s2 = pair_of(-sf, -sf);
+  // under the largest scale alone a quotient can be far above the largest code
+  const bool huge = sb == 0x7bffu;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     uint32_t w[2];
@@ -192,16 +304,26 @@ __device__ __forceinline__ uint16_t quantise(const float (&v)[2][8], uint2 (&cod
     for (int j = 0; j < 2; ++j) {
       float q[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = quotient(v[k][4 * j + i], sf, y);
+      for (int i = 0; i < 2; ++i) {
+        const f32x2 x = v[k].p[2 * j + i], q0 = mul2(x, y2);
+        const float2 r = both(fma2(fma2(q0, s2, x), y2, q0));
+        q[2 * i] = r.x;
+        q[2 * i + 1] = r.y;
+      }
       if constexpr (kFp8) {
         w[j] = e4m3x2_of(q[0], q[1]) | (e4m3x2_of(q[2], q[3]) << 16);
       } else {
-        // adding 1.5 * 2^23 rounds to an integer, ties to even, in the low bits
+        // adding 1.5 * 2^23 rounds to an integer, ties to even, in the low bits;
+        // two are clamped at a time as 16-bit halves
         uint32_t n[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          n[i] = __float_as_uint(__fadd_rn(fminf(fmaxf(q[i], -127.0f), 127.0f), 12582912.0f));
-        w[j] = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
+        for (int i = 0; i < 4; ++i) {
+          if (huge) q[i] = fminf(fmaxf(q[i], -127.0f), 127.0f);
+          n[i] = __float_as_uint(__fadd_rn(q[i], 12582912.0f));
+        }
+        const uint32_t lo = __vmins2(__vmaxs2(__byte_perm(n[0], n[1], 0x5410), 0xff81ff81u), 0x007f007fu);
+        const uint32_t hi = __vmins2(__vmaxs2(__byte_perm(n[2], n[3], 0x5410), 0xff81ff81u), 0x007f007fu);
+        w[j] = __byte_perm(lo, hi, 0x6420);
       }
     }
     codes[k] = make_uint2(w[0], w[1]);
@@ -210,11 +332,28 @@ __device__ __forceinline__ uint16_t quantise(const float (&v)[2][8], uint2 (&cod
 }
 
 // ---- where rows come from and go ------------------------------------------------
+// Quotients of numbers below 2^31: with 2^s >= d and m = ceil(2^(31 + s) / d), m d is at
+// most 2^s over 2^(31 + s), which moves r m / 2^(31 + s) by less than 1 / d.
+struct Divide {
+  uint32_t m;
+  int32_t shift;                           // s - 1; -1: by one
+  __device__ __forceinline__ int32_t operator()(int32_t r) const {
+    return shift < 0 ? r : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(r), m) >> shift);
+  }
+};
+Divide divide_by(int32_t d) {
+  int32_t s = 0;
+  while ((int64_t{1} << s) < d) ++s;
+  return Divide{static_cast<uint32_t>(((uint64_t{1} << (31 + s)) + static_cast<uint64_t>(d) - 1) / static_cast<uint64_t>(d)),
+                s - 1};
+}
+
 struct DenseIn {
   const uint16_t* x;
   int64_t st, sh;
   int32_t H;
-  __device__ __forceinline__ int32_t token(int32_t r) const { return r / H; }
+  Divide by_H;
+  __device__ __forceinline__ int32_t token(int32_t r) const { return by_H(r); }
   __device__ __forceinline__ const uint16_t* row(int32_t r, int32_t t) const {
     return x + t * st + (r - t * H) * sh;
   }
@@ -266,88 +405,132 @@ struct PagedOut {
   }
 };
 
-// Rows r0 .. r0 + kDepth * kThreads / G of `rows`, those of a warp in flight
-// together; the table of their tokens is made while they load.
-template <int D, int kMode, int kDepth, class In, class Out>
-__device__ __forceinline__ void pass(const In& in, const Out& out, const Prep& p,
-                                     const int32_t* positions, int32_t r0, int32_t rows, float2* table) {
-  constexpr int G = D / 16, kRows = kThreads / G;
-  const int l = threadIdx.x & (G - 1), g = threadIdx.x / G;
-  uint4 raw[kDepth][2];
-  int32_t tok[kDepth];
-  typename Out::Key key[kDepth];
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d) {
-    const int32_t r = min(r0 + d * kRows + g, rows - 1);
-    tok[d] = in.token(r);
-    const uint4* src = reinterpret_cast<const uint4*>(in.row(r, tok[d])) + l;
-    raw[d][0] = src[0];                    // coherent: the output may be the input
-    raw[d][1] = src[G];
-    key[d] = out.key(r);
+// Rows r0 .. end of a block, kThreads / G at a time: construct (loads the first ones),
+// fill the table of the rows' tokens from `t0` on, synchronise, run
+// (works on one set of rows while the next one loads).
+template <int D, int kMode, class In, class Out>
+struct Rows {
+  static constexpr int G = D / 16, kRows = kThreads / G;
+  const In& in;
+  const Out& out;
+  const Prep& p;
+  const int l;
+  int32_t r;
+  const int32_t end;
+  uint4 raw[2];
+  int32_t tok;
+  typename Out::Key key;
+
+  __device__ __forceinline__ Rows(const In& in_, const Out& out_, const Prep& p_, int32_t r0, int32_t end_)
+      : in(in_), out(out_), p(p_), l(threadIdx.x & (G - 1)), r(r0 + static_cast<int32_t>(threadIdx.x) / G), end(end_) {
+    load();
   }
-  const int32_t t0 = in.token(r0);
-  if (p.turn.pairs) {
-    fill_table(table, p.turn, positions, t0, in.token(min(r0 + kDepth * kRows, rows) - 1) - t0 + 1);
-    __syncthreads();
+  __device__ __forceinline__ void load() {
+    // lanes past the end read the last row, so that every lane takes part in the sums
+    const int32_t at = min(r, end - 1);
+    tok = in.token(at);
+    const uint4* src = reinterpret_cast<const uint4*>(in.row(at, tok)) + l;
+    raw[0] = src[0];                       // coherent: the output may be the input
+    raw[1] = src[G];
+    key = out.key(at);
   }
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d) {
-    const int32_t r = r0 + d * kRows + g;
-    float v[2][8];
-    unpack8(raw[d][0], v[0]);
-    unpack8(raw[d][1], v[1]);
-    normalise<G>(v, p, l);
-    turn_row<G>(v, p.turn, table + (tok[d] - t0) * p.turn.pairs, l);
-    uint16_t* scale = nullptr;
-    if constexpr (kMode == 0) {
-      uint8_t* dst = r < rows ? out.dest(r, tok[d], key[d], scale) : nullptr;
-      if (dst == nullptr) continue;
-      reinterpret_cast<uint4*>(dst)[l] = pack8(v[0]);
-      reinterpret_cast<uint4*>(dst)[l + G] = pack8(v[1]);
-    } else {
-      uint2 codes[2];
-      const uint16_t sb = quantise<G, kMode == QLI_QUANT_FP8>(v, codes);
-      uint8_t* dst = r < rows ? out.dest(r, tok[d], key[d], scale) : nullptr;
-      if (dst == nullptr) continue;
-      reinterpret_cast<uint2*>(dst)[l] = codes[0];
-      reinterpret_cast<uint2*>(dst)[l + G] = codes[1];
-      if (l == 0) *scale = sb;
+  __device__ __forceinline__ void run(const float2* table, int32_t t0) {
+    if (p.turn.half) run_norm<true>(table, t0); else run_norm<false>(table, t0);
+  }
+  template <bool kHalf>
+  __device__ __forceinline__ void run_norm(const float2* table, int32_t t0) {
+    if (p.norm == QLI_NORM_RMS) run_all<kHalf, QLI_NORM_RMS>(table, t0);
+    else if (p.norm == QLI_NORM_LAYER) run_all<kHalf, QLI_NORM_LAYER>(table, t0);
+    else run_all<kHalf, QLI_NORM_NONE>(table, t0);
+  }
+  template <bool kHalf, int kNorm>
+  __device__ __forceinline__ void run_all(const float2* table, int32_t t0) {
+    // the same number of turns for every thread of the block
+    const int32_t first = r - static_cast<int32_t>(threadIdx.x) / G;
+#pragma unroll 1
+    for (int32_t n = first; n < end; n += kRows) {
+      Unit v[2] = {unpack8(raw[0]), unpack8(raw[1])};
+      const int32_t t = tok, at = r;
+      const typename Out::Key to = key;
+      r += kRows;
+      if (n + kRows < end) load();
+      if constexpr (kNorm != QLI_NORM_NONE) normalise<G, kNorm>(v, p, l);
+      if (p.turn.pairs) turn_row<G, kHalf>(v, p.turn, table + (t - t0) * p.turn.pairs, l);
+      uint16_t* scale = nullptr;
+      if constexpr (kMode == 0) {
+        uint8_t* dst = at < end ? out.dest(at, t, to, scale) : nullptr;
+        if (dst == nullptr) continue;
+        reinterpret_cast<uint4*>(dst)[l] = pack8(v[0]);
+        reinterpret_cast<uint4*>(dst)[l + G] = pack8(v[1]);
+      } else {
+        uint2 codes[2];
+        const uint16_t sb = quantise<G, kMode == QLI_QUANT_FP8>(v, codes);
+        uint8_t* dst = at < end ? out.dest(at, t, to, scale) : nullptr;
+        if (dst == nullptr) continue;
+        reinterpret_cast<uint2*>(dst)[l] = codes[0];
+        reinterpret_cast<uint2*>(dst)[l + G] = codes[1];
+        if (l == 0) *scale = sb;
+      }
     }
   }
+};
+
+// Tokens that `count` rows in a row can belong to, of `rows` with H a token.
+int64_t tokens_of(int64_t count, int64_t rows, int64_t H) {
+  const int64_t in = rows < count ? rows : count;
+  const int64_t n = (in - 2 + H) / H + 1;
+  return n < in ? n : in;
 }
 
-// Entries of the table that a pass over rows of D values can need.
-template <int D, int kDepth>
-int64_t table_entries(int64_t rows, int64_t H, int32_t pairs) {
-  const int64_t most = kDepth * kThreads / (D / 16), in = rows < most ? rows : most;
-  return ((in - 1 + H - 1) / H + 1 < in ? (in - 1 + H - 1) / H + 1 : in) * pairs;
-}
+// Blocks an SM holds, by way of the registers: 4 with codes (64 registers; 3 blocks
+// without spills and 5 with more were slower), 5 with BF16 results.
+constexpr int kBlocksPerSm = 4, kBlocksPerSmBf16 = 5;
+// Sets of rows per block at most: the table and the start are paid once for them.
+constexpr int kSets = 4;
 
 // ---- queries --------------------------------------------------------------------
-constexpr int kQueryDepth = 1;
-
+// Bound by HBM with BF16 results: 2047 tokens of 64 heads x 512 with RMS norm and a
+// rotated tail (268 MB) take 44 us, 6.0 TB/s. With codes by the instructions, some 16 a
+// value: 4096 tokens of 64 heads x 128 to E4M3 (101 MB) take 23 us, 4.3 TB/s, 70% of
+// the issue slots. One set of rows a block, without the next one in flight, took 59
+// and 32 us; the norm's and the layout's branches inside the loop 51 and 26.
 template <int D, int kMode>
-__global__ void __launch_bounds__(kThreads) prepare_kernel(const __grid_constant__ Prep p, DenseIn in,
+__global__ void __launch_bounds__(kThreads, kMode == 0 ? kBlocksPerSmBf16 : kBlocksPerSm) prepare_kernel(const __grid_constant__ Prep p, DenseIn in,
                                                            DenseOut<kMode> out, const int32_t* positions,
-                                                           int32_t rows) {
-  extern __shared__ float2 table[];
-  constexpr int kRows = kQueryDepth * kThreads / (D / 16);
-  pass<D, kMode, kQueryDepth>(in, out, p, positions, static_cast<int32_t>(blockIdx.x) * kRows, rows, table);
+                                                           int32_t rows, int32_t block_rows) {
+  extern __shared__ float4 table4[];
+  float2* table = reinterpret_cast<float2*>(table4);
+  const int32_t r0 = static_cast<int32_t>(blockIdx.x) * block_rows, end = min(rows - r0, block_rows) + r0;
+  Rows<D, kMode, DenseIn, DenseOut<kMode>> work(in, out, p, r0, end);
+  const int32_t t0 = in.token(r0);
+  if (p.turn.pairs) {
+    fill_table(table, p.turn, positions, t0, in.token(end - 1) - t0 + 1);
+    __syncthreads();
+  }
+  work.run(table, t0);
 }
+
+constexpr int64_t kTableBytes = 16 * 1024;   // what one set needs at most: 2048 entries
 
 template <int D, int kMode>
 cudaError_t launch_prepare(const Prep& p, const DenseIn& in, const DenseOut<kMode>& out,
-                           const int32_t* positions, int32_t rows, cudaStream_t s) {
-  constexpr int kRows = kQueryDepth * kThreads / (D / 16);
-  const size_t smem = sizeof(float2) * table_entries<D, kQueryDepth>(rows, in.H, p.turn.pairs);
-  prepare_kernel<D, kMode><<<static_cast<unsigned>((rows - 1) / kRows + 1), kThreads, smem, s>>>(
-      p, in, out, positions, rows);
+                           const int32_t* positions, int32_t rows, int sms, cudaStream_t s) {
+  constexpr int kRows = kThreads / (D / 16);
+  const int64_t sets = (static_cast<int64_t>(rows) - 1) / kRows + 1;
+  int64_t each = sets / (static_cast<int64_t>(sms) * kBlocksPerSm);
+  each = each < 1 ? 1 : each > kSets ? kSets : each;
+  const auto bytes = [&] {
+    return static_cast<int64_t>(sizeof(float2)) * tokens_of(each * kRows, rows, in.H) * p.turn.pairs;
+  };
+  while (each > 1 && bytes() > kTableBytes) --each;
+  const int32_t block_rows = static_cast<int32_t>(each) * kRows;
+  const size_t smem = static_cast<size_t>(bytes());
+  prepare_kernel<D, kMode><<<static_cast<unsigned>((rows - 1) / block_rows + 1), kThreads, smem, s>>>(
+      p, in, out, positions, rows, block_rows);
   return cudaGetLastError();
 }
 
 // ---- cache rows -----------------------------------------------------------------
-constexpr int kKvDepth = 1, kIndexDepth = 1;
-
 template <int kKv, int kIndex>
 struct AppendArgs {
   Prep kv, index;
@@ -355,21 +538,34 @@ struct AppendArgs {
   PagedOut<kKv> kv_out;
   PagedOut<kIndex> index_out;
   const int32_t* positions;
-  int32_t n, kv_blocks;
+  int32_t n, block_rows;
+  int32_t index_table;                     // entry of the table where the index K's begins; 0: the same one
 };
 
-// The first blocks take the KV rows, the others the index K rows.
+// A block takes a few tokens: their KV rows, then their index K rows, by one table where
+// they turn alike. Bound by the instructions: 65536 tokens to E4M3 (127 MB) take 37 us,
+// 3.4 TB/s; separate blocks for the two kinds, each with its table, took 54.
 template <int kKv, int kIndex>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs<kKv, kIndex> a) {
-  extern __shared__ float2 table[];
-  const int32_t b = static_cast<int32_t>(blockIdx.x);
-  if (b < a.kv_blocks) {
-    constexpr int kRows = kKvDepth * kThreads / (kKvRow / 16);
-    pass<kKvRow, kKv, kKvDepth>(a.kv_in, a.kv_out, a.kv, a.positions, b * kRows, a.n, table);
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const __grid_constant__ AppendArgs<kKv, kIndex> a) {
+  extern __shared__ float4 table4[];
+  float2* table = reinterpret_cast<float2*>(table4);
+  const int32_t r0 = static_cast<int32_t>(blockIdx.x) * a.block_rows, end = min(a.n - r0, a.block_rows) + r0;
+  const auto turns = [&] {
+    if (a.kv.turn.pairs) fill_table(table, a.kv.turn, a.positions, r0, end - r0);
+    if (a.index.turn.pairs && (a.index_table || !a.kv.turn.pairs))
+      fill_table(table + a.index_table, a.index.turn, a.positions, r0, end - r0);
+    __syncthreads();
+  };
+  if (a.kv_in.x) {
+    Rows<kKvRow, kKv, FlatIn, PagedOut<kKv>> work(a.kv_in, a.kv_out, a.kv, r0, end);
+    turns();
+    work.run(table, r0);
   } else {
-    constexpr int kRows = kIndexDepth * kThreads / (kIndexRow / 16);
-    pass<kIndexRow, kIndex, kIndexDepth>(a.index_in, a.index_out, a.index, a.positions,
-                                         (b - a.kv_blocks) * kRows, a.n, table);
+    turns();
+  }
+  if (a.index_in.x) {
+    Rows<kIndexRow, kIndex, FlatIn, PagedOut<kIndex>> work(a.index_in, a.index_out, a.index, r0, end);
+    work.run(table + a.index_table, r0);
   }
 }
 
@@ -388,7 +584,8 @@ struct RotateArgs {
 };
 
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
-  extern __shared__ float2 table[];
+  extern __shared__ float4 table4[];
+  float2* table = reinterpret_cast<float2*>(table4);
   const int32_t r0 = static_cast<int32_t>(blockIdx.x) * a.block_rows;
   const int32_t n = min(a.block_rows, a.rows - r0), t0 = r0 / a.H;
   const int h8 = a.turn.pairs / 8;
@@ -404,19 +601,13 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
   fill_table(table, a.turn, a.positions, t0, (r0 + n - 1) / a.H - t0 + 1);
   __syncthreads();
   if (some) {
-    float x[8], y[8];
-    unpack8(v0, x);
-    unpack8(v1, y);
+    Unit x = unpack8(v0), y = unpack8(v1);
     const int w = u - a.turn.o8;
     const float2* cs = table + (t - t0) * a.turn.pairs;
     if (a.turn.half) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 c = cs[8 * w + i];
-        const float p = x[i], q = y[i];
-        x[i] = p * c.x - q * c.y;
-        y[i] = q * c.x + p * c.y;
-      }
+      const Unit was = x;
+      turn_half(x, y, cs + 8 * w, -1.0f);
+      turn_half(y, was, cs + 8 * w, 1.0f);
     } else {
       turn_neighbours(x, cs + 4 * w);
       turn_neighbours(y, cs + 4 * (w + h8));
@@ -453,6 +644,7 @@ Turn make_turn(const qli_rotary& r, bool inverse) {
   w.pairs = r.pairs;
   w.half = r.layout == QLI_ROTARY_HALF ? 1 : 0;
   w.o8 = r.offset / 8;
+  w.per_pair = static_cast<uint32_t>(((uint64_t{1} << 32) - 1) / static_cast<uint32_t>(r.pairs) + 1);
   w.cos_scale = inverse ? 1.0f / r.magnitude : r.magnitude;
   w.sin_scale = inverse ? -w.cos_scale : w.cos_scale;
   std::memcpy(w.turns, r.turns, sizeof(uint64_t) * static_cast<size_t>(r.pairs));
@@ -500,46 +692,56 @@ qli_status check_dense(const void* x, int64_t x_st, int64_t x_sh, int32_t T, int
 }
 
 template <int kMode>
-cudaError_t launch_width(const qli_prepare_args& a, const Prep& p, int32_t width, cudaStream_t s) {
-  const DenseIn in{a.x, a.x_stride_t, a.x_stride_h, a.H};
+cudaError_t launch_width(const qli_prepare_args& a, const Prep& p, int32_t width, int sms, cudaStream_t s) {
+  const DenseIn in{a.x, a.x_stride_t, a.x_stride_h, a.H, divide_by(a.H)};
   const int64_t unit = kMode == 0 ? 2 : 1;
   const DenseOut<kMode> out{static_cast<uint8_t*>(a.out), a.out_stride_t * unit, a.out_stride_h * unit, a.scale_out, a.H};
   const int32_t rows = a.T * a.H;
   if constexpr (kMode == 0) {
-    if (width == 64) return launch_prepare<64, 0>(p, in, out, a.positions, rows, s);
-    if (width == 256) return launch_prepare<256, 0>(p, in, out, a.positions, rows, s);
-    if (width == 512) return launch_prepare<512, 0>(p, in, out, a.positions, rows, s);
+    if (width == 64) return launch_prepare<64, 0>(p, in, out, a.positions, rows, sms, s);
+    if (width == 256) return launch_prepare<256, 0>(p, in, out, a.positions, rows, sms, s);
+    if (width == 512) return launch_prepare<512, 0>(p, in, out, a.positions, rows, sms, s);
   }
-  return launch_prepare<128, kMode>(p, in, out, a.positions, rows, s);
+  return launch_prepare<128, kMode>(p, in, out, a.positions, rows, sms, s);
 }
 
+// Tokens per block: enough for whole warps of index K rows while there are blocks for
+// the SMs to hold, else one set of KV rows.
+constexpr int kFewTokens = kThreads / (kKvRow / 16), kManyTokens = kThreads / (kIndexRow / 16);
+
 template <int kKv, int kIndex>
-cudaError_t launch_append(const qli_append_args& a, const qli_row_prep* kv, const qli_row_prep* index, cudaStream_t s) {
+cudaError_t launch_append(const qli_append_args& a, const qli_row_prep* kv, const qli_row_prep* index, int sms,
+                          cudaStream_t s) {
   AppendArgs<kKv, kIndex> d{};
   d.positions = a.positions;
   d.n = static_cast<int32_t>(a.n);
+  d.block_rows = a.n >= static_cast<int64_t>(sms) * kBlocksPerSm * kManyTokens ? kManyTokens : kFewTokens;
   const int64_t slots = a.num_pages * a.rows_per_page;
   const int32_t log2R = a.rows_per_page == 64 ? 6 : 7;
-  int64_t blocks = 0, table = 0;
+  const int64_t tokens = tokens_of(d.block_rows, a.n, 1);
   if (a.kv) {
     d.kv = make_prep(*kv);
     d.kv_in = FlatIn{a.kv, a.kv_stride};
     d.kv_out = PagedOut<kKv>{a.slot_mapping, a.cache, slots, a.page_stride, a.kv_offset, a.kv_scale_offset, log2R,
                              kKv == 0 ? 2 * kKvRow : kKvRow, a.err_word};
-    blocks = (a.n - 1) / (kKvDepth * kThreads / (kKvRow / 16)) + 1;
-    table = table_entries<kKvRow, kKvDepth>(a.n, 1, d.kv.turn.pairs);
   }
-  d.kv_blocks = static_cast<int32_t>(blocks);
+  int64_t entries = tokens * d.kv.turn.pairs;
   if (a.index_k) {
     d.index = make_prep(*index);
     d.index_in = FlatIn{a.index_k, a.index_stride};
     d.index_out = PagedOut<kIndex>{a.slot_mapping, a.cache, slots, a.page_stride, a.k_offset, a.scale_offset, log2R,
                                    kIndexRow, a.err_word};
-    blocks += (a.n - 1) / (kIndexDepth * kThreads / (kIndexRow / 16)) + 1;
-    const int64_t more = table_entries<kIndexRow, kIndexDepth>(a.n, 1, d.index.turn.pairs);
-    table = more > table ? more : table;
+    const Turn &x = d.kv.turn, &y = d.index.turn;
+    // the same angles and magnitude: one table, whatever the layouts and offsets
+    const bool same = x.pairs == y.pairs && x.cos_scale == y.cos_scale &&
+                      std::memcmp(x.turns, y.turns, sizeof(x.turns)) == 0;
+    if (!same) {
+      d.index_table = static_cast<int32_t>(entries);
+      entries += tokens * y.pairs;
+    }
   }
-  append_kernel<kKv, kIndex><<<static_cast<unsigned>(blocks), kThreads, sizeof(float2) * table, s>>>(d);
+  append_kernel<kKv, kIndex><<<static_cast<unsigned>((a.n - 1) / d.block_rows + 1), kThreads,
+                               sizeof(float2) * static_cast<size_t>(entries), s>>>(d);
   return cudaGetLastError();
 }
 
@@ -612,9 +814,9 @@ extern "C" qli_status qli_prepare_q(const qli_prepare_args* a, const qli_row_pre
   if (st != QLI_OK) return st;
   const Prep p = make_prep(*prep);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->quant_mode == 0                ? launch_width<0>(*a, p, D, s)
-                        : a->quant_mode == QLI_QUANT_INT8 ? launch_width<QLI_QUANT_INT8>(*a, p, D, s)
-                                                          : launch_width<QLI_QUANT_FP8>(*a, p, D, s);
+  const cudaError_t e = a->quant_mode == 0                ? launch_width<0>(*a, p, D, sms, s)
+                        : a->quant_mode == QLI_QUANT_INT8 ? launch_width<QLI_QUANT_INT8>(*a, p, D, sms, s)
+                                                          : launch_width<QLI_QUANT_FP8>(*a, p, D, sms, s);
   return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
 }
 
@@ -675,14 +877,14 @@ extern "C" qli_status qli_append_kv(const qli_append_args* a, const qli_row_prep
   const bool f8 = a->quant_mode == QLI_QUANT_FP8;
   cudaError_t e = cudaErrorInvalidValue;
   if (a->kv_mode == 0)
-    e = f8 ? launch_append<0, QLI_QUANT_FP8>(*a, kv_prep, index_prep, s)
-           : launch_append<0, QLI_QUANT_INT8>(*a, kv_prep, index_prep, s);
+    e = f8 ? launch_append<0, QLI_QUANT_FP8>(*a, kv_prep, index_prep, sms, s)
+           : launch_append<0, QLI_QUANT_INT8>(*a, kv_prep, index_prep, sms, s);
   else if (a->kv_mode == QLI_QUANT_INT8)
-    e = f8 ? launch_append<QLI_QUANT_INT8, QLI_QUANT_FP8>(*a, kv_prep, index_prep, s)
-           : launch_append<QLI_QUANT_INT8, QLI_QUANT_INT8>(*a, kv_prep, index_prep, s);
+    e = f8 ? launch_append<QLI_QUANT_INT8, QLI_QUANT_FP8>(*a, kv_prep, index_prep, sms, s)
+           : launch_append<QLI_QUANT_INT8, QLI_QUANT_INT8>(*a, kv_prep, index_prep, sms, s);
   else
-    e = f8 ? launch_append<QLI_QUANT_FP8, QLI_QUANT_FP8>(*a, kv_prep, index_prep, s)
-           : launch_append<QLI_QUANT_FP8, QLI_QUANT_INT8>(*a, kv_prep, index_prep, s);
+    e = f8 ? launch_append<QLI_QUANT_FP8, QLI_QUANT_FP8>(*a, kv_prep, index_prep, sms, s)
+           : launch_append<QLI_QUANT_FP8, QLI_QUANT_INT8>(*a, kv_prep, index_prep, sms, s);
   return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
 }
 
