@@ -60,6 +60,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "qli_internal.h"
 #include "qli_meta.cuh"
@@ -95,7 +96,6 @@ struct Smem {
   uint8_t q[kTile];                            // 1024-aligned
   uint8_t p[2][kPos * 128];                    // 1024-aligned, by unit parity
   int32_t tokV[kChunkT], tokB[kChunkT];        // visible positions and request of the launch's tokens
-  int32_t treeP[kChunkT], treeR[kChunkT], treeN[kChunkT];  // drafted trees: see Tree
   const uint8_t* row[kSlots][kPos];            // the rows' codes, by unit modulo kSlots
   float rs[kSlots][kPos];                      // and scales; 0: no position
   float sl2[2][kHT];                           // by row tile parity: softmax scale in log2 over the
@@ -109,8 +109,24 @@ struct Smem {
   uint64_t full[2][2], empty[2][2], sfull[2], sfree[2], rowfull[kSlots], rowfree[kSlots], qfull, qempty, pready[2], done;
   uint32_t tmem_base;
 };
-constexpr int kSmemBytes = static_cast<int>(sizeof(Smem)) + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// What drafted trees add (see there), per token of the launch and per unit.
+constexpr int kMaxWords = 256;                 // of a token's mask
+constexpr int kMaxStack = 8;                   // tokens of a group
+constexpr int kTreeChunkT = 384;               // tokens planned per launch
+struct TreeSmem : Smem {
+  int32_t prefix[kTreeChunkT], rank0[kTreeChunkT];    // by token; rank0 by group
+  uint16_t nodes[kTreeChunkT], own[kTreeChunkT];      // the request's nodes in masks; those that the token sees
+  uint8_t tokens[kTreeChunkT], tiles[kTreeChunkT];    // by group: its tokens and row tiles (0: not the group's first token)
+  uint2 vis[kSlots][kPos];                     // rows of the row tile that see the position
+  uint32_t masked[kSlots][kRowWarps];          // 1: not all rows see all of a row warp's positions
+  uint8_t nan[kSlots][kPos];                   // 1: the position's row has NaN codes
+};
+template <bool kTree>
+using SmemOf = std::conditional_t<kTree, TreeSmem, Smem>;
+template <bool kTree>
+constexpr int kSmemBytes = static_cast<int>(sizeof(SmemOf<kTree>)) + 1024;
+static_assert(kSmemBytes<true> <= 227 * 1024, "shared memory");
 
 struct Args {
   const uint16_t* q;
@@ -129,7 +145,8 @@ struct Args {
   const int32_t* idx;
   int32_t K;
   const uint64_t* mask;        // drafted trees: [T][words], nodes that a token sees
-  int32_t words;
+  int32_t words, stack;        // words of a mask, tokens of a group
+  uint32_t per_head;           // 2^32 / H, rounded up
   float scale;
   uint16_t* out;
   int64_t o_st, o_sh;
@@ -341,11 +358,14 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 
 // The launch's units in order: token, row tile of the token, unit of kPos
 // positions. A token has at least one unit, so that every output is written.
+template <bool kTree = false>
 __device__ __forceinline__ int32_t positions_of(const Args& a, int32_t V) {
+  if constexpr (kTree) return V;
   return a.idx ? a.K : (a.window > 0 ? min(V, a.window) : V);
 }
+template <bool kTree = false>
 __device__ __forceinline__ int32_t units_of(const Args& a, int32_t V) {
-  const int32_t n = positions_of(a, V);
+  const int32_t n = positions_of<kTree>(a, V);
   return n <= kPos ? 1 : (n - 1) / kPos + 1;
 }
 
@@ -355,13 +375,24 @@ __device__ __forceinline__ int32_t share_begin(int32_t total, int32_t ctas, int3
   return each * c + min(c, total - each * ctas);
 }
 
-// A CTA's share, unit by unit.
+// A CTA's share, unit by unit. Of drafted trees, t is a group's first token.
+template <bool kTree>
 struct Walk {
+  typedef SmemOf<kTree> M;
   int32_t k, count;            // units behind, units of the share
   int32_t t, g, i, n;          // token (within the launch), row tile, unit of it, its units
-  __device__ __forceinline__ Walk(const Args& a, const Smem& S)
+  __device__ __forceinline__ Walk(const Args& a, const M& S)
       : k(0), count(S.count), t(S.start_t), g(S.start_g), i(S.start_i) {
-    n = units_of(a, S.tokV[t]);
+    n = units_of<kTree>(a, S.tokV[t]);
+  }
+  // the row tiles of t, and their rows: heads of one token or of several
+  __device__ __forceinline__ int32_t tiles(const Args& a, const M& S) const {
+    if constexpr (kTree) return S.tiles[t];
+    return a.hg;
+  }
+  __device__ __forceinline__ int32_t rows(const Args& a, const M& S) const {
+    if constexpr (kTree) return S.tokens[t] * a.H;
+    return a.H;
   }
   __device__ __forceinline__ bool valid() const { return k < count; }
   // first and last unit of the row tile in this CTA
@@ -369,13 +400,17 @@ struct Walk {
   __device__ __forceinline__ bool last() const { return i == n - 1 || k + 1 == count; }
   // at its last unit: whether the row tile began in this CTA
   __device__ __forceinline__ bool began_here() const { return k >= i; }
-  __device__ __forceinline__ void next(const Args& a, const Smem& S) {
+  __device__ __forceinline__ void next(const Args& a, const M& S) {
     ++k;
     if (++i < n) return;
     i = 0;
-    if (++g < a.hg) return;
+    if (++g < tiles(a, S)) return;
     g = 0;
-    if (++t < a.tc) n = units_of(a, S.tokV[t]);
+    ++t;
+    if constexpr (kTree) {
+      while (t < a.tc && S.tiles[t] == 0) ++t;
+    }
+    if (t < a.tc) n = units_of<kTree>(a, S.tokV[t]);
   }
 };
 
@@ -414,31 +449,40 @@ struct Requests {
 constexpr int kRequestsInSmem = 10000;
 static_assert((3 * kRequestsInSmem + 1) * 4 <= 2 * kTile, "the requests fit in the tiles");
 
-// Drafted trees. A request's last `nodes` positions (its tokens of the call) are
-// behind a prefix of P; a token sees the prefix and the nodes whose bits are set in
-// its mask, `seen` of them, in this order, and with a window the last n of these.
-// Its position e of n has the rank e + (seen - n) after the prefix's end: below 0
-// it is that far before the end, else the mask's set bit of that rank. So a unit
-// holds no position that the token does not see.
+// Drafted trees. A request's last positions are the nodes of a tree, its tokens of the
+// call; a token sees the prefix before them and the nodes whose bits are set in its
+// mask, with a window the last ones of these.
+// Up to `stack` neighbouring tokens of a request are a group, whose rows (token, head)
+// fill row tiles together: with fewer than 64 heads the products of a unit, which cost
+// the same for any, serve several tokens. A group's positions are the earliest window's
+// part of the prefix, then the nodes that any of its tokens sees; of a unit in which
+// some row does not see some position the row warps leave masks, by which the softmax
+// takes those scores as -inf. A position of rank e + rank0 below 0 is that far before
+// the prefix's end, else it is the set bit of that rank.
+// 16 tokens of 16 heads over 8K positions: XXX us, a token at a time XXX.
 __device__ __forceinline__ uint64_t tree_word(const Args& a, int32_t t, int32_t w, int32_t nodes) {
   const int32_t left = nodes - 64 * w;
   const uint64_t m = __ldg(reinterpret_cast<const unsigned long long*>(a.mask) + static_cast<int64_t>(t) * a.words + w);
   return left >= 64 ? m : left <= 0 ? 0u : m & ((uint64_t{1} << left) - 1);
 }
-// Positions that token t sees (n above) behind a prefix of P; seen - n.
-__device__ __forceinline__ int32_t tree_count(const Args& a, int32_t t, int32_t P, int32_t nodes, int32_t& rank0) {
-  int32_t seen = 0;
+// The nodes that any of `count` tokens from t on sees.
+__device__ __forceinline__ uint64_t tree_union(const Args& a, int32_t t, int32_t count, int32_t w, int32_t nodes) {
+  uint64_t m = 0u;
 #pragma unroll 1
-  for (int32_t w = 0; w < a.words && 64 * w < nodes; ++w) seen += __popcll(tree_word(a, t, w, nodes));
-  const int32_t n = a.window > 0 ? min(P + seen, a.window) : P + seen;
-  rank0 = seen - n;
+  for (int32_t k = 0; k < count; ++k) m |= tree_word(a, t + k, w, nodes);
+  return m;
+}
+__device__ __forceinline__ int32_t tree_count(const Args& a, int32_t t, int32_t count, int32_t nodes) {
+  int32_t n = 0;
+#pragma unroll 1
+  for (int32_t w = 0; 64 * w < nodes; ++w) n += __popcll(tree_union(a, t, count, w, nodes));
   return n;
 }
-// The set bit of that rank (from 0) in token t's mask; -1: there is none.
-__device__ __forceinline__ int32_t tree_node(const Args& a, int32_t t, int32_t nodes, int32_t rank) {
+// The set bit of that rank (from 0) in the tokens' union; -1: there is none.
+__device__ __forceinline__ int32_t tree_node(const Args& a, int32_t t, int32_t count, int32_t nodes, int32_t rank) {
 #pragma unroll 1
-  for (int32_t w = 0; w < a.words && 64 * w < nodes; ++w) {
-    uint64_t m = tree_word(a, t, w, nodes);
+  for (int32_t w = 0; 64 * w < nodes; ++w) {
+    uint64_t m = tree_union(a, t, count, w, nodes);
     const int32_t c = __popcll(m);
     if (rank >= c) {
       rank -= c;
@@ -457,6 +501,41 @@ __device__ __forceinline__ int32_t tree_node(const Args& a, int32_t t, int32_t n
     return at;
   }
   return -1;
+}
+// Whether token t (absolute), which sees `own` nodes, sees the node.
+__device__ __forceinline__ bool tree_sees(const Args& a, int32_t t, int32_t nodes, int32_t own, int32_t node) {
+  const uint64_t m = tree_word(a, t, node >> 6, nodes) >> (node & 63);
+  if (!(m & 1u)) return false;
+  if (a.window <= 0 || own <= a.window) return true;
+  // the window: nodes from this one on
+  int32_t later = __popcll(m);
+#pragma unroll 1
+  for (int32_t w = (node >> 6) + 1; 64 * w < nodes; ++w) later += __popcll(tree_word(a, t, w, nodes));
+  return later <= a.window;
+}
+// Rows of row tile g (64 bits) that see a position of the group of t: a node, or -1 and
+// a position `before` (1 or more) the prefix's end. Rows past the group's see all.
+__device__ __forceinline__ uint2 tree_rows(const Args& a, const TreeSmem& S, int32_t t, int32_t g, int32_t node,
+                                           int32_t before) {
+  uint64_t vis = ~uint64_t{0};
+#pragma unroll 1
+  for (int32_t k = 0; k < S.tokens[t]; ++k) {
+    const int32_t lo = max(0, k * a.H - g * a.ht), hi = min(64, (k + 1) * a.H - g * a.ht), own = S.own[t + k];
+    if (hi <= lo) continue;
+    const bool sees = node >= 0 ? tree_sees(a, a.t0 + t + k, S.nodes[t], own, node)
+                                : a.window <= 0 || before <= a.window - own;
+    if (!sees) vis &= ~((~uint64_t{0} >> (64 - (hi - lo))) << lo);
+  }
+  return make_uint2(static_cast<uint32_t>(vis), static_cast<uint32_t>(vis >> 32));
+}
+// The token of the group that row v (below 2^12) belongs to.
+__device__ __forceinline__ int32_t row_token(const Args& a, int32_t v) {
+  return a.H == 1 ? v : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(v), a.per_head));
+}
+// Element offset of row v of the group of t (within the launch) in a tensor [T, H, 512].
+__device__ __forceinline__ int64_t row_at(const Args& a, int32_t t, int32_t v, int64_t st, int64_t sh) {
+  const int32_t k = row_token(a, v);
+  return static_cast<int64_t>(a.t0 + t + k) * st + static_cast<int64_t>(v - k * a.H) * sh;
 }
 
 // What a thread loads before the CTA has set itself up, so that the latencies
@@ -500,7 +579,7 @@ __device__ __forceinline__ void record_cut(const Args& a, int32_t t, int32_t g, 
 // Plans the launch: every token's request and visible positions, and the CTA's
 // share. A thread takes one token.
 template <bool kTree>
-__device__ __forceinline__ void plan(const Args& a, Smem& S, const Early& early) {
+__device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Early& early) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Requests req{a.cu, a.k_lens, a.residual, a.T, a.B, a.ratio, a.cap};
   if (a.B <= kRequestsInSmem) {
@@ -518,29 +597,65 @@ __device__ __forceinline__ void plan(const Args& a, Smem& S, const Early& early)
     if (a.residual) req.residual = residual;
   }
   __syncthreads();
-  int32_t V = 0, units = 0;
-  if (tid < a.tc) {
+  int32_t V = 0, units = 0, tiles = a.hg;
+  [[maybe_unused]] int32_t group = 1;
+  if constexpr (kTree) {
+    // groups rest on requests that follow each other; where the boundaries fall
+    // (flagged below) each token stays alone
+    bool falls = false;
+#pragma unroll 1
+    for (int32_t b = tid; b < a.B; b += kThreads) falls |= req.cu[b] > req.cu[b + 1];
+    const int32_t stack = __syncthreads_or(falls) ? 1 : a.stack;
+    const int32_t t = a.t0 + tid;
+    int32_t P = -1, nodes = 0, own = 0, first = t;
+    if (tid < a.tc) {
+      const int32_t b = request_of(req.cu, a.B, a.T, t);
+      int32_t q0, q1, lk, res;
+      sanitize_request(req, b, q0, q1, lk, res);
+      if (q0 <= t && t < q1) {
+        P = lk - (q1 - q0);
+        nodes = P < 0 ? 0 : min(q1 - q0, 64 * a.words);
+        own = tree_count(a, t, 1, nodes);
+        first = t - (t - max(q0, a.t0)) % stack;
+        group = min(stack, min(q1, a.t0 + a.tc) - t);
+      }
+      S.tokB[tid] = b;
+      S.prefix[tid] = P;
+      S.nodes[tid] = static_cast<uint16_t>(nodes);
+      S.own[tid] = static_cast<uint16_t>(own);
+    }
+    __syncthreads();
+    tiles = 0;
+    if (tid < a.tc && first == t) {
+      int32_t least = own;
+#pragma unroll 1
+      for (int32_t k = 1; k < group; ++k) least = min(least, static_cast<int32_t>(S.own[tid + k]));
+      if (P >= 0) {
+        const int32_t any = group > 1 ? tree_count(a, t, group, nodes) : own;
+        V = any + (a.window > 0 ? min(P, max(0, a.window - least)) : P);
+        // alone, a token sees all of its group's positions but those before its window
+        if (group == 1 && a.window > 0) V = min(V, a.window);
+        S.rank0[tid] = any - V;
+      }
+      S.tokV[tid] = V;
+      S.tokens[tid] = static_cast<uint8_t>(group);
+      tiles = (group * a.H + a.ht - 1) / a.ht;
+      units = units_of<kTree>(a, V);
+    }
+    if (tid < a.tc) S.tiles[tid] = static_cast<uint8_t>(tiles);
+  } else if (tid < a.tc) {
     const int32_t t = a.t0 + tid, b = request_of(req.cu, a.B, a.T, t);
     if (!a.idx) {
       int32_t q0, q1, lk, res;
       sanitize_request(req, b, q0, q1, lk, res);
-      if constexpr (kTree) {
-        const int32_t nodes = q1 - q0, P = lk - nodes;
-        int32_t rank0 = 0;
-        if (q0 <= t && t < q1 && P >= 0) V = tree_count(a, t, P, nodes, rank0);
-        S.treeP[tid] = P;
-        S.treeR[tid] = rank0;
-        S.treeN[tid] = nodes;
-      } else {
-        if (q0 <= t && t < q1) V = visible_count(lk, res, a.ratio, q1 - q0, t - q0);
-      }
+      if (q0 <= t && t < q1) V = visible_count(lk, res, a.ratio, q1 - q0, t - q0);
     }
     S.tokV[tid] = V;
     S.tokB[tid] = b;
     units = units_of(a, V);
   }
   if (blockIdx.x == 0) flag_requests<kTree>(a, tid);
-  if (a.whole) {
+  if (!kTree && a.whole) {
     __syncthreads();
     if (tid == 0) {
       S.start_t = static_cast<int32_t>(blockIdx.x) / a.hg;
@@ -568,7 +683,8 @@ __device__ __forceinline__ void plan(const Args& a, Smem& S, const Early& early)
     __syncthreads();
     return;
   }
-  const int32_t mine = units * a.hg;
+  // whole row tiles are shared out by number
+  const int32_t mine = (kTree && a.whole ? 1 : units) * tiles;
   int32_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -586,6 +702,18 @@ __device__ __forceinline__ void plan(const Args& a, Smem& S, const Early& early)
   }
   const int32_t total = __shfl_sync(0xffffffffu, sums, 31);
   const int32_t at = __shfl_sync(0xffffffffu, sums, warp) - own + incl - mine;
+  if (kTree && a.whole) {
+    const int32_t c = static_cast<int32_t>(blockIdx.x);
+    if (at <= c && c < at + mine) {
+      S.start_t = tid;
+      S.start_g = c - at;
+      S.start_i = 0;
+      S.count = units;
+    }
+    if (tid == 0 && c >= total) S.count = 0;
+    __syncthreads();
+    return;
+  }
   share_of(a, total, u0, u1);
   if (at <= u0 && u0 < at + mine) {
     S.start_t = tid;
@@ -597,7 +725,7 @@ __device__ __forceinline__ void plan(const Args& a, Smem& S, const Early& early)
     if (tid == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   } else if (at <= u1 - 1 && u1 - 1 < at + mine) {
     const int32_t g = (u1 - 1 - at) / units, first = at + g * units;
-    record_cut(a, tid, g, first, first + units, u0, u1, total);
+    record_cut(a, tid, kTree ? g | group << 16 : g, first, first + units, u0, u1, total);
   }
   __syncthreads();
 }
@@ -618,13 +746,15 @@ __device__ __align__(16) const uint8_t kZeroRow[kD] = {};
 // The row tile's queries as FP16 times a power of two per head that brings the
 // head's largest magnitude to [2^13, 2^14); rows past the row tile's heads are
 // zero. A warp takes every eighth row.
-__device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, int32_t g,
+template <bool kTree>
+__device__ __forceinline__ void load_queries(const Args& a, SmemOf<kTree>& S, const Walk<kTree>& w_,
                                              uint32_t parity, int lw) {
+  const int32_t t = w_.t, g = w_.g;
   const int lane = threadIdx.x & 31;
   constexpr int kRows = kHT / kLoadWarps, kBatch = 4;
   // lane l holds values 16l .. 16l + 15: unit l & 7 of quarter l >> 3
   const uint32_t dst = smem_u32(S.q) + (lane >> 3) * 2 * kRegion;
-  const int heads = min(a.ht, a.H - g * a.ht);
+  const int heads = min(a.ht, w_.rows(a, S) - g * a.ht);
   const uint16_t* q = a.q + static_cast<int64_t>(a.t0 + t) * a.q_st + g * a.ht * a.q_sh + 16 * lane;
 #pragma unroll 1
   for (int k0 = 0; k0 < kRows; k0 += kBatch) {
@@ -634,7 +764,9 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
       const int r = kLoadWarps * (k0 + k) + lw;
       v[k][0] = v[k][1] = make_uint4(0u, 0u, 0u, 0u);
       if (r < heads) {
-        const uint4* src = reinterpret_cast<const uint4*>(q + r * a.q_sh);
+        const uint16_t* at = q + r * a.q_sh;
+        if constexpr (kTree) at = a.q + row_at(a, t, g * a.ht + r, a.q_st, a.q_sh) + 16 * lane;
+        const uint4* src = reinterpret_cast<const uint4*>(at);
         v[k][0] = __ldg(src);
         v[k][1] = __ldg(src + 1);
       }
@@ -671,15 +803,16 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem& S, int32_t t, 
 // one before. Positions
 // past the table and pages outside the pool are skipped and flagged.
 template <bool kTree>
-__device__ __forceinline__ bool run_rows(const Args& a, Smem& S, int32_t entry) {
+__device__ __forceinline__ bool run_rows(const Args& a, SmemOf<kTree>& S, int32_t entry) {
   const int lane = threadIdx.x & 31, r = threadIdx.x - 32 * kRowWarp0;
   bool bad = false;
-  Walk w(a, S);                                       // unit m + 3
+  Walk<kTree> w(a, S);                                // unit m + 3
   int32_t j3 = -1, b3 = 0;                            // position, request
   int32_t j2 = -1, page2 = -1;                        // position, page
   const uint8_t* codes1 = kZeroRow;                   // codes and scale
   uint16_t s1 = 0;
   bool live1 = false;
+  [[maybe_unused]] uint2 vis1 = make_uint2(~0u, ~0u), vis2 = vis1, vis3 = vis1;   // rows that see the position
 #pragma unroll 1
   for (int32_t m = -3; m < w.count; ++m) {
     if (m >= 0) {
@@ -692,8 +825,21 @@ __device__ __forceinline__ bool run_rows(const Args& a, Smem& S, int32_t entry) 
       const bool zero = live1 && s == 0.0f;
       S.row[slot][r] = zero ? kZeroRow : codes1;
       S.rs[slot][r] = live1 ? (zero ? 5.9604645e-8f : s) : 0.0f;
+      if constexpr (kTree) {
+        // a place without a position: no row sees it, whatever its query holds
+        if (!live1) vis1 = make_uint2(0u, 0u);
+        const bool some = __any_sync(0xffffffffu, (vis1.x & vis1.y) != ~0u);
+        S.vis[slot][r] = vis1;
+        S.nan[slot][r] = 0;
+        if (lane == 0) S.masked[slot][r >> 5] = some;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.rowfull[slot]);
+    }
+    if constexpr (kTree) {
+      vis1 = vis2;
+      vis2 = vis3;
+      vis3 = make_uint2(~0u, ~0u);
     }
     // unit m + 1
     codes1 = kZeroRow;
@@ -714,18 +860,23 @@ __device__ __forceinline__ bool run_rows(const Args& a, Smem& S, int32_t entry) 
     // unit m + 3
     j3 = -1;
     if (w.valid()) {
-      const int32_t V = S.tokV[w.t], n = positions_of(a, V), e = w.i * kPos + r;
+      const int32_t V = S.tokV[w.t], n = positions_of<kTree>(a, V), e = w.i * kPos + r;
       b3 = S.tokB[w.t];
       if constexpr (kTree) {
-        const int32_t rank = S.treeR[w.t] + e;
-        if (e < n) j3 = S.treeP[w.t] + (rank < 0 ? rank : tree_node(a, a.t0 + w.t, S.treeN[w.t], rank));
+        if (e < n) {
+          const int32_t rank = S.rank0[w.t] + e, count = S.tokens[w.t];
+          const int32_t node = rank < 0 ? -1 : tree_node(a, a.t0 + w.t, count, S.nodes[w.t], rank);
+          j3 = S.prefix[w.t] + (rank < 0 ? rank : node);
+          if (count > 1 && (rank >= 0 || a.window > 0)) vis3 = tree_rows(a, S, w.t, w.g, node, -rank);
+        }
       } else if (e < n) {
         j3 = !a.idx ? V - n + e : m == -3 ? entry : __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e);
       }
       if (w.first()) {
         // the row tile's queries, into L2: head r, 128 bytes at a time
-        const int h = w.g * a.ht + r, end = r < a.ht ? a.H : 0;
+        const int h = w.g * a.ht + r, end = r < a.ht ? w.rows(a, S) : 0;
         const uint16_t* q = a.q + static_cast<int64_t>(a.t0 + w.t) * a.q_st + h * a.q_sh;
+        if constexpr (kTree) q = a.q + row_at(a, w.t, h, a.q_st, a.q_sh);
 #pragma unroll 1
         for (int c = 0; c < 8 && h < end; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + c * 64));
       }
@@ -740,19 +891,41 @@ __device__ __forceinline__ bool run_rows(const Args& a, Smem& S, int32_t entry) 
 // other as they come free, then loads unit n + 1 (32 KB in flight on the SM
 // while unit n is worked on). A warp has eight rows; a warp
 // instruction loads one quarter of four.
-template <bool kFp8>
-__device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
+template <bool kFp8, bool kTree>
+__device__ __forceinline__ bool run_loaders(const Args& a, SmemOf<kTree>& S) {
   const int lane = threadIdx.x & 31, lw = (threadIdx.x >> 5) - kLoadWarp0;
   const int r0 = kPos / kLoadWarps * lw + (lane >> 3), off = (lane & 7) * 16;
   // rows 4 apart: 512 bytes on, and bit 2 of the swizzled unit flips
   const uint32_t at0 = smem_u32(S.kv) + sw(r0, lane & 7), at1 = (at0 ^ 64u) + 512;
   uint32_t seg = 0;
-  Walk w(a, S);                                       // unit n + 1
+  Walk<kTree> w(a, S);                                // unit n + 1
   uint4 x[2][4];
+  // Of a unit that not all rows see, NaN codes are taken out and noted: a weight of
+  // 0 times NaN would reach the rows that do not see them.
+  [[maybe_unused]] bool masked = false;
 #pragma unroll 1
   for (int32_t n = -1; n < w.count; ++n) {
     if (n >= 0) {
       const int buf = n & 1;
+      if constexpr (kTree && kFp8) {
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t bad = 0u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t* v = reinterpret_cast<uint32_t*>(&x[k][c]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t no = __vcmpeq4(v[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                v[i] &= ~no;
+                bad |= no;
+              }
+            }
+            if (bad) S.nan[n & (kSlots - 1)][r0 + 4 * k] = 1;
+          }
+        }
+      }
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         if (!wait(&S.empty[buf][f], ((n >> 1) & 1) ^ 1)) return false;
@@ -781,6 +954,7 @@ __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
         const uint32_t slot = (n + 1) & (kSlots - 1);
         if (!wait(&S.rowfull[slot], ((n + 1) / kSlots) & 1)) return false;
         const uint8_t* r[2] = {S.row[slot][r0] + off, S.row[slot][r0 + 4] + off};
+        if constexpr (kTree) masked = (S.masked[slot][0] | S.masked[slot][1]) != 0u;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -792,7 +966,7 @@ __device__ __forceinline__ bool run_loaders(const Args& a, Smem& S) {
         // the products with the previous row tile's queries are done, and the
         // softmax is past its wait for them
         if (!wait(&S.qempty, (seg & 1) ^ 1)) return false;
-        load_queries(a, S, w.t, w.g, seg & 1, lw);
+        load_queries<kTree>(a, S, w, seg & 1, lw);
         ++seg;
         fence_proxy_async_smem();
         __syncwarp();
@@ -846,14 +1020,15 @@ __device__ __forceinline__ bool drain(Smem& S) {
   return wait(&S.done, 0);
 }
 
-__device__ __forceinline__ bool run_scores(const Args& a, Smem& S, uint32_t tmem_any) {
+template <bool kTree>
+__device__ __forceinline__ bool run_scores(const Args& a, SmemOf<kTree>& S, uint32_t tmem_any) {
   constexpr uint32_t id = idesc_f16(kPos, kHT, false, false), hi = sdesc_hi(1024);
   const uint32_t k_lo = sdesc_lo(smem_u32(S.kv), 16), q_lo = sdesc_lo(smem_u32(S.q), 16);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
   bool ok = true;
   uint32_t n = 0, seg = 0;
 #pragma unroll 1
-  for (Walk w(a, S); ok && w.valid(); w.next(a, S), ++n) {
+  for (Walk<kTree> w(a, S); ok && w.valid(); w.next(a, S), ++n) {
     const uint32_t buf = n & 1, parity = (n >> 1) & 1;
     const bool last = w.last();
     if (w.first()) ok = wait(&S.qfull, seg++ & 1);
@@ -882,7 +1057,8 @@ __device__ __forceinline__ bool run_scores(const Args& a, Smem& S, uint32_t tmem
   return drain(S) && ok;
 }
 
-__device__ __forceinline__ bool run_values(const Args& a, Smem& S, uint32_t tmem_any) {
+template <bool kTree>
+__device__ __forceinline__ bool run_values(const Args& a, SmemOf<kTree>& S, uint32_t tmem_any) {
   constexpr uint32_t id = idesc_f16(128, kHT, true, true), hi = sdesc_hi(1024);
   const uint32_t v_lo = sdesc_lo(smem_u32(S.kv), kRegion), p_lo = sdesc_lo(smem_u32(S.p), 1024);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
@@ -892,7 +1068,7 @@ __device__ __forceinline__ bool run_values(const Args& a, Smem& S, uint32_t tmem
 #endif
   uint32_t n = 0;
 #pragma unroll 1
-  for (Walk w(a, S); ok && w.valid(); w.next(a, S), ++n) {
+  for (Walk<kTree> w(a, S); ok && w.valid(); w.next(a, S), ++n) {
     const uint32_t more = w.first() ? 0u : 1u, tile = v_lo + (n & 1) * (kTile >> 4);
     const uint32_t pe = p_lo + (n & 1) * (kPos * 128 >> 4);
     ok = wait(&S.pready[n & 1], (n >> 1) & 1);
@@ -951,9 +1127,12 @@ __device__ __forceinline__ int head_of(int lane) {
 // of at least those: head i at dst + i * kD, in the order of the rows (likewise;
 // merge_pieces_kernel reorders). A row tile without positions (`none`) gives zeros
 // whatever a query that is not finite has left in the accumulators.
-template <bool kOut, class T>
+// The heads may go on in the next token (`head` and `heads`: the first one's number in
+// its token and how many those have, `on`: from a token's last head to the next one's
+// first).
+template <bool kOut, bool kTree, class T>
 __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int pos, int32_t nh, bool none,
-                                       T* dst, int64_t stride) {
+                                       T* dst, int64_t stride, int32_t head = 0, int32_t heads = 0, int64_t on = 0) {
 #pragma unroll 1
   for (int c = 0; c < 8; ++c) {
     const int i0 = (c & 1) * 16;
@@ -966,13 +1145,26 @@ __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int
         *reinterpret_cast<const float4*>(S.alpha + h0 + i0 + 4 * i);
     tmem_ld_wait();
     T* at = dst + i0 * stride + (kOut ? value_of(c >> 1, pos) : 128 * (c >> 1) + pos);
+    int32_t left = 0;                                 // heads up to the token's end
+    if constexpr (kOut && kTree) {
+      left = heads - head - i0;
+      while (left <= 0) {
+        left += heads;
+        at += on - stride;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float v = none ? 0.0f : __uint_as_float(o[i]) * al[i];
       if constexpr (kOut) {
         const __nv_bfloat16 y = __float2bfloat16_rn(v);
         if (i0 + i < nh) *at = *reinterpret_cast<const uint16_t*>(&y);
-        at += stride;
+        if (kTree && --left == 0) {
+          left = heads;
+          at += on;
+        } else {
+          at += stride;
+        }
       } else {
         at[i * kD] = v;
       }
@@ -984,7 +1176,8 @@ __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int
 // 16 of every 32 TMEM lanes) of the 32 heads from 32 sub on; a lane has two
 // positions, lane / 4 and 8 further, of four pairs of heads. The four warps of a
 // `sub` share a named barrier.
-__device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tmem) {
+template <bool kTree>
+__device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uint32_t tmem) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int qw = warp & 3, sub = warp >> 2, bar = 1 + sub;
   const uint32_t lanes = static_cast<uint32_t>(32 * qw) << 16;
@@ -1000,6 +1193,9 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
   f32x2 l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) l[i] = pair_of(0.0f, 0.0f);
+  // of drafted trees, where rows see different positions: the lane's row has seen one,
+  // all of this sub's rows have
+  [[maybe_unused]] bool row_seen = false, all_seen = false;
   uint32_t n = 0, seg = 0;
   // A wait that gives up clears `ok`. The warp still runs through the named
   // barriers, on whatever TMEM holds, but arrives nowhere else, so that nobody
@@ -1007,12 +1203,13 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
   // waits that give up too. What it adds to a normaliser is NaN, and so are its
   // outputs: a row tile that was not finished does not look like a result, in
   // `out` or, by way of its piece, in a join.
-  for (Walk w(a, S); w.valid(); w.next(a, S), ++n) {
+  for (Walk<kTree> w(a, S); w.valid(); w.next(a, S), ++n) {
     const uint32_t buf = n & 1, parity = (n >> 1) & 1;
     if (w.first()) {                                  // the heads' factors
       if (ok && !wait(&S.qfull, seg & 1)) ok = false;
       ++seg;
       seen = live = false;
+      if constexpr (kTree) row_seen = all_seen = false;
       // the queries after these wait for this warp too, so that it sees every
       // phase of the barrier
       if (lane == 0 && ok) mbar_arrive(&S.qempty);
@@ -1025,7 +1222,9 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     f32x2 cs[2][4], es[2][4], inv2[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const float s = S.rs[slot][pos + 8 * k], ls = lg2(s), inv_s = s != 0.0f ? ex2(-ls) : 0.0f;
+      const float s = S.rs[slot][pos + 8 * k], ls = lg2(s);
+      // (a NaN scale must not reach the normalisers of rows that do not see it)
+      const float inv_s = (kTree ? s > 0.0f : s != 0.0f) ? ex2(-ls) : 0.0f;
       live |= s != 0.0f;
       const f32x2* c2 = reinterpret_cast<const f32x2*>(S.sl2[(seg - 1) & 1] + h0);
       const f32x2 s2 = pair_of(s, s), ls2 = pair_of(ls + kShift, ls + kShift);
@@ -1052,13 +1251,38 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
         for (int k = 0; k < 2; ++k) {
           d[k][i] = fma2(pair_of(__uint_as_float(r[4 * i + 2 * k]), __uint_as_float(r[4 * i + 2 * k + 1])),
                          cs[k][i], es[k][i]);
+        }
+      }
+      if constexpr (kTree) {
+        if (S.masked[slot][qw >> 1]) {
+          // (the loaders' notes come with the tile, which is there)
+          if (ok && !wait(&S.full[buf][1], parity)) ok = false;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint2 both_subs = S.vis[slot][pos + 8 * k];
+            const uint32_t vis = (sub ? both_subs.y : both_subs.x) >> (2 * (lane & 3));
+            const bool nan = S.nan[slot][pos + 8 * k] != 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float2 u = both(d[k][i]);
+              u.x = !(vis >> (8 * i) & 1u) ? -INFINITY : nan ? NAN : u.x;
+              u.y = !(vis >> (8 * i) & 2u) ? -INFINITY : nan ? NAN : u.y;
+              d[k][i] = pair_of(u.x, u.y);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
           const float2 u = both(d[k][i]);
           over = fmaxf(over, fmaxf(u.x, u.y));
         }
       }
     }
-    // until something was seen, any position sets the references
-    const bool rises = over > (seen ? kSlack + kShift : -INFINITY);
+    // until something was seen (by every row), any position sets the references
+    const bool rises = over > ((kTree ? all_seen : seen) ? kSlack + kShift : -INFINITY);
     // the weights of the unit before last have been used
     if (ok && !wait(&S.empty[buf][1], parity ^ 1)) ok = false;
     if (named_bar_any(bar, 128, rises)) {
@@ -1073,11 +1297,16 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
       part[qw * 32 + head_of(lane)] = across(t, lane, [](float p, float q) { return fmaxf(p, q); });
       named_bar(bar, 128);
       float up = fmaxf(fmaxf(part[lane], part[32 + lane]), fmaxf(part[64 + lane], part[96 + lane])) - kShift;
-      if ((seen && !(up > kSlack)) || !(fabsf(up) < INFINITY)) up = 0.0f;
+      const bool was = kTree ? row_seen : seen;
+      if constexpr (kTree) {
+        row_seen |= !(up == -INFINITY);
+        all_seen = __all_sync(0xffffffffu, row_seen);
+      }
+      if ((was && !(up > kSlack)) || !(fabsf(up) < INFINITY)) up = 0.0f;
       if (qw == 0) {
         S.m[32 * sub + lane] += up;
         S.delta[32 * sub + lane] = up;
-        S.alpha[32 * sub + lane] = seen ? ex2(-up) : 1.0f;
+        S.alpha[32 * sub + lane] = was ? ex2(-up) : 1.0f;
       }
       named_bar(bar, 128);
 #pragma unroll
@@ -1157,20 +1386,26 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
     }
     tc_fence_after();
     const int32_t h = w.g * a.ht + 32 * sub;          // first head of this sub
-    const int32_t nh = min(min(32, a.ht - 32 * sub), a.H - h);  // heads to write
+    const int32_t nh = min(min(32, a.ht - 32 * sub), w.rows(a, S) - h);  // heads to write
     const uint32_t oe = tmem + lanes + kOCol + 32 * sub;
     if (w.i == w.n - 1 && w.began_here()) {
       if (qw == 0 && lane < nh && a.lse)
         a.lse[static_cast<int64_t>(a.t0 + w.t) * a.H + h + lane] = lse2 * kLn2;
-      uint16_t* orow = a.out + static_cast<int64_t>(a.t0 + w.t) * a.o_st + h * a.o_sh;
-      output<true>(S, oe, 32 * sub, 32 * qw + lane, nh, none, orow, a.o_sh);
+      if constexpr (kTree) {
+        const int32_t head = h - row_token(a, h) * a.H;
+        output<true, true>(S, oe, 32 * sub, 32 * qw + lane, nh, none, a.out + row_at(a, w.t, h, a.o_st, a.o_sh),
+                           a.o_sh, head, a.H, a.o_st - (a.H - 1) * a.o_sh);
+      } else {
+        uint16_t* orow = a.out + static_cast<int64_t>(a.t0 + w.t) * a.o_st + h * a.o_sh;
+        output<true, false>(S, oe, 32 * sub, 32 * qw + lane, nh, none, orow, a.o_sh);
+      }
     } else {
       // a row tile that began in an earlier CTA goes to slot 0, one that goes
       // on in the next to slot 1
       const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (w.began_here() ? 1 : 0);
       if (qw == 0) a.piece_lse[piece * kHT + 32 * sub + lane] = lse2;
-      output<false>(S, oe, 32 * sub, 32 * qw + lane, nh, none, a.piece + piece * kPieceRow + (32 * sub) * kD,
-                    static_cast<int64_t>(kD));
+      output<false, kTree>(S, oe, 32 * sub, 32 * qw + lane, nh, none, a.piece + piece * kPieceRow + (32 * sub) * kD,
+                           static_cast<int64_t>(kD));
     }
     named_bar(bar, 128);                              // the factors are read
   }
@@ -1180,7 +1415,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, Smem& S, uint32_t tme
 template <bool kFp8, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
   extern __shared__ uint8_t smem_raw[];
-  Smem& S = *reinterpret_cast<Smem*>(
+  SmemOf<kTree>& S = *reinterpret_cast<SmemOf<kTree>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
@@ -1214,14 +1449,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
     bool ok = true;
     if (warp < kSoftWarps) {
       more_registers<kSoftRegs>();
-      ok = run_softmax(a, S, tmem);
+      ok = run_softmax<kTree>(a, S, tmem);
     } else if (warp < kScoreWarp) {
       more_registers<kLoadRegs>();
-      ok = run_loaders<kFp8>(a, S);
+      ok = run_loaders<kFp8, kTree>(a, S);
     } else {
       fewer_registers<kIssueRegs>();
-      if (warp == kScoreWarp) ok = run_scores(a, S, tmem);
-      if (warp == kValueWarp) ok = run_values(a, S, tmem);
+      if (warp == kScoreWarp) ok = run_scores<kTree>(a, S, tmem);
+      if (warp == kValueWarp) ok = run_values<kTree>(a, S, tmem);
       if (warp >= kRowWarp0) ok = run_rows<kTree>(a, S, early.entry);
     }
     if (!ok && lane == 0 && a.err) atomicOr(a.err, QLI_DEVERR_TIMEOUT);
@@ -1240,13 +1475,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = kJoinThreads / 32;
 
+template <bool kTree>
 __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a, int32_t ctas) {
   pdl_wait();
   const int lane = threadIdx.x & 31, c = blockIdx.x + 1;
   const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
   const int4 tile = __ldcg(a.cut + c - 1);
-  const int32_t h = tile.y * a.ht + row;
-  if (tile.x < 0 || h >= a.H || row >= a.ht) return;
+  const int32_t h = (kTree ? tile.y & 0xffff : tile.y) * a.ht + row;
+  if (tile.x < 0 || h >= (kTree ? tile.y >> 16 : 1) * a.H || row >= a.ht) return;
   // pieces: CTA c - 1's slot 1, then slot 0 of CTA c, c + 1, ... up to the end
   // (a CTA with units has all its predecessors with units)
   int32_t count = 2;
@@ -1300,7 +1536,7 @@ __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   const int64_t t = a.t0 + tile.x;
   // the lane's rows 4l .. 4l + 3 of each quarter are four values in a row
-  uint16_t* dst = a.out + t * a.o_st + h * a.o_sh;
+  uint16_t* dst = a.out + (kTree ? row_at(a, tile.x, h, a.o_st, a.o_sh) : t * a.o_st + h * a.o_sh);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv);
@@ -1386,11 +1622,32 @@ Args make_args(const qli_kv_attn_args& a) {
   return d;
 }
 
-// Most units a row tile can have.
+// Most units a row tile can have. A group's tokens see nodes behind their windows.
 int64_t most_units(const Args& d) {
   int64_t n = d.idx ? static_cast<int64_t>(d.K) : d.cap < INT32_MAX ? d.cap : INT32_MAX;
-  if (!d.idx && d.window > 0 && d.window < n) n = d.window;
+  if (!d.idx && d.window > 0) {
+    const int64_t nodes = d.stack > 1 ? (d.T < 64 * d.words ? d.T : 64 * d.words) : 0;
+    if (d.window + nodes < n) n = d.window + nodes;
+  }
   return n <= kPos ? 1 : (n - 1) / kPos + 1;
+}
+
+// Most groups of up to `stack` tokens that `tokens` in a row can make: every request
+// may leave one that is not full.
+int64_t most_groups(const Args& d, int64_t tokens) {
+  const int64_t n = tokens / d.stack + d.B + 1;
+  return n < tokens ? n : tokens;
+}
+
+// Tokens that share row tiles: what leaves the fewest rows of the tiles empty, the
+// fewest tokens among equals, and no more than a request has on average.
+int32_t stack_of(int32_t H, int32_t T, int32_t B) {
+  const int32_t most = (T - 1) / (B > 0 ? B : 1) + 1;
+  int32_t best = 1;
+  const auto tiles = [&](int32_t k) { return (k * H - 1) / kHT + 1; };
+  for (int32_t k = 2; k <= kMaxStack && k <= most; ++k)
+    if (tiles(k) * best < tiles(best) * k) best = k;
+  return best;
 }
 
 // Row tiles of at most this many units are not cut while there is an SM for
@@ -1405,8 +1662,9 @@ constexpr int kWholeUnits = 2;
 // positions: 16.6 us with 64 heads a tile, 14.6 with 16; 64 tokens of 32 heads over
 // a window of 128: 14.5 and 13.1.
 int32_t heads_per_tile(const Args& d, int64_t most, int sms) {
+  const int64_t groups = most_groups(d, d.T), H = static_cast<int64_t>(d.stack) * d.H;
   int32_t ht = kHT;
-  while (ht > 16 && (most <= kWholeUnits ? 1 : most) * d.T * ((d.H + ht / 2 - 1) / (ht / 2)) <= sms) ht /= 2;
+  while (ht > 16 && (most <= kWholeUnits ? 1 : most) * groups * ((H + ht / 2 - 1) / (ht / 2)) <= sms) ht /= 2;
   return ht;
 }
 
@@ -1426,27 +1684,29 @@ Layout layout_for(int sms) {
 template <bool kFp8, bool kTree>
 cudaError_t launch(Args d, int sms, cudaStream_t s) {
   const auto kernel = kv_attn_kernel<kFp8, kTree>;
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kSmemBytes,
+  constexpr int kBytes = kSmemBytes<kTree>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kBytes,
                                     g_smem_kv_attn[(kTree ? 2 : 0) + (kFp8 ? 1 : 0)]);
   const int64_t most = most_units(d);
   d.ht = heads_per_tile(d, most, sms);
-  d.hg = (d.H + d.ht - 1) / d.ht;
+  d.hg = (d.stack * d.H + d.ht - 1) / d.ht;
   // tokens per launch: what one plan holds, and fewer than 2^30 units
   const int64_t fit = (int64_t{1} << 30) / (most * d.hg);
-  const int32_t chunk = static_cast<int32_t>(fit < kChunkT ? fit : kChunkT);
+  constexpr int32_t kChunk = kTree ? kTreeChunkT : kChunkT;
+  const int32_t chunk = static_cast<int32_t>(fit < kChunk ? fit : kChunk);
   for (d.t0 = 0; e == cudaSuccess && d.t0 < d.T; d.t0 += chunk) {
     d.tc = d.T - d.t0 < chunk ? d.T - d.t0 : chunk;
-    const int64_t tiles = static_cast<int64_t>(d.tc) * d.hg;
+    const int64_t tiles = most_groups(d, d.tc) * d.hg;
     d.whole = most <= kWholeUnits && tiles <= sms ? 1 : 0;
     // one CTA per SM, and no more than there can be units
     const int64_t units = tiles * most;
     const int32_t ctas = static_cast<int32_t>(d.whole ? tiles : units < sms ? units : sms);
-    kernel<<<static_cast<unsigned>(ctas), kThreads, kSmemBytes, s>>>(d);
+    kernel<<<static_cast<unsigned>(ctas), kThreads, kBytes, s>>>(d);
     e = cudaGetLastError();
     if (e == cudaSuccess && ctas > 1 && !d.whole)
-      e = launch_pdl(merge_pieces_kernel,
+      e = launch_pdl(merge_pieces_kernel<kTree>,
                      dim3(static_cast<unsigned>(ctas - 1),
-                          static_cast<unsigned>(((d.H < d.ht ? d.H : d.ht) + kJoinRows - 1) / kJoinRows)),
+                          static_cast<unsigned>(((d.stack * d.H < d.ht ? d.stack * d.H : d.ht) + kJoinRows - 1) / kJoinRows)),
                      dim3(kJoinThreads), 0, s, d, ctas);
   }
   return e;
@@ -1478,7 +1738,7 @@ qli_status attend(const qli_kv_attn_args* a, const uint64_t* mask, int32_t words
   if (st != QLI_OK) return st;
   if (kTree) {
     if (a->indices != nullptr || words < 1) return QLI_ERR_INVALID_ARG;
-    if (a->ratio != 1) return QLI_ERR_UNSUPPORTED;
+    if (a->ratio != 1 || words > kMaxWords) return QLI_ERR_UNSUPPORTED;
     if (a->T > 0 && mask == nullptr) return QLI_ERR_INVALID_ARG;
     if (!aligned(mask, 8)) return QLI_ERR_ALIGNMENT;
   }
@@ -1496,6 +1756,8 @@ qli_status attend(const qli_kv_attn_args* a, const uint64_t* mask, int32_t words
   d.piece_lse = reinterpret_cast<float*>(w + L.lse);
   d.mask = mask;
   d.words = words;
+  d.stack = kTree ? stack_of(a->H, a->T, a->B) : 1;
+  d.per_head = static_cast<uint32_t>(0xffffffffu / static_cast<uint32_t>(a->H) + 1);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       a->quant_mode == QLI_QUANT_FP8 ? launch<true, kTree>(d, sms, s) : launch<false, kTree>(d, sms, s);

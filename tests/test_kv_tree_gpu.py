@@ -132,10 +132,11 @@ def test_more_words_than_nodes():
     check(TreeCase(53, [300, 20], [5, 3], 32, kv8.FP8, "any", words=3))
 
 
-def test_a_chain_is_the_causal_attention():
-    """Bit for bit: the units hold the same positions."""
+@pytest.mark.parametrize("H", [64, 128])
+def test_a_chain_is_the_causal_attention(H):
+    """Bit for bit where tokens do not share row tiles: the units hold the same positions."""
     import torch
-    case = TreeCase(54, [900, 64, 131], [7, 64, 3], 40, kv8.INT8, "chain")
+    case = TreeCase(54, [900, 64, 131], [7, 64, 3], H, kv8.INT8, "chain")
     kw = case.upload()
     tree = qli.kv_tree_attention(scale=SCALE, **kw)
     kw.pop("tree_mask")
@@ -144,17 +145,14 @@ def test_a_chain_is_the_causal_attention():
 
 
 def test_requests_shorter_than_their_tree_are_flagged():
-    import torch
     case = TreeCase(55, [300, 50], [4, 6], 64, kv8.FP8, "tree")
     case.k_lens = case.k_lens.copy()
     case.k_lens[1] = 5
     out, lse = run(case, err_want=2)
     assert not out[4:].any() and np.isneginf(lse[4:]).all()
-    case.positions_of_second = None
     good = TreeCase(55, [300, 50], [4, 6], 64, kv8.FP8, "tree")
     want, _ = run(good)
     assert np.array_equal(out[:4], want[:4])
-    del torch
 
 
 def test_pages_outside_the_pool_are_skipped_and_flagged():
@@ -215,3 +213,112 @@ def test_queries_of_other_strides():
     out = torch.zeros(24, 9, 512, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
     got = qli.kv_tree_attention(scale=SCALE, out=out, **kw)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---- tokens that share row tiles ----------------------------------------------------
+
+def stack_of(H, T, B):
+    """Tokens that share row tiles, as the library chooses them."""
+    best = 1
+    for k in range(2, min(8, (T - 1) // B + 1) + 1):
+        if -(-k * H // 64) * best < -(-best * H // 64) * k:
+            best = k
+    return best
+
+
+SHARED = [(1, 3), (5, 8), (8, 8), (16, 4), (16, 7), (20, 6), (32, 2), (32, 9), (40, 8), (48, 5), (96, 4), (100, 8)]
+
+
+@pytest.mark.parametrize("window", [0, 5, 40])
+@pytest.mark.parametrize("H,n", SHARED, ids=lambda v: str(v))
+def test_tokens_that_share_tiles(H, n, window):
+    assert stack_of(H, 3 * n, 3) > 1 or H == 100 or n < 3
+    check(TreeCase(71 + H + n, [700, 66, n], [n, n, n], H, kv8.FP8, "any" if H % 3 else "tree"), window)
+
+
+@pytest.mark.parametrize("H", [8, 16, 48])
+def test_trees_of_uneven_sizes_share_tiles(H):
+    check(TreeCase(72, [900, 70, 64, 130, 3], [9, 1, 0, 17, 3], H, kv8.INT8, "tree"))
+
+
+def test_groups_across_launches():
+    """384 tokens are planned at a time; the trees do not end there."""
+    check(TreeCase(73, [150] * 17, [50] * 17, 16, kv8.FP8, "tree"))
+
+
+def _shared_case():
+    """Two branches of one tree in one row tile: nodes 0, 1 and nodes 2, 3."""
+    case = TreeCase(74, [100], [4], 16, kv8.FP8, "tree")
+    case.masks = [0b0001, 0b0011, 0b0100, 0b1100]
+    return case
+
+
+@pytest.mark.parametrize("what", ["codes", "scale", "infinite-scale"])
+def test_nan_in_rows_of_another_branch(what):
+    """A drafted token whose row is not finite (the last one of a branch) makes the
+    tokens that see it NaN, not their neighbours in the row tile."""
+    import torch
+    case = _shared_case()
+    kw = case.upload()
+    want = [t.clone() for t in qli.kv_tree_attention(scale=SCALE, **kw)]
+    j = 97                                                       # node 1
+    page, row = int(case.bt[0, j // case.R]), j % case.R
+    if what == "codes":
+        at = case.layout["kv_offset"] + 512 * row
+        kw["cache"][page, at + 3] = 0x7F
+        kw["cache"][page, at + 500] = 0xFF
+    else:
+        at = case.layout["kv_scale_offset"] + 2 * row
+        bits = 0x7E00 if what == "scale" else 0x7C00
+        kw["cache"][page, at:at + 2] = torch.tensor([bits & 255, bits >> 8], dtype=torch.uint8)
+    out, lse = qli.kv_tree_attention(scale=SCALE, **kw)
+    for t in (0, 2, 3):
+        assert torch.equal(out[t], want[0][t]) and torch.equal(lse[t], want[1][t]), t
+    assert not torch.isfinite(out[1]).any()
+
+
+def test_a_query_that_is_not_finite_stays_alone():
+    import torch
+    for masks in ([0b0001, 0b0011, 0b0100, 0b1100], [1, 0, 4, 8]):
+        case = _shared_case()
+        case.masks = masks
+        kw = case.upload()
+        if masks[1] == 0:                                        # and without a position
+            kw["k_lens"] = torch.tensor([4], dtype=torch.int32, device="cuda")
+        want = [t.clone() for t in qli.kv_tree_attention(scale=SCALE, **kw)]
+        kw["q"][1, 3, 7] = float("nan")
+        kw["q"][1, 4] = float("inf")
+        out, lse = qli.kv_tree_attention(scale=SCALE, **kw)
+        for t in (0, 2, 3):
+            assert torch.equal(out[t], want[0][t]) and torch.equal(lse[t], want[1][t]), t
+        if masks[1] == 0:
+            assert not out[1].any() and torch.isneginf(lse[1]).all()
+        else:
+            assert torch.isnan(out[1, 3]).all() and torch.isnan(out[1, 4]).all()
+            assert torch.equal(out[1, 5:], want[0][1, 5:]) and torch.equal(out[1, :3], want[0][1, :3])
+
+
+def test_rows_that_see_their_first_position_late():
+    """Rows of one tile with far smaller scores than the others, whose first positions
+    come after units of which they see nothing: each row has its own reference."""
+    n = 150
+    case = TreeCase(75, [n], [n], 16, kv8.INT8, "tree")
+    case.masks = [(1 << t + 1) - 1 if t % 2 == 0 else 1 << t for t in range(n)]
+    for t in range(1, n, 2):
+        case.masks[t] = (1 << t) | (1 << n - 1) | (1 << n - 3)   # its own and the last nodes
+    q = kv8.bf16_to_f64(case.q)
+    q[1::2] *= 40.0                                              # references far from 0, on both sides
+    case.q = kv8.f32_to_bf16(q)
+    check(case)
+
+
+def test_requests_whose_boundaries_fall_stay_in_bounds():
+    """Boundaries that go back are flagged; every token gets a finite answer."""
+    import torch
+    case = TreeCase(76, [300, 300, 300], [8, 8, 8], 16, kv8.FP8, "tree")
+    kw = case.upload()
+    kw["cu_seqlens_q"] = torch.tensor([0, 16, 8, 24], dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = qli.kv_tree_attention(scale=SCALE, err_word=err, **kw)
+    assert int(err.item()) & 1
+    assert torch.isfinite(out.float()).all() and not torch.isnan(lse).any()
