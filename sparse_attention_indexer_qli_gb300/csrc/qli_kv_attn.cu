@@ -113,11 +113,11 @@ struct Smem {
 // What drafted trees add (see there), per token of the launch and per unit.
 constexpr int kMaxWords = 256;                 // of a token's mask
 constexpr int kMaxStack = 8;                   // tokens of a group
-constexpr int kTreeChunkT = 384;               // tokens planned per launch
 struct TreeSmem : Smem {
-  int32_t prefix[kTreeChunkT], rank0[kTreeChunkT];    // by token; rank0 by group
-  uint16_t nodes[kTreeChunkT], own[kTreeChunkT];      // the request's nodes in masks; those that the token sees
-  uint8_t tokens[kTreeChunkT], tiles[kTreeChunkT];    // by group: its tokens and row tiles (0: not the group's first token)
+  int32_t prefix[kChunkT];                     // positions before the request's nodes
+  uint16_t nodes[kChunkT], own[kChunkT];       // the request's nodes in masks; those that the token sees
+  uint16_t any[kChunkT];                       // by group: the nodes that some token sees,
+  uint8_t tokens[kChunkT], tiles[kChunkT];     //   its tokens and row tiles: its tokens and row tiles (0: not the group's first token)
   uint2 vis[kSlots][kPos];                     // rows of the row tile that see the position
   uint32_t masked[kSlots][kRowWarps];          // 1: not all rows see all of a row warp's positions
   uint8_t nan[kSlots][kPos];                   // 1: the position's row has NaN codes
@@ -375,6 +375,13 @@ __device__ __forceinline__ int32_t share_begin(int32_t total, int32_t ctas, int3
   return each * c + min(c, total - each * ctas);
 }
 
+// The CTA whose share has unit u of `total`.
+__device__ __forceinline__ int32_t share_of_unit(int32_t total, int32_t ctas, int32_t u) {
+  const int32_t each = total / ctas, more = total - each * ctas;   // the first `more` CTAs have one unit more
+  const int32_t of_more = more * (each + 1);
+  return u < of_more ? u / (each + 1) : more + (u - of_more) / each;
+}
+
 // A CTA's share, unit by unit. Of drafted trees, t is a group's first token.
 template <bool kTree>
 struct Walk {
@@ -447,7 +454,7 @@ struct Requests {
   int64_t cap;
 };
 constexpr int kRequestsInSmem = 10000;
-static_assert((3 * kRequestsInSmem + 1) * 4 <= 2 * kTile, "the requests fit in the tiles");
+static_assert((3 * kRequestsInSmem + 1) * 4 + 8 * kChunkT <= 2 * kTile, "requests and masks fit in the tiles");
 
 // Drafted trees. A request's last positions are the nodes of a tree, its tokens of the
 // call; a token sees the prefix before them and the nodes whose bits are set in its
@@ -457,13 +464,16 @@ static_assert((3 * kRequestsInSmem + 1) * 4 <= 2 * kTile, "the requests fit in t
 // the same for any, serve several tokens. A group's positions are the earliest window's
 // part of the prefix, then the nodes that any of its tokens sees; of a unit in which
 // some row does not see some position the row warps leave masks, by which the softmax
-// takes those scores as -inf. A position of rank e + rank0 below 0 is that far before
-// the prefix's end, else it is the set bit of that rank.
-// 16 tokens of 16 heads over 8K positions: XXX us, a token at a time XXX.
+// takes those scores as -inf. Position e of n has the rank e - n + (nodes): below 0 it is
+// that far before the prefix's end, else the set bit of that rank.
+// 16 trees of 16 tokens over 8K positions, E4M3: 16 heads 110 us (0.62 PFLOP/s), a token
+// at a time 329; 96 heads, where two tokens fill three row tiles, 531 and 681.
+__device__ __forceinline__ uint64_t low_bits(uint64_t m, int32_t n) {
+  return n >= 64 ? m : n <= 0 ? 0u : m & ((uint64_t{1} << n) - 1);
+}
 __device__ __forceinline__ uint64_t tree_word(const Args& a, int32_t t, int32_t w, int32_t nodes) {
-  const int32_t left = nodes - 64 * w;
-  const uint64_t m = __ldg(reinterpret_cast<const unsigned long long*>(a.mask) + static_cast<int64_t>(t) * a.words + w);
-  return left >= 64 ? m : left <= 0 ? 0u : m & ((uint64_t{1} << left) - 1);
+  return low_bits(__ldg(reinterpret_cast<const unsigned long long*>(a.mask) + static_cast<int64_t>(t) * a.words + w),
+                  nodes - 64 * w);
 }
 // The nodes that any of `count` tokens from t on sees.
 __device__ __forceinline__ uint64_t tree_union(const Args& a, int32_t t, int32_t count, int32_t w, int32_t nodes) {
@@ -478,6 +488,20 @@ __device__ __forceinline__ int32_t tree_count(const Args& a, int32_t t, int32_t 
   for (int32_t w = 0; 64 * w < nodes; ++w) n += __popcll(tree_union(a, t, count, w, nodes));
   return n;
 }
+// The set bit of that rank (from 0, below their number).
+__device__ __forceinline__ int32_t bit_of(uint64_t m, int32_t rank) {
+  int32_t at = 0;
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) {
+    const int32_t low = __popcll(m & ((uint64_t{1} << s) - 1));
+    if (rank >= low) {
+      rank -= low;
+      m >>= s;
+      at += s;
+    }
+  }
+  return at;
+}
 // The set bit of that rank (from 0) in the tokens' union; -1: there is none.
 __device__ __forceinline__ int32_t tree_node(const Args& a, int32_t t, int32_t count, int32_t nodes, int32_t rank) {
 #pragma unroll 1
@@ -488,17 +512,7 @@ __device__ __forceinline__ int32_t tree_node(const Args& a, int32_t t, int32_t c
       rank -= c;
       continue;
     }
-    int32_t at = 64 * w;
-#pragma unroll 1
-    for (int s = 32; s > 0; s >>= 1) {
-      const int32_t low = __popcll(m & ((uint64_t{1} << s) - 1));
-      if (rank >= low) {
-        rank -= low;
-        m >>= s;
-        at += s;
-      }
-    }
-    return at;
+    return 64 * w + bit_of(m, rank);
   }
   return -1;
 }
@@ -513,21 +527,44 @@ __device__ __forceinline__ bool tree_sees(const Args& a, int32_t t, int32_t node
   for (int32_t w = (node >> 6) + 1; 64 * w < nodes; ++w) later += __popcll(tree_word(a, t, w, nodes));
   return later <= a.window;
 }
-// Rows of row tile g (64 bits) that see a position of the group of t: a node, or -1 and
-// a position `before` (1 or more) the prefix's end. Rows past the group's see all.
-__device__ __forceinline__ uint2 tree_rows(const Args& a, const TreeSmem& S, int32_t t, int32_t g, int32_t node,
-                                           int32_t before) {
-  uint64_t vis = ~uint64_t{0};
-#pragma unroll 1
-  for (int32_t k = 0; k < S.tokens[t]; ++k) {
-    const int32_t lo = max(0, k * a.H - g * a.ht), hi = min(64, (k + 1) * a.H - g * a.ht), own = S.own[t + k];
-    if (hi <= lo) continue;
-    const bool sees = node >= 0 ? tree_sees(a, a.t0 + t + k, S.nodes[t], own, node)
-                                : a.window <= 0 || before <= a.window - own;
-    if (!sees) vis &= ~((~uint64_t{0} >> (64 - (hi - lo))) << lo);
+// The masks of the group whose units a row warp is at: with one word to a mask, lane k
+// has token k's, and all have the union.
+struct Group {
+  int32_t t = -1;
+  uint64_t mine = 0u, any = 0u;
+  __device__ __forceinline__ void enter(const Args& a, const TreeSmem& S, int32_t t_) {
+    if (t == t_ || a.words > 1) return;
+    t = t_;
+    const int lane = threadIdx.x & 31;
+    mine = lane < S.tokens[t] ? tree_word(a, a.t0 + t + lane, 0, S.nodes[t]) : 0u;
+    any = static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(mine >> 32))) << 32 |
+          __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(mine));
   }
-  return make_uint2(static_cast<uint32_t>(vis), static_cast<uint32_t>(vis >> 32));
-}
+  __device__ __forceinline__ int32_t node(const Args& a, const TreeSmem& S, int32_t t_, int32_t rank) const {
+    return a.words > 1 ? tree_node(a, a.t0 + t_, S.tokens[t_], S.nodes[t_], rank) : bit_of(any, rank);
+  }
+  __device__ __forceinline__ bool sees(const Args& a, const TreeSmem& S, int32_t t_, int32_t k, int32_t node) const {
+    const int32_t own = S.own[t_ + k];
+    if (a.words > 1) return tree_sees(a, a.t0 + t_ + k, S.nodes[t_], own, node);
+    const uint64_t m = __shfl_sync(0xffffffffu, mine, k) >> (node & 63);
+    return (m & 1u) && (a.window <= 0 || own <= a.window || __popcll(m) <= a.window);
+  }
+  // Rows of row tile g (64 bits) that see a lane's position: a node, or -1 and a position
+  // `before` (1 or more) the prefix's end. Rows past the group's see all. (The whole warp.)
+  __device__ __forceinline__ uint2 rows(const Args& a, const TreeSmem& S, int32_t t_, int32_t g, int32_t node,
+                                        int32_t before) const {
+    uint64_t vis = ~uint64_t{0};
+#pragma unroll 1
+    for (int32_t k = 0; k < S.tokens[t_]; ++k) {
+      const int32_t lo = max(0, k * a.H - g * a.ht), hi = min(64, (k + 1) * a.H - g * a.ht);
+      if (hi <= lo) continue;
+      const bool of_node = sees(a, S, t_, k, max(node, 0));
+      const bool see = node >= 0 ? of_node : a.window <= 0 || before <= a.window - S.own[t_ + k];
+      if (!see) vis &= ~((~uint64_t{0} >> (64 - (hi - lo))) << lo);
+    }
+    return make_uint2(static_cast<uint32_t>(vis), static_cast<uint32_t>(vis >> 32));
+  }
+};
 // The token of the group that row v (below 2^12) belongs to.
 __device__ __forceinline__ int32_t row_token(const Args& a, int32_t v) {
   return a.H == 1 ? v : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(v), a.per_head));
@@ -543,6 +580,7 @@ __device__ __forceinline__ int64_t row_at(const Args& a, int32_t t, int32_t v, i
 // follows from sizes alone) a row warp's entry of the CTA's first unit.
 struct Early {
   int32_t cu, k_len, residual, entry;
+  uint64_t mask;                       // of drafted trees: the first word of the thread's token
 };
 
 // The CTA's share [u0, u1) of `total` units.
@@ -552,9 +590,13 @@ __device__ __forceinline__ void share_of(const Args& a, int32_t total, int32_t& 
   u1 = share_begin(total, ctas, c + 1);
 }
 
+template <bool kTree>
 __device__ __forceinline__ Early load_early(const Args& a) {
   const int tid = threadIdx.x, r = tid - 32 * kRowWarp0;
-  Early v{0, 0, 0, -1};
+  Early v{0, 0, 0, -1, 0u};
+  if constexpr (kTree) {
+    if (tid < a.tc) v.mask = tree_word(a, a.t0 + tid, 0, 64);
+  }
   if (tid <= a.B) v.cu = __ldg(a.cu + tid);
   if (!a.idx) {
     if (tid < a.B) v.k_len = __ldg(a.k_lens + tid);
@@ -602,6 +644,7 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
   if constexpr (kTree) {
     // groups rest on requests that follow each other; where the boundaries fall
     // (flagged below) each token stays alone
+    uint64_t* masks = reinterpret_cast<uint64_t*>(S.kv[1] + kTile) - kChunkT;   // behind the requests
     bool falls = false;
 #pragma unroll 1
     for (int32_t b = tid; b < a.B; b += kThreads) falls |= req.cu[b] > req.cu[b + 1];
@@ -615,7 +658,7 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
       if (q0 <= t && t < q1) {
         P = lk - (q1 - q0);
         nodes = P < 0 ? 0 : min(q1 - q0, 64 * a.words);
-        own = tree_count(a, t, 1, nodes);
+        own = a.words > 1 ? tree_count(a, t, 1, nodes) : __popcll(low_bits(early.mask, nodes));
         first = t - (t - max(q0, a.t0)) % stack;
         group = min(stack, min(q1, a.t0 + a.tc) - t);
       }
@@ -623,6 +666,7 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
       S.prefix[tid] = P;
       S.nodes[tid] = static_cast<uint16_t>(nodes);
       S.own[tid] = static_cast<uint16_t>(own);
+      masks[tid] = low_bits(early.mask, nodes);
     }
     __syncthreads();
     tiles = 0;
@@ -631,12 +675,19 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
 #pragma unroll 1
       for (int32_t k = 1; k < group; ++k) least = min(least, static_cast<int32_t>(S.own[tid + k]));
       if (P >= 0) {
-        const int32_t any = group > 1 ? tree_count(a, t, group, nodes) : own;
+        int32_t any = own;
+        if (group > 1 && a.words > 1) any = tree_count(a, t, group, nodes);
+        if (group > 1 && a.words == 1) {
+          uint64_t m = 0u;
+          for (int32_t k = 0; k < group; ++k) m |= masks[tid + k];
+          any = __popcll(m);
+        }
         V = any + (a.window > 0 ? min(P, max(0, a.window - least)) : P);
         // alone, a token sees all of its group's positions but those before its window
         if (group == 1 && a.window > 0) V = min(V, a.window);
-        S.rank0[tid] = any - V;
+        S.any[tid] = static_cast<uint16_t>(any);
       }
+      if (P < 0) S.any[tid] = 0;
       S.tokV[tid] = V;
       S.tokens[tid] = static_cast<uint8_t>(group);
       tiles = (group * a.H + a.ht - 1) / a.ht;
@@ -812,7 +863,9 @@ __device__ __forceinline__ bool run_rows(const Args& a, SmemOf<kTree>& S, int32_
   const uint8_t* codes1 = kZeroRow;                   // codes and scale
   uint16_t s1 = 0;
   bool live1 = false;
+  [[maybe_unused]] Group group;
   [[maybe_unused]] uint2 vis1 = make_uint2(~0u, ~0u), vis2 = vis1, vis3 = vis1;   // rows that see the position
+  [[maybe_unused]] bool shared1 = false, shared2 = false, shared3 = false;         // several tokens in the row tile
 #pragma unroll 1
   for (int32_t m = -3; m < w.count; ++m) {
     if (m >= 0) {
@@ -826,8 +879,8 @@ __device__ __forceinline__ bool run_rows(const Args& a, SmemOf<kTree>& S, int32_
       S.row[slot][r] = zero ? kZeroRow : codes1;
       S.rs[slot][r] = live1 ? (zero ? 5.9604645e-8f : s) : 0.0f;
       if constexpr (kTree) {
-        // a place without a position: no row sees it, whatever its query holds
-        if (!live1) vis1 = make_uint2(0u, 0u);
+        // a place without a position: no token of a group sees it, whatever its query holds
+        if (!live1 && shared1) vis1 = make_uint2(0u, 0u);
         const bool some = __any_sync(0xffffffffu, (vis1.x & vis1.y) != ~0u);
         S.vis[slot][r] = vis1;
         S.nan[slot][r] = 0;
@@ -840,6 +893,8 @@ __device__ __forceinline__ bool run_rows(const Args& a, SmemOf<kTree>& S, int32_
       vis1 = vis2;
       vis2 = vis3;
       vis3 = make_uint2(~0u, ~0u);
+      shared1 = shared2;
+      shared2 = shared3;
     }
     // unit m + 1
     codes1 = kZeroRow;
@@ -863,12 +918,16 @@ __device__ __forceinline__ bool run_rows(const Args& a, SmemOf<kTree>& S, int32_
       const int32_t V = S.tokV[w.t], n = positions_of<kTree>(a, V), e = w.i * kPos + r;
       b3 = S.tokB[w.t];
       if constexpr (kTree) {
+        const int32_t rank = S.any[w.t] - n + e;
+        int32_t node = -1;
+        group.enter(a, S, w.t);
         if (e < n) {
-          const int32_t rank = S.rank0[w.t] + e, count = S.tokens[w.t];
-          const int32_t node = rank < 0 ? -1 : tree_node(a, a.t0 + w.t, count, S.nodes[w.t], rank);
+          if (rank >= 0) node = group.node(a, S, w.t, rank);
           j3 = S.prefix[w.t] + (rank < 0 ? rank : node);
-          if (count > 1 && (rank >= 0 || a.window > 0)) vis3 = tree_rows(a, S, w.t, w.g, node, -rank);
         }
+        shared3 = S.tokens[w.t] > 1;
+        if (shared3 && (a.window > 0 || __any_sync(0xffffffffu, node >= 0)))
+          vis3 = group.rows(a, S, w.t, w.g, node, -rank);
       } else if (e < n) {
         j3 = !a.idx ? V - n + e : m == -3 ? entry : __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e);
       }
@@ -1419,7 +1478,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
-  const Early early = load_early(a);
+  const Early early = load_early<kTree>(a);
   if (warp == kScoreWarp) tmem_alloc(&S.tmem_base, kTmemCols);
   if (tid < kHT) S.m[tid] = 0.0f;
   if (tid == 0) {
@@ -1475,19 +1534,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = kJoinThreads / 32;
 
-template <bool kTree>
+// kFew: a launch of few row tiles, each in many pieces. Block (i, k) takes the i-th row
+// tile that goes on in another CTA, four warps a row with a quarter of its values each
+// and four times as many pieces in flight. One tree of 8 tokens of 64 heads over 2048
+// positions, 8 row tiles in 19 pieces each: 25.7 us without, 19.9 with.
+template <bool kTree, bool kFew>
 __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a, int32_t ctas) {
   pdl_wait();
-  const int lane = threadIdx.x & 31, c = blockIdx.x + 1;
-  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  constexpr int kSplit = kFew ? 4 : 1, kQuads = 4 / kSplit;       // warps of a row, float4s of a lane
+  constexpr int kBatch = 4 * kSplit;                  // pieces whose loads are in flight together
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kSplit;
+  const int row = blockIdx.y * (kJoinRows / kSplit) + warp / kSplit;
+  int c = blockIdx.x + 1;
+  if constexpr (kFew) {
+    __shared__ int32_t found, counts[kJoinRows];
+    if (threadIdx.x == 0) found = 0;
+    const bool here = threadIdx.x < ctas && __ldcg(a.cut + threadIdx.x).x >= 0;
+    const uint32_t of_warp = __ballot_sync(0xffffffffu, here);
+    if (lane == 0) counts[warp] = __popc(of_warp);
+    __syncthreads();
+    int32_t before = __popc(of_warp & ((1u << lane) - 1));
+    for (int i = 0; i < warp; ++i) before += counts[i];
+    if (here && before == static_cast<int32_t>(blockIdx.x)) found = static_cast<int32_t>(threadIdx.x) + 1;
+    __syncthreads();
+    c = found;
+    if (c == 0) return;
+  }
   const int4 tile = __ldcg(a.cut + c - 1);
   const int32_t h = (kTree ? tile.y & 0xffff : tile.y) * a.ht + row;
   if (tile.x < 0 || h >= (kTree ? tile.y >> 16 : 1) * a.H || row >= a.ht) return;
   // pieces: CTA c - 1's slot 1, then slot 0 of CTA c, c + 1, ... up to the end
   // (a CTA with units has all its predecessors with units)
-  int32_t count = 2;
-#pragma unroll 1
-  while (c + count - 1 < ctas && share_begin(tile.w, ctas, c + count - 1) < tile.z) ++count;
+  const int32_t count = share_of_unit(tile.w, ctas, tile.z - 1) - (c - 1) + 1;
   const auto slot = [&](int32_t k) -> int64_t {
     return k == 0 ? 2 * static_cast<int64_t>(c - 1) + 1 : 2 * static_cast<int64_t>(c - 1 + k);
   };
@@ -1498,18 +1576,17 @@ __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a
   float m = first;
 #pragma unroll 1
   for (int32_t k = lane + 32; k < count; k += 32) m = fmaxf(m, lse_of(k));
-  float acc[16], total = 0.0f;
+  float acc[4 * kQuads], total = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-  const float4* src = reinterpret_cast<const float4*>(a.piece + static_cast<int64_t>(row) * kD) + lane;
-  constexpr int kBatch = 4;                           // pieces whose loads are in flight together
+  for (int i = 0; i < 4 * kQuads; ++i) acc[i] = 0.0f;
+  const float4* src = reinterpret_cast<const float4*>(a.piece + static_cast<int64_t>(row) * kD) + lane + 32 * part;
 #pragma unroll 1
   for (int32_t k0 = 0; k0 < count; k0 += kBatch) {
-    float4 v[kBatch][4];
+    float4 v[kBatch][kQuads];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kQuads; ++i)
         v[k][i] = k0 + k < count ? __ldcg(src + slot(k0 + k) * (kPieceRow / 4) + 32 * i)
                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
@@ -1525,7 +1602,7 @@ __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a
       if (w == 0.0f) continue;
       total += w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kQuads; ++i) {
         acc[4 * i] = fmaf(w, v[k][i].x, acc[4 * i]);
         acc[4 * i + 1] = fmaf(w, v[k][i].y, acc[4 * i + 1]);
         acc[4 * i + 2] = fmaf(w, v[k][i].z, acc[4 * i + 2]);
@@ -1538,13 +1615,13 @@ __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a
   // the lane's rows 4l .. 4l + 3 of each quarter are four values in a row
   uint16_t* dst = a.out + (kTree ? row_at(a, tile.x, h, a.o_st, a.o_sh) : t * a.o_st + h * a.o_sh);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kQuads; ++i) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv);
     const __nv_bfloat162 y = __floats2bfloat162_rn(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
-    *reinterpret_cast<uint2*>(dst + value_of(i, 4 * lane)) =
+    *reinterpret_cast<uint2*>(dst + value_of(part + i, 4 * lane)) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
-  if (lane == 0 && a.lse)
+  if (lane == 0 && part == 0 && a.lse)
     a.lse[t * a.H + h] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
 }
 
@@ -1654,6 +1731,10 @@ int32_t stack_of(int32_t H, int32_t T, int32_t B) {
 // each. 64 tokens over a window of 128 positions (two units): 21.6 us cut and
 // joined, 19.6 us whole.
 constexpr int kWholeUnits = 2;
+// Those of groups of drafted tokens, whose windows together make a third unit of a
+// window's two, a unit or two more: 64 trees of up to 8 tokens, 16 heads over a window
+// of 128: 30.4 us cut and joined, 21.3 us whole.
+constexpr int kWholeGroupUnits = 4;
 
 // Heads per row tile: 64, what the products are made for, or 32 or 16 while
 // every unit (or uncut row tile) still has an SM of its own. The conversions and
@@ -1681,6 +1762,20 @@ Layout layout_for(int sms) {
   return L;
 }
 
+// Joins the pieces of a launch of up to `tiles` row tiles.
+template <bool kTree>
+cudaError_t launch_join(const Args& d, int32_t ctas, int64_t tiles, cudaStream_t s) {
+  const int32_t rows = d.stack * d.H < d.ht ? d.stack * d.H : d.ht;
+  const auto grid = [&](int64_t x, int32_t of_block) {
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>((rows + of_block - 1) / of_block));
+  };
+  if constexpr (kTree) {
+    if (4 * tiles <= ctas && ctas <= kJoinThreads)
+      return launch_pdl(merge_pieces_kernel<true, true>, grid(tiles, kJoinRows / 4), dim3(kJoinThreads), 0, s, d, ctas);
+  }
+  return launch_pdl(merge_pieces_kernel<kTree, false>, grid(ctas - 1, kJoinRows), dim3(kJoinThreads), 0, s, d, ctas);
+}
+
 template <bool kFp8, bool kTree>
 cudaError_t launch(Args d, int sms, cudaStream_t s) {
   const auto kernel = kv_attn_kernel<kFp8, kTree>;
@@ -1692,22 +1787,20 @@ cudaError_t launch(Args d, int sms, cudaStream_t s) {
   d.hg = (d.stack * d.H + d.ht - 1) / d.ht;
   // tokens per launch: what one plan holds, and fewer than 2^30 units
   const int64_t fit = (int64_t{1} << 30) / (most * d.hg);
-  constexpr int32_t kChunk = kTree ? kTreeChunkT : kChunkT;
-  const int32_t chunk = static_cast<int32_t>(fit < kChunk ? fit : kChunk);
+  const int32_t chunk = static_cast<int32_t>(fit < kChunkT ? fit : kChunkT);
   for (d.t0 = 0; e == cudaSuccess && d.t0 < d.T; d.t0 += chunk) {
     d.tc = d.T - d.t0 < chunk ? d.T - d.t0 : chunk;
     const int64_t tiles = most_groups(d, d.tc) * d.hg;
-    d.whole = most <= kWholeUnits && tiles <= sms ? 1 : 0;
+    // between the row tiles there are if all groups are full and if none is
+    const int64_t likely = (tiles + (static_cast<int64_t>(d.tc) - 1 + d.stack) / d.stack * d.hg) / 2;
+    d.whole = d.stack > 1 ? most <= kWholeGroupUnits && likely <= sms : most <= kWholeUnits && tiles <= sms;
     // one CTA per SM, and no more than there can be units
     const int64_t units = tiles * most;
     const int32_t ctas = static_cast<int32_t>(d.whole ? tiles : units < sms ? units : sms);
     kernel<<<static_cast<unsigned>(ctas), kThreads, kBytes, s>>>(d);
     e = cudaGetLastError();
     if (e == cudaSuccess && ctas > 1 && !d.whole)
-      e = launch_pdl(merge_pieces_kernel<kTree>,
-                     dim3(static_cast<unsigned>(ctas - 1),
-                          static_cast<unsigned>(((d.stack * d.H < d.ht ? d.stack * d.H : d.ht) + kJoinRows - 1) / kJoinRows)),
-                     dim3(kJoinThreads), 0, s, d, ctas);
+      e = launch_join<kTree>(d, ctas, tiles, s);
   }
   return e;
 }
