@@ -26,7 +26,7 @@ namespace qli {
 namespace rows {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kKvRow = 512, kIndexRow = 128;
 
 // A rotation: pairs of a row's values from unit `o8` on (units are 8 values).
@@ -482,18 +482,20 @@ int64_t tokens_of(int64_t count, int64_t rows, int64_t H) {
   return n < in ? n : in;
 }
 
-// Blocks an SM holds, by way of the registers: 4 with codes (64 registers; 3 blocks
-// without spills and 5 with more were slower), 5 with BF16 results.
-constexpr int kBlocksPerSm = 4, kBlocksPerSmBf16 = 5;
-// Sets of rows per block at most: the table and the start are paid once for them.
+// Blocks an SM holds, by way of the registers: 8 with codes (64 registers a thread: half
+// again as many without spills, and fewer with more of them, took 8% and 5% longer), 9
+// with BF16 results. Blocks of 256 threads, half as many, took 2 to 5% longer.
+constexpr int kBlocksPerSm = 8, kBlocksPerSmBf16 = 9;
+// Sets of rows per block at most: the table and the start are paid once for them (with
+// 2 the queries below took 7% longer, with 8 the same).
 constexpr int kSets = 4;
 
 // ---- queries --------------------------------------------------------------------
 // Bound by HBM with BF16 results: 2047 tokens of 64 heads x 512 with RMS norm and a
-// rotated tail (268 MB) take 44 us, 6.0 TB/s. With codes by the instructions, some 16 a
-// value: 4096 tokens of 64 heads x 128 to E4M3 (101 MB) take 23 us, 4.3 TB/s, 70% of
-// the issue slots. One set of rows a block, without the next one in flight, took 59
-// and 32 us; the norm's and the layout's branches inside the loop 51 and 26.
+// rotated tail (268 MB) take 43 us, 6.2 TB/s. With codes by the instructions, some 16 a
+// value: 4096 tokens of 64 heads x 128 to E4M3 (101 MB) take 22.4 us, 4.5 TB/s, with 64%
+// of the issue slots taken. One set of rows a block, without the next one in flight,
+// took 59 and 32 us; the norm's and the layout's branches inside the loop 51 and 26.
 template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, kMode == 0 ? kBlocksPerSmBf16 : kBlocksPerSm) prepare_kernel(const __grid_constant__ Prep p, DenseIn in,
                                                            DenseOut<kMode> out, const int32_t* positions,
@@ -543,8 +545,8 @@ struct AppendArgs {
 };
 
 // A block takes a few tokens: their KV rows, then their index K rows, by one table where
-// they turn alike. Bound by the instructions: 65536 tokens to E4M3 (127 MB) take 37 us,
-// 3.4 TB/s; separate blocks for the two kinds, each with its table, took 54.
+// they turn alike. Bound by the instructions, 440 a token and warp: 65536 tokens to E4M3
+// (127 MB) take 35 us, 3.6 TB/s; separate blocks for the two kinds, each with its table, took 54.
 template <int kKv, int kIndex>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const __grid_constant__ AppendArgs<kKv, kIndex> a) {
   extern __shared__ float4 table4[];
@@ -572,7 +574,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const __
 // ---- rotation alone ---------------------------------------------------------------
 // A thread has two units of a row, h8 apart: eight pairs of the half layout, or
 // two times four neighbouring ones. In place nothing else of the row is touched;
-// otherwise the block copies the rest of its rows.
+// otherwise the block copies the rest of its rows. Bound by HBM: 4093 tokens of 33 heads
+// x 512 out of wider rows (277 MB) take 44.8 us, 6.2 TB/s; 64 tokens of 64 heads in
+// place 1.8 us, the time of a launch.
 struct RotateArgs {
   const uint16_t* x;
   int64_t x_st, x_sh;
