@@ -497,7 +497,7 @@ typedef struct qli_rotate_args {
     const uint16_t *x;           /* (t, h, d) at x[t*x_stride_t + h*x_stride_h + d]; 16-byte aligned,
                                     strides in elements, multiples of 8; 0 broadcasts */
     int64_t x_stride_t, x_stride_h;
-    int32_t T, H, D;             /* D: a multiple of 8, at least 16; T * H below 2^31 */
+    int32_t T, H, D;             /* D: a multiple of 8, 16..65536; T * H at most 2^30 */
     int32_t inverse;
     const int32_t *positions;    /* [T] */
     uint16_t *out;               /* likewise; rows that do not overlap */
@@ -529,7 +529,7 @@ typedef struct qli_row_prep {
 typedef struct qli_prepare_args {
     const uint16_t *x;           /* as in qli_rotate_args */
     int64_t x_stride_t, x_stride_h;
-    int32_t T, H;
+    int32_t T, H;                /* T * H at most 2^30 */
     const int32_t *positions;    /* [T], or NULL without a rotation */
     void *out;                   /* BF16 or codes [T, H, width]: strides in elements, multiples of 16 bytes;
                                     16-byte aligned; rows that do not overlap */
@@ -552,7 +552,7 @@ typedef struct qli_append_args {
     int64_t kv_stride;
     const uint16_t *index_k;     /* row i: 128 BF16 values at index_k + i * index_stride; or NULL */
     int64_t index_stride;
-    int64_t n;                   /* below 2^31 */
+    int64_t n;                   /* at most 2^30 */
     const int32_t *positions;    /* [n], or NULL without a rotation */
     const int64_t *slot_mapping; /* [n]: page * rows_per_page + row; negative: padding */
     uint8_t *cache;

@@ -556,7 +556,7 @@ struct Group {
     uint64_t vis = ~uint64_t{0};
 #pragma unroll 1
     for (int32_t k = 0; k < S.tokens[t_]; ++k) {
-      const int32_t lo = max(0, k * a.H - g * a.ht), hi = min(64, (k + 1) * a.H - g * a.ht);
+      const int32_t lo = max(0, k * a.H - g * a.ht), hi = min(a.ht, (k + 1) * a.H - g * a.ht);
       if (hi <= lo) continue;
       const bool of_node = sees(a, S, t_, k, max(node, 0));
       const bool see = node >= 0 ? of_node : a.window <= 0 || before <= a.window - S.own[t_ + k];
@@ -618,6 +618,10 @@ __device__ __forceinline__ void record_cut(const Args& a, int32_t t, int32_t g, 
   a.cut[blockIdx.x] = make_int4(end > u1 && first >= u0 ? t : -1, g, end, total);
 }
 
+// Row tiles of the group of t (0: not its first token).
+__device__ __forceinline__ int32_t tiles_at(const TreeSmem& S, int32_t t) { return S.tiles[t]; }
+__device__ __forceinline__ int32_t tiles_at(const Smem&, int32_t) { return 1; }
+
 // Plans the launch: every token's request and visible positions, and the CTA's
 // share. A thread takes one token.
 template <bool kTree>
@@ -655,13 +659,18 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
       const int32_t b = request_of(req.cu, a.B, a.T, t);
       int32_t q0, q1, lk, res;
       sanitize_request(req, b, q0, q1, lk, res);
+      // the request's tokens, or those before or behind all requests, which see nothing
+      int32_t begin = t < q0 ? 0 : q0, end = t < q0 ? q0 : q1;
       if (q0 <= t && t < q1) {
         P = lk - (q1 - q0);
         nodes = P < 0 ? 0 : min(q1 - q0, 64 * a.words);
         own = a.words > 1 ? tree_count(a, t, 1, nodes) : __popcll(low_bits(early.mask, nodes));
-        first = t - (t - max(q0, a.t0)) % stack;
-        group = min(stack, min(q1, a.t0 + a.tc) - t);
+      } else if (t >= q1) {
+        begin = q1;
+        end = a.T;
       }
+      first = t - (t - max(begin, a.t0)) % stack;
+      group = min(stack, min(end, a.t0 + a.tc) - t);
       S.tokB[tid] = b;
       S.prefix[tid] = P;
       S.nodes[tid] = static_cast<uint16_t>(nodes);
@@ -754,14 +763,30 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
   const int32_t total = __shfl_sync(0xffffffffu, sums, 31);
   const int32_t at = __shfl_sync(0xffffffffu, sums, warp) - own + incl - mine;
   if (kTree && a.whole) {
-    const int32_t c = static_cast<int32_t>(blockIdx.x);
-    if (at <= c && c < at + mine) {
+    // a row tile a CTA; more only where boundaries fall (see most_groups)
+    const int32_t ctas = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
+    const int32_t begin = total <= ctas ? c : share_begin(total, ctas, c);
+    const int32_t end = total <= ctas ? c + 1 : share_begin(total, ctas, c + 1);
+    if (at <= begin && begin < at + mine) {
       S.start_t = tid;
-      S.start_g = c - at;
+      S.start_g = begin - at;
       S.start_i = 0;
       S.count = units;
     }
-    if (tid == 0 && c >= total) S.count = 0;
+    if (tid == 0 && begin >= total) S.count = 0;
+    __syncthreads();
+    if (end - begin > 1 && tid == 0) {
+      int32_t t = S.start_t, g = S.start_g, count = 0;
+#pragma unroll 1
+      for (int32_t k = begin; k < end; ++k) {
+        count += units_of<kTree>(a, S.tokV[t]);
+        if (++g == tiles_at(S, t)) {
+          g = 0;
+          do ++t; while (t < a.tc && tiles_at(S, t) == 0);
+        }
+      }
+      S.count = count;
+    }
     __syncthreads();
     return;
   }
@@ -959,7 +984,7 @@ __device__ __forceinline__ bool run_loaders(const Args& a, SmemOf<kTree>& S) {
   uint32_t seg = 0;
   Walk<kTree> w(a, S);                                // unit n + 1
   uint4 x[2][4];
-  // Of a unit that not all rows see, NaN codes are taken out and noted: a weight of
+  // Of positions that not all rows see, NaN codes are taken out and noted: a weight of
   // 0 times NaN would reach the rows that do not see them.
   [[maybe_unused]] bool masked = false;
 #pragma unroll 1
@@ -1013,7 +1038,7 @@ __device__ __forceinline__ bool run_loaders(const Args& a, SmemOf<kTree>& S) {
         const uint32_t slot = (n + 1) & (kSlots - 1);
         if (!wait(&S.rowfull[slot], ((n + 1) / kSlots) & 1)) return false;
         const uint8_t* r[2] = {S.row[slot][r0] + off, S.row[slot][r0 + 4] + off};
-        if constexpr (kTree) masked = (S.masked[slot][0] | S.masked[slot][1]) != 0u;
+        if constexpr (kTree) masked = S.masked[slot][lw / (kLoadWarps / kRowWarps)] != 0u;   // of the warp's rows
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -1534,32 +1559,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = kJoinThreads / 32;
 
-// kFew: a launch of few row tiles, each in many pieces. Block (i, k) takes the i-th row
-// tile that goes on in another CTA, four warps a row with a quarter of its values each
-// and four times as many pieces in flight. One tree of 8 tokens of 64 heads over 2048
-// positions, 8 row tiles in 19 pieces each: 25.7 us without, 19.9 with.
-template <bool kTree, bool kFew>
-__global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a, int32_t ctas) {
-  pdl_wait();
-  constexpr int kSplit = kFew ? 4 : 1, kQuads = 4 / kSplit;       // warps of a row, float4s of a lane
+// Row `row` of the row tile that began in CTA c - 1, by a warp, or by kSplit of them
+// with a quarter (of kSplit 4) of its values each.
+template <bool kTree, int kSplit>
+__device__ __forceinline__ void join_row(const Args& a, int32_t ctas, int32_t c, int32_t row, int part) {
+  constexpr int kQuads = 4 / kSplit;                  // float4s of a lane
   constexpr int kBatch = 4 * kSplit;                  // pieces whose loads are in flight together
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kSplit;
-  const int row = blockIdx.y * (kJoinRows / kSplit) + warp / kSplit;
-  int c = blockIdx.x + 1;
-  if constexpr (kFew) {
-    __shared__ int32_t found, counts[kJoinRows];
-    if (threadIdx.x == 0) found = 0;
-    const bool here = threadIdx.x < ctas && __ldcg(a.cut + threadIdx.x).x >= 0;
-    const uint32_t of_warp = __ballot_sync(0xffffffffu, here);
-    if (lane == 0) counts[warp] = __popc(of_warp);
-    __syncthreads();
-    int32_t before = __popc(of_warp & ((1u << lane) - 1));
-    for (int i = 0; i < warp; ++i) before += counts[i];
-    if (here && before == static_cast<int32_t>(blockIdx.x)) found = static_cast<int32_t>(threadIdx.x) + 1;
-    __syncthreads();
-    c = found;
-    if (c == 0) return;
-  }
+  const int lane = threadIdx.x & 31;
   const int4 tile = __ldcg(a.cut + c - 1);
   const int32_t h = (kTree ? tile.y & 0xffff : tile.y) * a.ht + row;
   if (tile.x < 0 || h >= (kTree ? tile.y >> 16 : 1) * a.H || row >= a.ht) return;
@@ -1623,6 +1629,36 @@ __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a
   }
   if (lane == 0 && part == 0 && a.lse)
     a.lse[t * a.H + h] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
+}
+
+// kFew: a launch of few row tiles, each in many pieces. Block (i, k) takes the i-th row
+// tile that goes on in another CTA, four warps a row with a quarter of its values each
+// and four times as many pieces in flight. One tree of 8 tokens of 64 heads over 2048
+// positions, 8 row tiles in 19 pieces each: 25.7 us without, 19.9 with.
+template <bool kTree, bool kFew>
+__global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a, int32_t ctas) {
+  pdl_wait();
+  constexpr int kSplit = kFew ? 4 : 1;                // warps of a row
+  [[maybe_unused]] const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kSplit;
+  const int row = blockIdx.y * (kJoinRows / kSplit) + warp / kSplit;
+  if constexpr (!kFew) {
+    join_row<kTree, 1>(a, ctas, blockIdx.x + 1, row, part);
+  } else {
+    __shared__ int32_t cuts[kJoinThreads], counts[kJoinRows];
+    const bool here = threadIdx.x < ctas && __ldcg(a.cut + threadIdx.x).x >= 0;
+    const uint32_t of_warp = __ballot_sync(0xffffffffu, here);
+    if (lane == 0) counts[warp] = __popc(of_warp);
+    __syncthreads();
+    int32_t before = __popc(of_warp & ((1u << lane) - 1)), all = 0;
+    for (int i = 0; i < kJoinRows; ++i) {
+      if (i < warp) before += counts[i];
+      all += counts[i];
+    }
+    if (here) cuts[before] = static_cast<int32_t>(threadIdx.x) + 1;
+    __syncthreads();
+#pragma unroll 1
+    for (int32_t i = blockIdx.x; i < all; i += gridDim.x) join_row<kTree, kSplit>(a, ctas, cuts[i], row, part);
+  }
 }
 
 std::atomic<uint64_t> g_smem_kv_attn[4];
@@ -1710,9 +1746,10 @@ int64_t most_units(const Args& d) {
 }
 
 // Most groups of up to `stack` tokens that `tokens` in a row can make: every request
-// may leave one that is not full.
+// may leave one that is not full, and so may what lies before and behind them all and
+// the end of the launch. (Of boundaries that fall there may be more: a group a token.)
 int64_t most_groups(const Args& d, int64_t tokens) {
-  const int64_t n = tokens / d.stack + d.B + 1;
+  const int64_t n = tokens / d.stack + d.B + 3;
   return n < tokens ? n : tokens;
 }
 

@@ -28,6 +28,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kKvRow = 512, kIndexRow = 128;
+constexpr int64_t kMostRows = int64_t{1} << 30;   // of a call: row numbers and a block's beyond are 32 bits
+constexpr int32_t kMostValues = 1 << 16;          // of a row that is rotated
 
 // A rotation: pairs of a row's values from unit `o8` on (units are 8 values).
 struct Turn {
@@ -45,7 +47,7 @@ struct Prep {
 };
 
 // Cosine and sine of 2^-32 `frac` turns. Within an eighth of a turn of the nearest
-// quarter, |t| <= pi / 4, the Taylor series up to t^9 and t^10 leave 2^-29 and 2^-30;
+// quarter, |t| <= pi / 4, the Taylor series up to t^9 and t^10 leave 2^-29 and 2^-33;
 // what is off is the rounding of t and of the sums, about 2^-24 together.
 __device__ __forceinline__ void turn_of(uint32_t frac, float& c, float& s) {
   const uint32_t quarter = (frac + 0x20000000u) >> 30;
@@ -691,7 +693,7 @@ qli_status check_dense(const void* x, int64_t x_st, int64_t x_sh, int32_t T, int
   if (!apart(T, H, o_st, o_sh, width)) return QLI_ERR_INVALID_ARG;
   // in place: the same rows
   if (x == out && ((T > 1 && x_st != o_st) || (H > 1 && x_sh != o_sh))) return QLI_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(T) * H > INT32_MAX) return QLI_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(T) * H > kMostRows) return QLI_ERR_UNSUPPORTED;
   return QLI_OK;
 }
 
@@ -761,7 +763,7 @@ extern "C" qli_status qli_rotate(const qli_rotate_args* a, const qli_rotary* rot
   using namespace qli::rows;
   if (a == nullptr || rotary == nullptr) return QLI_ERR_INVALID_ARG;
   if (a->T < 0 || a->H < 1) return QLI_ERR_INVALID_ARG;
-  if (a->D < 16 || a->D % 8 != 0) return QLI_ERR_UNSUPPORTED;
+  if (a->D < 16 || a->D > kMostValues || a->D % 8 != 0) return QLI_ERR_UNSUPPORTED;
   qli_status st = check_rotary(*rotary, a->D);
   if (st != QLI_OK) return st;
   if (a->inverse && rotary->magnitude == 0.0f) return QLI_ERR_INVALID_ARG;
@@ -832,7 +834,7 @@ extern "C" qli_status qli_append_kv(const qli_append_args* a, const qli_row_prep
   if (a->quant_mode != QLI_QUANT_INT8 && a->quant_mode != QLI_QUANT_FP8) return QLI_ERR_UNSUPPORTED;
   if (a->n < 0 || a->num_pages < 0) return QLI_ERR_INVALID_ARG;
   if (a->n == 0) return QLI_OK;
-  if (a->n > INT32_MAX) return QLI_ERR_UNSUPPORTED;
+  if (a->n > kMostRows) return QLI_ERR_UNSUPPORTED;
   if (a->kv == nullptr && a->index_k == nullptr) return QLI_ERR_INVALID_ARG;
   if (a->cache == nullptr || a->slot_mapping == nullptr) return QLI_ERR_INVALID_ARG;
   const int32_t R = a->rows_per_page;

@@ -253,6 +253,24 @@ def _shared_case():
     return case
 
 
+def test_nan_in_rows_that_all_see():
+    """A prefix row that is not finite reaches every token, whichever half of the unit it
+    is in (node positions are in the other one)."""
+    for j in (3, 40, 70, 96):                                    # units of 64: nodes are 96 .. 99
+        case = _shared_case()
+        kw = case.upload()
+        want = qli.kv_tree_attention(scale=SCALE, **kw)
+        page, row = int(case.bt[0, j // case.R]), j % case.R
+        kw["cache"][page, case.layout["kv_offset"] + 512 * row + 9] = 0x7F
+        out, lse = qli.kv_tree_attention(scale=SCALE, **kw)
+        import torch
+        for t in range(4):
+            if j < 96 or t < 2:                                  # node 0 is in the path of tokens 0 and 1
+                assert not torch.isfinite(out[t]).any(), (j, t)
+            else:
+                assert torch.equal(out[t], want[0][t]), (j, t)
+
+
 @pytest.mark.parametrize("what", ["codes", "scale", "infinite-scale"])
 def test_nan_in_rows_of_another_branch(what):
     """A drafted token whose row is not finite (the last one of a branch) makes the
@@ -312,13 +330,49 @@ def test_rows_that_see_their_first_position_late():
     check(case)
 
 
-def test_requests_whose_boundaries_fall_stay_in_bounds():
-    """Boundaries that go back are flagged; every token gets a finite answer."""
+@pytest.mark.parametrize("window", [0, 64])
+def test_boundaries_that_fall_are_flagged(window):
+    """No access leaves its buffer and every token gets an answer, in shared and in whole
+    row tiles."""
     import torch
-    case = TreeCase(76, [300, 300, 300], [8, 8, 8], 16, kv8.FP8, "tree")
+    case = TreeCase(76, [300] * 12, [8] * 12, 16, kv8.FP8, "tree")
     kw = case.upload()
-    kw["cu_seqlens_q"] = torch.tensor([0, 16, 8, 24], dtype=torch.int32, device="cuda")
+    cu = [8 * b for b in range(13)]
+    cu[3], cu[7] = 40, 16
+    kw["cu_seqlens_q"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out, lse = qli.kv_tree_attention(scale=SCALE, err_word=err, **kw)
+    out = torch.full((96, 16, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((96, 16), float("nan"), device="cuda")
+    qli.kv_tree_attention(scale=SCALE, err_word=err, window=window, out=out, lse=lse, **kw)
     assert int(err.item()) & 1
     assert torch.isfinite(out.float()).all() and not torch.isnan(lse).any()
+
+
+@pytest.mark.parametrize("window", [0, 64])
+@pytest.mark.parametrize("H", [16, 64])
+def test_tokens_that_no_request_covers(H, window):
+    """A padded batch: tokens before the first and behind the last request are flagged
+    and see nothing; the others are as without them."""
+    import torch
+    case = TreeCase(77, [400, 90], [9, 6], H, kv8.FP8, "tree")
+    kw = case.upload()
+    want = qli.kv_tree_attention(scale=SCALE, window=window, **kw)
+    for before, behind in ((0, 600), (3, 0), (11, 50)):
+        T = 15 + before + behind
+        q = torch.full((T, H, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+        mask = torch.full((T, 1), -1, dtype=torch.int64, device="cuda")
+        q[before:before + 15], mask[before:before + 15] = kw["q"], kw["tree_mask"]
+        cu = torch.tensor([before, before + 9, before + 15], dtype=torch.int32, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full((T, H, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((T, H), float("nan"), device="cuda")
+        qli.kv_tree_attention(scale=SCALE, window=window, err_word=err, out=out, lse=lse,
+                              **dict(kw, q=q, tree_mask=mask, cu_seqlens_q=cu))
+        assert int(err.item()) == 1
+        a, b = out[before:before + 15].float(), want[0].float()
+        # other shares of the work round differently: BF16 steps of the output (2^-8 of it
+        # each way), and FP16 weights (2^-11 of the largest value)
+        assert torch.all((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -9 * b.abs().amax())
+        assert torch.all((lse[before:before + 15] - want[1]).abs() <= 2.0 ** -10)
+        rest = torch.cat([torch.arange(before), torch.arange(before + 15, T)])
+        assert not out[rest].any() and torch.isneginf(lse[rest]).all()

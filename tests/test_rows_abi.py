@@ -72,7 +72,7 @@ def test_rotate_refuses_rotations(L, over, want):
     (dict(out_stride_h=64), INVALID), (dict(out_stride_t=512), INVALID),          # rows that overlap
     (dict(out_stride_t=128, out_stride_h=256), INVALID),
     (dict(out=P, out_stride_h=256, out_stride_t=2048), INVALID),                 # in place at other strides
-    (dict(T=1 << 27, H=16, out_stride_t=2048), UNSUPPORTED)])
+    (dict(T=(1 << 27) + 1, out_stride_t=1024), UNSUPPORTED), (dict(D=65544), UNSUPPORTED)])
 def test_rotate_refuses(L, over, want):
     assert L.qli_rotate(ctypes.byref(good_rotate(**over)), ctypes.byref(rotary()), None) == want
 
@@ -143,7 +143,7 @@ def _append(L, kv_prep=None, index_prep=None, **over):
 
 @pytest.mark.parametrize("over,want", [
     (dict(kv_mode=3), UNSUPPORTED), (dict(quant_mode=0), UNSUPPORTED), (dict(n=-1), INVALID),
-    (dict(num_pages=-1), INVALID), (dict(n=1 << 31), UNSUPPORTED), (dict(kv=None, index_k=None), INVALID),
+    (dict(num_pages=-1), INVALID), (dict(n=(1 << 30) + 1), UNSUPPORTED), (dict(kv=None, index_k=None), INVALID),
     (dict(cache=None), INVALID), (dict(slot_mapping=None), INVALID), (dict(rows_per_page=32), UNSUPPORTED),
     (dict(page_stride=0), INVALID), (dict(kv_stride=504), INVALID), (dict(index_stride=120), INVALID),
     (dict(kv_stride=516), ALIGNMENT), (dict(index_stride=132), ALIGNMENT), (dict(kv=P + 8), ALIGNMENT),
