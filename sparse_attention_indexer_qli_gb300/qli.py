@@ -950,30 +950,33 @@ class RowPrep:
                                         rotary.args(offset) if rotary is not None else RotaryArgs()))
 
 
-def _positions(positions, n, device):
+def _positions(positions, n, device, int32):
     """The address of a call's positions [n]."""
-    import torch
-    _check_cuda("positions", positions, torch.int32, device)
+    _check_cuda("positions", positions, int32, device)
     if positions.numel() != n or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous [%d] tensor" % n)
     return positions.data_ptr()
 
 
-def _row_strides(t, T, H, D):
-    """Strides of t [T, H, D] over its tokens and heads; those of a dimension of size
-    one may be any number."""
-    st, sh, _ = t.stride()
+def _row_strides(st, sh, T, H, D):
+    """Strides of a [T, H, D] tensor over its tokens and heads; those of a dimension of
+    size one may be any number."""
     return (st if T > 1 else H * D), (sh if H > 1 else D)
 
 
-def _row_output(name, out, dtype, shape, device, stream):
-    import torch
+def _row_output(out, dtype, shape, device, stream):
+    """(out, its strides), made or checked."""
     if out is None:
-        return _empty(shape, dtype, torch.device("cuda", device), stream)
-    _check_cuda(name, out, dtype, device)
-    if out.shape != shape or out.stride(-1) != 1:
-        raise ValueError("%s must be %s with unit stride in the last dim" % (name, list(shape)))
-    return out
+        import torch
+        out = _empty(shape, dtype, torch.device("cuda", device), stream)
+        return out, shape[1] * shape[2], shape[2]
+    _check_cuda("out", out, dtype, device)
+    if out.shape != shape:
+        raise ValueError("out must be %s" % list(shape))
+    st, sh, step = out.stride()
+    if step != 1:
+        raise ValueError("out must have unit stride in the last dim")
+    return out, st, sh
 
 
 def rotate(x, positions, rotary: Rotary, *, offset: int = 0, inverse: bool = False, out=None,
@@ -984,14 +987,17 @@ def rotate(x, positions, rotary: Rotary, *, offset: int = 0, inverse: bool = Fal
     place. Returns out [T, H, D]."""
     import torch
     device = _first_cuda("x", x, torch.bfloat16, torch.cuda.current_device)
-    if x.dim() != 3 or x.stride(2) != 1:
+    shape, strides = x.shape, x.stride()
+    if len(shape) != 3 or strides[2] != 1:
         raise ValueError("x must be [T, H, D] with unit stride in the last dim")
-    T, H, D = x.shape
-    pos = _positions(positions, T, device)
-    out = _row_output("out", out, torch.bfloat16, x.shape, device, stream)
+    T, H, D = shape
+    pos = _positions(positions, T, device, torch.int32)
+    x_t, x_h = o_t, o_h = _row_strides(strides[0], strides[1], T, H, D)
+    if out is not x:
+        out, o_t, o_h = _row_output(out, torch.bfloat16, shape, device, stream)
+        o_t, o_h = _row_strides(o_t, o_h, T, H, D)
     raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    a = _pack_rotate(x.data_ptr(), *_row_strides(x, T, H, D), T, H, D, int(inverse), pos,
-                     out.data_ptr(), *_row_strides(out, T, H, D))
+    a = _pack_rotate(x.data_ptr(), x_t, x_h, T, H, D, inverse, pos, out.data_ptr(), o_t, o_h)
     _check((_lib or lib()).qli_rotate(a, rotary.packed(offset), raw), "qli_rotate")
     return out
 
@@ -1005,35 +1011,59 @@ def prepare_q(x, positions, prep: RowPrep, *, out=None, scale_out=None, stream=N
     int8 [T, H, 128] and FP16 scale bits int16 [T, H], as quantize_q does."""
     import torch
     device = _first_cuda("x", x, torch.bfloat16, torch.cuda.current_device)
-    if x.dim() != 3 or x.stride(2) != 1 or x.shape[2] != prep.width:
+    shape, strides = x.shape, x.stride()
+    if len(shape) != 3 or strides[2] != 1 or shape[2] != prep.width:
         raise ValueError("x must be [T, H, %d] with unit stride in the last dim" % prep.width)
     if prep.device is not None and prep.device != device:
         raise ValueError("the weights of prep are on CUDA device %d, x on device %d" % (prep.device, device))
-    T, H, D = x.shape
+    T, H, D = shape
     if positions is not None:
-        pos = _positions(positions, T, device)
+        pos = _positions(positions, T, device, torch.int32)
     elif prep.rotary is None:
         pos = 0
     else:
         raise ValueError("a rotation needs positions")
+    x_t, x_h = o_t, o_h = _row_strides(strides[0], strides[1], T, H, D)
     sc = 0
     if quant_mode is None:
         if scale_out is not None:
             raise ValueError("scale_out needs a quant_mode")
-        out = _row_output("out", out, torch.bfloat16, x.shape, device, stream)
+        if out is not x:
+            out, o_t, o_h = _row_output(out, torch.bfloat16, shape, device, stream)
     else:
         if quant_mode not in (QUANT_INT8, QUANT_FP8):
             raise ValueError("quant_mode must be QUANT_INT8 or QUANT_FP8")
-        out = _row_output("out", out, torch.int8, x.shape, device, stream)
-        scale_out = _row_output("scale_out", scale_out, torch.int16, x.shape[:2], device, stream)
-        if not scale_out.is_contiguous():
-            raise ValueError("scale_out must be contiguous [T, H]")
+        out, o_t, o_h = _row_output(out, torch.int8, shape, device, stream)
+        if scale_out is None:
+            scale_out = _empty((T, H), torch.int16, torch.device("cuda", device), stream)
+        else:
+            _check_cuda("scale_out", scale_out, torch.int16, device)
+            if scale_out.shape != (T, H) or not scale_out.is_contiguous():
+                raise ValueError("scale_out must be a contiguous [T, H] tensor")
         sc = scale_out.data_ptr()
+    o_t, o_h = _row_strides(o_t, o_h, T, H, D)
     raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    a = _pack_prepare(x.data_ptr(), *_row_strides(x, T, H, D), T, H, pos, out.data_ptr(),
-                      *_row_strides(out, T, H, D), sc, quant_mode or 0, 0)
+    a = _pack_prepare(x.data_ptr(), x_t, x_h, T, H, pos, out.data_ptr(), o_t, o_h, sc, quant_mode or 0, 0)
     _check((_lib or lib()).qli_prepare_q(a, prep.packed, raw), "qli_prepare_q")
     return out if quant_mode is None else (out, scale_out)
+
+
+def _append_rows(name, x, prep, width, n, dtype, device):
+    """(address, stride) of the n rows of one kind."""
+    _check_cuda(name, x, dtype, device)
+    if x.dim() != 2:
+        raise ValueError("%s must be [n, %d]" % (name, width))
+    (rows, values), (pitch, step) = x.shape, x.stride()
+    if values != width or step != 1:
+        raise ValueError("%s must be [n, %d] with unit stride in the last dim" % (name, width))
+    if rows != n:
+        raise ValueError("one slot per row")
+    if prep is None or prep.width != width:
+        raise ValueError("%s needs a RowPrep of width %d" % (name, width))
+    if prep.device is not None and prep.device != device:
+        raise ValueError("the weights of %s's RowPrep are on CUDA device %d, the call's tensors on device %d"
+                         % (name, prep.device, device))
+    return x.data_ptr(), pitch if n > 1 else width
 
 
 def append_kv(kv, index_k, positions, slot_mapping, cache, *, rows_per_page: int, page_stride: int,
@@ -1057,30 +1087,22 @@ def append_kv(kv, index_k, positions, slot_mapping, cache, *, rows_per_page: int
         err = err_word.data_ptr()
     if not cache.is_contiguous() or not slot_mapping.is_contiguous():
         raise ValueError("cache and slot_mapping must be contiguous")
-    n, turns, at = slot_mapping.numel(), False, []
-    for name, x, prep, width in (("kv", kv, kv_prep, 512), ("index_k", index_k, index_prep, 128)):
-        if x is None:
-            at += [0, width]
-            continue
-        _check_cuda(name, x, torch.bfloat16, device)
-        if x.dim() != 2 or x.shape[1] != width or x.stride(1) != 1:
-            raise ValueError("%s must be [n, %d] with unit stride in the last dim" % (name, width))
-        if x.shape[0] != n:
-            raise ValueError("one slot per row")
-        if prep is None or prep.width != width:
-            raise ValueError("%s needs a RowPrep of width %d" % (name, width))
-        if prep.device is not None and prep.device != device:
-            raise ValueError("the weights of %s's RowPrep are on CUDA device %d, the call's tensors on device %d"
-                             % (name, prep.device, device))
-        turns |= prep.rotary is not None
-        at += [x.data_ptr(), x.stride(0) if n > 1 else width]
+    n, bf16 = slot_mapping.numel(), torch.bfloat16
+    rows = rows_i = (0, 0)
+    turns = False
+    if kv is not None:
+        rows = _append_rows("kv", kv, kv_prep, 512, n, bf16, device)
+        turns = kv_prep.rotary is not None
+    if index_k is not None:
+        rows_i = _append_rows("index_k", index_k, index_prep, 128, n, bf16, device)
+        turns |= index_prep.rotary is not None
     if positions is not None:
-        pos = _positions(positions, n, device)
+        pos = _positions(positions, n, device, torch.int32)
     elif turns:
         raise ValueError("a rotation needs positions")
     else:
         pos = 0
-    a = _pack_append(*at, n, pos, slot_mapping.data_ptr(), cache.data_ptr(), cache.numel() // page_stride,
+    a = _pack_append(*rows, *rows_i, n, pos, slot_mapping.data_ptr(), cache.data_ptr(), cache.numel() // page_stride,
                      page_stride, rows_per_page, kv_mode, quant_mode, 0, kv_offset, kv_scale_offset,
                      k_offset, scale_offset, err)
     raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
