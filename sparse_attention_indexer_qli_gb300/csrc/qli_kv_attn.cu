@@ -115,16 +115,24 @@ constexpr int kMaxWords = 256;                 // of a token's mask
 constexpr int kMaxStack = 8;                   // tokens of a group
 struct TreeSmem : Smem {
   int32_t prefix[kChunkT];                     // positions before the request's nodes
-  uint16_t nodes[kChunkT], own[kChunkT];       // the request's nodes in masks; those that the token sees
-  uint16_t any[kChunkT];                       // by group: the nodes that some token sees,
-  uint8_t tokens[kChunkT], tiles[kChunkT];     //   its tokens and row tiles: its tokens and row tiles (0: not the group's first token)
-  uint2 vis[kSlots][kPos];                     // rows of the row tile that see the position
-  uint32_t masked[kSlots][kRowWarps];          // 1: not all rows see all of a row warp's positions
-  uint8_t nan[kSlots][kPos];                   // 1: the position's row has NaN codes
+  uint16_t nodes[kChunkT];                     // the request's nodes in masks
+  uint8_t tokens[kChunkT], tiles[kChunkT];     // by group: its tokens and row tiles (0: not the group's first token)
+  union {
+    uint64_t mask[kChunkT];                    // masks of one word, without bits past the nodes
+    struct {                                   // of more words: nodes that the token sees, and
+      uint16_t own[kChunkT], any[kChunkT];     // by group those that some token sees
+    } many;
+  };
+  uint8_t vis[kSlots][kPos];                   // the group's tokens that see the position
+  uint8_t masked[kSlots][kRowWarps];           // 1: not all tokens see all of a row warp's positions
+  uint32_t nan[kSlots][kRowWarps];             // positions of a row warp whose rows have NaN codes
 };
-template <bool kTree>
-using SmemOf = std::conditional_t<kTree, TreeSmem, Smem>;
-template <bool kTree>
+// What a kernel is made for: listed or causally visible positions, or drafted trees with
+// a row tile of one token or of several.
+enum : int { kPlain = 0, kSingle = 1, kGroups = 2 };
+template <int kTree>
+using SmemOf = std::conditional_t<(kTree != kPlain), TreeSmem, Smem>;
+template <int kTree>
 constexpr int kSmemBytes = static_cast<int>(sizeof(SmemOf<kTree>)) + 1024;
 static_assert(kSmemBytes<true> <= 227 * 1024, "shared memory");
 
@@ -358,12 +366,12 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 
 // The launch's units in order: token, row tile of the token, unit of kPos
 // positions. A token has at least one unit, so that every output is written.
-template <bool kTree = false>
+template <int kTree = kPlain>
 __device__ __forceinline__ int32_t positions_of(const Args& a, int32_t V) {
-  if constexpr (kTree) return V;
+  if constexpr (kTree != kPlain) return V;
   return a.idx ? a.K : (a.window > 0 ? min(V, a.window) : V);
 }
-template <bool kTree = false>
+template <int kTree = kPlain>
 __device__ __forceinline__ int32_t units_of(const Args& a, int32_t V) {
   const int32_t n = positions_of<kTree>(a, V);
   return n <= kPos ? 1 : (n - 1) / kPos + 1;
@@ -383,7 +391,7 @@ __device__ __forceinline__ int32_t share_of_unit(int32_t total, int32_t ctas, in
 }
 
 // A CTA's share, unit by unit. Of drafted trees, t is a group's first token.
-template <bool kTree>
+template <int kTree>
 struct Walk {
   typedef SmemOf<kTree> M;
   int32_t k, count;            // units behind, units of the share
@@ -394,11 +402,11 @@ struct Walk {
   }
   // the row tiles of t, and their rows: heads of one token or of several
   __device__ __forceinline__ int32_t tiles(const Args& a, const M& S) const {
-    if constexpr (kTree) return S.tiles[t];
+    if constexpr (kTree == kGroups) return S.tiles[t];
     return a.hg;
   }
   __device__ __forceinline__ int32_t rows(const Args& a, const M& S) const {
-    if constexpr (kTree) return S.tokens[t] * a.H;
+    if constexpr (kTree == kGroups) return S.tokens[t] * a.H;
     return a.H;
   }
   __device__ __forceinline__ bool valid() const { return k < count; }
@@ -414,7 +422,7 @@ struct Walk {
     if (++g < tiles(a, S)) return;
     g = 0;
     ++t;
-    if constexpr (kTree) {
+    if constexpr (kTree == kGroups) {
       while (t < a.tc && S.tiles[t] == 0) ++t;
     }
     if (t < a.tc) n = units_of<kTree>(a, S.tokV[t]);
@@ -433,7 +441,7 @@ __device__ __forceinline__ int32_t request_of(const int32_t* cu, int32_t B, int3
 }
 
 // Flags requests with bad metadata, once a call.
-template <bool kTree>
+template <int kTree>
 __device__ __forceinline__ void flag_requests(const Args& a, int tid) {
   if (a.idx || a.t0 != 0 || !a.err) return;
   uint32_t e = 0u;
@@ -441,7 +449,7 @@ __device__ __forceinline__ void flag_requests(const Args& a, int tid) {
   for (int b = tid; b < a.B; b += kThreads) {
     int32_t q0, q1, lk, res;
     e |= sanitize_request(a, b, q0, q1, lk, res);
-    if (kTree && lk < q1 - q0) e |= QLI_DEVERR_KLEN;
+    if (kTree != kPlain && lk < q1 - q0) e |= QLI_DEVERR_KLEN;
   }
   if (e) atomicOr(a.err, e);
 }
@@ -454,7 +462,7 @@ struct Requests {
   int64_t cap;
 };
 constexpr int kRequestsInSmem = 10000;
-static_assert((3 * kRequestsInSmem + 1) * 4 + 8 * kChunkT <= 2 * kTile, "requests and masks fit in the tiles");
+static_assert((3 * kRequestsInSmem + 1) * 4 <= 2 * kTile, "the requests fit in the tiles");
 
 // Drafted trees. A request's last positions are the nodes of a tree, its tokens of the
 // call; a token sees the prefix before them and the nodes whose bits are set in its
@@ -527,42 +535,48 @@ __device__ __forceinline__ bool tree_sees(const Args& a, int32_t t, int32_t node
   for (int32_t w = (node >> 6) + 1; 64 * w < nodes; ++w) later += __popcll(tree_word(a, t, w, nodes));
   return later <= a.window;
 }
-// The masks of the group whose units a row warp is at: with one word to a mask, lane k
-// has token k's, and all have the union.
+// Nodes that token t of the launch sees.
+__device__ __forceinline__ int32_t own_nodes(const Args& a, const TreeSmem& S, int32_t t) {
+  return a.words > 1 ? S.many.own[t] : __popcll(S.mask[t]);
+}
+
+// The group whose units a row warp is at.
 struct Group {
-  int32_t t = -1;
-  uint64_t mine = 0u, any = 0u;
+  int32_t t = -1, any = 0;                     // first token; nodes that some token sees
+  uint64_t masks = 0u;                         // their mask, of one word
   __device__ __forceinline__ void enter(const Args& a, const TreeSmem& S, int32_t t_) {
-    if (t == t_ || a.words > 1) return;
+    if (t == t_) return;
     t = t_;
-    const int lane = threadIdx.x & 31;
-    mine = lane < S.tokens[t] ? tree_word(a, a.t0 + t + lane, 0, S.nodes[t]) : 0u;
-    any = static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(mine >> 32))) << 32 |
-          __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(mine));
-  }
-  __device__ __forceinline__ int32_t node(const Args& a, const TreeSmem& S, int32_t t_, int32_t rank) const {
-    return a.words > 1 ? tree_node(a, a.t0 + t_, S.tokens[t_], S.nodes[t_], rank) : bit_of(any, rank);
-  }
-  __device__ __forceinline__ bool sees(const Args& a, const TreeSmem& S, int32_t t_, int32_t k, int32_t node) const {
-    const int32_t own = S.own[t_ + k];
-    if (a.words > 1) return tree_sees(a, a.t0 + t_ + k, S.nodes[t_], own, node);
-    const uint64_t m = __shfl_sync(0xffffffffu, mine, k) >> (node & 63);
-    return (m & 1u) && (a.window <= 0 || own <= a.window || __popcll(m) <= a.window);
-  }
-  // Rows of row tile g (64 bits) that see a lane's position: a node, or -1 and a position
-  // `before` (1 or more) the prefix's end. Rows past the group's see all. (The whole warp.)
-  __device__ __forceinline__ uint2 rows(const Args& a, const TreeSmem& S, int32_t t_, int32_t g, int32_t node,
-                                        int32_t before) const {
-    uint64_t vis = ~uint64_t{0};
-#pragma unroll 1
-    for (int32_t k = 0; k < S.tokens[t_]; ++k) {
-      const int32_t lo = max(0, k * a.H - g * a.ht), hi = min(a.ht, (k + 1) * a.H - g * a.ht);
-      if (hi <= lo) continue;
-      const bool of_node = sees(a, S, t_, k, max(node, 0));
-      const bool see = node >= 0 ? of_node : a.window <= 0 || before <= a.window - S.own[t_ + k];
-      if (!see) vis &= ~((~uint64_t{0} >> (64 - (hi - lo))) << lo);
+    if (a.words > 1) {
+      any = S.many.any[t];
+      return;
     }
-    return make_uint2(static_cast<uint32_t>(vis), static_cast<uint32_t>(vis >> 32));
+    masks = 0u;
+#pragma unroll 1
+    for (int32_t k = 0; k < S.tokens[t]; ++k) masks |= S.mask[t + k];
+    any = __popcll(masks);
+  }
+  __device__ __forceinline__ int32_t node(const Args& a, const TreeSmem& S, int32_t rank) const {
+    return a.words > 1 ? tree_node(a, a.t0 + t, S.tokens[t], S.nodes[t], rank) : bit_of(masks, rank);
+  }
+  // Tokens that see a position: a node, or -1 and a position `before` (1 or more) the
+  // prefix's end.
+  __device__ __forceinline__ uint32_t seers(const Args& a, const TreeSmem& S, int32_t node, int32_t before) const {
+    uint32_t vis = 0xffu;
+#pragma unroll 1
+    for (int32_t k = 0; k < S.tokens[t]; ++k) {
+      bool sees;
+      if (node < 0) {
+        sees = a.window <= 0 || before <= a.window - own_nodes(a, S, t + k);
+      } else if (a.words > 1) {
+        sees = tree_sees(a, a.t0 + t + k, S.nodes[t], S.many.own[t + k], node);
+      } else {
+        const uint64_t m = S.mask[t + k] >> node;
+        sees = (m & 1u) && (a.window <= 0 || __popcll(m) <= a.window);
+      }
+      if (!sees) vis &= ~(1u << k);
+    }
+    return vis;
   }
 };
 // The token of the group that row v (below 2^12) belongs to.
@@ -590,11 +604,11 @@ __device__ __forceinline__ void share_of(const Args& a, int32_t total, int32_t& 
   u1 = share_begin(total, ctas, c + 1);
 }
 
-template <bool kTree>
+template <int kTree>
 __device__ __forceinline__ Early load_early(const Args& a) {
   const int tid = threadIdx.x, r = tid - 32 * kRowWarp0;
   Early v{0, 0, 0, -1, 0u};
-  if constexpr (kTree) {
+  if constexpr (kTree != kPlain) {
     if (tid < a.tc) v.mask = tree_word(a, a.t0 + tid, 0, 64);
   }
   if (tid <= a.B) v.cu = __ldg(a.cu + tid);
@@ -624,7 +638,7 @@ __device__ __forceinline__ int32_t tiles_at(const Smem&, int32_t) { return 1; }
 
 // Plans the launch: every token's request and visible positions, and the CTA's
 // share. A thread takes one token.
-template <bool kTree>
+template <int kTree>
 __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Early& early) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Requests req{a.cu, a.k_lens, a.residual, a.T, a.B, a.ratio, a.cap};
@@ -645,14 +659,16 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
   __syncthreads();
   int32_t V = 0, units = 0, tiles = a.hg;
   [[maybe_unused]] int32_t group = 1;
-  if constexpr (kTree) {
+  if constexpr (kTree != kPlain) {
     // groups rest on requests that follow each other; where the boundaries fall
     // (flagged below) each token stays alone
-    uint64_t* masks = reinterpret_cast<uint64_t*>(S.kv[1] + kTile) - kChunkT;   // behind the requests
-    bool falls = false;
+    int32_t stack = a.stack;
+    if (stack > 1) {
+      bool falls = false;
 #pragma unroll 1
-    for (int32_t b = tid; b < a.B; b += kThreads) falls |= req.cu[b] > req.cu[b + 1];
-    const int32_t stack = __syncthreads_or(falls) ? 1 : a.stack;
+      for (int32_t b = tid; b < a.B; b += kThreads) falls |= req.cu[b] > req.cu[b + 1];
+      if (__syncthreads_or(falls)) stack = 1;
+    }
     const int32_t t = a.t0 + tid;
     int32_t P = -1, nodes = 0, own = 0, first = t;
     if (tid < a.tc) {
@@ -664,39 +680,43 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
       if (q0 <= t && t < q1) {
         P = lk - (q1 - q0);
         nodes = P < 0 ? 0 : min(q1 - q0, 64 * a.words);
-        own = a.words > 1 ? tree_count(a, t, 1, nodes) : __popcll(low_bits(early.mask, nodes));
       } else if (t >= q1) {
         begin = q1;
         end = a.T;
       }
-      first = t - (t - max(begin, a.t0)) % stack;
-      group = min(stack, min(end, a.t0 + a.tc) - t);
+      if (stack > 1) {
+        first = t - (t - max(begin, a.t0)) % stack;
+        group = min(stack, min(end, a.t0 + a.tc) - t);
+      }
       S.tokB[tid] = b;
       S.prefix[tid] = P;
       S.nodes[tid] = static_cast<uint16_t>(nodes);
-      S.own[tid] = static_cast<uint16_t>(own);
-      masks[tid] = low_bits(early.mask, nodes);
+      if (a.words > 1) {
+        own = tree_count(a, t, 1, nodes);
+        S.many.own[tid] = static_cast<uint16_t>(own);
+      } else {
+        const uint64_t m = low_bits(early.mask, nodes);
+        own = __popcll(m);
+        S.mask[tid] = m;
+      }
     }
-    __syncthreads();
+    if (stack > 1) __syncthreads();
     tiles = 0;
     if (tid < a.tc && first == t) {
-      int32_t least = own;
+      int32_t least = own, any = own;
+      if (group > 1) {
+        uint64_t m = 0u;
 #pragma unroll 1
-      for (int32_t k = 1; k < group; ++k) least = min(least, static_cast<int32_t>(S.own[tid + k]));
-      if (P >= 0) {
-        int32_t any = own;
-        if (group > 1 && a.words > 1) any = tree_count(a, t, group, nodes);
-        if (group > 1 && a.words == 1) {
-          uint64_t m = 0u;
-          for (int32_t k = 0; k < group; ++k) m |= masks[tid + k];
-          any = __popcll(m);
+        for (int32_t k = 0; k < group; ++k) {
+          least = min(least, own_nodes(a, S, tid + k));
+          if (a.words == 1) m |= S.mask[tid + k];
         }
-        V = any + (a.window > 0 ? min(P, max(0, a.window - least)) : P);
-        // alone, a token sees all of its group's positions but those before its window
-        if (group == 1 && a.window > 0) V = min(V, a.window);
-        S.any[tid] = static_cast<uint16_t>(any);
+        any = a.words > 1 ? tree_count(a, t, group, nodes) : __popcll(m);
       }
-      if (P < 0) S.any[tid] = 0;
+      if (P >= 0) V = any + (a.window > 0 ? min(P, max(0, a.window - least)) : P);
+      // alone, a token sees all of its group's positions but those before its window
+      if (group == 1 && a.window > 0) V = min(V, a.window);
+      if (a.words > 1) S.many.any[tid] = static_cast<uint16_t>(any);
       S.tokV[tid] = V;
       S.tokens[tid] = static_cast<uint8_t>(group);
       tiles = (group * a.H + a.ht - 1) / a.ht;
@@ -715,13 +735,13 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
     units = units_of(a, V);
   }
   if (blockIdx.x == 0) flag_requests<kTree>(a, tid);
-  if (!kTree && a.whole) {
+  if (kTree != kGroups && a.whole) {
     __syncthreads();
     if (tid == 0) {
       S.start_t = static_cast<int32_t>(blockIdx.x) / a.hg;
       S.start_g = static_cast<int32_t>(blockIdx.x) % a.hg;
       S.start_i = 0;
-      S.count = units_of(a, S.tokV[S.start_t]);
+      S.count = units_of<kTree>(a, S.tokV[S.start_t]);
     }
     __syncthreads();
     return;
@@ -744,7 +764,7 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
     return;
   }
   // whole row tiles are shared out by number
-  const int32_t mine = (kTree && a.whole ? 1 : units) * tiles;
+  const int32_t mine = (kTree == kGroups && a.whole ? 1 : units) * tiles;
   int32_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -762,7 +782,7 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
   }
   const int32_t total = __shfl_sync(0xffffffffu, sums, 31);
   const int32_t at = __shfl_sync(0xffffffffu, sums, warp) - own + incl - mine;
-  if (kTree && a.whole) {
+  if (kTree == kGroups && a.whole) {
     // a row tile a CTA; more only where boundaries fall (see most_groups)
     const int32_t ctas = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
     const int32_t begin = total <= ctas ? c : share_begin(total, ctas, c);
@@ -801,7 +821,7 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
     if (tid == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   } else if (at <= u1 - 1 && u1 - 1 < at + mine) {
     const int32_t g = (u1 - 1 - at) / units, first = at + g * units;
-    record_cut(a, tid, kTree ? g | group << 16 : g, first, first + units, u0, u1, total);
+    record_cut(a, tid, kTree == kGroups ? g | group << 16 : g, first, first + units, u0, u1, total);
   }
   __syncthreads();
 }
@@ -822,7 +842,7 @@ __device__ __align__(16) const uint8_t kZeroRow[kD] = {};
 // The row tile's queries as FP16 times a power of two per head that brings the
 // head's largest magnitude to [2^13, 2^14); rows past the row tile's heads are
 // zero. A warp takes every eighth row.
-template <bool kTree>
+template <int kTree>
 __device__ __forceinline__ void load_queries(const Args& a, SmemOf<kTree>& S, const Walk<kTree>& w_,
                                              uint32_t parity, int lw) {
   const int32_t t = w_.t, g = w_.g;
@@ -841,7 +861,7 @@ __device__ __forceinline__ void load_queries(const Args& a, SmemOf<kTree>& S, co
       v[k][0] = v[k][1] = make_uint4(0u, 0u, 0u, 0u);
       if (r < heads) {
         const uint16_t* at = q + r * a.q_sh;
-        if constexpr (kTree) at = a.q + row_at(a, t, g * a.ht + r, a.q_st, a.q_sh) + 16 * lane;
+        if constexpr (kTree == kGroups) at = a.q + row_at(a, t, g * a.ht + r, a.q_st, a.q_sh) + 16 * lane;
         const uint4* src = reinterpret_cast<const uint4*>(at);
         v[k][0] = __ldg(src);
         v[k][1] = __ldg(src + 1);
@@ -878,7 +898,7 @@ __device__ __forceinline__ void load_queries(const Args& a, SmemOf<kTree>& S, co
 // position; `entry` is the first unit's), so that no step waits for the load of the
 // one before. Positions
 // past the table and pages outside the pool are skipped and flagged.
-template <bool kTree>
+template <int kTree>
 __device__ __forceinline__ bool run_rows(const Args& a, SmemOf<kTree>& S, int32_t entry) {
   const int lane = threadIdx.x & 31, r = threadIdx.x - 32 * kRowWarp0;
   bool bad = false;
@@ -889,8 +909,8 @@ __device__ __forceinline__ bool run_rows(const Args& a, SmemOf<kTree>& S, int32_
   uint16_t s1 = 0;
   bool live1 = false;
   [[maybe_unused]] Group group;
-  [[maybe_unused]] uint2 vis1 = make_uint2(~0u, ~0u), vis2 = vis1, vis3 = vis1;   // rows that see the position
-  [[maybe_unused]] bool shared1 = false, shared2 = false, shared3 = false;         // several tokens in the row tile
+  // tokens that see the position (0x100: and there are several in the row tile)
+  [[maybe_unused]] uint32_t vis1 = 0xffu, vis2 = vis1, vis3 = vis1;
 #pragma unroll 1
   for (int32_t m = -3; m < w.count; ++m) {
     if (m >= 0) {
@@ -903,23 +923,23 @@ __device__ __forceinline__ bool run_rows(const Args& a, SmemOf<kTree>& S, int32_
       const bool zero = live1 && s == 0.0f;
       S.row[slot][r] = zero ? kZeroRow : codes1;
       S.rs[slot][r] = live1 ? (zero ? 5.9604645e-8f : s) : 0.0f;
-      if constexpr (kTree) {
+      if constexpr (kTree == kGroups) {
         // a place without a position: no token of a group sees it, whatever its query holds
-        if (!live1 && shared1) vis1 = make_uint2(0u, 0u);
-        const bool some = __any_sync(0xffffffffu, (vis1.x & vis1.y) != ~0u);
-        S.vis[slot][r] = vis1;
-        S.nan[slot][r] = 0;
-        if (lane == 0) S.masked[slot][r >> 5] = some;
+        if (!live1 && (vis1 & 0x100u)) vis1 = 0u;
+        const bool some = __any_sync(0xffffffffu, (vis1 & 0xffu) != 0xffu);
+        S.vis[slot][r] = static_cast<uint8_t>(vis1);
+        if (lane == 0) {
+          S.masked[slot][r >> 5] = some;
+          S.nan[slot][r >> 5] = 0u;
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.rowfull[slot]);
     }
-    if constexpr (kTree) {
+    if constexpr (kTree == kGroups) {
       vis1 = vis2;
       vis2 = vis3;
-      vis3 = make_uint2(~0u, ~0u);
-      shared1 = shared2;
-      shared2 = shared3;
+      vis3 = 0xffu;
     }
     // unit m + 1
     codes1 = kZeroRow;
@@ -942,17 +962,18 @@ __device__ __forceinline__ bool run_rows(const Args& a, SmemOf<kTree>& S, int32_
     if (w.valid()) {
       const int32_t V = S.tokV[w.t], n = positions_of<kTree>(a, V), e = w.i * kPos + r;
       b3 = S.tokB[w.t];
-      if constexpr (kTree) {
-        const int32_t rank = S.any[w.t] - n + e;
-        int32_t node = -1;
+      if constexpr (kTree != kPlain) {
         group.enter(a, S, w.t);
+        const int32_t rank = group.any - n + e;
+        int32_t node = -1;
         if (e < n) {
-          if (rank >= 0) node = group.node(a, S, w.t, rank);
+          if (rank >= 0) node = group.node(a, S, rank);
           j3 = S.prefix[w.t] + (rank < 0 ? rank : node);
         }
-        shared3 = S.tokens[w.t] > 1;
-        if (shared3 && (a.window > 0 || __any_sync(0xffffffffu, node >= 0)))
-          vis3 = group.rows(a, S, w.t, w.g, node, -rank);
+        if (S.tokens[w.t] > 1) {
+          if (e < n && (rank >= 0 || a.window > 0)) vis3 = group.seers(a, S, node, -rank);
+          vis3 |= 0x100u;
+        }
       } else if (e < n) {
         j3 = !a.idx ? V - n + e : m == -3 ? entry : __ldg(a.idx + static_cast<int64_t>(a.t0 + w.t) * a.K + e);
       }
@@ -960,7 +981,7 @@ __device__ __forceinline__ bool run_rows(const Args& a, SmemOf<kTree>& S, int32_
         // the row tile's queries, into L2: head r, 128 bytes at a time
         const int h = w.g * a.ht + r, end = r < a.ht ? w.rows(a, S) : 0;
         const uint16_t* q = a.q + static_cast<int64_t>(a.t0 + w.t) * a.q_st + h * a.q_sh;
-        if constexpr (kTree) q = a.q + row_at(a, w.t, h, a.q_st, a.q_sh);
+        if constexpr (kTree == kGroups) q = a.q + row_at(a, w.t, h, a.q_st, a.q_sh);
 #pragma unroll 1
         for (int c = 0; c < 8 && h < end; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + c * 64));
       }
@@ -975,7 +996,7 @@ __device__ __forceinline__ bool run_rows(const Args& a, SmemOf<kTree>& S, int32_
 // other as they come free, then loads unit n + 1 (32 KB in flight on the SM
 // while unit n is worked on). A warp has eight rows; a warp
 // instruction loads one quarter of four.
-template <bool kFp8, bool kTree>
+template <bool kFp8, int kTree>
 __device__ __forceinline__ bool run_loaders(const Args& a, SmemOf<kTree>& S) {
   const int lane = threadIdx.x & 31, lw = (threadIdx.x >> 5) - kLoadWarp0;
   const int r0 = kPos / kLoadWarps * lw + (lane >> 3), off = (lane & 7) * 16;
@@ -991,7 +1012,7 @@ __device__ __forceinline__ bool run_loaders(const Args& a, SmemOf<kTree>& S) {
   for (int32_t n = -1; n < w.count; ++n) {
     if (n >= 0) {
       const int buf = n & 1;
-      if constexpr (kTree && kFp8) {
+      if constexpr (kTree == kGroups && kFp8) {
         if (masked) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -1006,7 +1027,8 @@ __device__ __forceinline__ bool run_loaders(const Args& a, SmemOf<kTree>& S) {
                 bad |= no;
               }
             }
-            if (bad) S.nan[n & (kSlots - 1)][r0 + 4 * k] = 1;
+            const int r = r0 + 4 * k;
+            if (bad) atomicOr(&S.nan[n & (kSlots - 1)][r >> 5], 1u << (r & 31));
           }
         }
       }
@@ -1038,7 +1060,7 @@ __device__ __forceinline__ bool run_loaders(const Args& a, SmemOf<kTree>& S) {
         const uint32_t slot = (n + 1) & (kSlots - 1);
         if (!wait(&S.rowfull[slot], ((n + 1) / kSlots) & 1)) return false;
         const uint8_t* r[2] = {S.row[slot][r0] + off, S.row[slot][r0 + 4] + off};
-        if constexpr (kTree) masked = S.masked[slot][lw / (kLoadWarps / kRowWarps)] != 0u;   // of the warp's rows
+        if constexpr (kTree == kGroups) masked = S.masked[slot][lw / (kLoadWarps / kRowWarps)] != 0;   // of the warp's rows
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -1104,7 +1126,7 @@ __device__ __forceinline__ bool drain(Smem& S) {
   return wait(&S.done, 0);
 }
 
-template <bool kTree>
+template <int kTree>
 __device__ __forceinline__ bool run_scores(const Args& a, SmemOf<kTree>& S, uint32_t tmem_any) {
   constexpr uint32_t id = idesc_f16(kPos, kHT, false, false), hi = sdesc_hi(1024);
   const uint32_t k_lo = sdesc_lo(smem_u32(S.kv), 16), q_lo = sdesc_lo(smem_u32(S.q), 16);
@@ -1141,7 +1163,7 @@ __device__ __forceinline__ bool run_scores(const Args& a, SmemOf<kTree>& S, uint
   return drain(S) && ok;
 }
 
-template <bool kTree>
+template <int kTree>
 __device__ __forceinline__ bool run_values(const Args& a, SmemOf<kTree>& S, uint32_t tmem_any) {
   constexpr uint32_t id = idesc_f16(128, kHT, true, true), hi = sdesc_hi(1024);
   const uint32_t v_lo = sdesc_lo(smem_u32(S.kv), kRegion), p_lo = sdesc_lo(smem_u32(S.p), 1024);
@@ -1214,7 +1236,7 @@ __device__ __forceinline__ int head_of(int lane) {
 // The heads may go on in the next token (`head` and `heads`: the first one's number in
 // its token and how many those have, `on`: from a token's last head to the next one's
 // first).
-template <bool kOut, bool kTree, class T>
+template <bool kOut, bool kGrouped, class T>
 __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int pos, int32_t nh, bool none,
                                        T* dst, int64_t stride, int32_t head = 0, int32_t heads = 0, int64_t on = 0) {
 #pragma unroll 1
@@ -1230,7 +1252,7 @@ __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int
     tmem_ld_wait();
     T* at = dst + i0 * stride + (kOut ? value_of(c >> 1, pos) : 128 * (c >> 1) + pos);
     int32_t left = 0;                                 // heads up to the token's end
-    if constexpr (kOut && kTree) {
+    if constexpr (kOut && kGrouped) {
       left = heads - head - i0;
       while (left <= 0) {
         left += heads;
@@ -1243,7 +1265,7 @@ __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int
       if constexpr (kOut) {
         const __nv_bfloat16 y = __float2bfloat16_rn(v);
         if (i0 + i < nh) *at = *reinterpret_cast<const uint16_t*>(&y);
-        if (kTree && --left == 0) {
+        if (kGrouped && --left == 0) {
           left = heads;
           at += on;
         } else {
@@ -1260,7 +1282,7 @@ __device__ __forceinline__ void output(const Smem& S, uint32_t tmem, int h0, int
 // 16 of every 32 TMEM lanes) of the 32 heads from 32 sub on; a lane has two
 // positions, lane / 4 and 8 further, of four pairs of heads. The four warps of a
 // `sub` share a named barrier.
-template <bool kTree>
+template <int kTree>
 __device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uint32_t tmem) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int qw = warp & 3, sub = warp >> 2, bar = 1 + sub;
@@ -1280,6 +1302,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uin
   // of drafted trees, where rows see different positions: the lane's row has seen one,
   // all of this sub's rows have
   [[maybe_unused]] bool row_seen = false, all_seen = false;
+  [[maybe_unused]] uint32_t row_tokens = 0u;          // tokens of the lane's rows in their group (15: none), 4 bits each
   uint32_t n = 0, seg = 0;
   // A wait that gives up clears `ok`. The warp still runs through the named
   // barriers, on whatever TMEM holds, but arrives nowhere else, so that nobody
@@ -1293,7 +1316,18 @@ __device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uin
       if (ok && !wait(&S.qfull, seg & 1)) ok = false;
       ++seg;
       seen = live = false;
-      if constexpr (kTree) row_seen = all_seen = false;
+      if constexpr (kTree == kGroups) {
+        row_seen = all_seen = false;
+        row_tokens = 0u;
+        if (S.tokens[w.t] > 1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = h0 + 8 * (i >> 1) + (i & 1), v = w.g * a.ht + r;
+            const uint32_t k = r < a.ht && v < w.rows(a, S) ? row_token(a, v) : 15u;
+            row_tokens |= k << (4 * i);
+          }
+        }
+      }
       // the queries after these wait for this warp too, so that it sees every
       // phase of the barrier
       if (lane == 0 && ok) mbar_arrive(&S.qempty);
@@ -1308,7 +1342,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uin
     for (int k = 0; k < 2; ++k) {
       const float s = S.rs[slot][pos + 8 * k], ls = lg2(s);
       // (a NaN scale must not reach the normalisers of rows that do not see it)
-      const float inv_s = (kTree ? s > 0.0f : s != 0.0f) ? ex2(-ls) : 0.0f;
+      const float inv_s = (kTree == kGroups ? s > 0.0f : s != 0.0f) ? ex2(-ls) : 0.0f;
       live |= s != 0.0f;
       const f32x2* c2 = reinterpret_cast<const f32x2*>(S.sl2[(seg - 1) & 1] + h0);
       const f32x2 s2 = pair_of(s, s), ls2 = pair_of(ls + kShift, ls + kShift);
@@ -1337,20 +1371,20 @@ __device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uin
                          cs[k][i], es[k][i]);
         }
       }
-      if constexpr (kTree) {
+      if constexpr (kTree == kGroups) {
         if (S.masked[slot][qw >> 1]) {
           // (the loaders' notes come with the tile, which is there)
           if (ok && !wait(&S.full[buf][1], parity)) ok = false;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint2 both_subs = S.vis[slot][pos + 8 * k];
-            const uint32_t vis = (sub ? both_subs.y : both_subs.x) >> (2 * (lane & 3));
-            const bool nan = S.nan[slot][pos + 8 * k] != 0;
+            const int r = pos + 8 * k;
+            const uint32_t vis = 0xff00u | S.vis[slot][r];
+            const bool nan = (S.nan[slot][qw >> 1] >> (r & 31)) & 1u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float2 u = both(d[k][i]);
-              u.x = !(vis >> (8 * i) & 1u) ? -INFINITY : nan ? NAN : u.x;
-              u.y = !(vis >> (8 * i) & 2u) ? -INFINITY : nan ? NAN : u.y;
+              u.x = !(vis >> (row_tokens >> (8 * i) & 15u) & 1u) ? -INFINITY : nan ? NAN : u.x;
+              u.y = !(vis >> (row_tokens >> (8 * i + 4) & 15u) & 1u) ? -INFINITY : nan ? NAN : u.y;
               d[k][i] = pair_of(u.x, u.y);
             }
           }
@@ -1366,7 +1400,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uin
       }
     }
     // until something was seen (by every row), any position sets the references
-    const bool rises = over > ((kTree ? all_seen : seen) ? kSlack + kShift : -INFINITY);
+    const bool rises = over > ((kTree == kGroups ? all_seen : seen) ? kSlack + kShift : -INFINITY);
     // the weights of the unit before last have been used
     if (ok && !wait(&S.empty[buf][1], parity ^ 1)) ok = false;
     if (named_bar_any(bar, 128, rises)) {
@@ -1381,8 +1415,8 @@ __device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uin
       part[qw * 32 + head_of(lane)] = across(t, lane, [](float p, float q) { return fmaxf(p, q); });
       named_bar(bar, 128);
       float up = fmaxf(fmaxf(part[lane], part[32 + lane]), fmaxf(part[64 + lane], part[96 + lane])) - kShift;
-      const bool was = kTree ? row_seen : seen;
-      if constexpr (kTree) {
+      const bool was = kTree == kGroups ? row_seen : seen;
+      if constexpr (kTree == kGroups) {
         row_seen |= !(up == -INFINITY);
         all_seen = __all_sync(0xffffffffu, row_seen);
       }
@@ -1475,7 +1509,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uin
     if (w.i == w.n - 1 && w.began_here()) {
       if (qw == 0 && lane < nh && a.lse)
         a.lse[static_cast<int64_t>(a.t0 + w.t) * a.H + h + lane] = lse2 * kLn2;
-      if constexpr (kTree) {
+      if constexpr (kTree == kGroups) {
         const int32_t head = h - row_token(a, h) * a.H;
         output<true, true>(S, oe, 32 * sub, 32 * qw + lane, nh, none, a.out + row_at(a, w.t, h, a.o_st, a.o_sh),
                            a.o_sh, head, a.H, a.o_st - (a.H - 1) * a.o_sh);
@@ -1488,7 +1522,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uin
       // on in the next to slot 1
       const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (w.began_here() ? 1 : 0);
       if (qw == 0) a.piece_lse[piece * kHT + 32 * sub + lane] = lse2;
-      output<false, kTree>(S, oe, 32 * sub, 32 * qw + lane, nh, none, a.piece + piece * kPieceRow + (32 * sub) * kD,
+      output<false, (kTree == kGroups)>(S, oe, 32 * sub, 32 * qw + lane, nh, none, a.piece + piece * kPieceRow + (32 * sub) * kD,
                            static_cast<int64_t>(kD));
     }
     named_bar(bar, 128);                              // the factors are read
@@ -1496,7 +1530,7 @@ __device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uin
   return ok;
 }
 
-template <bool kFp8, bool kTree>
+template <bool kFp8, int kTree>
 __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const Args a) {
   extern __shared__ uint8_t smem_raw[];
   SmemOf<kTree>& S = *reinterpret_cast<SmemOf<kTree>*>(
@@ -1561,14 +1595,14 @@ constexpr int kJoinRows = kJoinThreads / 32;
 
 // Row `row` of the row tile that began in CTA c - 1, by a warp, or by kSplit of them
 // with a quarter (of kSplit 4) of its values each.
-template <bool kTree, int kSplit>
+template <bool kGrouped, int kSplit>
 __device__ __forceinline__ void join_row(const Args& a, int32_t ctas, int32_t c, int32_t row, int part) {
   constexpr int kQuads = 4 / kSplit;                  // float4s of a lane
   constexpr int kBatch = 4 * kSplit;                  // pieces whose loads are in flight together
   const int lane = threadIdx.x & 31;
   const int4 tile = __ldcg(a.cut + c - 1);
-  const int32_t h = (kTree ? tile.y & 0xffff : tile.y) * a.ht + row;
-  if (tile.x < 0 || h >= (kTree ? tile.y >> 16 : 1) * a.H || row >= a.ht) return;
+  const int32_t h = (kGrouped ? tile.y & 0xffff : tile.y) * a.ht + row;
+  if (tile.x < 0 || h >= (kGrouped ? tile.y >> 16 : 1) * a.H || row >= a.ht) return;
   // pieces: CTA c - 1's slot 1, then slot 0 of CTA c, c + 1, ... up to the end
   // (a CTA with units has all its predecessors with units)
   const int32_t count = share_of_unit(tile.w, ctas, tile.z - 1) - (c - 1) + 1;
@@ -1619,7 +1653,7 @@ __device__ __forceinline__ void join_row(const Args& a, int32_t ctas, int32_t c,
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   const int64_t t = a.t0 + tile.x;
   // the lane's rows 4l .. 4l + 3 of each quarter are four values in a row
-  uint16_t* dst = a.out + (kTree ? row_at(a, tile.x, h, a.o_st, a.o_sh) : t * a.o_st + h * a.o_sh);
+  uint16_t* dst = a.out + (kGrouped ? row_at(a, tile.x, h, a.o_st, a.o_sh) : t * a.o_st + h * a.o_sh);
 #pragma unroll
   for (int i = 0; i < kQuads; ++i) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv);
@@ -1635,14 +1669,14 @@ __device__ __forceinline__ void join_row(const Args& a, int32_t ctas, int32_t c,
 // tile that goes on in another CTA, four warps a row with a quarter of its values each
 // and four times as many pieces in flight. One tree of 8 tokens of 64 heads over 2048
 // positions, 8 row tiles in 19 pieces each: 25.7 us without, 19.9 with.
-template <bool kTree, bool kFew>
+template <bool kGrouped, bool kFew>
 __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a, int32_t ctas) {
   pdl_wait();
   constexpr int kSplit = kFew ? 4 : 1;                // warps of a row
   [[maybe_unused]] const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kSplit;
   const int row = blockIdx.y * (kJoinRows / kSplit) + warp / kSplit;
   if constexpr (!kFew) {
-    join_row<kTree, 1>(a, ctas, blockIdx.x + 1, row, part);
+    join_row<kGrouped, 1>(a, ctas, blockIdx.x + 1, row, part);
   } else {
     __shared__ int32_t cuts[kJoinThreads], counts[kJoinRows];
     const bool here = threadIdx.x < ctas && __ldcg(a.cut + threadIdx.x).x >= 0;
@@ -1657,11 +1691,11 @@ __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a
     if (here) cuts[before] = static_cast<int32_t>(threadIdx.x) + 1;
     __syncthreads();
 #pragma unroll 1
-    for (int32_t i = blockIdx.x; i < all; i += gridDim.x) join_row<kTree, kSplit>(a, ctas, cuts[i], row, part);
+    for (int32_t i = blockIdx.x; i < all; i += gridDim.x) join_row<kGrouped, kSplit>(a, ctas, cuts[i], row, part);
   }
 }
 
-std::atomic<uint64_t> g_smem_kv_attn[4];
+std::atomic<uint64_t> g_smem_kv_attn[6];
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
@@ -1753,17 +1787,6 @@ int64_t most_groups(const Args& d, int64_t tokens) {
   return n < tokens ? n : tokens;
 }
 
-// Tokens that share row tiles: what leaves the fewest rows of the tiles empty, the
-// fewest tokens among equals, and no more than a request has on average.
-int32_t stack_of(int32_t H, int32_t T, int32_t B) {
-  const int32_t most = (T - 1) / (B > 0 ? B : 1) + 1;
-  int32_t best = 1;
-  const auto tiles = [&](int32_t k) { return (k * H - 1) / kHT + 1; };
-  for (int32_t k = 2; k <= kMaxStack && k <= most; ++k)
-    if (tiles(k) * best < tiles(best) * k) best = k;
-  return best;
-}
-
 // Row tiles of at most this many units are not cut while there is an SM for
 // each. 64 tokens over a window of 128 positions (two units): 21.6 us cut and
 // joined, 19.6 us whole.
@@ -1772,6 +1795,22 @@ constexpr int kWholeUnits = 2;
 // window's two, a unit or two more: 64 trees of up to 8 tokens, 16 heads over a window
 // of 128: 30.4 us cut and joined, 21.3 us whole.
 constexpr int kWholeGroupUnits = 4;
+
+// Tokens that share row tiles: what leaves the fewest rows of the tiles empty, the
+// fewest tokens among equals, and no more than a request has on average. One where every
+// unit (or uncut row tile) of single tokens has an SM of its own: 64 trees of 2 tokens,
+// 16 heads over a window of 128: 18.0 us by two, 11.3 by one.
+int32_t stack_of(Args d, int sms) {
+  const int32_t most = (d.T - 1) / (d.B > 0 ? d.B : 1) + 1;
+  const auto tiles = [&](int64_t k) { return (k * d.H - 1) / kHT + 1; };
+  d.stack = 1;
+  const int64_t units = most_units(d);
+  if ((units <= kWholeUnits ? 1 : units) * d.T * tiles(1) <= sms) return 1;
+  int32_t best = 1;
+  for (int32_t k = 2; k <= kMaxStack && k <= most; ++k)
+    if (tiles(k) * best < tiles(best) * k) best = k;
+  return best;
+}
 
 // Heads per row tile: 64, what the products are made for, or 32 or 16 while
 // every unit (or uncut row tile) still has an SM of its own. The conversions and
@@ -1782,7 +1821,7 @@ constexpr int kWholeGroupUnits = 4;
 int32_t heads_per_tile(const Args& d, int64_t most, int sms) {
   const int64_t groups = most_groups(d, d.T), H = static_cast<int64_t>(d.stack) * d.H;
   int32_t ht = kHT;
-  while (ht > 16 && (most <= kWholeUnits ? 1 : most) * groups * ((H + ht / 2 - 1) / (ht / 2)) <= sms) ht /= 2;
+  while (ht > 16 && (most <= (d.stack > 1 ? kWholeGroupUnits : kWholeUnits) ? 1 : most) * groups * ((H + ht / 2 - 1) / (ht / 2)) <= sms) ht /= 2;
   return ht;
 }
 
@@ -1800,25 +1839,25 @@ Layout layout_for(int sms) {
 }
 
 // Joins the pieces of a launch of up to `tiles` row tiles.
-template <bool kTree>
+template <int kTree>
 cudaError_t launch_join(const Args& d, int32_t ctas, int64_t tiles, cudaStream_t s) {
   const int32_t rows = d.stack * d.H < d.ht ? d.stack * d.H : d.ht;
   const auto grid = [&](int64_t x, int32_t of_block) {
     return dim3(static_cast<unsigned>(x), static_cast<unsigned>((rows + of_block - 1) / of_block));
   };
-  if constexpr (kTree) {
+  if constexpr (kTree != kPlain) {
     if (4 * tiles <= ctas && ctas <= kJoinThreads)
-      return launch_pdl(merge_pieces_kernel<true, true>, grid(tiles, kJoinRows / 4), dim3(kJoinThreads), 0, s, d, ctas);
+      return launch_pdl(merge_pieces_kernel<(kTree == kGroups), true>, grid(tiles, kJoinRows / 4), dim3(kJoinThreads), 0, s, d, ctas);
   }
-  return launch_pdl(merge_pieces_kernel<kTree, false>, grid(ctas - 1, kJoinRows), dim3(kJoinThreads), 0, s, d, ctas);
+  return launch_pdl(merge_pieces_kernel<(kTree == kGroups), false>, grid(ctas - 1, kJoinRows), dim3(kJoinThreads), 0, s, d, ctas);
 }
 
-template <bool kFp8, bool kTree>
+template <bool kFp8, int kTree>
 cudaError_t launch(Args d, int sms, cudaStream_t s) {
   const auto kernel = kv_attn_kernel<kFp8, kTree>;
   constexpr int kBytes = kSmemBytes<kTree>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kBytes,
-                                    g_smem_kv_attn[(kTree ? 2 : 0) + (kFp8 ? 1 : 0)]);
+                                    g_smem_kv_attn[2 * kTree + (kFp8 ? 1 : 0)]);
   const int64_t most = most_units(d);
   d.ht = heads_per_tile(d, most, sms);
   d.hg = (d.stack * d.H + d.ht - 1) / d.ht;
@@ -1886,11 +1925,18 @@ qli_status attend(const qli_kv_attn_args* a, const uint64_t* mask, int32_t words
   d.piece_lse = reinterpret_cast<float*>(w + L.lse);
   d.mask = mask;
   d.words = words;
-  d.stack = kTree ? stack_of(a->H, a->T, a->B) : 1;
+  d.stack = 1;
   d.per_head = static_cast<uint32_t>(0xffffffffu / static_cast<uint32_t>(a->H) + 1);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      a->quant_mode == QLI_QUANT_FP8 ? launch<true, kTree>(d, sms, s) : launch<false, kTree>(d, sms, s);
+  const bool fp8 = a->quant_mode == QLI_QUANT_FP8;
+  cudaError_t e;
+  if constexpr (!kTree) {
+    e = fp8 ? launch<true, kPlain>(d, sms, s) : launch<false, kPlain>(d, sms, s);
+  } else {
+    d.stack = stack_of(d, sms);
+    if (d.stack == 1) e = fp8 ? launch<true, kSingle>(d, sms, s) : launch<false, kSingle>(d, sms, s);
+    else e = fp8 ? launch<true, kGroups>(d, sms, s) : launch<false, kGroups>(d, sms, s);
+  }
   return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
 }
 
