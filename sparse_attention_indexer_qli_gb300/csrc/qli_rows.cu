@@ -68,7 +68,20 @@ __device__ __forceinline__ void turn_of(uint32_t frac, float& c, float& s) {
   s = quarter & 2u ? -b : b;
 }
 
-// (cos, sin) times the magnitude of the tokens t0 .. t0 + n, by token and pair.
+// (cos, sin) times the magnitude of the tokens t0 .. t0 + n, two pairs to a float4. The
+// pairs of a unit (four neighbouring ones, or eight of which it holds one half) are a
+// column: float4 i of unit u of a token at kColumns i + u, so that lanes side by side
+// read side by side. In the order of the pairs they met in the same banks, four to
+// eight at a time: 3561 tokens of 64 heads x 128, all rotated by halves, to INT8 took 45 us
+// where they take 26.
+constexpr int kTokenEntries = QLI_ROTARY_PAIRS;       // of the table, whatever the number of pairs
+constexpr int64_t kTableBytes = 16 * 1024;            // of a table at most: 32 tokens
+template <bool kHalf>
+constexpr int kColumns = kHalf ? QLI_ROTARY_PAIRS / 8 : QLI_ROTARY_PAIRS / 4;
+__device__ __forceinline__ int32_t table_place(const Turn& w, int32_t pair) {
+  return w.half ? 2 * (((pair & 7) >> 1) * kColumns<true> + (pair >> 3)) + (pair & 1)
+                : 2 * (((pair & 3) >> 1) * kColumns<false> + (pair >> 2)) + (pair & 1);
+}
 __device__ __forceinline__ void fill_table(float2* table, const Turn& w, const int32_t* positions,
                                            int32_t t0, int32_t n) {
 #pragma unroll 1
@@ -80,7 +93,7 @@ __device__ __forceinline__ void fill_table(float2* table, const Turn& w, const i
     const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(__ldg(positions + t0 + t))) * f;
     float s, c;
     turn_of(static_cast<uint32_t>(frac >> 32), c, s);
-    table[i] = make_float2(c * w.cos_scale, s * w.sin_scale);
+    table[t * kTokenEntries + table_place(w, p)] = make_float2(c * w.cos_scale, s * w.sin_scale);
   }
 }
 
@@ -136,40 +149,28 @@ __device__ __forceinline__ uint4 pack8(const Unit& u) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Four entries of the table.
-__device__ __forceinline__ void load4(const float2* cs, float2 (&t)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 v = reinterpret_cast<const float4*>(cs)[i];
-    t[2 * i] = make_float2(v.x, v.y);
-    t[2 * i + 1] = make_float2(v.z, v.w);
-  }
-}
-
-// Four neighbouring pairs in one unit.
-__device__ __forceinline__ void turn_neighbours(Unit& u, const float2* cs) {
-  float2 t[4];
-  load4(cs, t);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = both(u.p[i]);
-    u.p[i] = fma2(pair_of(-v.y, v.x), pair_of(t[i].y, t[i].y), mul2(u.p[i], pair_of(t[i].x, t[i].x)));
-  }
-}
-
-// Eight values and the eight that are their pairs' other halves (`w`), by their own
-// eight entries: a cos + sign w sin, the sign -1 for first halves and 1 for second.
-__device__ __forceinline__ void turn_half(Unit& u, const Unit& w, const float2* cs, float sign) {
+// Four neighbouring pairs in one unit, column `u`.
+__device__ __forceinline__ void turn_neighbours(Unit& x, const float2* cs, int u) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    float2 t[4];
-    load4(cs + 4 * k, t);
+    const float4 t = reinterpret_cast<const float4*>(cs)[k * kColumns<false> + u];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const f32x2 c = pair_of(t[2 * i].x, t[2 * i + 1].x), s = pair_of(t[2 * i].y, t[2 * i + 1].y);
-      f32x2& a = u.p[2 * k + i];
-      a = fma2(mul2(w.p[2 * k + i], pair_of(sign, sign)), s, mul2(a, c));
+      const float c = i ? t.z : t.x, s = i ? t.w : t.y;
+      f32x2& p = x.p[2 * k + i];
+      const float2 v = both(p);
+      p = fma2(pair_of(-v.y, v.x), pair_of(s, s), mul2(p, pair_of(c, c)));
     }
+  }
+}
+
+// Eight values and the eight that are their pairs' other halves (`w`), column `u`:
+// a cos + sign w sin, the sign -1 for first halves and 1 for second.
+__device__ __forceinline__ void turn_half(Unit& x, const Unit& w, const float2* cs, int u, float sign) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 t = reinterpret_cast<const float4*>(cs)[i * kColumns<true> + u];
+    x.p[i] = fma2(mul2(w.p[i], pair_of(sign, sign)), pair_of(t.y, t.w), mul2(x.p[i], pair_of(t.x, t.z)));
   }
 }
 
@@ -234,15 +235,22 @@ __device__ __forceinline__ void normalise(Unit (&v)[2], const Prep& p, int l) {
 }
 
 // `cs`: the row's token in the table.
-template <int G, bool kHalf>
+enum : int { kNeighbours = 0, kHalves = 1, kOwnHalves = 2 };   // the last: pairs half a row apart, in one lane
+template <int G, int kLayout>
 __device__ __forceinline__ void turn_row(Unit (&v)[2], const Turn& w, const float2* cs, int l) {
   const int r8 = w.pairs / 4;
-  if constexpr (!kHalf) {
+  if constexpr (kLayout == kNeighbours) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int u = l + k * G - w.o8;
-      if (u >= 0 && u < r8) turn_neighbours(v[k], cs + 4 * u);
+      if (u >= 0 && u < r8) turn_neighbours(v[k], cs, u);
     }
+    return;
+  }
+  if constexpr (kLayout == kOwnHalves) {
+    const Unit was = v[0];
+    turn_half(v[0], v[1], cs, l, -1.0f);
+    turn_half(v[1], was, cs, l, 1.0f);
     return;
   }
   // a value's partner is h8 units away, in another lane or in this one's other
@@ -251,7 +259,7 @@ __device__ __forceinline__ void turn_row(Unit (&v)[2], const Turn& w, const floa
   const bool slot0 = w.o8 < G, slot1 = w.o8 + r8 > G;
   const auto partner = [&](int u) { return u < 0 || u >= r8 ? l : (u < h8 ? u + h8 : u - h8) + w.o8; };
   const auto turn = [&](Unit& x, const Unit& y, int u) {
-    if (u >= 0 && u < r8) turn_half(x, y, cs + 8 * (u < h8 ? u : u - h8), u < h8 ? -1.0f : 1.0f);
+    if (u >= 0 && u < r8) turn_half(x, y, cs, u < h8 ? u : u - h8, u < h8 ? -1.0f : 1.0f);
   };
   Unit other[2];
   if (slot0 && slot1) {
@@ -297,35 +305,36 @@ __device__ __forceinline__ uint16_t quantise(const Unit (&v)[2], uint2 (&codes)[
   if (sf == 0.0f) return 0u;
   const float y = __frcp_rn(sf);
   const f32x2 y2 = pair_of(y, y), s2 = pair_of(-sf, -sf);
-  // under the largest scale alone a quotient can be far above the largest code
-  const bool huge = sb == 0x7bffu;
+  // A scale that is a normal number is within 2^-11 of amax / Q, so that quotients end
+  // at Q and a fraction. A subnormal one may be smaller, and the largest one cuts.
+  const bool clamp = !kFp8 && (sb < 0x0400u || sb == 0x7bffu);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     uint32_t w[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float q[4];
+      f32x2 q[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const f32x2 x = v[k].p[2 * j + i], q0 = mul2(x, y2);
-        const float2 r = both(fma2(fma2(q0, s2, x), y2, q0));
-        q[2 * i] = r.x;
-        q[2 * i + 1] = r.y;
+        q[i] = fma2(fma2(q0, s2, x), y2, q0);
       }
       if constexpr (kFp8) {
-        w[j] = e4m3x2_of(q[0], q[1]) | (e4m3x2_of(q[2], q[3]) << 16);
+        const float2 lo = both(q[0]), hi = both(q[1]);
+        w[j] = e4m3x2_of(lo.x, lo.y) | (e4m3x2_of(hi.x, hi.y) << 16);
       } else {
-        // adding 1.5 * 2^23 rounds to an integer, ties to even, in the low bits;
-        // two are clamped at a time as 16-bit halves
-        uint32_t n[4];
+        if (clamp) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (huge) q[i] = fminf(fmaxf(q[i], -127.0f), 127.0f);
-          n[i] = __float_as_uint(__fadd_rn(q[i], 12582912.0f));
+          for (int i = 0; i < 2; ++i) {
+            const float2 x = both(q[i]);
+            q[i] = pair_of(fminf(fmaxf(x.x, -127.0f), 127.0f), fminf(fmaxf(x.y, -127.0f), 127.0f));
+          }
         }
-        const uint32_t lo = __vmins2(__vmaxs2(__byte_perm(n[0], n[1], 0x5410), 0xff81ff81u), 0x007f007fu);
-        const uint32_t hi = __vmins2(__vmaxs2(__byte_perm(n[2], n[3], 0x5410), 0xff81ff81u), 0x007f007fu);
-        w[j] = __byte_perm(lo, hi, 0x6420);
+        // adding 1.5 * 2^23 rounds to an integer, ties to even, in the low bits
+        const f32x2 magic = pair_of(12582912.0f, 12582912.0f);
+        const float2 lo = both(add2(q[0], magic)), hi = both(add2(q[1], magic));
+        w[j] = __byte_perm(__byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x0040),
+                           __byte_perm(__float_as_uint(hi.x), __float_as_uint(hi.y), 0x0040), 0x5410);
       }
     }
     codes[k] = make_uint2(w[0], w[1]);
@@ -437,15 +446,17 @@ struct Rows {
     key = out.key(at);
   }
   __device__ __forceinline__ void run(const float2* table, int32_t t0) {
-    if (p.turn.half) run_norm<true>(table, t0); else run_norm<false>(table, t0);
+    if (!p.turn.half) run_norm<kNeighbours>(table, t0);
+    else if (p.turn.pairs == 8 * G) run_norm<kOwnHalves>(table, t0);
+    else run_norm<kHalves>(table, t0);
   }
-  template <bool kHalf>
+  template <int kLayout>
   __device__ __forceinline__ void run_norm(const float2* table, int32_t t0) {
-    if (p.norm == QLI_NORM_RMS) run_all<kHalf, QLI_NORM_RMS>(table, t0);
-    else if (p.norm == QLI_NORM_LAYER) run_all<kHalf, QLI_NORM_LAYER>(table, t0);
-    else run_all<kHalf, QLI_NORM_NONE>(table, t0);
+    if (p.norm == QLI_NORM_RMS) run_all<kLayout, QLI_NORM_RMS>(table, t0);
+    else if (p.norm == QLI_NORM_LAYER) run_all<kLayout, QLI_NORM_LAYER>(table, t0);
+    else run_all<kLayout, QLI_NORM_NONE>(table, t0);
   }
-  template <bool kHalf, int kNorm>
+  template <int kLayout, int kNorm>
   __device__ __forceinline__ void run_all(const float2* table, int32_t t0) {
     // the same number of turns for every thread of the block
     const int32_t first = r - static_cast<int32_t>(threadIdx.x) / G;
@@ -457,7 +468,7 @@ struct Rows {
       r += kRows;
       if (n + kRows < end) load();
       if constexpr (kNorm != QLI_NORM_NONE) normalise<G, kNorm>(v, p, l);
-      if (p.turn.pairs) turn_row<G, kHalf>(v, p.turn, table + (t - t0) * p.turn.pairs, l);
+      if (p.turn.pairs) turn_row<G, kLayout>(v, p.turn, table + (t - t0) * kTokenEntries, l);
       uint16_t* scale = nullptr;
       if constexpr (kMode == 0) {
         uint8_t* dst = at < end ? out.dest(at, t, to, scale) : nullptr;
@@ -514,7 +525,6 @@ __global__ void __launch_bounds__(kThreads, kMode == 0 ? kBlocksPerSmBf16 : kBlo
   work.run(table, t0);
 }
 
-constexpr int64_t kTableBytes = 16 * 1024;   // what one set needs at most: 2048 entries
 
 template <int D, int kMode>
 cudaError_t launch_prepare(const Prep& p, const DenseIn& in, const DenseOut<kMode>& out,
@@ -524,7 +534,7 @@ cudaError_t launch_prepare(const Prep& p, const DenseIn& in, const DenseOut<kMod
   int64_t each = sets / (static_cast<int64_t>(sms) * kBlocksPerSm);
   each = each < 1 ? 1 : each > kSets ? kSets : each;
   const auto bytes = [&] {
-    return static_cast<int64_t>(sizeof(float2)) * tokens_of(each * kRows, rows, in.H) * p.turn.pairs;
+    return p.turn.pairs ? static_cast<int64_t>(sizeof(float2)) * tokens_of(each * kRows, rows, in.H) * kTokenEntries : 0;
   };
   while (each > 1 && bytes() > kTableBytes) --each;
   const int32_t block_rows = static_cast<int32_t>(each) * kRows;
@@ -609,14 +619,14 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
   if (some) {
     Unit x = unpack8(v0), y = unpack8(v1);
     const int w = u - a.turn.o8;
-    const float2* cs = table + (t - t0) * a.turn.pairs;
+    const float2* cs = table + (t - t0) * kTokenEntries;
     if (a.turn.half) {
       const Unit was = x;
-      turn_half(x, y, cs + 8 * w, -1.0f);
-      turn_half(y, was, cs + 8 * w, 1.0f);
+      turn_half(x, y, cs, w, -1.0f);
+      turn_half(y, was, cs, w, 1.0f);
     } else {
-      turn_neighbours(x, cs + 4 * w);
-      turn_neighbours(y, cs + 4 * (w + h8));
+      turn_neighbours(x, cs, w);
+      turn_neighbours(y, cs, w + h8);
     }
     uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.o_st + (r - t * a.H) * a.o_sh) + u;
     *dst = pack8(x);
@@ -711,8 +721,10 @@ cudaError_t launch_width(const qli_prepare_args& a, const Prep& p, int32_t width
   return launch_prepare<128, kMode>(p, in, out, a.positions, rows, sms, s);
 }
 
-// Tokens per block: enough for whole warps of index K rows while there are blocks for
-// the SMs to hold, else one set of KV rows.
+// Tokens per block: enough for whole warps of index K rows while that leaves each SM two
+// blocks, down to one set of KV rows. (12000 tokens: 12.8 us with 4 a block, 9.1 with 16;
+// 1000: 4.3 and 6.2.)
+constexpr int kMinBlocks = 2;
 constexpr int kFewTokens = kThreads / (kKvRow / 16), kManyTokens = kThreads / (kIndexRow / 16);
 
 template <int kKv, int kIndex>
@@ -721,7 +733,8 @@ cudaError_t launch_append(const qli_append_args& a, const qli_row_prep* kv, cons
   AppendArgs<kKv, kIndex> d{};
   d.positions = a.positions;
   d.n = static_cast<int32_t>(a.n);
-  d.block_rows = a.n >= static_cast<int64_t>(sms) * kBlocksPerSm * kManyTokens ? kManyTokens : kFewTokens;
+  d.block_rows = kManyTokens;
+  while (d.block_rows > kFewTokens && a.n < kMinBlocks * sms * static_cast<int64_t>(d.block_rows)) d.block_rows /= 2;
   const int64_t slots = a.num_pages * a.rows_per_page;
   const int32_t log2R = a.rows_per_page == 64 ? 6 : 7;
   const int64_t tokens = tokens_of(d.block_rows, a.n, 1);
@@ -731,19 +744,19 @@ cudaError_t launch_append(const qli_append_args& a, const qli_row_prep* kv, cons
     d.kv_out = PagedOut<kKv>{a.slot_mapping, a.cache, slots, a.page_stride, a.kv_offset, a.kv_scale_offset, log2R,
                              kKv == 0 ? 2 * kKvRow : kKvRow, a.err_word};
   }
-  int64_t entries = tokens * d.kv.turn.pairs;
+  int64_t entries = d.kv.turn.pairs ? tokens * kTokenEntries : 0;
   if (a.index_k) {
     d.index = make_prep(*index);
     d.index_in = FlatIn{a.index_k, a.index_stride};
     d.index_out = PagedOut<kIndex>{a.slot_mapping, a.cache, slots, a.page_stride, a.k_offset, a.scale_offset, log2R,
                                    kIndexRow, a.err_word};
     const Turn &x = d.kv.turn, &y = d.index.turn;
-    // the same angles and magnitude: one table, whatever the layouts and offsets
-    const bool same = x.pairs == y.pairs && x.cos_scale == y.cos_scale &&
+    // the same angles, magnitude and layout: one table, whatever the offsets
+    const bool same = x.pairs == y.pairs && x.half == y.half && x.cos_scale == y.cos_scale &&
                       std::memcmp(x.turns, y.turns, sizeof(x.turns)) == 0;
     if (!same) {
       d.index_table = static_cast<int32_t>(entries);
-      entries += tokens * y.pairs;
+      entries += y.pairs ? tokens * kTokenEntries : 0;
     }
   }
   append_kernel<kKv, kIndex><<<static_cast<unsigned>((a.n - 1) / d.block_rows + 1), kThreads,
@@ -788,9 +801,11 @@ extern "C" qli_status qli_rotate(const qli_rotate_args* a, const qli_rotary* rot
   d.units = a->x == a->out ? 0 : a->D / 8;
   d.block_rows = kThreads / (rotary->pairs / 8);
   d.turn = make_turn(*rotary, a->inverse != 0);
-  const int64_t in = d.rows < d.block_rows ? d.rows : d.block_rows;
-  const int64_t tokens = (in - 2 + a->H) / a->H + 1;
-  const size_t smem = sizeof(float2) * static_cast<size_t>((tokens < in ? tokens : in) * rotary->pairs);
+  const auto bytes = [&] {
+    return static_cast<int64_t>(sizeof(float2)) * tokens_of(d.block_rows, d.rows, a->H) * kTokenEntries;
+  };
+  while (bytes() > kTableBytes) d.block_rows /= 2;
+  const size_t smem = static_cast<size_t>(bytes());
   rotate_kernel<<<static_cast<unsigned>((d.rows - 1) / d.block_rows + 1), kThreads, smem,
                   static_cast<cudaStream_t>(stream)>>>(d);
   return cudaGetLastError() == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;

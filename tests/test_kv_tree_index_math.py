@@ -189,6 +189,33 @@ def test_table_entries_by_token_and_pair(pairs):
     assert all((i * per_pair >> 32) == i // pairs for i in range(1 << 14))
 
 
+def table_place(half, pair):
+    log2, columns = (3, 8) if half else (2, 16)
+    return 2 * (((pair & (1 << log2) - 1) >> 1) * columns + (pair >> log2)) + (pair & 1)
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_pairs_of_a_token_in_the_table(half):
+    places = [table_place(half, p) for p in range(64)]
+    assert sorted(places) == list(range(64))
+    for u in range(8 if half else 16):                           # what a lane reads for unit u
+        of_unit = [8 * u + i for i in range(8)] if half else [4 * u + i for i in range(4)]
+        read = [2 * (k * (8 if half else 16) + u) + i for k in range(4 if half else 2) for i in range(2)]
+        assert [places[p] for p in of_unit] == read
+
+
+@pytest.mark.parametrize("pairs", range(8, 72, 8))
+def test_tables_of_rotated_rows_fit(pairs):
+    for H in (1, 2, 3, 64):
+        for rows in (1, 5, 100, 10 ** 6):
+            block = 128 // (pairs // 8)
+            while 512 * tokens_of(block, rows, H) > 16 * 1024:
+                block //= 2
+            assert block >= 1
+    for D in (64, 128, 256, 512):                                # one set of prepared rows
+        assert 512 * tokens_of(128 // (D // 16), 10 ** 6, 1) <= 16 * 1024
+
+
 def turn_of(frac):
     """The kernel's cosine and sine of 2^-32 frac turns, in double precision."""
     quarter = (frac + 0x20000000 & 0xFFFFFFFF) >> 30

@@ -83,7 +83,8 @@ ROTATE = [
     (1, 1, 16, 16, 0, False, 0), (1, 64, 512, 64, 448, False, 0), (7, 3, 192, 32, 0, True, 8),
     (64, 64, 512, 64, 448, True, 0), (5, 33, 128, 128, 0, True, 64), (300, 1, 128, 48, 8, False, 0),
     (257, 2, 72, 48, 24, True, 8), (3, 5, 200, 112, 88, False, 0), (1000, 9, 64, 64, 0, False, 24),
-    (2, 700, 128, 80, 40, True, 0), (600, 1, 1024, 96, 504, False, 0)]
+    (2, 700, 128, 80, 40, True, 0), (600, 1, 1024, 96, 504, False, 0), (1100, 1, 64, 16, 8, True, 0),
+    (999, 2, 32, 16, 16, False, 8), (130, 1, 16, 16, 0, True, 0), (257, 1, 64, 32, 32, False, 0)]
 
 
 @pytest.mark.parametrize("inplace", [False, True], ids=["out", "inplace"])
