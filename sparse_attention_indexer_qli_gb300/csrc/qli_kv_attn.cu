@@ -134,7 +134,7 @@ template <int kTree>
 using SmemOf = std::conditional_t<(kTree != kPlain), TreeSmem, Smem>;
 template <int kTree>
 constexpr int kSmemBytes = static_cast<int>(sizeof(SmemOf<kTree>)) + 1024;
-static_assert(kSmemBytes<true> <= 227 * 1024, "shared memory");
+static_assert(kSmemBytes<kGroups> <= 227 * 1024, "shared memory");
 
 struct Args {
   const uint16_t* q;
@@ -474,8 +474,8 @@ static_assert((3 * kRequestsInSmem + 1) * 4 <= 2 * kTile, "the requests fit in t
 // some row does not see some position the row warps leave masks, by which the softmax
 // takes those scores as -inf. Position e of n has the rank e - n + (nodes): below 0 it is
 // that far before the prefix's end, else the set bit of that rank.
-// 16 trees of 16 tokens over 8K positions, E4M3: 16 heads 110 us (0.62 PFLOP/s), a token
-// at a time 329; 96 heads, where two tokens fill three row tiles, 531 and 681.
+// 16 trees of 16 tokens over 8K positions, E4M3: 16 heads 112 us (0.61 PFLOP/s), a token
+// at a time 329; 96 heads, where two tokens fill three row tiles, 540 and 681.
 __device__ __forceinline__ uint64_t low_bits(uint64_t m, int32_t n) {
   return n >= 64 ? m : n <= 0 ? 0u : m & ((uint64_t{1} << n) - 1);
 }

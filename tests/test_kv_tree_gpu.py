@@ -180,6 +180,23 @@ def test_the_same_call_gives_the_same_bits():
         assert all(torch.equal(a, b) for a, b in zip(one, qli.kv_tree_attention(scale=SCALE, **kw)))
 
 
+@pytest.mark.parametrize("H,window", [(64, 0), (16, 0), (64, 100), (16, 100)])
+def test_several_launches_give_the_same_bits(H, window):
+    """More tokens than three launches hold, over short and uneven contexts; some of the
+    last launch's row tiles are whole."""
+    import torch
+    raw = [30 + 61 * (i % 7) for i in range(55)]
+    case = TreeCase(84, raw, [30] * 55, H, kv8.FP8, "tree", row_size=0.5)
+    kw = case.upload()
+    one = [t.clone() for t in qli.kv_tree_attention(scale=SCALE, window=window, **kw)]
+    for _ in range(12):
+        got = qli.kv_tree_attention(scale=SCALE, window=window, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(one, got))
+    from test_kv_attn_gpu import compare
+    got = tuple(t.float().cpu().numpy().astype(np.float64) for t in one)
+    compare(case, got, window=window, tokens=[0, 511, 512, 513, 700, 1023, 1024, 1100, 1535, 1536, case.T - 1])
+
+
 def test_on_another_stream_and_in_a_graph():
     import torch
     case = TreeCase(58, [2500, 400], [12, 3], 64, kv8.FP8, "tree")
