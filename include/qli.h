@@ -484,7 +484,8 @@ typedef struct qli_rotary {
     int32_t pairs;               /* 8..64, a multiple of 8 */
     int32_t layout;              /* QLI_ROTARY_INTERLEAVED or QLI_ROTARY_HALF */
     int32_t offset;              /* first rotated value, a multiple of 8 */
-    float magnitude;             /* finite */
+    int32_t reserved;
+    double magnitude;            /* finite, in FP32 too */
     uint64_t turns[QLI_ROTARY_PAIRS]; /* turns per position, in units of 2^-64 (modulo 1) */
 } qli_rotary;
 

@@ -35,7 +35,8 @@ constexpr int32_t kMostValues = 1 << 16;          // of a row that is rotated
 struct Turn {
   int32_t pairs, half, o8;
   uint32_t per_pair;                       // 2^32 / pairs, rounded up
-  float cos_scale, sin_scale;              // the magnitude; sin's sign is the direction
+  float scale, scale_lo;                   // the magnitude, in two numbers
+  int32_t inverse;
   uint64_t turns[QLI_ROTARY_PAIRS];
 };
 
@@ -46,26 +47,33 @@ struct Prep {
   Turn turn;
 };
 
-// Cosine and sine of 2^-32 `frac` turns. Within an eighth of a turn of the nearest
-// quarter, |t| <= pi / 4, the Taylor series up to t^9 and t^10 leave 2^-29 and 2^-33;
-// what is off is the rounding of t and of the sums, about 2^-24 together.
-__device__ __forceinline__ void turn_of(uint32_t frac, float& c, float& s) {
+// Cosine and sine of 2^-32 `frac` turns, times the magnitude. Within an eighth of a turn
+// of the nearest quarter, |t| <= pi / 4, the Taylor series up to t^9 and t^10 leave 2^-29
+// and 2^-33. The angle is t + e and the magnitude has two parts, so that little more than
+// the last rounding is off (2^-24 without them, which moved twice as many 8-bit codes over
+// the borders of their steps).
+__device__ __forceinline__ void turn_of(uint32_t frac, const Turn& w, float& c, float& s) {
+  constexpr float kHi = 1.4629181200e-09f, kLo = -4.0709402679e-17f;   // 2 pi / 2^32
   const uint32_t quarter = (frac + 0x20000000u) >> 30;
-  const float t = static_cast<float>(static_cast<int32_t>(frac - (quarter << 30))) *
-                  1.4629180792671596e-9f;  // 2 pi / 2^32
-  const float t2 = t * t;
+  const int32_t rest = static_cast<int32_t>(frac - (quarter << 30));
+  const float hi = static_cast<float>(rest), lo = static_cast<float>(rest - static_cast<int32_t>(hi));
+  const float t = hi * kHi, e = fmaf(hi, kHi, -t) + fmaf(hi, kLo, lo * kHi);
+  const float t2 = t * t, t2e = fmaf(t, t, -t2);
   float p = fmaf(t2, 1.0f / 362880.0f, -1.0f / 5040.0f);
   p = fmaf(p, t2, 1.0f / 120.0f);
   p = fmaf(p, t2, -1.0f / 6.0f);
-  const float sin_t = fmaf(p * t2, t, t);
   float q = fmaf(t2, -1.0f / 3628800.0f, 1.0f / 40320.0f);
   q = fmaf(q, t2, -1.0f / 720.0f);
   q = fmaf(q, t2, 1.0f / 24.0f);
-  q = fmaf(q, t2, -0.5f);
-  const float cos_t = fmaf(q, t2, 1.0f);
+  // sin = t + sin_r, cos = one + cos_r, where one is 1 - t2 / 2 rounded
+  const float sin_r = fmaf(t * t2, p, fmaf(-0.5f * t2, e, e));
+  const float one = 1.0f - 0.5f * t2;
+  const float cos_r = fmaf(t2 * t2, q, ((1.0f - one) - 0.5f * t2) - fmaf(t, e, 0.5f * t2e));
+  const float sin_t = fmaf(w.scale, t, fmaf(w.scale, sin_r, w.scale_lo * t));
+  const float cos_t = fmaf(w.scale, one, fmaf(w.scale, cos_r, w.scale_lo * one));
   const float a = quarter & 1u ? sin_t : cos_t, b = quarter & 1u ? cos_t : sin_t;
   c = (quarter + 1u) & 2u ? -a : a;
-  s = quarter & 2u ? -b : b;
+  s = ((quarter >> 1) & 1u) != static_cast<uint32_t>(w.inverse) ? -b : b;
 }
 
 // (cos, sin) times the magnitude of the tokens t0 .. t0 + n, two pairs to a float4. The
@@ -92,8 +100,8 @@ __device__ __forceinline__ void fill_table(float2* table, const Turn& w, const i
     asm volatile("ld.u64 %0, [%1];" : "=l"(f) : "l"(w.turns + p));
     const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(__ldg(positions + t0 + t))) * f;
     float s, c;
-    turn_of(static_cast<uint32_t>(frac >> 32), c, s);
-    table[t * kTokenEntries + table_place(w, p)] = make_float2(c * w.cos_scale, s * w.sin_scale);
+    turn_of(static_cast<uint32_t>(frac >> 32), w, c, s);
+    table[t * kTokenEntries + table_place(w, p)] = make_float2(c, s);
   }
 }
 
@@ -124,6 +132,8 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+
+constexpr f32x2 kOnes = 0x3f8000003f800000ull;
 
 // Eight values of a row, in pairs of neighbours.
 struct Unit {
@@ -215,21 +225,24 @@ __device__ __forceinline__ void normalise(Unit (&v)[2], const Prep& p, int l) {
 #pragma unroll
   for (int i = 1; i < 8; ++i) s = fma2(v[i >> 2].p[i & 3], v[i >> 2].p[i & 3], s);
   const float2 e = both(s);
-  const float r = rsqrtf(fmaf(row_sum<G>(e.x + e.y), kInv, p.eps));
+  // with one step of Newton's, since what is off here moves the whole row
+  const float x = fmaf(row_sum<G>(e.x + e.y), kInv, p.eps), y = rsqrtf(x);
+  const float r = y < INFINITY ? fmaf(0.5f * y, fmaf(-x * y, y, 1.0f), y) : y;
   const f32x2 r2 = pair_of(r, r);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i >> 2].p[i & 3] = mul2(v[i >> 2].p[i & 3], r2);
+  if (!p.weight && !(kNorm == QLI_NORM_LAYER && p.bias)) return;
+  const Unit ones = {{kOnes, kOnes, kOnes, kOnes}};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (p.weight) {
-      const Unit w = vector_of<G>(p.weight, l + k * G);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[k].p[i] = mul2(v[k].p[i], w.p[i]);
-    }
+    const Unit w = p.weight ? vector_of<G>(p.weight, l + k * G) : ones;
     if (kNorm == QLI_NORM_LAYER && p.bias) {
       const Unit b = vector_of<G>(p.bias, l + k * G);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[k].p[i] = add2(v[k].p[i], b.p[i]);
+      for (int i = 0; i < 4; ++i) v[k].p[i] = fma2(v[k].p[i], w.p[i], b.p[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[k].p[i] = mul2(v[k].p[i], w.p[i]);
     }
   }
 }
@@ -650,7 +663,7 @@ qli_status check_rotary(const qli_rotary& r, int64_t width) {
   if (r.layout != QLI_ROTARY_INTERLEAVED && r.layout != QLI_ROTARY_HALF) return QLI_ERR_UNSUPPORTED;
   if (r.pairs < 8 || r.pairs > QLI_ROTARY_PAIRS || r.pairs % 8 != 0 || r.offset % 8 != 0)
     return QLI_ERR_UNSUPPORTED;
-  if (r.offset < 0 || r.offset + 2 * static_cast<int64_t>(r.pairs) > width || !std::isfinite(r.magnitude))
+  if (r.offset < 0 || r.offset + 2 * static_cast<int64_t>(r.pairs) > width || !std::isfinite(static_cast<float>(r.magnitude)))
     return QLI_ERR_INVALID_ARG;
   return QLI_OK;
 }
@@ -661,8 +674,10 @@ Turn make_turn(const qli_rotary& r, bool inverse) {
   w.half = r.layout == QLI_ROTARY_HALF ? 1 : 0;
   w.o8 = r.offset / 8;
   w.per_pair = static_cast<uint32_t>(((uint64_t{1} << 32) - 1) / static_cast<uint32_t>(r.pairs) + 1);
-  w.cos_scale = inverse ? 1.0f / r.magnitude : r.magnitude;
-  w.sin_scale = inverse ? -w.cos_scale : w.cos_scale;
+  const double scale = inverse ? 1.0 / r.magnitude : r.magnitude;
+  w.scale = static_cast<float>(scale);
+  w.scale_lo = static_cast<float>(scale - static_cast<double>(w.scale));
+  w.inverse = inverse ? 1 : 0;
   std::memcpy(w.turns, r.turns, sizeof(uint64_t) * static_cast<size_t>(r.pairs));
   return w;
 }
@@ -752,7 +767,7 @@ cudaError_t launch_append(const qli_append_args& a, const qli_row_prep* kv, cons
                                    kIndexRow, a.err_word};
     const Turn &x = d.kv.turn, &y = d.index.turn;
     // the same angles, magnitude and layout: one table, whatever the offsets
-    const bool same = x.pairs == y.pairs && x.half == y.half && x.cos_scale == y.cos_scale &&
+    const bool same = x.pairs == y.pairs && x.half == y.half && x.scale == y.scale && x.scale_lo == y.scale_lo &&
                       std::memcmp(x.turns, y.turns, sizeof(x.turns)) == 0;
     if (!same) {
       d.index_table = static_cast<int32_t>(entries);
@@ -779,7 +794,7 @@ extern "C" qli_status qli_rotate(const qli_rotate_args* a, const qli_rotary* rot
   if (a->D < 16 || a->D > kMostValues || a->D % 8 != 0) return QLI_ERR_UNSUPPORTED;
   qli_status st = check_rotary(*rotary, a->D);
   if (st != QLI_OK) return st;
-  if (a->inverse && rotary->magnitude == 0.0f) return QLI_ERR_INVALID_ARG;
+  if (a->inverse && !std::isfinite(static_cast<float>(1.0 / rotary->magnitude))) return QLI_ERR_INVALID_ARG;
   if (a->T == 0) return QLI_OK;
   st = check_dense(a->x, a->x_stride_t, a->x_stride_h, a->T, a->H, a->D, a->out, a->out_stride_t, a->out_stride_h, 8);
   if (st != QLI_OK) return st;

@@ -115,7 +115,8 @@ KV_BF16 = 0              # kv_mode of append_kv: rows of 1024 bytes
 class RotaryArgs(ctypes.Structure):
     """Mirror of `qli_rotary` (field order and types as in include/qli.h)."""
     _fields_ = [("pairs", c_int32), ("layout", c_int32), ("offset", c_int32),
-                ("magnitude", ctypes.c_float), ("turns", c_uint64 * ROTARY_PAIRS)]
+                ("reserved", c_int32),
+                ("magnitude", ctypes.c_double), ("turns", c_uint64 * ROTARY_PAIRS)]
 
 
 class RowPrepArgs(ctypes.Structure):
@@ -912,7 +913,7 @@ class Rotary:
 
     def args(self, offset: int) -> RotaryArgs:
         """The library's structure for rows whose rotated values start at `offset`."""
-        return RotaryArgs(self.dim // 2, ROTARY_LAYOUTS[self.layout], offset, self.magnitude,
+        return RotaryArgs(self.dim // 2, ROTARY_LAYOUTS[self.layout], offset, 0, self.magnitude,
                           (c_uint64 * ROTARY_PAIRS)(*self._turns))
 
     def packed(self, offset: int) -> bytes:

@@ -5,6 +5,7 @@ that see them, the bounds the launches rest on, and the whole-number angles."""
 import math
 import random
 
+import numpy as np
 import pytest
 
 from oracle import rows as oracle
@@ -216,24 +217,48 @@ def test_tables_of_rotated_rows_fit(pairs):
         assert 512 * tokens_of(128 // (D // 16), 10 ** 6, 1) <= 16 * 1024
 
 
-def turn_of(frac):
-    """The kernel's cosine and sine of 2^-32 frac turns, in double precision."""
+def turn_of(frac, scale=1.0, inverse=False):
+    """The kernel's cosine and sine of 2^-32 frac turns in FP32 (fused products by way of
+    FP64, which holds them but for the double rounding)."""
+    f = np.float32
+    fma = lambda a, b, c: f(np.float64(a) * np.float64(b) + np.float64(c))  # noqa: E731
+    hi_c = f(2 * math.pi / 2 ** 32)
+    lo_c = f(2 * math.pi / 2 ** 32 - float(hi_c))
+    s_hi = f(scale)
+    s_lo = f(scale - float(s_hi))
     quarter = (frac + 0x20000000 & 0xFFFFFFFF) >> 30
-    rest = frac - (quarter << 30)
-    rest = (rest + 2 ** 31) % 2 ** 32 - 2 ** 31
-    t = rest * 2 * math.pi / 2 ** 32
-    assert abs(t) <= math.pi / 4 + 1e-9
-    sin = t + t ** 3 * (-1 / 6 + t ** 2 * (1 / 120 + t ** 2 * (-1 / 5040 + t ** 2 / 362880)))
-    cos = 1 + t ** 2 * (-1 / 2 + t ** 2 * (1 / 24 + t ** 2 * (-1 / 720 + t ** 2 * (1 / 40320 - t ** 2 / 3628800))))
-    a, b = (sin, cos) if quarter & 1 else (cos, sin)
-    return (-a if quarter + 1 & 2 else a), (-b if quarter & 2 else b)
+    rest = (frac - (quarter << 30) + 2 ** 31) % 2 ** 32 - 2 ** 31
+    hi = f(rest)
+    lo = f(rest - int(hi))
+    t = f(hi * hi_c)
+    e = f(fma(hi, hi_c, -t) + fma(hi, lo_c, f(lo * hi_c)))
+    t2 = f(t * t)
+    t2e = fma(t, t, -t2)
+    p = fma(t2, f(1 / 362880), f(-1 / 5040))
+    p = fma(p, t2, f(1 / 120))
+    p = fma(p, t2, f(-1 / 6))
+    q = fma(t2, f(-1 / 3628800), f(1 / 40320))
+    q = fma(q, t2, f(-1 / 720))
+    q = fma(q, t2, f(1 / 24))
+    sin_r = fma(f(t * t2), p, fma(f(f(-0.5) * t2), e, e))
+    one = f(f(1) - f(f(0.5) * t2))
+    cos_r = fma(f(t2 * t2), q, f(f(f(f(1) - one) - f(f(0.5) * t2)) - fma(t, e, f(f(0.5) * t2e))))
+    sin_t = fma(s_hi, t, fma(s_hi, sin_r, f(s_lo * t)))
+    cos_t = fma(s_hi, one, fma(s_hi, cos_r, f(s_lo * one)))
+    a, b = (sin_t, cos_t) if quarter & 1 else (cos_t, sin_t)
+    return (-a if quarter + 1 & 2 else a), (-b if (quarter >> 1 & 1) != inverse else b)
 
 
-def test_cosine_and_sine_of_a_turn():
+@pytest.mark.parametrize("scale", [1.0, 1.2772588722239782, 0.3])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_cosine_and_sine_of_a_turn(scale, inverse):
+    """Within the last rounding (half a step of what lies below the next power of two of
+    the magnitude: 2^-25 of that), the sine series' rest of t^11 / 11! < 2^-29, and what
+    the sums before the last one are off: numbers below 2^-3 in four roundings, 4 * 2^-28 / 2
+    at most, and the part of the products that FP64 rounds."""
     rng = random.Random(7)
-    for frac in [0, 1, 2 ** 29 - 1, 2 ** 29, 2 ** 30, 2 ** 31, 3 << 30, 2 ** 32 - 1] + [rng.randrange(2 ** 32) for _ in range(5000)]:
-        c, s = turn_of(frac)
-        angle = 2 * math.pi * frac / 2 ** 32
-        # either may come of either series: the larger rest is the sine's, t^11 / 11! at
-        # t = pi / 4, 0.0702 / 39916800 = 1.76e-9 < 2^-29 = 1.86e-9
-        assert abs(c - math.cos(angle)) < 2.0 ** -29 and abs(s - math.sin(angle)) < 2.0 ** -29
+    bound = 2.0 ** (math.ceil(math.log2(scale)) - 25) + scale * (2.0 ** -29 + 2.0 ** -27)
+    for frac in [0, 1, 2 ** 29 - 1, 2 ** 29, 2 ** 30, 2 ** 31, 3 << 30, 2 ** 32 - 1] + [rng.randrange(2 ** 32) for _ in range(3000)]:
+        c, s = turn_of(frac, scale, inverse)
+        angle = 2 * math.pi * frac / 2 ** 32 * (-1 if inverse else 1)
+        assert abs(float(c) - scale * math.cos(angle)) < bound and abs(float(s) - scale * math.sin(angle)) < bound

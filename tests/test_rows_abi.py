@@ -49,7 +49,7 @@ def rotary(**over):
 ROTARY_REJECT = [(dict(layout=2), UNSUPPORTED), (dict(pairs=4), UNSUPPORTED), (dict(pairs=12), UNSUPPORTED),
                  (dict(pairs=72), UNSUPPORTED), (dict(pairs=-8), UNSUPPORTED), (dict(offset=4), UNSUPPORTED),
                  (dict(offset=-8), INVALID), (dict(offset=72), INVALID), (dict(magnitude=float("nan")), INVALID),
-                 (dict(magnitude=float("inf")), INVALID)]
+                 (dict(magnitude=float("inf")), INVALID), (dict(magnitude=1e300), INVALID)]
 
 
 def good_rotate(**over):

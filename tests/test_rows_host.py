@@ -262,4 +262,4 @@ def test_none_as_a_tree_mask_is_refused(lib):
 
 
 def test_the_whole_number_of_bytes():
-    assert ctypes.sizeof(qli.RotaryArgs) == len(ROT.packed(0)) == 528
+    assert ctypes.sizeof(qli.RotaryArgs) == len(ROT.packed(0)) == 536
