@@ -519,7 +519,7 @@ constexpr int kSets = 4;
 // ---- queries --------------------------------------------------------------------
 // Bound by HBM with BF16 results: 2047 tokens of 64 heads x 512 with RMS norm and a
 // rotated tail (268 MB) take 43 us, 6.2 TB/s. With codes by the instructions, some 16 a
-// value: 4096 tokens of 64 heads x 128 to E4M3 (101 MB) take 22.4 us, 4.5 TB/s, with 64%
+// value: 4096 tokens of 64 heads x 128 to E4M3 (101 MB) take 22.7 us, 4.4 TB/s, with 68%
 // of the issue slots taken. One set of rows a block, without the next one in flight,
 // took 59 and 32 us; the norm's and the layout's branches inside the loop 51 and 26.
 template <int D, int kMode>
@@ -570,8 +570,8 @@ struct AppendArgs {
 };
 
 // A block takes a few tokens: their KV rows, then their index K rows, by one table where
-// they turn alike. Bound by the instructions, 440 a token and warp: 65536 tokens to E4M3
-// (127 MB) take 35 us, 3.6 TB/s; separate blocks for the two kinds, each with its table, took 54.
+// they turn alike. Bound by the instructions, some 450 of a warp a token: 65536 tokens to
+// E4M3 (127 MB) take 38 us, 3.3 TB/s; separate blocks for the two kinds, each with its table, took 54.
 template <int kKv, int kIndex>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const __grid_constant__ AppendArgs<kKv, kIndex> a) {
   extern __shared__ float4 table4[];
