@@ -88,6 +88,13 @@ CASES = [
     ("window-128", [3000, 128, 140], [8, 8, 8], 16, "tree", 128),
     ("window-any", [500, 90], [90, 90], 48, "any", 33),
     ("window-wide", [5000, 64], [5, 2], 64, "tree", 3000),
+    ("two-words-any", [400, 130], [65, 130], 16, "any", 0),
+    ("two-words-window", [400, 200], [65, 130], 16, "any", 50),
+    ("five-words", [300, 1000], [300, 280], 24, "any", 0),
+    ("five-words-window", [310], [300], 64, "tree", 9),
+    ("one-head", [500, 90], [20, 90], 1, "any", 0),
+    ("two-heads", [500, 30], [9, 30], 2, "tree", 0),
+    ("three-heads-window", [700, 50], [30, 17], 3, "any", 25),
 ]
 
 
