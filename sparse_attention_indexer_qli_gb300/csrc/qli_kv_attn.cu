@@ -632,10 +632,6 @@ __device__ __forceinline__ void record_cut(const Args& a, int32_t t, int32_t g, 
   a.cut[blockIdx.x] = make_int4(end > u1 && first >= u0 ? t : -1, g, end, total);
 }
 
-// Row tiles of the group of t (0: not its first token).
-__device__ __forceinline__ int32_t tiles_at(const TreeSmem& S, int32_t t) { return S.tiles[t]; }
-__device__ __forceinline__ int32_t tiles_at(const Smem&, int32_t) { return 1; }
-
 // Plans the launch: every token's request and visible positions, and the CTA's
 // share. A thread takes one token.
 template <int kTree>
@@ -782,33 +778,35 @@ __device__ __forceinline__ void plan(const Args& a, SmemOf<kTree>& S, const Earl
   }
   const int32_t total = __shfl_sync(0xffffffffu, sums, 31);
   const int32_t at = __shfl_sync(0xffffffffu, sums, warp) - own + incl - mine;
-  if (kTree == kGroups && a.whole) {
-    // a row tile a CTA; more only where boundaries fall (see most_groups)
-    const int32_t ctas = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
-    const int32_t begin = total <= ctas ? c : share_begin(total, ctas, c);
-    const int32_t end = total <= ctas ? c + 1 : share_begin(total, ctas, c + 1);
-    if (at <= begin && begin < at + mine) {
-      S.start_t = tid;
-      S.start_g = begin - at;
-      S.start_i = 0;
-      S.count = units;
-    }
-    if (tid == 0 && begin >= total) S.count = 0;
-    __syncthreads();
-    if (end - begin > 1 && tid == 0) {
-      int32_t t = S.start_t, g = S.start_g, count = 0;
-#pragma unroll 1
-      for (int32_t k = begin; k < end; ++k) {
-        count += units_of<kTree>(a, S.tokV[t]);
-        if (++g == tiles_at(S, t)) {
-          g = 0;
-          do ++t; while (t < a.tc && tiles_at(S, t) == 0);
-        }
+  if constexpr (kTree == kGroups) {
+    if (a.whole) {
+      // a row tile a CTA; more only where boundaries fall (see most_groups)
+      const int32_t ctas = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
+      const int32_t begin = total <= ctas ? c : share_begin(total, ctas, c);
+      const int32_t end = total <= ctas ? c + 1 : share_begin(total, ctas, c + 1);
+      if (at <= begin && begin < at + mine) {
+        S.start_t = tid;
+        S.start_g = begin - at;
+        S.start_i = 0;
+        S.count = units;
       }
-      S.count = count;
+      if (tid == 0 && begin >= total) S.count = 0;
+      __syncthreads();
+      if (end - begin > 1 && tid == 0) {
+        int32_t t = S.start_t, g = S.start_g, count = 0;
+#pragma unroll 1
+        for (int32_t k = begin; k < end; ++k) {
+          count += units_of<kTree>(a, S.tokV[t]);
+          if (++g == S.tiles[t]) {
+            g = 0;
+            do ++t; while (t < a.tc && S.tiles[t] == 0);
+          }
+        }
+        S.count = count;
+      }
+      __syncthreads();
+      return;
     }
-    __syncthreads();
-    return;
   }
   share_of(a, total, u0, u1);
   if (at <= u0 && u0 < at + mine) {
@@ -1060,7 +1058,8 @@ __device__ __forceinline__ bool run_loaders(const Args& a, SmemOf<kTree>& S) {
         const uint32_t slot = (n + 1) & (kSlots - 1);
         if (!wait(&S.rowfull[slot], ((n + 1) / kSlots) & 1)) return false;
         const uint8_t* r[2] = {S.row[slot][r0] + off, S.row[slot][r0 + 4] + off};
-        if constexpr (kTree == kGroups) masked = S.masked[slot][lw / (kLoadWarps / kRowWarps)] != 0;   // of the warp's rows
+        // of the warp's rows
+        if constexpr (kTree == kGroups) masked = S.masked[slot][lw / (kLoadWarps / kRowWarps)] != 0;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -1522,8 +1521,8 @@ __device__ __forceinline__ bool run_softmax(const Args& a, SmemOf<kTree>& S, uin
       // on in the next to slot 1
       const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (w.began_here() ? 1 : 0);
       if (qw == 0) a.piece_lse[piece * kHT + 32 * sub + lane] = lse2;
-      output<false, (kTree == kGroups)>(S, oe, 32 * sub, 32 * qw + lane, nh, none, a.piece + piece * kPieceRow + (32 * sub) * kD,
-                           static_cast<int64_t>(kD));
+      output<false, (kTree == kGroups)>(S, oe, 32 * sub, 32 * qw + lane, nh, none,
+                                        a.piece + piece * kPieceRow + (32 * sub) * kD, static_cast<int64_t>(kD));
     }
     named_bar(bar, 128);                              // the factors are read
   }
@@ -1820,8 +1819,9 @@ int32_t stack_of(Args d, int sms) {
 // a window of 128: 14.5 and 13.1.
 int32_t heads_per_tile(const Args& d, int64_t most, int sms) {
   const int64_t groups = most_groups(d, d.T), H = static_cast<int64_t>(d.stack) * d.H;
+  const int64_t units = groups * (most <= (d.stack > 1 ? kWholeGroupUnits : kWholeUnits) ? 1 : most);
   int32_t ht = kHT;
-  while (ht > 16 && (most <= (d.stack > 1 ? kWholeGroupUnits : kWholeUnits) ? 1 : most) * groups * ((H + ht / 2 - 1) / (ht / 2)) <= sms) ht /= 2;
+  while (ht > 16 && units * ((H + ht / 2 - 1) / (ht / 2)) <= sms) ht /= 2;
   return ht;
 }
 
@@ -1841,15 +1841,17 @@ Layout layout_for(int sms) {
 // Joins the pieces of a launch of up to `tiles` row tiles.
 template <int kTree>
 cudaError_t launch_join(const Args& d, int32_t ctas, int64_t tiles, cudaStream_t s) {
+  constexpr bool kGrouped = kTree == kGroups;
+  const dim3 block(kJoinThreads);
   const int32_t rows = d.stack * d.H < d.ht ? d.stack * d.H : d.ht;
   const auto grid = [&](int64_t x, int32_t of_block) {
     return dim3(static_cast<unsigned>(x), static_cast<unsigned>((rows + of_block - 1) / of_block));
   };
   if constexpr (kTree != kPlain) {
     if (4 * tiles <= ctas && ctas <= kJoinThreads)
-      return launch_pdl(merge_pieces_kernel<(kTree == kGroups), true>, grid(tiles, kJoinRows / 4), dim3(kJoinThreads), 0, s, d, ctas);
+      return launch_pdl(merge_pieces_kernel<kGrouped, true>, grid(tiles, kJoinRows / 4), block, 0, s, d, ctas);
   }
-  return launch_pdl(merge_pieces_kernel<(kTree == kGroups), false>, grid(ctas - 1, kJoinRows), dim3(kJoinThreads), 0, s, d, ctas);
+  return launch_pdl(merge_pieces_kernel<kGrouped, false>, grid(ctas - 1, kJoinRows), block, 0, s, d, ctas);
 }
 
 template <bool kFp8, int kTree>

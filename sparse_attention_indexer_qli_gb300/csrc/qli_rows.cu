@@ -227,7 +227,7 @@ __device__ __forceinline__ void normalise(Unit (&v)[2], const Prep& p, int l) {
   const float2 e = both(s);
   // with one step of Newton's, since what is off here moves the whole row
   const float x = fmaf(row_sum<G>(e.x + e.y), kInv, p.eps), y = rsqrtf(x);
-  const float r = y < INFINITY ? fmaf(0.5f * y, fmaf(-x * y, y, 1.0f), y) : y;
+  const float r = y > 0.0f && y < INFINITY ? fmaf(0.5f * y, fmaf(-x * y, y, 1.0f), y) : y;
   const f32x2 r2 = pair_of(r, r);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i >> 2].p[i & 3] = mul2(v[i >> 2].p[i & 3], r2);
@@ -523,9 +523,9 @@ constexpr int kSets = 4;
 // of the issue slots taken. One set of rows a block, without the next one in flight,
 // took 59 and 32 us; the norm's and the layout's branches inside the loop 51 and 26.
 template <int D, int kMode>
-__global__ void __launch_bounds__(kThreads, kMode == 0 ? kBlocksPerSmBf16 : kBlocksPerSm) prepare_kernel(const __grid_constant__ Prep p, DenseIn in,
-                                                           DenseOut<kMode> out, const int32_t* positions,
-                                                           int32_t rows, int32_t block_rows) {
+__global__ void __launch_bounds__(kThreads, kMode == 0 ? kBlocksPerSmBf16 : kBlocksPerSm)
+    prepare_kernel(const __grid_constant__ Prep p, DenseIn in, DenseOut<kMode> out, const int32_t* positions,
+                   int32_t rows, int32_t block_rows) {
   extern __shared__ float4 table4[];
   float2* table = reinterpret_cast<float2*>(table4);
   const int32_t r0 = static_cast<int32_t>(blockIdx.x) * block_rows, end = min(rows - r0, block_rows) + r0;
@@ -537,7 +537,6 @@ __global__ void __launch_bounds__(kThreads, kMode == 0 ? kBlocksPerSmBf16 : kBlo
   }
   work.run(table, t0);
 }
-
 
 template <int D, int kMode>
 cudaError_t launch_prepare(const Prep& p, const DenseIn& in, const DenseOut<kMode>& out,
@@ -571,9 +570,11 @@ struct AppendArgs {
 
 // A block takes a few tokens: their KV rows, then their index K rows, by one table where
 // they turn alike. Bound by the instructions, some 450 of a warp a token: 65536 tokens to
-// E4M3 (127 MB) take 38 us, 3.3 TB/s; separate blocks for the two kinds, each with its table, took 54.
+// E4M3 (127 MB) take 38 us, 3.3 TB/s; separate blocks for the two kinds, each with its
+// table, took 54.
 template <int kKv, int kIndex>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const __grid_constant__ AppendArgs<kKv, kIndex> a) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    append_kernel(const __grid_constant__ AppendArgs<kKv, kIndex> a) {
   extern __shared__ float4 table4[];
   float2* table = reinterpret_cast<float2*>(table4);
   const int32_t r0 = static_cast<int32_t>(blockIdx.x) * a.block_rows, end = min(a.n - r0, a.block_rows) + r0;
@@ -663,7 +664,8 @@ qli_status check_rotary(const qli_rotary& r, int64_t width) {
   if (r.layout != QLI_ROTARY_INTERLEAVED && r.layout != QLI_ROTARY_HALF) return QLI_ERR_UNSUPPORTED;
   if (r.pairs < 8 || r.pairs > QLI_ROTARY_PAIRS || r.pairs % 8 != 0 || r.offset % 8 != 0)
     return QLI_ERR_UNSUPPORTED;
-  if (r.offset < 0 || r.offset + 2 * static_cast<int64_t>(r.pairs) > width || !std::isfinite(static_cast<float>(r.magnitude)))
+  if (r.offset < 0 || r.offset + 2 * static_cast<int64_t>(r.pairs) > width ||
+      !std::isfinite(static_cast<float>(r.magnitude)))
     return QLI_ERR_INVALID_ARG;
   return QLI_OK;
 }

@@ -180,7 +180,8 @@ def _tree(L, mask=P, words=1, **over):
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(mask=None), INVALID), (dict(mask=P + 4), ALIGNMENT), (dict(words=0), INVALID), (dict(words=-1), INVALID), (dict(words=257), UNSUPPORTED),
+    (dict(mask=None), INVALID), (dict(mask=P + 4), ALIGNMENT), (dict(words=0), INVALID), (dict(words=-1), INVALID),
+    (dict(words=257), UNSUPPORTED),
     (dict(indices=P, K=4), INVALID), (dict(ratio=2), UNSUPPORTED), (dict(residual=P), 4), (dict(window=-1), INVALID),
     (dict(k_lens=None), INVALID), (dict(D=576), UNSUPPORTED), (dict(q=P + 8), ALIGNMENT)])
 def test_tree_refuses(L, kw, want):
