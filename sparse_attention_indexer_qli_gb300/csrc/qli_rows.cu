@@ -301,7 +301,10 @@ __device__ __forceinline__ void turn_row(Unit (&v)[2], const Turn& w, const floa
 }
 
 // The row's codes and the FP16 bits of its scale: s = FP16(max |x| / Q), code(x / s),
-// the quotient as the other writers take it (qli_codes.cuh), two at a time.
+// the quotient as the other writers take it (qli_codes.cuh), two at a time. E4M3 has two
+// zeros, and the quotient's is x's: the correction step ends in +0 where x / s is a zero, so
+// it works on -x / s, whose zeros are +0 then for x < 0 and -0 for x > 0, and the codes'
+// signs are turned over (4096 tokens of 64 heads: 23.2 us, 22.95 without).
 template <int G, bool kFp8>
 __device__ __forceinline__ uint16_t quantise(const Unit (&v)[2], uint2 (&codes)[2]) {
   float m = 0.0f;
@@ -316,8 +319,9 @@ __device__ __forceinline__ uint16_t quantise(const Unit (&v)[2], uint2 (&codes)[
   const float sf = __half2float(__ushort_as_half(sb));
   codes[0] = codes[1] = make_uint2(0u, 0u);
   if (sf == 0.0f) return 0u;
-  const float y = __frcp_rn(sf);
-  const f32x2 y2 = pair_of(y, y), s2 = pair_of(-sf, -sf);
+  constexpr float kSign = kFp8 ? -1.0f : 1.0f;
+  const float y = kSign * __frcp_rn(sf);
+  const f32x2 y2 = pair_of(y, y), s2 = pair_of(-kSign * sf, -kSign * sf);
   // A scale that is a normal number is within 2^-11 of amax / Q, so that quotients end
   // at Q and a fraction. A subnormal one may be smaller, and the largest one cuts.
   const bool clamp = !kFp8 && (sb < 0x0400u || sb == 0x7bffu);
@@ -334,7 +338,7 @@ __device__ __forceinline__ uint16_t quantise(const Unit (&v)[2], uint2 (&codes)[
       }
       if constexpr (kFp8) {
         const float2 lo = both(q[0]), hi = both(q[1]);
-        w[j] = e4m3x2_of(lo.x, lo.y) | (e4m3x2_of(hi.x, hi.y) << 16);
+        w[j] = (e4m3x2_of(lo.x, lo.y) | (e4m3x2_of(hi.x, hi.y) << 16)) ^ 0x80808080u;
       } else {
         if (clamp) {
 #pragma unroll
