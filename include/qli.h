@@ -546,7 +546,10 @@ qli_status qli_prepare_q(const qli_prepare_args *a, const qli_row_prep *prep, vo
  * qli_write_kv) and index K rows of 128 (the 8-bit rows of qli_write_index_k), the
  * codes taken of the FP32 values. Either kind may be left out (NULL). Slots,
  * padding, distinctness and err_word as for qli_write_kv; the parts of a page that
- * are written must not overlap. One kernel on `stream`; asynchronous. */
+ * are written must not overlap. A row with Inf or NaN does not reach other rows: 8-bit
+ * KV rows that are not finite after norm and rotation get a scale of NaN, so that what attends
+ * to them is NaN too; other such rows unspecified codes. One kernel on `stream`;
+ * asynchronous. */
 typedef struct qli_append_args {
     const uint16_t *kv;          /* row i: 512 BF16 values at kv + i * kv_stride (elements, a multiple
                                     of 8, at least 512), 16-byte aligned; or NULL */

@@ -300,6 +300,17 @@ __device__ __forceinline__ void turn_row(Unit (&v)[2], const Turn& w, const floa
   }
 }
 
+// The largest of three. Of KV rows NaN is above all, as for the KV writer: the scale is NaN
+// then, and so is what attends to the row (without that a norm over a NaN leaves a row of
+// zeros). The quantisers of queries and index K pass over it.
+template <int G>
+__device__ __forceinline__ float largest(float a, float b, float c) {
+  if constexpr (16 * G != kKvRow) return fmaxf(fmaxf(a, b), c);
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // The row's codes and the FP16 bits of its scale: s = FP16(max |x| / Q), code(x / s),
 // the quotient as the other writers take it (qli_codes.cuh), two at a time. E4M3 has two
 // zeros, and the quotient's is x's: the correction step ends in +0 where x / s is a zero, so
@@ -311,10 +322,10 @@ __device__ __forceinline__ uint16_t quantise(const Unit (&v)[2], uint2 (&codes)[
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 x = both(v[i >> 2].p[i & 3]);
-    m = fmaxf(fmaxf(m, fabsf(x.x)), fabsf(x.y));
+    m = largest<G>(m, fabsf(x.x), fabsf(x.y));
   }
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = G / 2; o > 0; o >>= 1) m = largest<G>(m, m, __shfl_xor_sync(0xffffffffu, m, o));
   const uint16_t sb = scale_bits_of<kFp8>(m);
   const float sf = __half2float(__ushort_as_half(sb));
   codes[0] = codes[1] = make_uint2(0u, 0u);

@@ -60,3 +60,32 @@ def test_cache_rows_left_as_they_are(quant):
     qli.write_kv(kv, slots, two, **at_kv, **pages)
     qli.write_index_k(k, slots, two, **at_k, **pages)
     assert torch.equal(one, two)
+
+
+@pytest.mark.parametrize("quant", [kv8.INT8, kv8.FP8], ids=["i8", "f8"])
+@pytest.mark.parametrize("norm", [None, "rms", "layer"])
+def test_cache_rows_that_are_not_finite_do_not_become_finite(norm, quant):
+    """What reads such a row gets NaN in all of it, as after write_kv; its neighbours are
+    those of a call without it."""
+    import torch
+    n, L = 40, synth.kv8_layout(64)
+    x = np.random.default_rng(25).standard_normal((n, 512))
+    pages = dict(rows_per_page=64, page_stride=L["page_stride"], quant_mode=quant, kv_offset=L["kv_offset"],
+                 kv_scale_offset=L["kv_scale_offset"])
+    slots = up(np.random.default_rng(26).permutation(64)[:n])
+    prep = qli.RowPrep(512, norm=norm, rotary=qli.Rotary(64), offset=448)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+
+    def rows(x):
+        cache = torch.zeros(1, L["page_stride"], dtype=torch.uint8, device="cuda")
+        kw = dict(pages, kv_mode=quant)
+        qli.append_kv(x, None, pos, slots, cache, kv_prep=prep, **kw)
+        return cache
+
+    fine = bf16(kv8.f32_to_bf16(x))
+    bad = fine.clone()
+    bad[3, 7], bad[9, 500], bad[20, 0], bad[31] = float("nan"), float("nan"), float("-inf"), float("nan")
+    hit = torch.zeros(n, dtype=torch.bool, device="cuda")
+    hit[[3, 9, 20, 31]] = True
+    got, want = (qli.read_kv(rows(t), slots, **pages) for t in (bad, fine))
+    assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], want[~hit])
