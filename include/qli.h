@@ -509,7 +509,9 @@ qli_status qli_rotate(const qli_rotate_args *a, const qli_rotary *rotary, void *
 /* What is done to a row of `width` values before it is rounded: the norm
  *     rms:   y = x / sqrt(mean(x^2) + eps) * weight
  *     layer: y = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * weight + bias
- * and the rotation, in FP32 (squares are summed in FP32: magnitudes below 2^59).
+ * and the rotation, in FP32. Squares are summed in FP32: magnitudes below 2^59, and
+ * however small, also with eps 0 (where a row of zeros, or for the layer norm of equal
+ * values, gives NaN: 0 / 0).
  * A host structure; weight and bias are device pointers. */
 enum { QLI_NORM_NONE = 0, QLI_NORM_RMS = 1, QLI_NORM_LAYER = 2 };
 typedef struct qli_row_prep {

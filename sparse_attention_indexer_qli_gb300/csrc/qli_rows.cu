@@ -208,8 +208,31 @@ __device__ __forceinline__ Unit vector_of(const float* from, int at) {
   return u;
 }
 
+// Under an eps that does not cover them, squares of values below 2^-63 leave FP32's range.
+// Rows up to 2^-40 are taken 2^90 times as large then: 2^50 at most, and from 2^-43 (the
+// smallest BF16 number) on. Of others a value is a multiple of 2^-48, or a mean at least
+// 2^-57 off some value. Returns the row's eps.
+constexpr float kSmallEps = 7.888609052e-31f;         // 2^-100
+bool small_eps(const Prep& p) { return p.norm != QLI_NORM_NONE && p.eps < kSmallEps; }
+template <int G>
+__device__ __forceinline__ float enlarge(Unit (&v)[2], float eps) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = both(v[i >> 2].p[i & 3]);
+    m = fmaxf(fmaxf(m, fabsf(x.x)), fabsf(x.y));
+  }
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float up = m < 0x1p-40f ? 0x1p90f : 1.0f;
+  const f32x2 up2 = pair_of(up, up);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i >> 2].p[i & 3] = mul2(v[i >> 2].p[i & 3], up2);
+  return eps * up * up;
+}
+
 template <int G, int kNorm>
-__device__ __forceinline__ void normalise(Unit (&v)[2], const Prep& p, int l) {
+__device__ __forceinline__ void normalise(Unit (&v)[2], const Prep& p, int l, float eps) {
   constexpr float kInv = 1.0f / (16 * G);
   if constexpr (kNorm == QLI_NORM_LAYER) {
     f32x2 s = add2(v[0].p[0], v[1].p[0]);
@@ -226,7 +249,7 @@ __device__ __forceinline__ void normalise(Unit (&v)[2], const Prep& p, int l) {
   for (int i = 1; i < 8; ++i) s = fma2(v[i >> 2].p[i & 3], v[i >> 2].p[i & 3], s);
   const float2 e = both(s);
   // with one step of Newton's, since what is off here moves the whole row
-  const float x = fmaf(row_sum<G>(e.x + e.y), kInv, p.eps), y = rsqrtf(x);
+  const float x = fmaf(row_sum<G>(e.x + e.y), kInv, eps), y = rsqrtf(x);
   const float r = y > 0.0f && y < INFINITY ? fmaf(0.5f * y, fmaf(-x * y, y, 1.0f), y) : y;
   const f32x2 r2 = pair_of(r, r);
 #pragma unroll
@@ -249,6 +272,7 @@ __device__ __forceinline__ void normalise(Unit (&v)[2], const Prep& p, int l) {
 
 // `cs`: the row's token in the table.
 enum : int { kNeighbours = 0, kHalves = 1, kOwnHalves = 2 };   // the last: pairs half a row apart, in one lane
+constexpr int kAny = -1;                               // of layouts and norms: see Rows
 template <int G, int kLayout>
 __device__ __forceinline__ void turn_row(Unit (&v)[2], const Turn& w, const float2* cs, int l) {
   const int r8 = w.pairs / 4;
@@ -446,8 +470,10 @@ struct PagedOut {
 
 // Rows r0 .. end of a block, kThreads / G at a time: construct (loads the first ones),
 // fill the table of the rows' tokens from `t0` on, synchronise, run
-// (works on one set of rows while the next one loads).
-template <int D, int kMode, class In, class Out>
+// (works on one set of rows while the next one loads). kSmall: under an eps that does not
+// cover small rows; kernels of their own, since the others took up to 2% longer with a test
+// of the eps and up to 5% with a loop beside theirs (registers).
+template <int D, int kMode, bool kSmall, class In, class Out>
 struct Rows {
   static constexpr int G = D / 16, kRows = kThreads / G;
   const In& in;
@@ -474,7 +500,8 @@ struct Rows {
     key = out.key(at);
   }
   __device__ __forceinline__ void run(const float2* table, int32_t t0) {
-    if (!p.turn.half) run_norm<kNeighbours>(table, t0);
+    if constexpr (kSmall) run_all<kAny, kAny>(table, t0);
+    else if (!p.turn.half) run_norm<kNeighbours>(table, t0);
     else if (p.turn.pairs == 8 * G) run_norm<kOwnHalves>(table, t0);
     else run_norm<kHalves>(table, t0);
   }
@@ -484,6 +511,7 @@ struct Rows {
     else if (p.norm == QLI_NORM_LAYER) run_all<kLayout, QLI_NORM_LAYER>(table, t0);
     else run_all<kLayout, QLI_NORM_NONE>(table, t0);
   }
+  // kAny: any layout and norm.
   template <int kLayout, int kNorm>
   __device__ __forceinline__ void run_all(const float2* table, int32_t t0) {
     // the same number of turns for every thread of the block
@@ -495,8 +523,19 @@ struct Rows {
       const typename Out::Key to = key;
       r += kRows;
       if (n + kRows < end) load();
-      if constexpr (kNorm != QLI_NORM_NONE) normalise<G, kNorm>(v, p, l);
-      if (p.turn.pairs) turn_row<G, kLayout>(v, p.turn, table + (t - t0) * kTokenEntries, l);
+      const float2* cs = table + (t - t0) * kTokenEntries;
+      if constexpr (kNorm == kAny) {
+        if (p.norm != QLI_NORM_NONE) {
+          const float eps = p.eps < kSmallEps ? enlarge<G>(v, p.eps) : p.eps;
+          if (p.norm == QLI_NORM_RMS) normalise<G, QLI_NORM_RMS>(v, p, l, eps);
+          else normalise<G, QLI_NORM_LAYER>(v, p, l, eps);
+        }
+        if (p.turn.pairs && p.turn.half) turn_row<G, kHalves>(v, p.turn, cs, l);
+        else if (p.turn.pairs) turn_row<G, kNeighbours>(v, p.turn, cs, l);
+      } else {
+        if constexpr (kNorm != QLI_NORM_NONE) normalise<G, kNorm>(v, p, l, p.eps);
+        if (p.turn.pairs) turn_row<G, kLayout>(v, p.turn, cs, l);
+      }
       uint16_t* scale = nullptr;
       if constexpr (kMode == 0) {
         uint8_t* dst = at < end ? out.dest(at, t, to, scale) : nullptr;
@@ -537,14 +576,14 @@ constexpr int kSets = 4;
 // value: 4096 tokens of 64 heads x 128 to E4M3 (101 MB) take 22.7 us, 4.4 TB/s, with 68%
 // of the issue slots taken. One set of rows a block, without the next one in flight,
 // took 59 and 32 us; the norm's and the layout's branches inside the loop 51 and 26.
-template <int D, int kMode>
+template <int D, int kMode, bool kSmall>
 __global__ void __launch_bounds__(kThreads, kMode == 0 ? kBlocksPerSmBf16 : kBlocksPerSm)
     prepare_kernel(const __grid_constant__ Prep p, DenseIn in, DenseOut<kMode> out, const int32_t* positions,
                    int32_t rows, int32_t block_rows) {
   extern __shared__ float4 table4[];
   float2* table = reinterpret_cast<float2*>(table4);
   const int32_t r0 = static_cast<int32_t>(blockIdx.x) * block_rows, end = min(rows - r0, block_rows) + r0;
-  Rows<D, kMode, DenseIn, DenseOut<kMode>> work(in, out, p, r0, end);
+  Rows<D, kMode, kSmall, DenseIn, DenseOut<kMode>> work(in, out, p, r0, end);
   const int32_t t0 = in.token(r0);
   if (p.turn.pairs) {
     fill_table(table, p.turn, positions, t0, in.token(end - 1) - t0 + 1);
@@ -566,8 +605,9 @@ cudaError_t launch_prepare(const Prep& p, const DenseIn& in, const DenseOut<kMod
   while (each > 1 && bytes() > kTableBytes) --each;
   const int32_t block_rows = static_cast<int32_t>(each) * kRows;
   const size_t smem = static_cast<size_t>(bytes());
-  prepare_kernel<D, kMode><<<static_cast<unsigned>((rows - 1) / block_rows + 1), kThreads, smem, s>>>(
-      p, in, out, positions, rows, block_rows);
+  const auto kernel = small_eps(p) ? prepare_kernel<D, kMode, true> : prepare_kernel<D, kMode, false>;
+  kernel<<<static_cast<unsigned>((rows - 1) / block_rows + 1), kThreads, smem, s>>>(p, in, out, positions, rows,
+                                                                                    block_rows);
   return cudaGetLastError();
 }
 
@@ -587,7 +627,7 @@ struct AppendArgs {
 // they turn alike. Bound by the instructions, some 450 of a warp a token: 65536 tokens to
 // E4M3 (127 MB) take 38 us, 3.3 TB/s; separate blocks for the two kinds, each with its
 // table, took 54.
-template <int kKv, int kIndex>
+template <int kKv, int kIndex, bool kSmall>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     append_kernel(const __grid_constant__ AppendArgs<kKv, kIndex> a) {
   extern __shared__ float4 table4[];
@@ -600,14 +640,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     __syncthreads();
   };
   if (a.kv_in.x) {
-    Rows<kKvRow, kKv, FlatIn, PagedOut<kKv>> work(a.kv_in, a.kv_out, a.kv, r0, end);
+    Rows<kKvRow, kKv, kSmall, FlatIn, PagedOut<kKv>> work(a.kv_in, a.kv_out, a.kv, r0, end);
     turns();
     work.run(table, r0);
   } else {
     turns();
   }
   if (a.index_in.x) {
-    Rows<kIndexRow, kIndex, FlatIn, PagedOut<kIndex>> work(a.index_in, a.index_out, a.index, r0, end);
+    Rows<kIndexRow, kIndex, kSmall, FlatIn, PagedOut<kIndex>> work(a.index_in, a.index_out, a.index, r0, end);
     work.run(table + a.index_table, r0);
   }
 }
@@ -791,8 +831,10 @@ cudaError_t launch_append(const qli_append_args& a, const qli_row_prep* kv, cons
       entries += y.pairs ? tokens * kTokenEntries : 0;
     }
   }
-  append_kernel<kKv, kIndex><<<static_cast<unsigned>((a.n - 1) / d.block_rows + 1), kThreads,
-                               sizeof(float2) * static_cast<size_t>(entries), s>>>(d);
+  const auto kernel = small_eps(d.kv) || small_eps(d.index) ? append_kernel<kKv, kIndex, true>
+                                                            : append_kernel<kKv, kIndex, false>;
+  kernel<<<static_cast<unsigned>((a.n - 1) / d.block_rows + 1), kThreads,
+           sizeof(float2) * static_cast<size_t>(entries), s>>>(d);
   return cudaGetLastError();
 }
 
