@@ -137,3 +137,27 @@ def test_a_query_that_is_not_finite_stays_alone(cut, masks, quant):
             assert torch.isnan(out[t, 3:5]).all()
             heads = [h for h in range(H) if h not in (3, 4)]
             assert torch.equal(out[t, heads], want[0][t, heads]) and torch.equal(lse[t, heads], want[1][t, heads])
+
+
+# ---- every way of sharing, with and without a window -------------------------------------
+
+def compared(case, window=0, kw=None, err_want=0):
+    from test_kv_attn_gpu import compare
+    got = attend(case.upload() if kw is None else kw, window, err_want)
+    compare(case, tuple(t.double().cpu().numpy() for t in got), window=window)
+
+
+SHARED = [(1, 3), (2, 8), (5, 8), (8, 8), (16, 4), (16, 7), (20, 6), (32, 2), (32, 9), (40, 8), (48, 5), (96, 4), (100, 8),
+          (16, 70), (96, 70), (24, 130)]
+
+
+@pytest.mark.parametrize("window", [0, 1, 5, 40, 100, 200])
+@pytest.mark.parametrize("H,n", SHARED, ids=lambda v: str(v))
+def test_tokens_that_share_tiles(H, n, window):
+    """As many requests as it takes; any masks (empty ones too) or trees."""
+    words, B = -(-n // 64), 3
+    while plan.stack_of(H, B * n, B, words, window, 768, sms()) == 1:
+        B += 1
+    raw = [[700, 66 + n, n, 300, 129 + n][b % 5] for b in range(B)]
+    compared(TreeCase(76 + H + n, raw, [n] * B, H, [kv8.FP8, kv8.INT8][(H + n + window) % 2], "any" if H % 3 else "tree"),
+             window)
