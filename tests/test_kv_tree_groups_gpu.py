@@ -4,6 +4,7 @@ import pytest
 
 import tree_launches as plan
 from oracle import kv8
+from oracle import rows as oracle
 from sparse_attention_indexer_qli_gb300 import build as libbuild
 from sparse_attention_indexer_qli_gb300 import qli
 from test_kv_tree_gpu import SCALE, TreeCase
@@ -161,3 +162,72 @@ def test_tokens_that_share_tiles(H, n, window):
     raw = [[700, 66 + n, n, 300, 129 + n][b % 5] for b in range(B)]
     compared(TreeCase(76 + H + n, raw, [n] * B, H, [kv8.FP8, kv8.INT8][(H + n + window) % 2], "any" if H % 3 else "tree"),
              window)
+
+
+# ---- boundaries that fall, tokens that no request covers ----------------------------------
+
+class Disturbed(TreeCase):
+    """Other boundaries than the tokens were made for; each token belongs to the last
+    request that a search over the clamped boundaries finds to start at or before it."""
+
+    def disturb(self, cu):
+        self.given = cu
+        return self
+
+    def range_of(self, t):
+        cu, lo, hi = [min(max(c, 0), self.T) for c in self.given], 0, self.B - 1
+        while lo < hi:
+            mid = (lo + hi + 1) // 2
+            lo, hi = (mid, hi) if cu[mid] <= t else (lo, mid - 1)
+        return lo, cu[lo], max(cu[lo], cu[lo + 1])
+
+    def request(self, t):
+        return self.range_of(t)[0]
+
+    def positions(self, t, window=0):
+        b, q0, q1 = self.range_of(t)
+        if not q0 <= t < q1:
+            return super().positions(t, window)[:0]
+        n = q1 - q0
+        return oracle.tree_positions(int(self.k_lens[b]), n, self.masks[t] & (1 << min(n, 64 * self.words)) - 1, window)
+
+    def upload(self, dev="cuda"):
+        import torch
+        return dict(super().upload(dev), cu_seqlens_q=torch.tensor(self.given, dtype=torch.int32, device=dev))
+
+
+def disturbed(H, swaps, seed=78):
+    """Trees of 8 tokens, as many as it takes for groups under a window; boundary i of
+    `swaps` by another value."""
+    B = sms() // 8 + 1
+    case = Disturbed(seed, [300 + 7 * (b % 9) for b in range(B)], [8] * B, H, kv8.FP8)
+    cu = case.cu.tolist()
+    for i, v in swaps.items():
+        cu[i % (B + 1)] = v if v >= 0 else cu[-1] + v
+    return case.disturb(cu)
+
+
+@pytest.mark.parametrize("window", [64, 128])
+@pytest.mark.parametrize("H", [16, 32])
+@pytest.mark.parametrize("swaps", [{3: 40, 7: 16}, {1: 100}, {-2: 5, 4: 0}], ids=["two", "one", "last"])
+def test_boundaries_that_fall_in_whole_tiles(swaps, H, window):
+    """Each token stays alone then, which makes more row tiles than the launch has CTAs:
+    they take several each, and every token gets the answer of its request."""
+    import torch
+    case = disturbed(H, swaps)
+    kw = case.upload()
+    (kind, ctas), = plan.split_of(kw, window, sms())                   # nothing is joined
+    assert kind == "groups" and ctas < case.T
+    out = torch.full((case.T, H, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((case.T, H), float("nan"), device="cuda")
+    got = attend(kw, window, err_want=1, out=out, lse=lse)
+    from test_kv_attn_gpu import compare
+    compare(case, tuple(t.double().cpu().numpy() for t in got), window=window)
+
+
+@pytest.mark.parametrize("window", [0, 64])
+@pytest.mark.parametrize("H", [16, 32])
+def test_tokens_that_no_request_covers_in_groups(H, window):
+    """Before the first boundary and behind the last; a request without tokens among them."""
+    case = disturbed(H, {0: 5, 2: 8, -1: -3})
+    compared(case, window, err_want=1)
