@@ -4,7 +4,8 @@ import numpy as np
 
 
 def frequencies(dim, base=10000.0, factor=1.0, trained=None, ramp=(1.0, 32.0)):
-    """Radians per position of each pair."""
+    """Radians per position of each pair; between the turns of the ramp the part that stays
+    is linear in the turns."""
     f = np.asarray(base, dtype=np.float64) ** (-np.arange(0, dim, 2) / dim)
     keep = np.zeros(dim // 2)
     if trained is not None:
