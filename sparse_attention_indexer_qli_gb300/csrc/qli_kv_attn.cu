@@ -1666,8 +1666,10 @@ __device__ __forceinline__ void join_row(const Args& a, int32_t ctas, int32_t c,
 
 // kFew: a launch of few row tiles, each in many pieces. Block (i, k) takes the i-th row
 // tile that goes on in another CTA, four warps a row with a quarter of its values each
-// and four times as many pieces in flight. One tree of 8 tokens of 64 heads over 2048
-// positions, 8 row tiles in 19 pieces each: 25.7 us without, 19.9 with.
+// and four times as many pieces in flight. One tree of 8 tokens of 64 heads over 1024 and
+// 4096 positions, 8 row tiles in 19 pieces each: 15.9 and 24.0 us, without 19.5 and 28.3;
+// of 18 tokens 19.9 and 31.6, without 20.7 and 32.0; of 20 tokens, 7 or 8 pieces each,
+// 25.7 and 36.3, without 24.2 and 34.7: so up to an eighth of the CTAs (launch_join).
 template <bool kGrouped, bool kFew>
 __global__ void __launch_bounds__(kJoinThreads) merge_pieces_kernel(const Args a, int32_t ctas) {
   pdl_wait();
@@ -1838,9 +1840,9 @@ Layout layout_for(int sms) {
   return L;
 }
 
-// Joins the pieces of a launch of up to `tiles` row tiles.
+// Joins the pieces of a launch of up to `tiles` row tiles, `likely` as a rule.
 template <int kTree>
-cudaError_t launch_join(const Args& d, int32_t ctas, int64_t tiles, cudaStream_t s) {
+cudaError_t launch_join(const Args& d, int32_t ctas, int64_t tiles, int64_t likely, cudaStream_t s) {
   constexpr bool kGrouped = kTree == kGroups;
   const dim3 block(kJoinThreads);
   const int32_t rows = d.stack * d.H < d.ht ? d.stack * d.H : d.ht;
@@ -1848,7 +1850,7 @@ cudaError_t launch_join(const Args& d, int32_t ctas, int64_t tiles, cudaStream_t
     return dim3(static_cast<unsigned>(x), static_cast<unsigned>((rows + of_block - 1) / of_block));
   };
   if constexpr (kTree != kPlain) {
-    if (4 * tiles <= ctas && ctas <= kJoinThreads)
+    if (8 * likely <= ctas && ctas <= kJoinThreads)
       return launch_pdl(merge_pieces_kernel<kGrouped, true>, grid(tiles, kJoinRows / 4), block, 0, s, d, ctas);
   }
   return launch_pdl(merge_pieces_kernel<kGrouped, false>, grid(ctas - 1, kJoinRows), block, 0, s, d, ctas);
@@ -1878,7 +1880,7 @@ cudaError_t launch(Args d, int sms, cudaStream_t s) {
     kernel<<<static_cast<unsigned>(ctas), kThreads, kBytes, s>>>(d);
     e = cudaGetLastError();
     if (e == cudaSuccess && ctas > 1 && !d.whole)
-      e = launch_join<kTree>(d, ctas, tiles, s);
+      e = launch_join<kTree>(d, ctas, tiles, likely, s);
   }
   return e;
 }

@@ -12,7 +12,8 @@ SMS = 152
 def _shapes(n=60, seed=41):
     rng = random.Random(seed)
     out = [(16, 512, 64, 1, 128, 32768), (16, 128, 64, 1, 128, 32768), (64, 8, 1, 1, 0, 2048), (64, 200, 16, 1, 0, 32768),
-           (128, 126, 2, 1, 0, 65536), (16, 320, 40, 1, 64, 32768), (96, 40, 5, 1, 0, 8192), (16, 2000, 9, 4, 300, 4096)]
+           (128, 126, 2, 1, 0, 65536), (16, 320, 40, 1, 64, 32768), (64, 19, 1, 1, 0, 2048), (64, 20, 1, 1, 0, 2048), (16, 96, 6, 1, 0, 4096), (16, 64, 4, 1, 0, 4096),
+           (96, 40, 5, 1, 0, 8192), (16, 2000, 9, 4, 300, 4096)]
     while len(out) < n:
         B = rng.choice([1, 2, 5, 16, 64])
         out.append((rng.choice([1, 3, 8, 16, 20, 32, 40, 48, 64, 96, 100, 128]), B * rng.choice([1, 2, 4, 7, 8, 16, 30]), B,
@@ -34,6 +35,8 @@ def test_groups_are_formed_where_single_tokens_have_no_sm_a_unit():
     assert plan.split(16, 416, 64, 1, 128, 32768, SMS) == [("groups", 171)]   # of up to 8: whole row tiles
     assert plan.split(16, 512, 64, 1, 128, 32768, SMS) == [("groups", 152), ("join", False)]
     assert plan.split(64, 8, 1, 1, 0, 2048, SMS) == [("single", 152), ("join", True)]
+    assert plan.split(64, 19, 1, 1, 0, 2048, SMS) == [("single", 152), ("join", True)]
+    assert plan.split(64, 20, 1, 1, 0, 2048, SMS) == [("single", 152), ("join", False)]
 
 
 @pytest.mark.gpu

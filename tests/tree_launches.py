@@ -54,7 +54,7 @@ def split(H, T, B, words, window, positions, sms):
         ctas = n if whole else min(n * most, sms)
         out.append((KINDS[2 if stack > 1 else 1], ctas))
         if ctas > 1 and not whole:
-            out.append(("join", 4 * n <= ctas <= 256))
+            out.append(("join", 8 * likely <= ctas <= 256))
     return out
 
 
