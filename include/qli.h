@@ -433,10 +433,10 @@ qli_status qli_kv_attention(const qli_kv_attn_args *a, void *workspace, size_t w
  * (number of nodes) + i. Token t sees all positions before the nodes and the nodes
  * i whose bit i % 64 of tree_mask[t * mask_words + i / 64] is set (as a rule the node
  * itself and its ancestors); nodes from 64 * mask_words on are not seen, bits from
- * the number of nodes on mean nothing; mask_words is at most 256. window > 0: the last `window` of the
- * positions it sees. A request of fewer positions than tokens is flagged
- * (QLI_DEVERR_KLEN) and its tokens see none. Without indices and residual, with
- * ratio 1; otherwise arguments, workspace and results as for qli_kv_attention. */
+ * the number of nodes on mean nothing. mask_words is at most 256. window > 0: the
+ * last `window` of the positions it sees. A request of fewer positions than tokens
+ * is flagged (QLI_DEVERR_KLEN) and its tokens see none. Without indices and residual,
+ * with ratio 1; otherwise arguments, workspace and results as for qli_kv_attention. */
 qli_status qli_kv_tree_attention(const qli_kv_attn_args *a, const uint64_t *tree_mask,
                                  int32_t mask_words, void *workspace, size_t workspace_bytes,
                                  void *stream);

@@ -162,11 +162,12 @@ struct Args {
   uint32_t* err;
   int32_t t0, tc;              // tokens of this launch: t0 .. t0 + tc
   int32_t ht;                  // heads per row tile, at most kHT
-  int32_t hg;                  // row tiles per token
+  int32_t hg;                  // row tiles per token, or of a full group
   int32_t whole;               // 1: CTA c has row tile c, whole; 0: even shares
   // workspace
-  int4* cut;                   // [CTAs] the row tile that goes on in the next CTA: token, row tile,
-                               // first unit past it (token -1: none)
+  int4* cut;                   // [CTAs] the row tile that goes on in the next CTA: token (-1: none), row
+                               // tile (of a group: and its tokens << 16), first unit past it, the
+                               // launch's units
   float* piece;                // [2 * CTAs][64][512]
   float* piece_lse;            // [2 * CTAs][64], log2
 };
@@ -1793,14 +1794,22 @@ int64_t most_groups(const Args& d, int64_t tokens) {
 // joined, 19.6 us whole.
 constexpr int kWholeUnits = 2;
 // Those of groups of drafted tokens, whose windows together make a third unit of a
-// window's two, a unit or two more: 64 trees of up to 8 tokens, 16 heads over a window
-// of 128: 30.4 us cut and joined, 21.3 us whole.
+// window's two, a unit or two more. Whole and cut, trees of 8 tokens over a window of 128
+// (three units): 20 trees of 16 heads 18.6 and 19.7 us, 60 of up to 8 tokens 20.5 and 30.1,
+// 20 of 32 heads 18.6 and 26.5; of 192 (four): 20.7 and 21.7, 22.5 and 31.4, 20.4 and 28.0.
+// Fewer heads make a tile's queries cheap and lose up to 60 trees: 20 of 8 heads 20.6 and
+// 19.6, 23.0 and 20.3; 60 22.0 and 26.7, 24.1 and 27.8. Of 256 (five units, cut): 20 of 8
+// heads 24.9 and 20.9, of 16 heads 22.3 and 26.9.
 constexpr int kWholeGroupUnits = 4;
 
 // Tokens that share row tiles: what leaves the fewest rows of the tiles empty, the
 // fewest tokens among equals, and no more than a request has on average. One where every
-// unit (or uncut row tile) of single tokens has an SM of its own: 64 trees of 2 tokens,
-// 16 heads over a window of 128: 18.0 us by two, 11.3 by one.
+// unit (or uncut row tile) of single tokens has an SM of its own. Single and sharing, 16
+// heads over a window of 128: 64 trees of 2 tokens 11.4 and 17.3 us, 38 of 4 tokens (an SM
+// each) 11.5 and 19.9, 40 18.3 and 19.8, 64 20.5 and 20.2. Where tiles are cut the turn lies
+// further on, and not at one place: a tree of 4 tokens over 2048 positions (0.8 units an SM)
+// 14.1 and 18.1, 3136 (1.3) 21.4 and 21.0, 5568 (2.3) 20.3 and 25.9; 4 trees of 8 tokens over
+// 704 (2.3) 18.6 and 18.3; of 40 heads over 1536 (5) 28.7 and 25.5.
 int32_t stack_of(Args d, int sms) {
   const int32_t most = (d.T - 1) / (d.B > 0 ? d.B : 1) + 1;
   const auto tiles = [&](int64_t k) { return (k * d.H - 1) / kHT + 1; };
@@ -1871,7 +1880,10 @@ cudaError_t launch(Args d, int sms, cudaStream_t s) {
   for (d.t0 = 0; e == cudaSuccess && d.t0 < d.T; d.t0 += chunk) {
     d.tc = d.T - d.t0 < chunk ? d.T - d.t0 : chunk;
     const int64_t tiles = most_groups(d, d.tc) * d.hg;
-    // between the row tiles there are if all groups are full and if none is
+    // Between the row tiles there are if all groups are full and if none is. By the first
+    // number alone 64 trees of 8 tokens, 16 heads, a window of 128 would be whole (20.5 us,
+    // cut 26.2), and 56 of 9 tokens too (32.2, cut 30.3: more tiles than SMs); by the second
+    // 48 of 9 tokens would be cut (29.9, whole 20.5).
     const int64_t likely = (tiles + (static_cast<int64_t>(d.tc) - 1 + d.stack) / d.stack * d.hg) / 2;
     d.whole = d.stack > 1 ? most <= kWholeGroupUnits && likely <= sms : most <= kWholeUnits && tiles <= sms;
     // one CTA per SM, and no more than there can be units
