@@ -528,7 +528,8 @@ typedef struct qli_row_prep {
  * to BF16 (quant_mode 0; width 64, 128, 256 or 512) or, for the indexer's queries
  * (width 128), to the codes and scales of qli_quantize_q (QLI_QUANT_INT8) or
  * qli_quantize_q_fp8 (QLI_QUANT_FP8), taken of the FP32 values. BF16 results may
- * replace x (same pointer and strides). One kernel on `stream`; asynchronous. */
+ * replace x (same pointer and strides); otherwise out, scale_out and x do not overlap.
+ * One kernel on `stream`; asynchronous. */
 typedef struct qli_prepare_args {
     const uint16_t *x;           /* as in qli_rotate_args */
     int64_t x_stride_t, x_stride_h;
@@ -548,10 +549,10 @@ qli_status qli_prepare_q(const qli_prepare_args *a, const qli_row_prep *prep, vo
  * qli_write_kv) and index K rows of 128 (the 8-bit rows of qli_write_index_k), the
  * codes taken of the FP32 values. Either kind may be left out (NULL). Slots,
  * padding, distinctness and err_word as for qli_write_kv; the parts of a page that
- * are written must not overlap. A row with Inf or NaN does not reach other rows: 8-bit
- * KV rows that are not finite after norm and rotation get a scale of NaN, so that what attends
- * to them is NaN too; other such rows unspecified codes. One kernel on `stream`;
- * asynchronous. */
+ * are written must not overlap each other or the inputs. A row with Inf or NaN does
+ * not reach other rows: an 8-bit KV row that is not finite after norm and rotation
+ * gets a scale of NaN, so that what attends to it is NaN too; any other such row
+ * unspecified codes. One kernel on `stream`; asynchronous. */
 typedef struct qli_append_args {
     const uint16_t *kv;          /* row i: 512 BF16 values at kv + i * kv_stride (elements, a multiple
                                     of 8, at least 512), 16-byte aligned; or NULL */

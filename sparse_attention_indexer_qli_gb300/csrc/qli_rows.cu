@@ -339,7 +339,7 @@ __device__ __forceinline__ float largest(float a, float b, float c) {
 // the quotient as the other writers take it (qli_codes.cuh), two at a time. E4M3 has two
 // zeros, and the quotient's is x's: the correction step ends in +0 where x / s is a zero, so
 // it works on -x / s, whose zeros are +0 then for x < 0 and -0 for x > 0, and the codes'
-// signs are turned over (4096 tokens of 64 heads: 23.2 us, 22.95 without).
+// signs are turned over (4096 tokens of 64 heads: 23.1 us, 22.8 without).
 template <int G, bool kFp8>
 __device__ __forceinline__ uint16_t quantise(const Unit (&v)[2], uint2 (&codes)[2]) {
   float m = 0.0f;
@@ -573,7 +573,7 @@ constexpr int kSets = 4;
 // ---- queries --------------------------------------------------------------------
 // Bound by HBM with BF16 results: 2047 tokens of 64 heads x 512 with RMS norm and a
 // rotated tail (268 MB) take 43 us, 6.2 TB/s. With codes by the instructions, some 16 a
-// value: 4096 tokens of 64 heads x 128 to E4M3 (101 MB) take 22.7 us, 4.4 TB/s, with 68%
+// value: 4096 tokens of 64 heads x 128 to E4M3 (101 MB) take 23.1 us, 4.4 TB/s, with 68%
 // of the issue slots taken. One set of rows a block, without the next one in flight,
 // took 59 and 32 us; the norm's and the layout's branches inside the loop 51 and 26.
 template <int D, int kMode, bool kSmall>
@@ -625,7 +625,7 @@ struct AppendArgs {
 
 // A block takes a few tokens: their KV rows, then their index K rows, by one table where
 // they turn alike. Bound by the instructions, some 450 of a warp a token: 65536 tokens to
-// E4M3 (127 MB) take 38 us, 3.3 TB/s; separate blocks for the two kinds, each with its
+// E4M3 (127 MB) take 38.6 us, 3.3 TB/s; separate blocks for the two kinds, each with its
 // table, took 54.
 template <int kKv, int kIndex, bool kSmall>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)

@@ -990,7 +990,7 @@ def rotate(x, positions, rotary: Rotary, *, offset: int = 0, inverse: bool = Fal
     """qli_rotate: x [T, H, D] (BF16, CUDA, unit stride in D) with the rotary.dim
     values from `offset` on (a multiple of 8) of every head rotated by its token's
     position in positions [T] (int32); inverse=True undoes that. out=x rotates in
-    place. Returns out [T, H, D]."""
+    place; any other out shares no memory with x. Returns out [T, H, D]."""
     import torch
     device = _first_cuda("x", x, torch.bfloat16, torch.cuda.current_device)
     shape, strides = x.shape, x.stride()
@@ -1013,8 +1013,9 @@ def prepare_q(x, positions, prep: RowPrep, *, out=None, scale_out=None, stream=N
     """qli_prepare_q: the norm and rotation of `prep` on every row of x [T, H, width]
     (BF16, CUDA, unit stride in the last dim; width 64, 128, 256 or 512) at its
     token's position in positions [T] (int32; None without a rotation). Returns out
-    [T, H, width] BF16 (out=x in place), or with quant_mode (rows of 128) the codes
-    int8 [T, H, 128] and FP16 scale bits int16 [T, H], as quantize_q does."""
+    [T, H, width] BF16 (out=x in place; any other out shares no memory with x), or with
+    quant_mode (rows of 128) the codes int8 [T, H, 128] and FP16 scale bits int16
+    [T, H], as quantize_q does."""
     import torch
     device = _first_cuda("x", x, torch.bfloat16, torch.cuda.current_device)
     shape, strides = x.shape, x.stride()
