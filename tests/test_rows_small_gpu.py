@@ -80,20 +80,30 @@ def test_rows_of_all_sizes_rotated(dim, offset, half, norm, quant):
         near_codes(codes.cpu().numpy().view(np.uint8)[:, 0], scales.cpu().numpy().view(np.uint16)[:, 0], y, err, quant)
 
 
+def of_usual_size(D, seed):
+    return kv8.f32_to_bf16(np.random.default_rng(seed).standard_normal((210, D)))
+
+
+@pytest.mark.parametrize("kinds", ["both", "kv-small", "index-small", "index-plain"])
 @pytest.mark.parametrize("norm", ["rms", "layer"])
-def test_cache_rows_of_all_sizes(norm):
+def test_cache_rows_of_all_sizes(norm, kinds):
+    """Also with the other kind under a usual eps, or without a norm."""
     import torch
-    x, k, n, stride = rows_of_all_sizes(512, 31), rows_of_all_sizes(128, 32), 210, 128 * (1024 + 130)
+    eps = {"both": (0.0, 0.0), "kv-small": (0.0, 1e-5), "index-small": (1e-5, 0.0), "index-plain": (0.0, None)}[kinds]
+    x, k = (rows_of_all_sizes(d, 31) if e == 0.0 else of_usual_size(d, 32) for d, e in zip((512, 128), eps))
+    n, stride = 210, 128 * (1024 + 130)
     w, wk = (np.random.default_rng(33).uniform(0.5, 2, d).astype(np.float32) for d in (512, 128))
+    index = qli.RowPrep(128) if eps[1] is None else qli.RowPrep(128, norm=norm, weight=up(wk), eps=eps[1])
     cache = torch.zeros(2, stride, dtype=torch.uint8, device="cuda")
     qli.append_kv(bf16_up(x), bf16_up(k), None, torch.arange(n, device="cuda"), cache, rows_per_page=128, page_stride=stride,
                   kv_mode=qli.KV_BF16, quant_mode=qli.QUANT_FP8, k_offset=128 * 1024, scale_offset=128 * 1152,
-                  kv_prep=qli.RowPrep(512, norm=norm, weight=up(w), eps=0.0),
-                  index_prep=qli.RowPrep(128, norm=norm, weight=up(wk), eps=0.0))
+                  kv_prep=qli.RowPrep(512, norm=norm, weight=up(w), eps=eps[0]), index_prep=index)
     page = cache.cpu().numpy()
     part = lambda at, width, kind: page[:, at:at + 128 * width].copy().view(kind).reshape(256, -1)[:n]  # noqa: E731
-    near_bf16(kv8.bf16_to_f64(part(0, 1024, np.uint16)), *normed(x, norm, w, None, 0.0))
-    near_codes(part(128 * 1024, 128, np.uint8), part(128 * 1152, 2, np.uint16)[:, 0], *normed(k, norm, wk, None, 0.0), kv8.FP8)
+    near_bf16(kv8.bf16_to_f64(part(0, 1024, np.uint16)), *normed(x, norm, w, None, float(np.float32(eps[0]))))
+    y, err = ((kv8.bf16_to_f64(k), np.zeros(k.shape)) if eps[1] is None else
+              normed(k, norm, wk, None, float(np.float32(eps[1]))))
+    near_codes(part(128 * 1024, 128, np.uint8), part(128 * 1152, 2, np.uint16)[:, 0], y, err, kv8.FP8)
 
 
 @pytest.mark.parametrize("norm", ["rms", "layer"])
